@@ -15,7 +15,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libe4b.so")
-SOURCES = ["api.cu", "route.cu", "gemm.cu", "stream.cu", "serve.cu", "noalloc.cu"]
+SOURCES = ["api.cu", "route.cu", "gemm.cu", "stream.cu", "serve.cu", "noalloc.cu",
+           "adapters.cu", "balance.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-DNDEBUG"]
@@ -30,7 +31,7 @@ def nvcc() -> str:
 
 def _deps_mtime() -> float:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(os.path.dirname(PKG), "include", "e4b.h"))
+    files += [os.path.join(os.path.dirname(PKG), "include", h) for h in ("e4b.h", "e4b_operators.h")]
     files.append(os.path.abspath(__file__))
     return max(os.path.getmtime(f) for f in files)
 

@@ -113,6 +113,100 @@ e4b_status check_bwd(const e4b_bwd_buffers* b) {
   return E4B_OK;
 }
 
+bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+e4b_status check_proj_dims(const e4b_proj_dims* d, int32_t T) {
+  if (d == nullptr || T < 0) return E4B_ERR_INVALID_ARG;
+  if (d->K <= 0 || d->K % 64 || d->K > (1 << 20) || d->N <= 0 || d->N % 8 || d->N > (1 << 20))
+    return E4B_ERR_UNSUPPORTED;
+  if (d->n_adapters < 1 || d->n_adapters > E4B_MAX_ADAPTERS) return E4B_ERR_UNSUPPORTED;
+  if (d->r < 8 || d->r > E4B_MAX_RANK || d->r % 8) return E4B_ERR_UNSUPPORTED;
+  if (d->blocksize != 64) return E4B_ERR_UNSUPPORTED;
+  if (T > (1 << 24)) return E4B_ERR_UNSUPPORTED;
+  return E4B_OK;
+}
+
+// Workspace of the serving call: the error word, then the grouping and p.
+struct ServeProjLayout {
+  size_t order, offsets, steps, low, total;
+};
+ServeProjLayout serve_proj_layout(const e4b_proj_dims* d, int32_t T) {
+  auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+  const int64_t rows = adapter_rows_cap(T, d->n_adapters);
+  ServeProjLayout l;
+  l.order = sizeof(DeviceError);
+  l.offsets = l.order + up((size_t)rows * 4);
+  l.steps = l.offsets + up((size_t)(d->n_adapters + 2) * 4);
+  l.low = l.steps + up((size_t)adapter_steps_layout(rows, d->n_adapters).total * 4);
+  l.total = l.low + up((size_t)rows * d->r * 2);
+  return l;
+}
+
+e4b_status check_groups(const e4b_adapter_groups* g) {
+  if (g == nullptr || !aligned16(g->order) || !aligned16(g->offsets) || !aligned16(g->steps))
+    return E4B_ERR_INVALID_ARG;
+  return E4B_OK;
+}
+
+e4b_status check_projection(const e4b_nf4_matrix* b, const e4b_adapter_factors* a) {
+  if (b == nullptr || !aligned16(b->nf4) || !aligned16(b->absmax)) return E4B_ERR_INVALID_ARG;
+  if (a == nullptr || !aligned16(a->A) || !aligned16(a->B) || !aligned4(a->scale)) return E4B_ERR_INVALID_ARG;
+  return E4B_OK;
+}
+
+AdapterProjHost proj_host(const e4b_proj_dims* d, int32_t T, const e4b_nf4_matrix* base,
+                          const e4b_adapter_factors* ad, const int32_t* order, const int32_t* offsets,
+                          const int32_t* steps, void* ws) {
+  AdapterProjHost h{};
+  h.T = T;
+  h.K = d->K;
+  h.N = d->N;
+  h.n = d->n_adapters;
+  h.r = d->r;
+  if (base != nullptr) {
+    h.nf4 = base->nf4;
+    h.absmax = base->absmax;
+  }
+  if (ad != nullptr) h.scale = ad->scale;
+  h.order = order;
+  h.offsets = offsets;
+  h.steps = steps;
+  h.rows_cap = adapter_rows_cap(T, d->n_adapters);
+  h.err = static_cast<DeviceError*>(ws);
+  h.timeout_ns = kDefaultTimeoutNs;
+  return h;
+}
+
+e4b_status check_balance_dims(const e4b_balance_dims* d, int32_t T) {
+  if (d == nullptr || T < 0) return E4B_ERR_INVALID_ARG;
+  if (d->E < 1 || d->E > E4B_MAX_EXPERTS) return E4B_ERR_UNSUPPORTED;
+  if (d->top_k < 1 || d->top_k > d->E || d->top_k > E4B_MAX_TOP_K) return E4B_ERR_UNSUPPORTED;
+  if (d->S < 1 || d->S > (1 << 20) || T > (1 << 24)) return E4B_ERR_UNSUPPORTED;
+  if (!isfinite(d->balance_coef) || !isfinite(d->z_coef)) return E4B_ERR_INVALID_ARG;
+  return E4B_OK;
+}
+
+BalanceHost balance_host(const e4b_balance_dims* d, int32_t T, const float* logits, const int32_t* ids,
+                         const int32_t* seq_offsets, const uint8_t* mask, const e4b_balance_stats* st, float* loss) {
+  BalanceHost h{};
+  h.T = T;
+  h.E = d->E;
+  h.k = d->top_k;
+  h.S = d->S;
+  h.c_b = d->balance_coef;
+  h.c_z = d->z_coef;
+  h.logits = logits;
+  h.ids = ids;
+  h.offsets = seq_offsets;
+  h.mask = mask;
+  h.counts = st->counts;
+  h.prob_sum = st->prob_sum;
+  h.tokens = st->tokens;
+  h.lse = st->lse;
+  h.loss = loss;
+  return h;
+}
+
 #define E4B_TRY(expr)                     \
   do {                                    \
     const e4b_status _s = (expr);         \
@@ -640,6 +734,151 @@ e4b_status e4b_nf4_quantize(const e4b_bf16* w, int64_t n, uint8_t* packed, float
   int sms = 0;
   E4B_CUDA(device_sms(&sms));
   E4B_CUDA(launch_nf4_quantize(reinterpret_cast<const uint16_t*>(w), n, packed, absmax, sms, (cudaStream_t)stream));
+  return E4B_OK;
+}
+
+e4b_status e4b_proj_get_sizes(const e4b_proj_dims* dims, int32_t T, e4b_proj_sizes* out) {
+  E4B_TRY(check_proj_dims(dims, T));
+  if (out == nullptr) return E4B_ERR_INVALID_ARG;
+  out->rows_cap = adapter_rows_cap(T, dims->n_adapters);
+  out->steps_cap = adapter_steps_layout(out->rows_cap, dims->n_adapters).total;
+  out->workspace_bytes = sizeof(DeviceError);
+  out->serve_workspace_bytes = serve_proj_layout(dims, T).total;
+  return E4B_OK;
+}
+
+e4b_status e4b_adapter_group(const e4b_proj_dims* dims, int32_t T, const int32_t* ids,
+                             const e4b_adapter_groups* groups, e4b_stream_t stream) {
+  E4B_TRY(check_proj_dims(dims, T));
+  if (T == 0) return E4B_OK;  // nothing is read or written: T-sized pointers may be NULL
+  E4B_TRY(check_groups(groups));
+  if (!aligned4(ids)) return E4B_ERR_INVALID_ARG;
+  E4B_CUDA(launch_adapter_group(ids, T, dims->n_adapters, groups->order, groups->offsets, groups->steps,
+                                (cudaStream_t)stream));
+  return E4B_OK;
+}
+
+e4b_status e4b_multi_lora_serve_fwd(const e4b_proj_dims* dims, int32_t T, const int32_t* ids, const e4b_bf16* x,
+                                    const e4b_nf4_matrix* base, const e4b_adapter_factors* adapters, e4b_bf16* y,
+                                    void* ws, size_t ws_bytes, e4b_stream_t stream) {
+  E4B_TRY(check_proj_dims(dims, T));
+  if (T == 0) return E4B_OK;
+  if (!aligned16(ws)) return E4B_ERR_INVALID_ARG;
+  const ServeProjLayout l = serve_proj_layout(dims, T);
+  if (ws_bytes < l.total) return E4B_ERR_WORKSPACE_TOO_SMALL;
+  E4B_TRY(check_projection(base, adapters));
+  if (!aligned4(ids) || !aligned16(x) || !aligned16(y)) return E4B_ERR_INVALID_ARG;
+  const cudaStream_t st = (cudaStream_t)stream;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  int32_t* order = reinterpret_cast<int32_t*>(w + l.order);
+  int32_t* offsets = reinterpret_cast<int32_t*>(w + l.offsets);
+  int32_t* steps = reinterpret_cast<int32_t*>(w + l.steps);
+  uint16_t* low = reinterpret_cast<uint16_t*>(w + l.low);
+  const AdapterProjHost h = proj_host(dims, T, base, adapters, order, offsets, steps, ws);
+  E4B_CUDA(launch_adapter_group(ids, T, dims->n_adapters, order, offsets, steps, st));
+  E4B_CUDA(launch_adapter_rows(h, false, x, adapters->A, low, st));
+  E4B_CUDA(launch_adapter_gemm(h, false, x, low, adapters->B, y, st));
+  return E4B_OK;
+}
+
+e4b_status e4b_multi_lora_fwd(const e4b_proj_dims* dims, int32_t T, const e4b_adapter_groups* groups,
+                              const e4b_bf16* x, const e4b_nf4_matrix* base, const e4b_adapter_factors* adapters,
+                              e4b_bf16* p, e4b_bf16* y, void* ws, size_t ws_bytes, e4b_stream_t stream) {
+  E4B_TRY(check_proj_dims(dims, T));
+  if (T == 0) return E4B_OK;
+  if (!aligned16(ws)) return E4B_ERR_INVALID_ARG;
+  if (ws_bytes < sizeof(DeviceError)) return E4B_ERR_WORKSPACE_TOO_SMALL;
+  E4B_TRY(check_groups(groups));
+  E4B_TRY(check_projection(base, adapters));
+  if (!aligned16(x) || !aligned16(p) || !aligned16(y)) return E4B_ERR_INVALID_ARG;
+  const cudaStream_t st = (cudaStream_t)stream;
+  const AdapterProjHost h = proj_host(dims, T, base, adapters, groups->order, groups->offsets, groups->steps, ws);
+  E4B_CUDA(launch_adapter_rows(h, false, x, adapters->A, p, st));
+  E4B_CUDA(launch_adapter_gemm(h, false, x, p, adapters->B, y, st));
+  return E4B_OK;
+}
+
+e4b_status e4b_multi_lora_dgrad(const e4b_proj_dims* dims, int32_t T, const e4b_adapter_groups* groups,
+                                const e4b_bf16* dY, const e4b_nf4_matrix* base, const e4b_adapter_factors* adapters,
+                                e4b_bf16* q, e4b_bf16* dx, void* ws, size_t ws_bytes, e4b_stream_t stream) {
+  E4B_TRY(check_proj_dims(dims, T));
+  if (T == 0) return E4B_OK;
+  if (!aligned16(ws)) return E4B_ERR_INVALID_ARG;
+  if (ws_bytes < sizeof(DeviceError)) return E4B_ERR_WORKSPACE_TOO_SMALL;
+  E4B_TRY(check_groups(groups));
+  E4B_TRY(check_projection(base, adapters));
+  if (!aligned16(dY) || !aligned16(q) || !aligned16(dx)) return E4B_ERR_INVALID_ARG;
+  const cudaStream_t st = (cudaStream_t)stream;
+  const AdapterProjHost h = proj_host(dims, T, base, adapters, groups->order, groups->offsets, groups->steps, ws);
+  E4B_CUDA(launch_adapter_rows(h, true, dY, adapters->B, q, st));
+  E4B_CUDA(launch_adapter_gemm(h, true, dY, q, adapters->A, dx, st));
+  return E4B_OK;
+}
+
+e4b_status e4b_multi_lora_wgrad(const e4b_proj_dims* dims, int32_t T, const e4b_adapter_groups* groups,
+                                const e4b_bf16* x, const e4b_bf16* dY, const e4b_bf16* p, const e4b_bf16* q,
+                                e4b_bf16* dA, e4b_bf16* dB, void* ws, size_t ws_bytes, e4b_stream_t stream) {
+  E4B_TRY(check_proj_dims(dims, T));
+  if (!aligned16(ws)) return E4B_ERR_INVALID_ARG;
+  if (ws_bytes < sizeof(DeviceError)) return E4B_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned16(dA) || !aligned16(dB)) return E4B_ERR_INVALID_ARG;
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (T == 0) {
+    // No tokens: every gradient is exactly zero.
+    E4B_CUDA(cudaMemsetAsync(dA, 0, (size_t)dims->n_adapters * dims->r * dims->K * 2, st));
+    E4B_CUDA(cudaMemsetAsync(dB, 0, (size_t)dims->n_adapters * dims->r * dims->N * 2, st));
+    return E4B_OK;
+  }
+  E4B_TRY(check_groups(groups));
+  if (!aligned16(x) || !aligned16(dY) || !aligned16(p) || !aligned16(q)) return E4B_ERR_INVALID_ARG;
+  const AdapterProjHost h = proj_host(dims, T, nullptr, nullptr, groups->order, groups->offsets, groups->steps, ws);
+  E4B_CUDA(launch_adapter_wgrad(h, x, dY, p, q, dA, dB, st));
+  return E4B_OK;
+}
+
+e4b_status e4b_balance_get_sizes(const e4b_balance_dims* dims, int32_t T, size_t* workspace_bytes) {
+  E4B_TRY(check_balance_dims(dims, T));
+  if (workspace_bytes == nullptr) return E4B_ERR_INVALID_ARG;
+  *workspace_bytes = balance_workspace_bytes(T, dims->E, dims->S);
+  return E4B_OK;
+}
+
+e4b_status e4b_balance_fwd(const e4b_balance_dims* dims, int32_t T, const float* logits, const int32_t* topk_ids,
+                           const int32_t* seq_offsets, const uint8_t* token_mask, const e4b_balance_stats* stats,
+                           float* loss, void* ws, size_t ws_bytes, e4b_stream_t stream) {
+  E4B_TRY(check_balance_dims(dims, T));
+  if (stats == nullptr || !aligned16(stats->counts) || !aligned16(stats->prob_sum) || !aligned16(stats->tokens) ||
+      !aligned4(loss))
+    return E4B_ERR_INVALID_ARG;
+  if (seq_offsets == nullptr ? dims->S != 1 : !aligned4(seq_offsets)) return E4B_ERR_INVALID_ARG;
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (T == 0) {
+    E4B_CUDA(cudaMemsetAsync(stats->counts, 0, (size_t)dims->S * dims->E * 4, st));
+    E4B_CUDA(cudaMemsetAsync(stats->prob_sum, 0, (size_t)dims->S * dims->E * 4, st));
+    E4B_CUDA(cudaMemsetAsync(stats->tokens, 0, (size_t)(dims->S + 2) * 4, st));
+    E4B_CUDA(cudaMemsetAsync(loss, 0, 12, st));
+    return E4B_OK;
+  }
+  if (!aligned16(ws)) return E4B_ERR_INVALID_ARG;
+  if (ws_bytes < balance_workspace_bytes(T, dims->E, dims->S)) return E4B_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(stats->lse)) return E4B_ERR_INVALID_ARG;
+  E4B_CUDA(launch_balance_fwd(balance_host(dims, T, logits, topk_ids, seq_offsets, token_mask, stats, loss), ws, st));
+  return E4B_OK;
+}
+
+e4b_status e4b_balance_bwd(const e4b_balance_dims* dims, int32_t T, const float* logits, const int32_t* seq_offsets,
+                           const uint8_t* token_mask, const e4b_balance_stats* stats, const float* dloss,
+                           int32_t accumulate, float* d_logits, e4b_stream_t stream) {
+  E4B_TRY(check_balance_dims(dims, T));
+  if (T == 0) return E4B_OK;  // nothing is read or written: T-sized pointers may be NULL
+  if (stats == nullptr || !aligned16(stats->counts) || !aligned16(stats->tokens) || !aligned16(stats->lse) ||
+      !aligned16(logits) || !aligned16(d_logits) || (dloss != nullptr && !aligned4(dloss)))
+    return E4B_ERR_INVALID_ARG;
+  if (seq_offsets == nullptr ? dims->S != 1 : !aligned4(seq_offsets)) return E4B_ERR_INVALID_ARG;
+  int sms = 0;
+  E4B_CUDA(device_sms(&sms));
+  E4B_CUDA(launch_balance_bwd(balance_host(dims, T, logits, nullptr, seq_offsets, token_mask, stats, nullptr), dloss,
+                              accumulate != 0, d_logits, sms, (cudaStream_t)stream));
   return E4B_OK;
 }
 

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "../../include/e4b.h"
+#include "../../include/e4b_operators.h"
 
 namespace e4b {
 
@@ -192,6 +193,70 @@ struct WgradHost {
   long long timeout_ns;
 };
 cudaError_t launch_wgrad(const WgradHost& h, int num_sms, cudaStream_t stream);
+
+// ---- adapters beside a shared projection (adapters.cu)
+constexpr int kAdapterUnitRows = 256;  // rows of a GEMM unit (a CTA pair)
+constexpr int kAdapterTaskRows = 128;  // rows of a low-rank projection task (one adapter's)
+inline int64_t adapter_rows_cap(int64_t T, int n) {
+  const int64_t groups = T < n + 1 ? T : n + 1;
+  return (T + 15 * groups + 255) / 256 * 256;
+}
+// Work list layout (int32): header ([0] units, [1] rows used, [2] entries, [3] tasks), the first entry of
+// each 256-row unit, entries (adapter, unit, first row, end row of the adapter) by unit with a sentinel
+// (unit -1), tasks (adapter, first row, end row of the adapter, 0).
+struct AdapterSteps {
+  int unit_start, entries, tasks;
+  int64_t total;
+};
+__host__ __device__ inline AdapterSteps adapter_steps_layout(int64_t rows_cap, int n) {
+  const int64_t units = rows_cap / kAdapterUnitRows;
+  AdapterSteps a;
+  a.unit_start = 8;
+  a.entries = (int)((8 + units + 1 + 3) / 4 * 4);
+  a.tasks = (int)(a.entries + 4 * (units + n + 1));
+  a.total = a.tasks + 4 * (rows_cap / kAdapterTaskRows + n);
+  return a;
+}
+cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int32_t* order, int32_t* offsets, int32_t* steps,
+                                 cudaStream_t stream);
+
+struct AdapterProjHost {
+  int T, K, N, n, r;
+  const uint8_t* nf4;      // [N, K/2]
+  const float* absmax;     // [N, K/64]
+  const float* scale;      // [n]
+  const int32_t *order, *offsets, *steps;
+  int64_t rows_cap;
+  DeviceError* err;
+  long long timeout_ns;
+};
+// out[row, :r] = bf16(s[a] src[t] . factor[a]): A [n, r, K] over x, or (mn) B [n, N, r] over dY.
+cudaError_t launch_adapter_rows(const AdapterProjHost& h, bool mn, const uint16_t* src, const uint16_t* fac,
+                                uint16_t* out, cudaStream_t stream);
+// out[t] = src[t] W^T + low[row] B[a]^T, or (mn) src[t] W + low[row] A[a].
+cudaError_t launch_adapter_gemm(const AdapterProjHost& h, bool mn, const uint16_t* src, const uint16_t* low,
+                                const uint16_t* fac, uint16_t* out, cudaStream_t stream);
+cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, const uint16_t* dY, const uint16_t* p,
+                                 const uint16_t* q, uint16_t* dA, uint16_t* dB, cudaStream_t stream);
+
+// ---- balance loss (balance.cu)
+struct BalanceHost {
+  int T, E, k, S;
+  float c_b, c_z;
+  const float* logits;
+  const int32_t* ids;
+  const int32_t* offsets;  // [S + 1] or nullptr
+  const uint8_t* mask;     // [T] or nullptr
+  int32_t* counts;
+  float* prob_sum;
+  int32_t* tokens;
+  float* lse;
+  float* loss;
+};
+size_t balance_workspace_bytes(int T, int E, int S);
+cudaError_t launch_balance_fwd(const BalanceHost& h, void* ws, cudaStream_t stream);
+cudaError_t launch_balance_bwd(const BalanceHost& h, const float* dloss, bool accumulate, float* d_logits,
+                               int num_sms, cudaStream_t stream);
 
 // Tensor maps of the operands (gemm.cu): row-major bf16 [rows, cols], bf16
 // stacks [E, rows, cols], byte stacks [E, rows, bytes].

@@ -1,4 +1,5 @@
-"""Python binding of the C ABI in ``include/e4b.h`` (ctypes; argument marshalling only).
+"""Python binding of the C ABI in ``include/e4b.h`` and ``include/e4b_operators.h`` (ctypes; argument marshalling
+only).
 
 Every function here forwards to the entry point of the same name in
 ``libe4b.so``; all computation runs in that library's CUDA kernels.  Tensors
@@ -25,6 +26,7 @@ from typing import Optional
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libe4b.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "e4b.h")
+OPERATORS_HEADER = os.path.join(os.path.dirname(PKG), "include", "e4b_operators.h")
 
 c_i32, c_i64, c_f32, c_vp, c_sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
 
@@ -72,6 +74,35 @@ class Sizes(ctypes.Structure):
     _fields_ = [("slots", c_i64), ("rows_cap", c_i64), ("tiles_cap", c_i64), ("workspace_bytes", c_sz)]
 
 
+class ProjDimsC(ctypes.Structure):
+    _fields_ = [("K", c_i32), ("N", c_i32), ("n_adapters", c_i32), ("r", c_i32), ("blocksize", c_i32)]
+
+
+class Nf4Matrix(ctypes.Structure):
+    _fields_ = [("nf4", c_vp), ("absmax", c_vp)]
+
+
+class AdapterFactors(ctypes.Structure):
+    _fields_ = [("A", c_vp), ("B", c_vp), ("scale", c_vp)]
+
+
+class AdapterGroups(ctypes.Structure):
+    _fields_ = [("order", c_vp), ("offsets", c_vp), ("steps", c_vp)]
+
+
+class ProjSizes(ctypes.Structure):
+    _fields_ = [("rows_cap", c_i64), ("steps_cap", c_i64), ("workspace_bytes", c_sz),
+                ("serve_workspace_bytes", c_sz)]
+
+
+class BalanceDims(ctypes.Structure):
+    _fields_ = [("E", c_i32), ("top_k", c_i32), ("S", c_i32), ("balance_coef", c_f32), ("z_coef", c_f32)]
+
+
+class BalanceStats(ctypes.Structure):
+    _fields_ = [("counts", c_vp), ("prob_sum", c_vp), ("tokens", c_vp), ("lse", c_vp)]
+
+
 class KernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 48), ("launches", c_i64), ("total_ms", ctypes.c_double)]
 
@@ -106,6 +137,23 @@ _SIGNATURES = {
                                     c_vp, c_vp]),
     "e4b_nf4_dequant": (c_i32, [c_vp, c_vp, c_i64, c_vp, c_vp]),
     "e4b_nf4_quantize": (c_i32, [c_vp, c_i64, c_vp, c_vp, c_vp]),
+    "e4b_proj_get_sizes": (c_i32, [ctypes.POINTER(ProjDimsC), c_i32, ctypes.POINTER(ProjSizes)]),
+    "e4b_adapter_group": (c_i32, [ctypes.POINTER(ProjDimsC), c_i32, c_vp, ctypes.POINTER(AdapterGroups), c_vp]),
+    "e4b_multi_lora_serve_fwd": (c_i32, [ctypes.POINTER(ProjDimsC), c_i32, c_vp, c_vp, ctypes.POINTER(Nf4Matrix),
+                                         ctypes.POINTER(AdapterFactors), c_vp, c_vp, c_sz, c_vp]),
+    "e4b_multi_lora_fwd": (c_i32, [ctypes.POINTER(ProjDimsC), c_i32, ctypes.POINTER(AdapterGroups), c_vp,
+                                   ctypes.POINTER(Nf4Matrix), ctypes.POINTER(AdapterFactors), c_vp, c_vp, c_vp, c_sz,
+                                   c_vp]),
+    "e4b_multi_lora_dgrad": (c_i32, [ctypes.POINTER(ProjDimsC), c_i32, ctypes.POINTER(AdapterGroups), c_vp,
+                                     ctypes.POINTER(Nf4Matrix), ctypes.POINTER(AdapterFactors), c_vp, c_vp, c_vp,
+                                     c_sz, c_vp]),
+    "e4b_multi_lora_wgrad": (c_i32, [ctypes.POINTER(ProjDimsC), c_i32, ctypes.POINTER(AdapterGroups), c_vp, c_vp,
+                                     c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "e4b_balance_get_sizes": (c_i32, [ctypes.POINTER(BalanceDims), c_i32, ctypes.POINTER(c_sz)]),
+    "e4b_balance_fwd": (c_i32, [ctypes.POINTER(BalanceDims), c_i32, c_vp, c_vp, c_vp, c_vp,
+                                ctypes.POINTER(BalanceStats), c_vp, c_vp, c_sz, c_vp]),
+    "e4b_balance_bwd": (c_i32, [ctypes.POINTER(BalanceDims), c_i32, c_vp, c_vp, c_vp, ctypes.POINTER(BalanceStats),
+                                c_vp, c_i32, c_vp, c_vp]),
     "e4b_debug_watchdog": (c_i32, [c_vp, c_sz, c_i64, c_vp]),
     "e4b_profiler_enable": (c_i32, [c_i32]),
     "e4b_profiler_read": (c_i32, [ctypes.POINTER(KernelTime), c_i32, ctypes.POINTER(c_i32)]),
@@ -290,6 +338,19 @@ def e4b_launch_count() -> int:
     return int(lib().e4b_launch_count())
 
 
+def e4b_proj_get_sizes(dims: "ProjDims", T: int) -> ProjSizes:
+    out = ProjSizes()
+    d = dims.c()
+    _check(lib().e4b_proj_get_sizes(ctypes.byref(d), T, ctypes.byref(out)), "e4b_proj_get_sizes")
+    return out
+
+
+def e4b_balance_get_sizes(dims: BalanceDims, T: int) -> int:
+    out = c_sz(0)
+    _check(lib().e4b_balance_get_sizes(ctypes.byref(dims), T, ctypes.byref(out)), "e4b_balance_get_sizes")
+    return int(out.value)
+
+
 class Block:
     """Device buffers of one block problem (``dims``, ``T`` tokens), allocated with torch.
 
@@ -465,3 +526,208 @@ def nf4_experts(gate_up_nf4, gate_up_absmax, down_nf4, down_absmax) -> Nf4Expert
 def lora_factors(A_gu, B_gu, A_d, B_d) -> Lora:
     """The per-expert LoRA factors, bf16 [E,r,H], [E,2I,r], [E,r,I], [E,H,r]."""
     return _make_struct(Lora, (A_gu, B_gu, A_d, B_d), ("bf16",) * 4)
+
+
+def _cuda_device(device):
+    import torch
+    dev = torch.device(device)
+    if dev.type != "cuda":
+        raise ValueError("device: a CUDA device is required, got %s" % dev)
+    return dev if dev.index is not None else torch.device("cuda", torch.cuda.current_device())
+
+
+def _alloc(shape, dtype, device):
+    """Zeroed tensor of ``shape`` whose address is valid (and 16-byte aligned) even when it is empty."""
+    import torch
+    n = 1
+    for d in shape:
+        n *= d
+    return torch.zeros(max(n, 8), dtype=dtype, device=device)[:n].view(*shape)
+
+
+class _OnDevice:
+    """Calls on the object's device, whatever device is current: its current stream by default, or a
+    stream of that device (a stream of another device is refused)."""
+
+    def _call(self, name, stream, *args):
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        elif stream.device != self.device:
+            raise ValueError("stream: on %s, the problem is on %s" % (stream.device, self.device))
+        fn = getattr(lib(), name)
+        if torch.cuda.current_device() == self.device.index:
+            status = fn(*args, stream.cuda_stream)
+        else:
+            with torch.cuda.device(self.device):
+                status = fn(*args, stream.cuda_stream)
+        if status != E4B_OK:
+            raise E4BError(status, name)
+
+
+@dataclass(frozen=True)
+class ProjDims:
+    """A projection W [N, K] with ``n_adapters`` adapters of rank ``r`` beside it."""
+    K: int
+    N: int
+    n_adapters: int
+    r: int
+
+    def c(self) -> ProjDimsC:
+        return ProjDimsC(self.K, self.N, self.n_adapters, self.r, 64)
+
+
+class Projection(_OnDevice):
+    """Device buffers of one NF4 projection with adapters for ``T`` tokens, allocated with torch.
+
+    Serving: :meth:`e4b_multi_lora_serve_fwd` into ``y``.  Training (``train=True``, the default):
+    :meth:`e4b_adapter_group`, then :meth:`e4b_multi_lora_fwd` (``y``), :meth:`e4b_multi_lora_dgrad`
+    (``dx``) and :meth:`e4b_multi_lora_wgrad` (``dA``, ``dB``).  Calls on one object share its buffers
+    and workspace, so they must not overlap on the GPU.
+    """
+
+    def __init__(self, dims: ProjDims, T: int, device="cuda", train: bool = True):
+        import torch
+        self.dims, self.T, self.train = dims, T, train
+        sz = e4b_proj_get_sizes(dims, T)
+        self.sizes = sz
+        self.device = dev = _cuda_device(device)
+        n, r, R = dims.n_adapters, dims.r, sz.rows_cap
+        bf, i32 = torch.bfloat16, torch.int32
+        self.y = _alloc((T, dims.N), bf, dev)
+        self.ws = _alloc((int(max(sz.workspace_bytes, sz.serve_workspace_bytes)),), torch.uint8, dev)
+        self._dims_c = dims.c()
+        self._dims_p = ctypes.byref(self._dims_c)
+        self._y_p, self._ws_p, self._ws_n = _ptr(self.y), _ptr(self.ws), self.ws.numel()
+        if train:
+            self.order, self.offsets = _alloc((R,), i32, dev), _alloc((n + 2,), i32, dev)
+            self.steps = _alloc((sz.steps_cap,), i32, dev)
+            self.p, self.q = _alloc((R, r), bf, dev), _alloc((R, r), bf, dev)
+            self.dx = _alloc((T, dims.K), bf, dev)
+            # the two gradients are views of one flat buffer (one collective in a data-parallel step)
+            na, nb = n * r * dims.K, n * dims.N * r
+            self.lora_grads = _alloc((na + nb,), bf, dev)
+            self.dA = self.lora_grads[:na].view(n, r, dims.K)
+            self.dB = self.lora_grads[na:].view(n, dims.N, r)
+            self._groups = AdapterGroups(_ptr(self.order), _ptr(self.offsets), _ptr(self.steps))
+        self._call("e4b_workspace_init", None, self._ws_p, self._ws_n)
+
+    def _tokens(self, t, dtype, cols, name):
+        return _dev(t, dtype, self.T * cols, name, self.device, optional=self.T == 0)
+
+    def _base(self, base: Nf4Matrix):
+        d = self.dims
+        _check_struct(base, {"nf4": d.N * d.K // 2, "absmax": d.N * d.K // 64}, self.device, "base")
+        return ctypes.byref(base)
+
+    def _adapters(self, ad: AdapterFactors):
+        d = self.dims
+        _check_struct(ad, {"A": d.n_adapters * d.r * d.K, "B": d.n_adapters * d.N * d.r, "scale": d.n_adapters},
+                      self.device, "adapters")
+        return ctypes.byref(ad)
+
+    def _training(self):
+        if not self.train:
+            raise ValueError("made with train=False: no training buffers")
+
+    def e4b_multi_lora_serve_fwd(self, ids, x, base: Nf4Matrix, adapters: AdapterFactors, stream=None):
+        """Serving forward into ``self.y`` (ids int32 [T], any id outside [0, n) for no adapter)."""
+        pi = self._tokens(ids, "i32", 1, "ids")
+        px = self._tokens(x, "bf16", self.dims.K, "x")
+        self._call("e4b_multi_lora_serve_fwd", stream, self._dims_p, self.T, pi, px, self._base(base),
+                   self._adapters(adapters), self._y_p, self._ws_p, self._ws_n)
+
+    def e4b_adapter_group(self, ids, stream=None):
+        """Groups the step's tokens by adapter for the training calls."""
+        self._training()
+        self._call("e4b_adapter_group", stream, self._dims_p, self.T, self._tokens(ids, "i32", 1, "ids"),
+                   ctypes.byref(self._groups))
+
+    def e4b_multi_lora_fwd(self, x, base: Nf4Matrix, adapters: AdapterFactors, stream=None):
+        self._training()
+        px = self._tokens(x, "bf16", self.dims.K, "x")
+        self._call("e4b_multi_lora_fwd", stream, self._dims_p, self.T, ctypes.byref(self._groups), px,
+                   self._base(base), self._adapters(adapters), _ptr(self.p), self._y_p, self._ws_p, self._ws_n)
+
+    def e4b_multi_lora_dgrad(self, dY, base: Nf4Matrix, adapters: AdapterFactors, stream=None):
+        self._training()
+        pd = self._tokens(dY, "bf16", self.dims.N, "dY")
+        self._call("e4b_multi_lora_dgrad", stream, self._dims_p, self.T, ctypes.byref(self._groups), pd,
+                   self._base(base), self._adapters(adapters), _ptr(self.q), _ptr(self.dx), self._ws_p, self._ws_n)
+
+    def e4b_multi_lora_wgrad(self, x, dY, stream=None):
+        """Adapter gradients from the ``p`` and ``q`` of the forward and the input gradient."""
+        self._training()
+        px = self._tokens(x, "bf16", self.dims.K, "x")
+        pd = self._tokens(dY, "bf16", self.dims.N, "dY")
+        self._call("e4b_multi_lora_wgrad", stream, self._dims_p, self.T, ctypes.byref(self._groups), px, pd,
+                   _ptr(self.p), _ptr(self.q), _ptr(self.dA), _ptr(self.dB), self._ws_p, self._ws_n)
+
+    def check_device_error(self, stream=None) -> int:
+        import torch
+        with torch.cuda.device(self.device):
+            return e4b_check_device_error(self.ws, stream)
+
+
+class RouterBalance(_OnDevice):
+    """Device buffers of the router's balance loss: ``E`` experts, ``top_k``, ``T`` tokens in ``S`` sequences.
+
+    :meth:`e4b_balance_fwd` writes ``loss`` (float32 [3]: loss, balance, z), ``counts`` (int32 [S, E]),
+    ``prob_sum`` (float32 [S, E]), ``tokens`` (int32 [S]) and ``lse``; :meth:`e4b_balance_bwd` the gradient
+    of the logits.  Calls on one object share its buffers, so they must not overlap on the GPU.
+    """
+
+    def __init__(self, E: int, top_k: int, T: int, S: int = 1, device="cuda"):
+        import torch
+        self.E, self.top_k, self.T, self.S = E, top_k, T, S
+        self._dims_c = BalanceDims(E, top_k, S, 0.0, 0.0)
+        self._dims_p = ctypes.byref(self._dims_c)
+        ws_bytes = e4b_balance_get_sizes(self._dims_c, T)
+        self.device = dev = _cuda_device(device)
+        f32, i32 = torch.float32, torch.int32
+        self.counts, self.prob_sum = _alloc((S, E), i32, dev), _alloc((S, E), f32, dev)
+        self._tokens = _alloc((S + 2,), i32, dev)
+        self.tokens = self._tokens[:S]
+        self.lse, self.loss = _alloc((T,), f32, dev), _alloc((3,), f32, dev)
+        self.ws = _alloc((ws_bytes,), torch.uint8, dev)
+        self._stats = BalanceStats(*(_ptr(t) for t in (self.counts, self.prob_sum, self._tokens, self.lse)))
+        self._stats_p = ctypes.byref(self._stats)
+        self._loss_p, self._ws_p, self._ws_n = _ptr(self.loss), _ptr(self.ws), self.ws.numel()
+
+    def _inputs(self, logits, seq_offsets, token_mask):
+        pl = _dev(logits, "f32", self.T * self.E, "logits", self.device, optional=self.T == 0)
+        if seq_offsets is None and self.S != 1:
+            raise ValueError("seq_offsets: required for %d sequences" % self.S)
+        ps = _dev(seq_offsets, "i32", self.S + 1, "seq_offsets", self.device, optional=True)
+        pm = _dev(token_mask, "u8", self.T, "token_mask", self.device, optional=True)
+        return pl, ps, pm
+
+    def e4b_balance_fwd(self, logits, topk_ids, seq_offsets=None, token_mask=None, balance_coef=1.0, z_coef=0.0,
+                        stream=None):
+        """Loss and per-expert counts.  seq_offsets: int32 [S + 1] ascending (None: one sequence of all
+        tokens); token_mask: uint8 [T], 0 for tokens that take no part."""
+        pl, ps, pm = self._inputs(logits, seq_offsets, token_mask)
+        pi = _dev(topk_ids, "i32", self.T * self.top_k, "topk_ids", self.device, optional=self.T == 0)
+        self._dims_c.balance_coef, self._dims_c.z_coef = balance_coef, z_coef
+        self._call("e4b_balance_fwd", stream, self._dims_p, self.T, pl, pi, ps, pm, self._stats_p, self._loss_p,
+                   self._ws_p, self._ws_n)
+
+    def e4b_balance_bwd(self, logits, d_logits, seq_offsets=None, token_mask=None, balance_coef=1.0, z_coef=0.0,
+                        dloss=None, accumulate=False, stream=None):
+        """d_logits = dloss * dloss/dlogits (dloss: float32 [1], None for 1), or += with ``accumulate``."""
+        pl, ps, pm = self._inputs(logits, seq_offsets, token_mask)
+        pd = _dev(d_logits, "f32", self.T * self.E, "d_logits", self.device, optional=self.T == 0)
+        pg = _dev(dloss, "f32", 1, "dloss", self.device, optional=True)
+        self._dims_c.balance_coef, self._dims_c.z_coef = balance_coef, z_coef
+        self._call("e4b_balance_bwd", stream, self._dims_p, self.T, pl, ps, pm, self._stats_p, pg,
+                   1 if accumulate else 0, pd)
+
+
+def nf4_matrix(nf4, absmax) -> Nf4Matrix:
+    """A frozen NF4 projection: codes u8 [N, K/2], block absmax f32 [N, K/64]."""
+    return _make_struct(Nf4Matrix, (nf4, absmax), ("u8", "f32"))
+
+
+def adapter_factors(A, B, scale) -> AdapterFactors:
+    """Adapters of a projection: bf16 A [n, r, K] and B [n, N, r], scale f32 [n]."""
+    return _make_struct(AdapterFactors, (A, B, scale), ("bf16", "bf16", "f32"))
