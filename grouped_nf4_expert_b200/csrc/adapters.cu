@@ -153,125 +153,6 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
   }
 }
 
-// ----------------------------------------------------------------------------
-// Plain kernels
-// ----------------------------------------------------------------------------
-__device__ __forceinline__ float bf(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
-__device__ __forceinline__ uint16_t to_bf(float f) {
-  const __nv_bfloat16 b = __float2bfloat16_rn(f);
-  return *reinterpret_cast<const uint16_t*>(&b);
-}
-__device__ __forceinline__ int adapter_of_row(const int32_t* offsets, int n, int row) {
-  int lo = 0, hi = n;  // the last group whose start is <= row (empty groups share a start with the next)
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (offsets[mid] <= row)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  return lo;
-}
-
-// out[row, j] = bf16(s sum_k src[t, k] F[a](k, j)): F = A[a][j][k], or B[a][k][j] with MN
-template <bool MN>
-__global__ void adapter_rows_kernel(const uint16_t* src, const uint16_t* fac, const float* scale,
-                                    const int32_t* order, const int32_t* offsets, int T, int K, int n, int r,
-                                    uint16_t* out) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int used = offsets[n];
-  for (int row = blockIdx.x; row < used; row += gridDim.x) {
-    const int a = adapter_of_row(offsets, n, row), t = order[row];
-    for (int j = warp; j < r; j += blockDim.x / 32) {
-      float acc = 0.0f;
-      if (t < T)
-        for (int k = lane; k < K; k += 32) {
-          const size_t i = MN ? ((size_t)a * K + k) * r + j : ((size_t)a * r + j) * K + k;
-          acc = fmaf(bf(src[(size_t)t * K + k]), bf(fac[i]), acc);
-        }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(kFull, acc, o);
-      if (lane == 0) out[(size_t)row * r + j] = to_bf(scale[a] * acc);
-    }
-  }
-}
-
-// 64 rows x 64 outputs a block: out[t, o] = sum_i src[t, i] W(o, i) + sum_j low[row, j] F[a](o, j)
-template <bool MN>
-__global__ void __launch_bounds__(256) adapter_gemm_kernel(const uint16_t* src, const uint8_t* nf4,
-                                                           const float* absmax, const uint16_t* low,
-                                                           const uint16_t* fac, const int32_t* order,
-                                                           const int32_t* offsets, int T, int K, int N, int n, int r,
-                                                           uint16_t* out) {
-  __shared__ float xs[32][65], ws[32][65];
-  __shared__ float lv[16];
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int R = MN ? N : K, O = MN ? K : N;
-  const int row0 = blockIdx.y * 64, o0 = blockIdx.x * 64;
-  if (row0 >= offsets[n + 1]) return;
-  if (tid < 16) lv[tid] = nf4_level(tid);
-  float acc[4][4] = {};
-  for (int i0 = 0; i0 < R; i0 += 32) {
-    __syncthreads();
-    for (int q = tid; q < 64 * 32; q += 256) {
-      const int i = q & 31, m = q >> 5, t = order[row0 + m];
-      xs[i][m] = (t < T && i0 + i < R) ? bf(src[(size_t)t * R + i0 + i]) : 0.0f;
-      const int wi = MN ? (q >> 6) : i, wo = MN ? (q & 63) : m;
-      const int nn = MN ? i0 + wi : o0 + wo, kk = MN ? o0 + wo : i0 + wi;
-      float w = 0.0f;
-      if (nn < N && kk < K) {
-        const uint8_t b = nf4[(size_t)nn * (K / 2) + kk / 2];
-        w = bf(to_bf(__fmul_rn(lv[(kk & 1) ? b & 15 : b >> 4], absmax[(size_t)nn * (K / 64) + kk / 64])));
-      }
-      ws[wi][wo] = w;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(xs[i][ty + 16 * u], ws[i][tx + 16 * v], acc[u][v]);
-  }
-  for (int u = 0; u < 4; ++u) {
-    const int row = row0 + ty + 16 * u, t = order[row];
-    if (t >= T) continue;
-    const int a = adapter_of_row(offsets, n, row);
-    for (int v = 0; v < 4; ++v) {
-      const int o = o0 + tx + 16 * v;
-      if (o >= O) continue;
-      float d = acc[u][v];
-      if (a < n)
-        for (int j = 0; j < r; ++j) {
-          const size_t i = MN ? ((size_t)a * r + j) * K + o : ((size_t)a * N + o) * r + j;
-          d = fmaf(bf(low[(size_t)row * r + j]), bf(fac[i]), d);
-        }
-      out[(size_t)t * O + o] = to_bf(d);
-    }
-  }
-}
-
-// out[a] = sum over its rows of low^T act: [r, F] (transposed) or [F, r]
-template <bool TR>
-__global__ void __launch_bounds__(256) adapter_wgrad_kernel(const uint16_t* act, const uint16_t* low,
-                                                            const int32_t* order, const int32_t* offsets, int T,
-                                                            int F, int r, uint16_t* out) {
-  const int a = blockIdx.y, f = blockIdx.x * 64 + (threadIdx.x & 63), jg = threadIdx.x >> 6;
-  if (f >= F) return;
-  float acc[16] = {};
-  for (int row = offsets[a]; row < offsets[a + 1]; ++row) {
-    const int t = order[row];
-    if (t >= T) continue;
-    const float v = bf(act[(size_t)t * F + f]);
-    for (int i = 0; i < 16; ++i)
-      if (jg + 4 * i < r) acc[i] = fmaf(v, bf(low[(size_t)row * r + jg + 4 * i]), acc[i]);
-  }
-  for (int i = 0; i < 16; ++i) {
-    const int j = jg + 4 * i;
-    if (j < r) out[TR ? ((size_t)a * r + j) * F + f : ((size_t)a * F + f) * r + j] = to_bf(acc[i]);
-  }
-}
-
 }  // namespace
 
 cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int32_t* order, int32_t* offsets, int32_t* steps,
@@ -283,41 +164,6 @@ cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int32_t* orde
   LaunchScope scope("adapter_group", stream);
   adapter_group_kernel<<<1, kGroupThreads, smem, stream>>>(ids, T, n, (int)adapter_rows_cap(T, n), order, offsets,
                                                            steps);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_adapter_rows(const AdapterProjHost& h, bool mn, const uint16_t* src, const uint16_t* fac,
-                                uint16_t* out, cudaStream_t stream) {
-  const int grid = (int)(h.rows_cap < 4096 ? h.rows_cap : 4096);
-  LaunchScope scope(mn ? "adapter_rows_dy" : "adapter_rows_x", stream);
-  if (mn)
-    adapter_rows_kernel<true><<<grid, 256, 0, stream>>>(src, fac, h.scale, h.order, h.offsets, h.T, h.N, h.n, h.r, out);
-  else
-    adapter_rows_kernel<false><<<grid, 256, 0, stream>>>(src, fac, h.scale, h.order, h.offsets, h.T, h.K, h.n, h.r,
-                                                         out);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_adapter_gemm(const AdapterProjHost& h, bool mn, const uint16_t* src, const uint16_t* low,
-                                const uint16_t* fac, uint16_t* out, cudaStream_t stream) {
-  const dim3 grid(((mn ? h.K : h.N) + 63) / 64, (unsigned)(h.rows_cap / 64));
-  LaunchScope scope(mn ? "adapter_gemm_dgrad" : "adapter_gemm_fwd", stream);
-  if (mn)
-    adapter_gemm_kernel<true><<<grid, 256, 0, stream>>>(src, h.nf4, h.absmax, low, fac, h.order, h.offsets, h.T, h.K,
-                                                        h.N, h.n, h.r, out);
-  else
-    adapter_gemm_kernel<false><<<grid, 256, 0, stream>>>(src, h.nf4, h.absmax, low, fac, h.order, h.offsets, h.T, h.K,
-                                                         h.N, h.n, h.r, out);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, const uint16_t* dY, const uint16_t* p,
-                                 const uint16_t* q, uint16_t* dA, uint16_t* dB, cudaStream_t stream) {
-  LaunchScope scope("adapter_wgrad", stream);
-  adapter_wgrad_kernel<true><<<dim3((h.K + 63) / 64, h.n), 256, 0, stream>>>(x, q, h.order, h.offsets, h.T, h.K, h.r,
-                                                                             dA);
-  adapter_wgrad_kernel<false><<<dim3((h.N + 63) / 64, h.n), 256, 0, stream>>>(dY, p, h.order, h.offsets, h.T, h.N, h.r,
-                                                                              dB);
   return cudaGetLastError();
 }
 

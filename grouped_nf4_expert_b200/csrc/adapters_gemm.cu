@@ -1,0 +1,1059 @@
+// Large batches of the NF4 projection with adapters of many requests, on the
+// 5th-generation tensor cores:
+//
+//  * adapter_gemm_kernel: persistent CTA pairs, one 256-row x 256-column
+//    output tile per work unit (cta_group::2 UMMAs): base product with the
+//    NF4 matrix decoded into shared memory, then one K = r step per adapter
+//    with rows in the tile, written to that adapter's rows only.
+//  * adapter_proj_kernel: p = s x A^T and q = s dY B, 128 rows of one adapter
+//    at a time.
+//  * adapter_wgrad_kernel: dA = q^T x and dB = dY^T p, K = the rows of one
+//    adapter.
+//
+// Rows are the tokens sorted by adapter.  No sorted copy of x or dY is made:
+// the tensor maps have one-row boxes and every load gathers four token rows by
+// index (tile::gather4), a warp's 32 lanes one 128-row tile; padding rows carry
+// the index T, outside the tensor, and read as zeros.  Every adapter's rows
+// start at a multiple of 16, the K step of one UMMA, so that the gradient
+// products never multiply two adapters' rows.
+//
+// The adapters of a tile share its accumulator: each K = r step names the
+// TMEM lanes (rows) it must not write (the disable-output-lane operand), so
+// the rows need not be split into tiles by adapter, and nothing an adapter or
+// a token holds reaches another request's rows.
+#include <math.h>
+
+#include "e4b_device.cuh"
+#include "e4b_internal.h"
+
+namespace e4b {
+
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+
+// Four rows of a 2-D tensor (one-row box) into consecutive 128-byte shared rows.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int4 rows) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+      "%5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z),
+      "r"(rows.w)
+      : "memory");
+}
+
+// The pair UMMA with output lanes disabled: bit i of the 256-bit mask keeps row i of the accumulator as it is.
+__device__ __forceinline__ void umma_bf16_2sm_masked(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                     const uint32_t (&off)[8]) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.b32 p, 1, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7, %8, %9, %10, %11}, p;\n"
+      "}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]), "r"(off[4]), "r"(off[5]),
+      "r"(off[6]), "r"(off[7])
+      : "memory");
+}
+
+// Mask word w (rows 32 w ..) with the bits outside rows [lo, hi) set.
+__device__ __forceinline__ uint32_t rows_off(int lo, int hi, int w) {
+  const int a = min(max(lo - 32 * w, 0), 32), b = min(max(hi - 32 * w, 0), 32);
+  const uint32_t below_b = b == 32 ? kFull : (1u << b) - 1;
+  const uint32_t below_a = a == 32 ? kFull : (1u << a) - 1;
+  return ~(below_b & ~below_a);
+}
+
+// Waits (with the limit) until the copies this role issued have landed, before its shared memory goes away.
+__device__ __forceinline__ void let_land(uint64_t* bars, int n, uint32_t issued, uint32_t last_par,
+                                         long long timeout_ns) {
+  for (int i = 0; i < n; ++i)
+    if (issued & (1u << i)) {
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(&bars[i], (last_par >> i) & 1u) && (long long)(globaltimer_ns() - t0) < timeout_ns) {
+      }
+    }
+}
+
+}  // namespace
+
+// =============================================================================
+// Base product with the adapters' steps
+// =============================================================================
+// Roles and rings as in the expert block's grouped GEMM: warp 0 codes, warp 1
+// TMEM owner and (even CTA) UMMA issuer, warp 2 relay of operand readiness to
+// the even CTA, warp 3 activation rows and low-rank operands, warps 4-19 four
+// decode groups taking the k-chunks round robin, warps 20-23 epilogue.  The
+// low-rank steps come after the k-chunks: a unit's two ring slots per adapter
+// hold its 128 p (or q) rows and 128 factor rows.
+namespace adg {
+constexpr int BM = 128, BN = 128, BK = 64;
+constexpr int A_BYTES = BM * BK * 2;
+constexpr int B_BYTES = BN * BK * 2;
+constexpr int kGroups = 4, kGroupWarps = 4;
+constexpr int SA = 6;         // activation ring
+constexpr int SB = kGroups;   // decoded-tile ring: group g's chunks use slot g
+constexpr int RAW_STAGES = 2 * kGroups;
+constexpr int RAW_BYTES = BN * BK / 2;
+constexpr int B_OFF = SA * A_BYTES;
+constexpr int RAW_OFF = B_OFF + SB * B_BYTES;
+constexpr int EPI_OFF = RAW_OFF + RAW_STAGES * RAW_BYTES;
+// Epilogue staging, per warp 32 rows x 64 columns; 144-byte rows keep both the row-wise writes and the
+// line-wise reads free of bank conflicts.
+constexpr int kEpiPitch = 144;
+constexpr int kEpiWarpBytes = 32 * kEpiPitch;
+constexpr int BAR_OFF = EPI_OFF + 4 * kEpiWarpBytes;
+constexpr int SMEM_BYTES = BAR_OFF + 1024 + 1024;
+constexpr int kEpiWarp0 = 4 + kGroups * kGroupWarps;
+constexpr int kThreads = 32 * (kEpiWarp0 + 4);
+constexpr int kTmemCols = 512;
+static_assert(BAR_OFF % 16 == 0 && SMEM_BYTES <= 232448, "shared memory budget");
+static_assert(BM * E4B_MAX_RANK * 2 <= A_BYTES && BN * E4B_MAX_RANK * 2 <= A_BYTES, "low-rank operands fit a slot");
+static_assert(RAW_STAGES % kGroups == 0, "code slots are owned by one decode group each");
+}  // namespace adg
+
+struct AdapterGemmParams {
+  const float* absmax;
+  const int32_t* order;
+  const int32_t* steps;
+  uint16_t* out;
+  DeviceError* err;
+  long long timeout_ns;
+  int R;        // reduction length (K, or N for the input gradient)
+  int O;        // output columns (N, or K)
+  int T, N, K, r_pad, n_nt;
+  int unit_start, entries;  // places in `steps`
+};
+
+template <bool kMN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
+    adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_raw,
+                        const __grid_constant__ CUtensorMap map_la, const __grid_constant__ CUtensorMap map_lb,
+                        const AdapterGemmParams p) {
+  using namespace adg;
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = align1024(smem_dyn);
+  uint8_t* aring = smem;
+  uint8_t* bring = smem + B_OFF;
+  uint8_t* rawbuf = smem + RAW_OFF;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_OFF);
+  uint64_t* raw_full = bars;                    // [RAW_STAGES] codes landed
+  uint64_t* raw_empty = raw_full + RAW_STAGES;  // [RAW_STAGES] codes read into registers (group's 4 warps)
+  uint64_t* xfull = raw_empty + RAW_STAGES;     // [SA] activation use landed
+  uint64_t* aempty = xfull + SA;                // [SA] activation slot consumed by the UMMAs
+  uint64_t* full = aempty + SA;                 // [SA] (even CTA) both CTAs' operands of an MMA step in place
+  uint64_t* bdone = full + SA;                  // [SB] this CTA's decoded tile written (group's 4 warps)
+  uint64_t* bempty = bdone + SB;                // [SB] decoded-tile slot consumed by the UMMAs
+  uint64_t* accfull = bempty + SB;              // [2] accumulator complete
+  uint64_t* accempty = accfull + 2;             // [2] (even CTA) accumulator drained in both CTAs
+  uint64_t* drain = accfull + 4;                // (even CTA) all issued UMMAs finished
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accfull + 5);
+  CtaControl* ctl = reinterpret_cast<CtaControl*>(accfull + 6);
+  uint32_t* sig = reinterpret_cast<uint32_t*>(accfull + 7);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  if (threadIdx.x == 0) {
+    for (int r = 0; r < RAW_STAGES; ++r) {
+      mbar_init(&raw_full[r], 1);
+      mbar_init(&raw_empty[r], kGroupWarps);
+    }
+    for (int s = 0; s < SA; ++s) {
+      mbar_init(&xfull[s], 1);
+      mbar_init(&aempty[s], 1);
+      mbar_init(&full[s], 1);
+    }
+    for (int s = 0; s < SB; ++s) {
+      mbar_init(&bdone[s], kGroupWarps);
+      mbar_init(&bempty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accfull[b], 1);
+      mbar_init(&accempty[b], 8);
+    }
+    mbar_init(drain, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_2sm(tmem_slot, kTmemCols);
+    tmem_relinquish_2sm();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int n_units = p.steps[0] * p.n_nt;
+  const int kchunks = (p.R + BK - 1) / BK;
+  const int blocks_per_row = p.K / 64;
+  const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  const int32_t* unit_start = p.steps + p.unit_start;
+  const int4* entries = reinterpret_cast<const int4*>(p.steps + p.entries);  // (adapter, unit, first row, end row)
+
+  if (warp == 0) {
+    // ------------------------------------------------ NF4 codes (one lane)
+    if (lane == 0) {
+      tma_prefetch_desc(&map_raw);
+      uint32_t j = 0, issued = 0, last_par = 0;
+      bool ok = true;
+      for (int u = pair; u < n_units && ok; u += n_pairs) {
+        const int c0 = (u % p.n_nt) * 256 + (int)rank * 128;  // this CTA's 128 output columns
+        for (int kc = 0; kc < kchunks; ++kc, ++j) {
+          const uint32_t r = j % RAW_STAGES, ph = (j / RAW_STAGES) & 1;
+          if (!(ok = mbar_wait_lazy(&raw_empty[r], ph ^ 1, ctl, p.err, p.timeout_ns, 311, 64))) break;
+          uint8_t* slot = rawbuf + r * RAW_BYTES;
+          mbar_arrive_expect_tx(&raw_full[r], (uint32_t)RAW_BYTES);
+          if (!kMN)
+            tma_load_2d(slot, &map_raw, &raw_full[r], kc * (BK / 2), c0);
+          else
+            tma_load_2d(slot, &map_raw, &raw_full[r], c0 / 2, kc * BK);
+          issued |= 1u << r;
+          last_par = (last_par & ~(1u << r)) | (ph << r);
+        }
+      }
+      if (!ok) let_land(raw_full, RAW_STAGES, issued, last_par, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------ activation rows (the whole warp) + low-rank operands
+    if (lane == 0) {
+      tma_prefetch_desc(&map_a);
+      tma_prefetch_desc(&map_la);
+      tma_prefetch_desc(&map_lb);
+    }
+    uint32_t s = 0, ph = 0, issued = 0, last_par = 0;
+    auto issued_next = [&]() {
+      issued |= 1u << s;
+      last_par = (last_par & ~(1u << s)) | (ph << s);
+      if (++s == SA) {
+        s = 0;
+        ph ^= 1;
+      }
+    };
+    const uint32_t a_u = smem_u32(aring);
+    auto tokens_of = [&](int u) -> int4 {  // the four tokens whose rows this lane loads
+      const int row = (u / p.n_nt) * 256 + (int)rank * 128 + 4 * lane;
+      return __ldg(reinterpret_cast<const int4*>(p.order + row));
+    };
+    bool ok = true;
+    int4 next = pair < n_units ? tokens_of(pair) : make_int4(0, 0, 0, 0);
+    for (int u = pair; u < n_units && ok; u += n_pairs) {
+      const int mu = u / p.n_nt, c0 = (u % p.n_nt) * 256 + (int)rank * 128;
+      const int4 tok = next;
+      if (u + n_pairs < n_units) next = tokens_of(u + n_pairs);
+      for (int kc = 0; kc < kchunks; ++kc) {
+        if (!(ok = __all_sync(kFull, mbar_wait(&aempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 312)))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&xfull[s], (uint32_t)A_BYTES);
+        __syncwarp();
+        tma_gather4(a_u + s * A_BYTES + lane * 512, &map_a, &xfull[s], kc * BK, tok);
+        issued_next();
+      }
+      if (!ok) break;
+      for (int i = __ldg(unit_start + mu);; ++i) {
+        const int4 en = __ldg(entries + i);
+        if (en.y != mu) break;
+        const uint32_t s1 = (s + 1 == SA) ? 0 : s + 1, ph1 = (s + 1 == SA) ? ph ^ 1 : ph;
+        ok = __all_sync(kFull, mbar_wait(&aempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 310) &&
+                                   mbar_wait(&aempty[s1], ph1 ^ 1, ctl, p.err, p.timeout_ns, 310));
+        if (!ok) break;
+        if (lane == 0) {
+          uint8_t* la = aring + s * A_BYTES;
+          uint8_t* lb = aring + s1 * A_BYTES;
+          mbar_arrive_expect_tx(&xfull[s], (uint32_t)(512 * p.r_pad));
+          tma_load_2d(la, &map_la, &xfull[s], 0, mu * 256 + (int)rank * 128);
+          if (!kMN) {
+            tma_load_3d(lb, &map_lb, &xfull[s], 0, c0, en.x);
+            tma_load_3d(lb + 128 * p.r_pad, &map_lb, &xfull[s], 0, c0 + 64, en.x);
+          } else {
+            tma_load_3d(lb, &map_lb, &xfull[s], c0, 0, en.x);
+            tma_load_3d(lb + 128 * p.r_pad, &map_lb, &xfull[s], c0 + 64, 0, en.x);
+          }
+          mbar_arrive(&xfull[s1]);
+        }
+        __syncwarp();
+        issued_next();
+        issued_next();
+      }
+    }
+    if (!ok) let_land(xfull, SA, issued, last_par, p.timeout_ns);
+    __syncwarp();
+  } else if (warp == 1 && rank == 0) {
+    // ------------------------------------------------ UMMA issuer (even CTA, one elected lane)
+    if (elect_one_sync()) {
+      const uint32_t idesc = make_idesc_bf16(256, 256, false, kMN);
+      const uint32_t lswz = swz_for_row_bytes(2 * p.r_pad);
+      const uint32_t a_u = smem_u32(aring), b_u = smem_u32(bring);
+      const uint32_t bstep = kMN ? 128u : 2u;
+      const uint64_t adesc0 = make_sdesc(a_u, 16, 1024, kSw128);
+      const uint64_t bdesc0 = kMN ? make_sdesc(b_u, 8192, 1024, kSw128) : make_sdesc(b_u, 16, 1024, kSw128);
+      uint32_t ti = 0;
+      uint32_t sa = 0, sb = 0;
+      uint32_t fs = 0, fph = 0;
+      bool ok = true;
+      auto next_a = [&]() { sa = (sa + 1 == SA) ? 0 : sa + 1; };
+      auto next_f = [&]() {
+        if (++fs == SA) {
+          fs = 0;
+          fph ^= 1;
+        }
+      };
+      auto wait_step = [&]() -> bool { return mbar_wait_cluster(&full[fs], fph, ctl, p.err, p.timeout_ns, 323); };
+      for (int u = pair; u < n_units && ok; u += n_pairs, ++ti) {
+        const int mu = u / p.n_nt;
+        const uint32_t b = ti & 1, use = ti >> 1;
+        const uint32_t d = tmem + b * 256;
+        int i = __ldg(unit_start + mu);
+        int4 en = __ldg(entries + i);
+        if (!(ok = mbar_wait_cluster(&accempty[b], (use & 1) ^ 1, ctl, p.err, p.timeout_ns, 320))) break;
+        tc_fence_after();
+        if (!(ok = wait_step())) break;
+        tc_fence_after();
+        for (int kc = 0; kc < kchunks; ++kc) {
+          const uint64_t adesc = adesc0 + (uint64_t)(sa * (A_BYTES >> 4));
+          const uint64_t bdesc = bdesc0 + (uint64_t)(sb * (B_BYTES >> 4));
+          const uint32_t fs1 = (fs + 1 == SA) ? 0 : fs + 1, fph1 = (fs + 1 == SA) ? fph ^ 1 : fph;
+          const bool more = kc + 1 < kchunks;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16 - 1; ++kk)
+            umma_bf16_2sm(d, adesc + 2 * kk, bdesc + bstep * kk, idesc, (kc > 0 || kk > 0) ? 1u : 0u);
+          // Peek at the next k-chunk while the UMMAs above execute.
+          const bool next_ready = more && mbar_test_wait_cluster(&full[fs1], fph1);
+          umma_bf16_2sm(d, adesc + 2 * (BK / 16 - 1), bdesc + bstep * (BK / 16 - 1), idesc, 1u);
+          umma_commit_2sm(&aempty[sa], 0x3);
+          umma_commit_2sm(&bempty[sb], 0x3);
+          next_a();
+          sb = (sb + 1 == SB) ? 0 : sb + 1;
+          fs = fs1;
+          fph = fph1;
+          if (more) {
+            if (!next_ready && !(ok = wait_step())) break;
+            tc_fence_after();
+          }
+        }
+        if (!ok) break;
+        // One K = r step per adapter of the tile, into its own rows.
+        for (; en.y == mu; en = __ldg(entries + ++i)) {
+          if (!(ok = wait_step())) break;
+          tc_fence_after();
+          const uint32_t sa1 = (sa + 1 == SA) ? 0 : sa + 1;
+          const uint32_t la_u = a_u + sa * A_BYTES, lb_u = a_u + sa1 * A_BYTES;
+          uint32_t off[8];
+#pragma unroll
+          for (int w = 0; w < 8; ++w) off[w] = rows_off(en.z - mu * 256, en.w - mu * 256, w);
+          for (int ks = 0; ks < p.r_pad / 16; ++ks) {
+            const uint64_t bd = kMN ? make_sdesc(lb_u + 2048 * ks, 128 * p.r_pad, 1024, kSw128)
+                                    : make_sdesc(lb_u + 32 * ks, 16, 16 * p.r_pad, lswz);
+            umma_bf16_2sm_masked(d, make_sdesc(la_u + 32 * ks, 16, 16 * p.r_pad, lswz), bd, idesc, off);
+          }
+          umma_commit_2sm(&aempty[sa], 0x3);
+          umma_commit_2sm(&aempty[sa1], 0x3);
+          next_a();
+          next_a();
+          next_f();
+        }
+        if (!ok) break;
+        umma_commit_2sm(&accfull[b], 0x3);
+      }
+      umma_commit_2sm(drain, 0x1);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(drain, 0) && (long long)(globaltimer_ns() - t0) < p.timeout_ns) {
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------ relays: this CTA's operands of a step -> even CTA's full[]
+    const uint32_t full_even = mapa_shared(smem_u32(full), 0);
+    const uint32_t sig_even = mapa_shared(smem_u32(sig), 0);
+    uint32_t sa = 0, pha = 0, jb = 0, fs = 0;
+    bool ok = true;
+    auto wait_a = [&]() -> bool {
+      const bool r = __all_sync(kFull, mbar_wait(&xfull[sa], pha, ctl, p.err, p.timeout_ns, 352));
+      if (++sa == SA) {
+        sa = 0;
+        pha ^= 1;
+      }
+      return r;
+    };
+    auto signal = [&]() {
+      if (lane == 0) {
+        if (rank == 0)
+          mbar_arrive_expect_tx(&full[fs], 4);
+        else
+          st_async_signal(sig_even, full_even + 8 * fs, 1u);
+      }
+      fs = (fs + 1 == SA) ? 0 : fs + 1;
+    };
+    for (int u = pair; u < n_units && ok; u += n_pairs) {
+      const int mu = u / p.n_nt;
+      for (int kc = 0; kc < kchunks; ++kc, ++jb) {
+        ok = __all_sync(kFull, mbar_wait(&bdone[jb % SB], (jb / SB) & 1, ctl, p.err, p.timeout_ns, 351));
+        if (!ok || !(ok = wait_a())) break;
+        signal();
+      }
+      if (!ok) break;
+      for (int i = __ldg(unit_start + mu); __ldg(entries + i).y == mu; ++i) {
+        if (!(ok = wait_a()) || !(ok = wait_a())) break;
+        signal();
+      }
+    }
+  } else if (warp >= 4 && warp < kEpiWarp0) {
+    // ------------------------------------------------ NF4 decode, groups take the k-chunks round robin
+    const uint32_t grp = (warp - 4) >> 2;
+    const int t = (threadIdx.x - 128) & 127;  // weight row (K-major) / code column pair of this thread
+    const Nf4Shift ks = nf4_shift_consts();
+    const int raw_off = kMN ? (t & 63) * 64 + (t >> 6) * 32 : t * 32;
+    const int drow = kMN ? (t & 63) : t;
+    const uint32_t drow_off = (kMN ? (t >> 6) * 8192 : 0) + (drow >> 3) * 1024 + (drow & 7) * 128;
+    const uint32_t b_u = smem_u32(bring) + grp * B_BYTES;
+    // A cursor over this group's chunks, one chunk ahead of the decode (for the block scales).
+    const uint32_t my_units = pair < n_units ? (uint32_t)((n_units - pair + n_pairs - 1) / n_pairs) : 0;
+    const uint32_t n_chunks = my_units * (uint32_t)kchunks;
+    int c_kc = (int)grp, c_u = pair;
+    while (c_kc >= kchunks) {
+      c_kc -= kchunks;
+      c_u += n_pairs;
+    }
+    int c_nt = c_u % p.n_nt;
+    auto advance = [&]() {
+      c_kc += kGroups;
+      while (c_kc >= kchunks) {
+        c_kc -= kchunks;
+        c_u += n_pairs;
+        c_nt = c_u % p.n_nt;
+      }
+    };
+    // Block scale of this thread's row for the cursor's chunk (0 past the ends of the matrix: zero decode).
+    auto block_scale = [&]() -> float {
+      if (c_u >= n_units) return 0.0f;
+      int row, blk;
+      if (!kMN) {
+        row = c_nt * 256 + (int)rank * 128 + t;
+        blk = c_kc;
+      } else {
+        row = c_kc * BK + (t & 63);
+        blk = c_nt * 4 + (int)rank * 2 + (t >> 6);
+      }
+      if (row >= p.N || blk >= blocks_per_row) return 0.0f;
+      return __ldg(p.absmax + (size_t)row * blocks_per_row + blk);
+    };
+    float amax_next = block_scale();
+    bool ok = true;
+    for (uint32_t jj = grp; jj < n_chunks && ok; jj += kGroups) {
+      const float amax = amax_next;
+      advance();
+      const uint32_t r = jj % RAW_STAGES, rph = (jj / RAW_STAGES) & 1;
+      ok = __all_sync(kFull, mbar_wait(&raw_full[r], rph, ctl, p.err, p.timeout_ns, 330));
+      if (!ok) break;
+      const uint8_t* slot = rawbuf + r * RAW_BYTES;
+      const uint4 q0 = *reinterpret_cast<const uint4*>(slot + raw_off);
+      const uint4 q1 = *reinterpret_cast<const uint4*>(slot + raw_off + 16);
+      const uint32_t codes[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+      fence_proxy_async_smem();  // these reads before the next TMA write of the slot
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&raw_empty[r]);
+      amax_next = block_scale();
+      const Nf4Planes pl = nf4_block_planes(amax);
+      uint32_t v[32];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) nf4_decode_word(codes[c], pl, ks, &v[4 * c]);
+      ok = __all_sync(kFull, mbar_wait(&bempty[grp], ((jj / kGroups) & 1) ^ 1, ctl, p.err, p.timeout_ns, 331));
+      if (!ok) break;
+      const uint32_t dbase = b_u + drow_off;
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        st_shared_v4(dbase + ((c ^ (drow & 7)) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+      fence_proxy_async_smem();  // the tile stores before the UMMA reads them
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bdone[grp]);
+    }
+  } else if (warp >= kEpiWarp0) {
+    // ------------------------------------------------ epilogue: 32 rows of this warp to their tokens
+    // 64 columns at a time through shared memory, so that a store instruction writes whole 128-byte lines
+    // of four tokens (a row's columns belong to one lane of TMEM).
+    const int qrt = warp & 3;
+    const uint32_t accempty_even = mapa_shared(smem_u32(accempty), 0);
+    uint8_t* ebuf = smem + EPI_OFF + qrt * kEpiWarpBytes;
+    const uint32_t ebuf_u = smem_u32(ebuf) + lane * kEpiPitch;
+    uint32_t ti = 0;
+    bool ok = true;
+    for (int u = pair; u < n_units && ok; u += n_pairs, ++ti) {
+      const int mu = u / p.n_nt, c0 = (u % p.n_nt) * 256;
+      const int tok = __ldg(p.order + mu * 256 + (int)rank * 128 + qrt * 32 + lane);
+      const uint32_t b = ti & 1, use = ti >> 1;
+      ok = __all_sync(kFull, mbar_wait(&accfull[b], use & 1, ctl, p.err, p.timeout_ns, 340));
+      if (!ok) break;
+      tc_fence_after();
+      const bool any = __any_sync(kFull, tok < p.T);
+      const uint32_t tl = tmem + b * 256 + ((uint32_t)(qrt * 32) << 16);
+#pragma unroll 1
+      for (int jj = 0; jj < 256; jj += 64) {
+        if (c0 + jj >= p.O || !any) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float v[32];
+          tmem_ld32(tl + jj + 32 * h, v);
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            st_shared_v4(ebuf_u + 64 * h + 16 * i, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+        __syncwarp();
+        const int col = c0 + jj + 8 * (lane & 7);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = 4 * i + (lane >> 3);
+          const int t = __shfl_sync(kFull, tok, row);
+          if (t < p.T && col < p.O)
+            *reinterpret_cast<uint4*>(p.out + (size_t)t * p.O + col) =
+                *reinterpret_cast<const uint4*>(ebuf + row * kEpiPitch + 16 * (lane & 7));
+        }
+        __syncwarp();
+      }
+      // The issuer needs this warp's TMEM reads only, not its global stores: a relaxed arrival.
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0)
+          mbar_arrive(&accempty[b]);
+        else
+          mbar_arrive_cluster_relaxed(accempty_even + 8 * b);
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_2sm(tmem, kTmemCols);
+  }
+}
+
+// =============================================================================
+// Low-rank rows: out[row] = bf16(s[a] src[token of row] . F[a])
+// =============================================================================
+namespace adp {
+constexpr int BM = 128, BK = 64, STAGES = 6;
+constexpr int A_BYTES = BM * BK * 2;
+constexpr int B_BYTES = BK * E4B_MAX_RANK * 2;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 1024;
+constexpr int kThreads = 192;  // warp 0 TMA, warp 1 MMA, warps 2-5 epilogue
+constexpr int kAccCols = 64;
+constexpr int kTmemCols = 2 * kAccCols;
+static_assert(STAGE_BYTES % 1024 == 0, "stage alignment");
+}  // namespace adp
+
+struct AdapterRowsParams {
+  const int32_t* order;
+  const int32_t* steps;
+  const float* scale;
+  uint16_t* out;
+  DeviceError* err;
+  long long timeout_ns;
+  int R, T, r, r_pad, tasks;  // tasks: place of the task list in `steps`
+};
+
+// F = A [n, r, R] (K-major), or B [n, R, r] (W_MN).
+template <bool W_MN>
+__global__ void __launch_bounds__(adp::kThreads)
+    adapter_proj_kernel(const __grid_constant__ CUtensorMap map_src, const __grid_constant__ CUtensorMap map_w,
+                        const AdapterRowsParams p) {
+  using namespace adp;
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = align1024(smem_dyn);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + STAGES;
+  uint64_t* accfull = bars + 2 * STAGES;  // [2]
+  uint64_t* accempty = accfull + 2;       // [2]
+  uint64_t* drain = accfull + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accfull + 5);
+  CtaControl* ctl = reinterpret_cast<CtaControl*>(accfull + 6);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accfull[b], 1);
+      mbar_init(&accempty[b], 4);
+    }
+    mbar_init(drain, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int n_tasks = p.steps[3];
+  const int4* tasks = reinterpret_cast<const int4*>(p.steps + p.tasks);  // (adapter, first row, end row, 0)
+  const int kchunks = (p.R + BK - 1) / BK;
+  const uint32_t b_bytes = BK * p.r_pad * 2;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&map_src);
+      tma_prefetch_desc(&map_w);
+    }
+    int s = 0;
+    uint32_t ph = 0, issued = 0, last_par = 0;
+    bool ok = true;
+    const uint32_t base = smem_u32(smem);
+    for (int u = blockIdx.x; u < n_tasks && ok; u += gridDim.x) {
+      const int4 tk = __ldg(tasks + u);
+      const int row = tk.y + 4 * lane;  // a task's rows start and end at multiples of 16
+      const int4 tok = row < tk.z ? __ldg(reinterpret_cast<const int4*>(p.order + row)) : make_int4(p.T, p.T, p.T, p.T);
+      for (int kc = 0; kc < kchunks; ++kc) {
+        if (!(ok = __all_sync(kFull, mbar_wait(&empty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 410)))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], A_BYTES + b_bytes);
+        __syncwarp();
+        tma_gather4(base + s * STAGE_BYTES + lane * 512, &map_src, &full[s], kc * BK, tok);
+        if (lane == 0) {
+          uint8_t* st = smem + s * STAGE_BYTES + A_BYTES;
+          if (W_MN)
+            tma_load_3d(st, &map_w, &full[s], 0, kc * BK, tk.x);
+          else
+            tma_load_3d(st, &map_w, &full[s], kc * BK, 0, tk.x);
+        }
+        __syncwarp();
+        issued |= 1u << s;
+        last_par = (last_par & ~(1u << s)) | (ph << s);
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (!ok) let_land(full, STAGES, issued, last_par, p.timeout_ns);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = make_idesc_bf16(BM, p.r_pad, false, W_MN);
+      const uint32_t wswz = swz_for_row_bytes(2 * p.r_pad);
+      int s = 0;
+      uint32_t ph = 0, ti = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < n_tasks && ok; u += gridDim.x, ++ti) {
+        const uint32_t b = ti & 1, use = ti >> 1;
+        if (!(ok = mbar_wait(&accempty[b], (use & 1) ^ 1, ctl, p.err, p.timeout_ns, 420))) break;
+        tc_fence_after();
+        const uint32_t acc = tmem + b * kAccCols;
+        for (int kc = 0; kc < kchunks; ++kc) {
+          if (!(ok = mbar_wait(&full[s], ph, ctl, p.err, p.timeout_ns, 421))) break;
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(smem + s * STAGE_BYTES), b0 = a0 + A_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t ad = make_sdesc(a0 + 32 * kk, 16, 1024, kSw128);
+            const uint64_t bd = W_MN ? make_sdesc(b0 + 32 * p.r_pad * kk, b_bytes, 16 * p.r_pad, wswz)
+                                     : make_sdesc(b0 + 32 * kk, 16, 1024, kSw128);
+            umma_bf16(acc, ad, bd, idesc, (kc > 0 || kk > 0) ? 1u : 0u);
+          }
+          umma_commit(&empty[s]);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        umma_commit(&accfull[b]);
+      }
+      umma_commit(drain);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(drain, 0) && (long long)(globaltimer_ns() - t0) < p.timeout_ns) {
+      }
+    }
+  } else {
+    const int q = ((warp & 3) << 5) | lane;  // TMEM lane of this thread
+    uint32_t ti = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < n_tasks && ok; u += gridDim.x, ++ti) {
+      const int4 tk = __ldg(tasks + u);
+      const float sc = __ldg(p.scale + tk.x);
+      const uint32_t b = ti & 1, use = ti >> 1;
+      const uint32_t tl = tmem + b * kAccCols + ((uint32_t)(32 * (warp & 3)) << 16);
+      const int row = tk.y + q;
+      ok = __all_sync(kFull, mbar_wait(&accfull[b], use & 1, ctl, p.err, p.timeout_ns, 430));
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int j = 0; j < p.r_pad; j += 16) {
+        float v[16];
+        tmem_ld16(tl + j, v);
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(sc * v[2 * i], sc * v[2 * i + 1]);
+        uint4* d = reinterpret_cast<uint4*>(p.out + (size_t)row * p.r + j);
+        if (row < tk.z) {
+          if (j < p.r) d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          if (j + 8 < p.r) d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&accempty[b]);
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// =============================================================================
+// Adapter gradients: dA[a] = q^T x (stored transposed), dB[a] = dY^T p
+// =============================================================================
+namespace adw {
+constexpr int BM = 128, BK = 64, STAGES = 4;
+constexpr int A_BYTES = BK * BM * 2;            // 64 rows x 128 features, MN-major SW128
+constexpr int B_BYTES = BK * E4B_MAX_RANK * 2;  // 64 rows x r_pad, MN-major
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 1024;
+constexpr int kThreads = 192;
+constexpr int kAccCols = 64;
+constexpr int kTmemCols = 2 * kAccCols;
+static_assert(STAGE_BYTES % 1024 == 0, "stage alignment");
+}  // namespace adw
+
+struct AdapterWgradParams {
+  uint16_t* out[2];  // dA [n, r, K], dB [n, N, r]
+  int F[2], n_ft[2];
+  const int32_t* order;
+  const int32_t* offsets;
+  DeviceError* err;
+  long long timeout_ns;
+  int T, n, r, r_pad;
+};
+
+struct AdapterWgradUnit {
+  int g, ft, a, row0, rows;
+};
+__device__ __forceinline__ AdapterWgradUnit adapter_wgrad_unit(const AdapterWgradParams& p, int u) {
+  AdapterWgradUnit w;
+  const int per = p.n_ft[0] + p.n_ft[1];
+  w.a = u / per;
+  w.ft = u - w.a * per;
+  w.g = w.ft >= p.n_ft[0];
+  if (w.g) w.ft -= p.n_ft[0];
+  w.row0 = __ldg(p.offsets + w.a);
+  w.rows = __ldg(p.offsets + w.a + 1) - w.row0;  // a multiple of 16
+  return w;
+}
+
+__global__ void __launch_bounds__(adw::kThreads)
+    adapter_wgrad_kernel(const __grid_constant__ CUtensorMap act0, const __grid_constant__ CUtensorMap act1,
+                         const __grid_constant__ CUtensorMap low0, const __grid_constant__ CUtensorMap low1,
+                         const AdapterWgradParams p) {
+  using namespace adw;
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = align1024(smem_dyn);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + STAGES;
+  uint64_t* accfull = bars + 2 * STAGES;  // [2]
+  uint64_t* accempty = accfull + 2;       // [2]
+  uint64_t* drain = accfull + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accfull + 5);
+  CtaControl* ctl = reinterpret_cast<CtaControl*>(accfull + 6);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accfull[b], 1);
+      mbar_init(&accempty[b], 4);
+    }
+    mbar_init(drain, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int n_units = p.n * (p.n_ft[0] + p.n_ft[1]);
+  const uint32_t b_bytes = BK * p.r_pad * 2;
+
+  if (warp == 0) {
+    int s = 0;
+    uint32_t ph = 0, issued = 0, last_par = 0;
+    bool ok = true;
+    const uint32_t base = smem_u32(smem);
+    for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
+      const AdapterWgradUnit w = adapter_wgrad_unit(p, u);
+      const CUtensorMap* act = w.g ? &act1 : &act0;
+      const CUtensorMap* low = w.g ? &low1 : &low0;
+      const int x = w.ft * BM + (lane >> 4) * 64;  // lanes 0-15: features 0-63 of the tile, 16-31: 64-127
+      for (int kc = 0; kc * BK < w.rows; ++kc) {
+        const int row = kc * BK + 4 * (lane & 15);
+        const int4 tok = row < w.rows ? __ldg(reinterpret_cast<const int4*>(p.order + w.row0 + row))
+                                      : make_int4(p.T, p.T, p.T, p.T);
+        if (!(ok = __all_sync(kFull, mbar_wait(&empty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 510)))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], A_BYTES + b_bytes);
+        __syncwarp();
+        tma_gather4(base + s * STAGE_BYTES + (lane >> 4) * (A_BYTES / 2) + (lane & 15) * 512, act, &full[s], x, tok);
+        if (lane == 0) tma_load_2d(smem + s * STAGE_BYTES + A_BYTES, low, &full[s], 0, w.row0 + kc * BK);
+        __syncwarp();
+        issued |= 1u << s;
+        last_par = (last_par & ~(1u << s)) | (ph << s);
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (!ok) let_land(full, STAGES, issued, last_par, p.timeout_ns);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = make_idesc_bf16(BM, p.r_pad, true, true);
+      const uint32_t lswz = swz_for_row_bytes(2 * p.r_pad);
+      int s = 0;
+      uint32_t ph = 0, ti = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++ti) {
+        const AdapterWgradUnit w = adapter_wgrad_unit(p, u);
+        const uint32_t b = ti & 1, use = ti >> 1;
+        if (!(ok = mbar_wait(&accempty[b], (use & 1) ^ 1, ctl, p.err, p.timeout_ns, 520))) break;
+        tc_fence_after();
+        const uint32_t acc = tmem + b * kAccCols;
+        for (int kc = 0; kc * BK < w.rows; ++kc) {
+          if (!(ok = mbar_wait(&full[s], ph, ctl, p.err, p.timeout_ns, 521))) break;
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(smem + s * STAGE_BYTES), b0 = a0 + A_BYTES;
+          const int steps = min(BK, w.rows - kc * BK) / 16;  // rows past the adapter's end take no part
+          for (int kk = 0; kk < steps; ++kk) {
+            const uint64_t ad = make_sdesc(a0 + 2048 * kk, A_BYTES / 2, 1024, kSw128);
+            const uint64_t bd = make_sdesc(b0 + 32 * p.r_pad * kk, b_bytes, 16 * p.r_pad, lswz);
+            umma_bf16(acc, ad, bd, idesc, (kc > 0 || kk > 0) ? 1u : 0u);
+          }
+          umma_commit(&empty[s]);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        umma_commit(&accfull[b]);
+      }
+      umma_commit(drain);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(drain, 0) && (long long)(globaltimer_ns() - t0) < p.timeout_ns) {
+      }
+    }
+  } else {
+    const int q = ((warp & 3) << 5) | lane;
+    uint32_t ti = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++ti) {
+      const AdapterWgradUnit w = adapter_wgrad_unit(p, u);
+      const uint32_t b = ti & 1, use = ti >> 1;
+      const uint32_t tl = tmem + b * kAccCols + ((uint32_t)(32 * (warp & 3)) << 16);
+      ok = __all_sync(kFull, mbar_wait(&accfull[b], use & 1, ctl, p.err, p.timeout_ns, 530));
+      if (!ok) break;
+      tc_fence_after();
+      const int F = p.F[w.g], m = w.ft * BM + q;
+      uint16_t* out = p.out[w.g];
+#pragma unroll 1
+      for (int j = 0; j < p.r_pad; j += 16) {
+        float v[16];
+        if (w.rows > 0) {
+          tmem_ld16(tl + j, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+        }
+        if (m < F) {
+          if (w.g) {  // dB [N, r]
+            uint32_t pw[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pw[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            uint4* d = reinterpret_cast<uint4*>(out + ((size_t)w.a * F + m) * p.r + j);
+            if (j < p.r) d[0] = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+            if (j + 8 < p.r) d[1] = make_uint4(pw[4], pw[5], pw[6], pw[7]);
+          } else {  // dA [r, K]: lanes write neighbouring features
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (j + i < p.r) {
+                const __nv_bfloat16 h = __float2bfloat16_rn(v[i]);
+                out[((size_t)w.a * p.r + j + i) * F + m] = *reinterpret_cast<const uint16_t*>(&h);
+              }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&accempty[b]);
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// =============================================================================
+// Host-side launchers
+// =============================================================================
+namespace {
+int rank_padded(int r) { return r <= 16 ? 16 : (r <= 32 ? 32 : 64); }
+
+template <typename K>
+cudaError_t set_smem(K kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// 2-D byte matrix [rows, bytes].
+cudaError_t map_u8_2d(CUtensorMap* m, const void* base, uint64_t bytes, uint64_t rows, uint32_t box_bytes,
+                      uint32_t box_rows) {
+  const uint64_t dims[2] = {bytes, rows};
+  const uint64_t strides[1] = {bytes};
+  const uint32_t box[2] = {box_bytes, box_rows};
+  return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box,
+                           CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// Token rows for gather4: one-row boxes of 64 columns.
+cudaError_t map_gather(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows) {
+  return map_bf16_2d(m, base, cols, rows, 64, 1, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+}  // namespace
+
+cudaError_t launch_adapter_gemm(const AdapterProjHost& h, bool mn, const uint16_t* src, const uint16_t* low,
+                                const uint16_t* fac, uint16_t* out, int num_sms, cudaStream_t stream) {
+  const int R = mn ? h.N : h.K, O = mn ? h.K : h.N, rp = rank_padded(h.r);
+  CUtensorMap ma, mraw, mla, mlb;
+  cudaError_t err;
+  if ((err = map_gather(&ma, src, R, h.T)) != cudaSuccess) return err;
+  if ((err = mn ? map_u8_2d(&mraw, h.nf4, h.K / 2, h.N, 64, 64) : map_u8_2d(&mraw, h.nf4, h.K / 2, h.N, 32, 128)) !=
+      cudaSuccess)
+    return err;
+  const CUtensorMapSwizzle rswz = swizzle_for_bytes(2 * rp);
+  if ((err = map_bf16_2d(&mla, low, h.r, h.rows_cap, rp, 128, rswz)) != cudaSuccess) return err;
+  if (!mn)  // B [n, N, r]
+    err = map_bf16_3d(&mlb, fac, h.r, h.N, h.n, rp, 64, rswz);
+  else  // A [n, r, K]
+    err = map_bf16_3d(&mlb, fac, h.K, h.r, h.n, 64, rp, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (err != cudaSuccess) return err;
+  const AdapterSteps lay = adapter_steps_layout(h.rows_cap, h.n);
+  AdapterGemmParams p;
+  p.absmax = h.absmax;
+  p.order = h.order;
+  p.steps = h.steps;
+  p.out = out;
+  p.err = h.err;
+  p.timeout_ns = h.timeout_ns;
+  p.R = R;
+  p.O = O;
+  p.T = h.T;
+  p.N = h.N;
+  p.K = h.K;
+  p.r_pad = rp;
+  p.n_nt = (O + 255) / 256;
+  p.unit_start = lay.unit_start;
+  p.entries = lay.entries;
+  const int64_t units = h.rows_cap / kAdapterUnitRows * p.n_nt;
+  const int grid = 2 * (int)(units < num_sms / 2 ? units : num_sms / 2);
+  LaunchScope scope(mn ? "adapter_gemm_dgrad" : "adapter_gemm_fwd", stream);
+  if (mn) {
+    if ((err = set_smem(adapter_gemm_kernel<true>, adg::SMEM_BYTES)) != cudaSuccess) return err;
+    adapter_gemm_kernel<true><<<grid, adg::kThreads, adg::SMEM_BYTES, stream>>>(ma, mraw, mla, mlb, p);
+  } else {
+    if ((err = set_smem(adapter_gemm_kernel<false>, adg::SMEM_BYTES)) != cudaSuccess) return err;
+    adapter_gemm_kernel<false><<<grid, adg::kThreads, adg::SMEM_BYTES, stream>>>(ma, mraw, mla, mlb, p);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_adapter_rows(const AdapterProjHost& h, bool mn, const uint16_t* src, const uint16_t* fac,
+                                uint16_t* out, int num_sms, cudaStream_t stream) {
+  const int R = mn ? h.N : h.K, rp = rank_padded(h.r);
+  CUtensorMap ms, mw;
+  cudaError_t err;
+  if ((err = map_gather(&ms, src, R, h.T)) != cudaSuccess) return err;
+  if (mn)  // B [n, N, r]
+    err = map_bf16_3d(&mw, fac, h.r, h.N, h.n, rp, 64, swizzle_for_bytes(2 * rp));
+  else  // A [n, r, K]
+    err = map_bf16_3d(&mw, fac, h.K, h.r, h.n, 64, rp, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (err != cudaSuccess) return err;
+  AdapterRowsParams p;
+  p.order = h.order;
+  p.steps = h.steps;
+  p.scale = h.scale;
+  p.out = out;
+  p.err = h.err;
+  p.timeout_ns = h.timeout_ns;
+  p.R = R;
+  p.T = h.T;
+  p.r = h.r;
+  p.r_pad = rp;
+  p.tasks = adapter_steps_layout(h.rows_cap, h.n).tasks;
+  const int64_t cap = h.rows_cap / kAdapterTaskRows + h.n;
+  const int grid = (int)(cap < num_sms ? cap : num_sms);
+  LaunchScope scope(mn ? "adapter_proj_dy" : "adapter_proj_x", stream);
+  if (mn) {
+    if ((err = set_smem(adapter_proj_kernel<true>, adp::SMEM_BYTES)) != cudaSuccess) return err;
+    adapter_proj_kernel<true><<<grid, adp::kThreads, adp::SMEM_BYTES, stream>>>(ms, mw, p);
+  } else {
+    if ((err = set_smem(adapter_proj_kernel<false>, adp::SMEM_BYTES)) != cudaSuccess) return err;
+    adapter_proj_kernel<false><<<grid, adp::kThreads, adp::SMEM_BYTES, stream>>>(ms, mw, p);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, const uint16_t* dY, const uint16_t* p_low,
+                                 const uint16_t* q_low, uint16_t* dA, uint16_t* dB, int num_sms, cudaStream_t stream) {
+  const int rp = rank_padded(h.r);
+  CUtensorMap mx, md, mq, mp;
+  cudaError_t err;
+  if ((err = map_gather(&mx, x, h.K, h.T)) != cudaSuccess) return err;
+  if ((err = map_gather(&md, dY, h.N, h.T)) != cudaSuccess) return err;
+  const CUtensorMapSwizzle rswz = swizzle_for_bytes(2 * rp);
+  if ((err = map_bf16_2d(&mq, q_low, h.r, h.rows_cap, rp, 64, rswz)) != cudaSuccess) return err;
+  if ((err = map_bf16_2d(&mp, p_low, h.r, h.rows_cap, rp, 64, rswz)) != cudaSuccess) return err;
+  AdapterWgradParams p;
+  p.out[0] = dA;
+  p.out[1] = dB;
+  p.F[0] = h.K;
+  p.F[1] = h.N;
+  p.n_ft[0] = (h.K + adw::BM - 1) / adw::BM;
+  p.n_ft[1] = (h.N + adw::BM - 1) / adw::BM;
+  p.order = h.order;
+  p.offsets = h.offsets;
+  p.err = h.err;
+  p.timeout_ns = h.timeout_ns;
+  p.T = h.T;
+  p.n = h.n;
+  p.r = h.r;
+  p.r_pad = rp;
+  const int64_t units = (int64_t)h.n * (p.n_ft[0] + p.n_ft[1]);
+  const int64_t cap = (int64_t)num_sms * 2;
+  const int grid = (int)(units < cap ? units : cap);
+  if ((err = set_smem(adapter_wgrad_kernel, adw::SMEM_BYTES)) != cudaSuccess) return err;
+  LaunchScope scope("adapter_wgrad", stream);
+  adapter_wgrad_kernel<<<grid, adw::kThreads, adw::SMEM_BYTES, stream>>>(mx, md, mq, mp, p);
+  return cudaGetLastError();
+}
+
+}  // namespace e4b

@@ -774,10 +774,12 @@ e4b_status e4b_multi_lora_serve_fwd(const e4b_proj_dims* dims, int32_t T, const 
   int32_t* offsets = reinterpret_cast<int32_t*>(w + l.offsets);
   int32_t* steps = reinterpret_cast<int32_t*>(w + l.steps);
   uint16_t* low = reinterpret_cast<uint16_t*>(w + l.low);
+  int sms = 0;
+  E4B_CUDA(device_sms(&sms));
   const AdapterProjHost h = proj_host(dims, T, base, adapters, order, offsets, steps, ws);
   E4B_CUDA(launch_adapter_group(ids, T, dims->n_adapters, order, offsets, steps, st));
-  E4B_CUDA(launch_adapter_rows(h, false, x, adapters->A, low, st));
-  E4B_CUDA(launch_adapter_gemm(h, false, x, low, adapters->B, y, st));
+  E4B_CUDA(launch_adapter_rows(h, false, x, adapters->A, low, sms, st));
+  E4B_CUDA(launch_adapter_gemm(h, false, x, low, adapters->B, y, sms, st));
   return E4B_OK;
 }
 
@@ -792,9 +794,11 @@ e4b_status e4b_multi_lora_fwd(const e4b_proj_dims* dims, int32_t T, const e4b_ad
   E4B_TRY(check_projection(base, adapters));
   if (!aligned16(x) || !aligned16(p) || !aligned16(y)) return E4B_ERR_INVALID_ARG;
   const cudaStream_t st = (cudaStream_t)stream;
+  int sms = 0;
+  E4B_CUDA(device_sms(&sms));
   const AdapterProjHost h = proj_host(dims, T, base, adapters, groups->order, groups->offsets, groups->steps, ws);
-  E4B_CUDA(launch_adapter_rows(h, false, x, adapters->A, p, st));
-  E4B_CUDA(launch_adapter_gemm(h, false, x, p, adapters->B, y, st));
+  E4B_CUDA(launch_adapter_rows(h, false, x, adapters->A, p, sms, st));
+  E4B_CUDA(launch_adapter_gemm(h, false, x, p, adapters->B, y, sms, st));
   return E4B_OK;
 }
 
@@ -809,9 +813,11 @@ e4b_status e4b_multi_lora_dgrad(const e4b_proj_dims* dims, int32_t T, const e4b_
   E4B_TRY(check_projection(base, adapters));
   if (!aligned16(dY) || !aligned16(q) || !aligned16(dx)) return E4B_ERR_INVALID_ARG;
   const cudaStream_t st = (cudaStream_t)stream;
+  int sms = 0;
+  E4B_CUDA(device_sms(&sms));
   const AdapterProjHost h = proj_host(dims, T, base, adapters, groups->order, groups->offsets, groups->steps, ws);
-  E4B_CUDA(launch_adapter_rows(h, true, dY, adapters->B, q, st));
-  E4B_CUDA(launch_adapter_gemm(h, true, dY, q, adapters->A, dx, st));
+  E4B_CUDA(launch_adapter_rows(h, true, dY, adapters->B, q, sms, st));
+  E4B_CUDA(launch_adapter_gemm(h, true, dY, q, adapters->A, dx, sms, st));
   return E4B_OK;
 }
 
@@ -831,8 +837,10 @@ e4b_status e4b_multi_lora_wgrad(const e4b_proj_dims* dims, int32_t T, const e4b_
   }
   E4B_TRY(check_groups(groups));
   if (!aligned16(x) || !aligned16(dY) || !aligned16(p) || !aligned16(q)) return E4B_ERR_INVALID_ARG;
+  int sms = 0;
+  E4B_CUDA(device_sms(&sms));
   const AdapterProjHost h = proj_host(dims, T, nullptr, nullptr, groups->order, groups->offsets, groups->steps, ws);
-  E4B_CUDA(launch_adapter_wgrad(h, x, dY, p, q, dA, dB, st));
+  E4B_CUDA(launch_adapter_wgrad(h, x, dY, p, q, dA, dB, sms, st));
   return E4B_OK;
 }
 

@@ -194,7 +194,7 @@ struct WgradHost {
 };
 cudaError_t launch_wgrad(const WgradHost& h, int num_sms, cudaStream_t stream);
 
-// ---- adapters beside a shared projection (adapters.cu)
+// ---- adapters beside a shared projection (adapters.cu, adapters_gemm.cu)
 constexpr int kAdapterUnitRows = 256;  // rows of a GEMM unit (a CTA pair)
 constexpr int kAdapterTaskRows = 128;  // rows of a low-rank projection task (one adapter's)
 inline int64_t adapter_rows_cap(int64_t T, int n) {
@@ -232,12 +232,12 @@ struct AdapterProjHost {
 };
 // out[row, :r] = bf16(s[a] src[t] . factor[a]): A [n, r, K] over x, or (mn) B [n, N, r] over dY.
 cudaError_t launch_adapter_rows(const AdapterProjHost& h, bool mn, const uint16_t* src, const uint16_t* fac,
-                                uint16_t* out, cudaStream_t stream);
+                                uint16_t* out, int num_sms, cudaStream_t stream);
 // out[t] = src[t] W^T + low[row] B[a]^T, or (mn) src[t] W + low[row] A[a].
 cudaError_t launch_adapter_gemm(const AdapterProjHost& h, bool mn, const uint16_t* src, const uint16_t* low,
-                                const uint16_t* fac, uint16_t* out, cudaStream_t stream);
+                                const uint16_t* fac, uint16_t* out, int num_sms, cudaStream_t stream);
 cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, const uint16_t* dY, const uint16_t* p,
-                                 const uint16_t* q, uint16_t* dA, uint16_t* dB, cudaStream_t stream);
+                                 const uint16_t* q, uint16_t* dA, uint16_t* dB, int num_sms, cudaStream_t stream);
 
 // ---- balance loss (balance.cu)
 struct BalanceHost {
