@@ -78,9 +78,10 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
   const int entry0 = block_scan(u1 - u0 + 1, 1);
   const int ntask = (padded + kAdapterTaskRows - 1) / kAdapterTaskRows;
   const int task0 = block_scan(ntask, 2);
-  const int none0 = block_total(0), entries = block_total(1), tasks = block_total(2);
+  const int none0 = block_total(0), entries = block_total(1), adapter_tasks = block_total(2);
   int nnone = 0;
   for (int w = 0; w < kGroupWarps; ++w) nnone += table[w * cols + n];
+  const int none_tasks = (nnone + kAdapterTaskRows - 1) / kAdapterTaskRows;
   const int used = none0 + nnone;
   const int units = (used + kAdapterUnitRows - 1) / kAdapterUnitRows;
   const AdapterSteps lay = adapter_steps_layout(rows_cap, n);
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
     steps[0] = units;
     steps[1] = used;
     steps[2] = entries;
-    steps[3] = tasks;
+    steps[3] = adapter_tasks + none_tasks;
     int32_t* en = steps + lay.entries + 4 * entries;  // sentinel
     en[0] = -1;
     en[1] = -1;
@@ -131,6 +132,13 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
       table[w * cols + n] = at;
       at += c;
     }
+  }
+  for (int i = tid; i < none_tasks; i += kGroupThreads) {
+    int32_t* tk = steps + lay.tasks + 4 * (adapter_tasks + i);
+    tk[0] = n;
+    tk[1] = none0 + i * kAdapterTaskRows;
+    tk[2] = used;
+    tk[3] = 0;
   }
   for (int i = used + tid; i < rows_cap; i += kGroupThreads) order[i] = T;
   __syncthreads();

@@ -10,12 +10,14 @@
 //  * adapter_wgrad_kernel: dA = q^T x and dB = dY^T p, K = the rows of one
 //    adapter.
 //
-// Rows are the tokens sorted by adapter.  No sorted copy of x or dY is made:
-// the tensor maps have one-row boxes and every load gathers four token rows by
-// index (tile::gather4), a warp's 32 lanes one 128-row tile; padding rows carry
-// the index T, outside the tensor, and read as zeros.  Every adapter's rows
-// start at a multiple of 16, the K step of one UMMA, so that the gradient
-// products never multiply two adapters' rows.
+// Rows are the tokens sorted by adapter; every adapter's rows start at a
+// multiple of 16, the K step of one UMMA, so that the gradient products never
+// multiply two adapters' rows.  The projection kernel gathers the token rows
+// (cp.async, 16 bytes a lane) and stores them in row order in passing, for the
+// base product to load as plain tiles.  TMA gathers by row index
+// (tile::gather4) were measured instead: about 77 cycles for every four rows
+// of 128 bytes, 5 times the time of the UMMAs they feed (T = 16384, K = 4096,
+// N = 14336: 4204 us against 1960 us with the copy).
 //
 // The adapters of a tile share its accumulator: each K = r step names the
 // TMEM lanes (rows) it must not write (the disable-output-lane operand), so
@@ -31,16 +33,6 @@ namespace e4b {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
-
-// Four rows of a 2-D tensor (one-row box) into consecutive 128-byte shared rows.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int4 rows) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
-      "%5, %6, %7}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z),
-      "r"(rows.w)
-      : "memory");
-}
 
 // The pair UMMA with output lanes disabled: bit i of the 256-bit mask keeps row i of the accumulator as it is.
 __device__ __forceinline__ void umma_bf16_2sm_masked(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -82,7 +74,7 @@ __device__ __forceinline__ void let_land(uint64_t* bars, int n, uint32_t issued,
 // =============================================================================
 // Roles and rings as in the expert block's grouped GEMM: warp 0 codes, warp 1
 // TMEM owner and (even CTA) UMMA issuer, warp 2 relay of operand readiness to
-// the even CTA, warp 3 activation rows and low-rank operands, warps 4-19 four
+// the even CTA, warp 3 activation tiles and low-rank operands, warps 4-19 four
 // decode groups taking the k-chunks round robin, warps 20-23 epilogue.  The
 // low-rank steps come after the k-chunks: a unit's two ring slots per adapter
 // hold its 128 p (or q) rows and 128 factor rows.
@@ -216,52 +208,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 3) {
-    // ------------------------------------------------ activation rows (the whole warp) + low-rank operands
+    // ------------------------------------------------ activation tiles + low-rank operands (one lane)
     if (lane == 0) {
       tma_prefetch_desc(&map_a);
       tma_prefetch_desc(&map_la);
       tma_prefetch_desc(&map_lb);
-    }
-    uint32_t s = 0, ph = 0, issued = 0, last_par = 0;
-    auto issued_next = [&]() {
-      issued |= 1u << s;
-      last_par = (last_par & ~(1u << s)) | (ph << s);
-      if (++s == SA) {
-        s = 0;
-        ph ^= 1;
-      }
-    };
-    const uint32_t a_u = smem_u32(aring);
-    auto tokens_of = [&](int u) -> int4 {  // the four tokens whose rows this lane loads
-      const int row = (u / p.n_nt) * 256 + (int)rank * 128 + 4 * lane;
-      return __ldg(reinterpret_cast<const int4*>(p.order + row));
-    };
-    bool ok = true;
-    int4 next = pair < n_units ? tokens_of(pair) : make_int4(0, 0, 0, 0);
-    for (int u = pair; u < n_units && ok; u += n_pairs) {
-      const int mu = u / p.n_nt, c0 = (u % p.n_nt) * 256 + (int)rank * 128;
-      const int4 tok = next;
-      if (u + n_pairs < n_units) next = tokens_of(u + n_pairs);
-      for (int kc = 0; kc < kchunks; ++kc) {
-        if (!(ok = __all_sync(kFull, mbar_wait(&aempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 312)))) break;
-        if (lane == 0) mbar_arrive_expect_tx(&xfull[s], (uint32_t)A_BYTES);
-        __syncwarp();
-        tma_gather4(a_u + s * A_BYTES + lane * 512, &map_a, &xfull[s], kc * BK, tok);
-        issued_next();
-      }
-      if (!ok) break;
-      for (int i = __ldg(unit_start + mu);; ++i) {
-        const int4 en = __ldg(entries + i);
-        if (en.y != mu) break;
-        const uint32_t s1 = (s + 1 == SA) ? 0 : s + 1, ph1 = (s + 1 == SA) ? ph ^ 1 : ph;
-        ok = __all_sync(kFull, mbar_wait(&aempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 310) &&
-                                   mbar_wait(&aempty[s1], ph1 ^ 1, ctl, p.err, p.timeout_ns, 310));
+      uint32_t s = 0, ph = 0, issued = 0, last_par = 0;
+      auto issued_next = [&]() {
+        issued |= 1u << s;
+        last_par = (last_par & ~(1u << s)) | (ph << s);
+        if (++s == SA) {
+          s = 0;
+          ph ^= 1;
+        }
+      };
+      bool ok = true;
+      for (int u = pair; u < n_units && ok; u += n_pairs) {
+        const int mu = u / p.n_nt, c0 = (u % p.n_nt) * 256 + (int)rank * 128, row0 = mu * 256 + (int)rank * 128;
+        for (int kc = 0; kc < kchunks; ++kc) {
+          if (!(ok = mbar_wait(&aempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 312))) break;
+          mbar_arrive_expect_tx(&xfull[s], (uint32_t)A_BYTES);
+          tma_load_2d(aring + s * A_BYTES, &map_a, &xfull[s], kc * BK, row0);
+          issued_next();
+        }
         if (!ok) break;
-        if (lane == 0) {
+        for (int i = __ldg(unit_start + mu);; ++i) {
+          const int4 en = __ldg(entries + i);
+          if (en.y != mu) break;
+          const uint32_t s1 = (s + 1 == SA) ? 0 : s + 1, ph1 = (s + 1 == SA) ? ph ^ 1 : ph;
+          if (!(ok = mbar_wait(&aempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 310))) break;
+          if (!(ok = mbar_wait(&aempty[s1], ph1 ^ 1, ctl, p.err, p.timeout_ns, 310))) break;
           uint8_t* la = aring + s * A_BYTES;
           uint8_t* lb = aring + s1 * A_BYTES;
           mbar_arrive_expect_tx(&xfull[s], (uint32_t)(512 * p.r_pad));
-          tma_load_2d(la, &map_la, &xfull[s], 0, mu * 256 + (int)rank * 128);
+          tma_load_2d(la, &map_la, &xfull[s], 0, row0);
           if (!kMN) {
             tma_load_3d(lb, &map_lb, &xfull[s], 0, c0, en.x);
             tma_load_3d(lb + 128 * p.r_pad, &map_lb, &xfull[s], 0, c0 + 64, en.x);
@@ -270,13 +250,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
             tma_load_3d(lb + 128 * p.r_pad, &map_lb, &xfull[s], c0 + 64, 0, en.x);
           }
           mbar_arrive(&xfull[s1]);
+          issued_next();
+          issued_next();
         }
-        __syncwarp();
-        issued_next();
-        issued_next();
       }
+      if (!ok) let_land(xfull, SA, issued, last_par, p.timeout_ns);
     }
-    if (!ok) let_land(xfull, SA, issued, last_par, p.timeout_ns);
     __syncwarp();
   } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------ UMMA issuer (even CTA, one elected lane)
@@ -534,42 +513,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
 }
 
 // =============================================================================
-// Low-rank rows: out[row] = bf16(s[a] src[token of row] . F[a])
+// Row gather with the low-rank projection:
+//   dst[row] = src[token of row]  (zero for padding rows)
+//   out[row] = bf16(s[a] dst[row] . F[a])
+// A task is up to 128 rows of one adapter (or of the tokens without one, which
+// are only gathered).  Four loader warps copy the rows' 128-byte pieces into
+// the UMMA's swizzled tile with cp.async (zeros for padding rows), the tensor
+// core projects the tile, and 16-row bulk stores (a task's rows are a multiple
+// of 16, and the next task's rows must not be touched) write it to dst.
 // =============================================================================
 namespace adp {
-constexpr int BM = 128, BK = 64, STAGES = 6;
+constexpr int BM = 128, BK = 64, STAGES = 4;
 constexpr int A_BYTES = BM * BK * 2;
 constexpr int B_BYTES = BK * E4B_MAX_RANK * 2;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 1024;
-constexpr int kThreads = 192;  // warp 0 TMA, warp 1 MMA, warps 2-5 epilogue
+constexpr int kLoadWarps = 4, kWLoadWarp = 4, kIssueWarp = 5, kStoreWarp = 6, kEpiWarp0 = 7;
+constexpr int kThreads = 11 * 32;
 constexpr int kAccCols = 64;
 constexpr int kTmemCols = 2 * kAccCols;
 static_assert(STAGE_BYTES % 1024 == 0, "stage alignment");
+static_assert(kAdapterTaskRows == BM, "a task is one tile");
 }  // namespace adp
 
 struct AdapterRowsParams {
+  const uint16_t* src;   // [T, R]
   const int32_t* order;
   const int32_t* steps;
   const float* scale;
   uint16_t* out;
   DeviceError* err;
   long long timeout_ns;
-  int R, T, r, r_pad, tasks;  // tasks: place of the task list in `steps`
+  int R, T, n, r, r_pad, tasks;  // tasks: place of the task list in `steps`
 };
 
 // F = A [n, r, R] (K-major), or B [n, R, r] (W_MN).
 template <bool W_MN>
-__global__ void __launch_bounds__(adp::kThreads)
-    adapter_proj_kernel(const __grid_constant__ CUtensorMap map_src, const __grid_constant__ CUtensorMap map_w,
+__global__ void __launch_bounds__(adp::kThreads, 2)
+    adapter_proj_kernel(const __grid_constant__ CUtensorMap map_dst, const __grid_constant__ CUtensorMap map_w,
                         const AdapterRowsParams p) {
   using namespace adp;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = align1024(smem_dyn);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
-  uint64_t* full = bars;
-  uint64_t* empty = bars + STAGES;
-  uint64_t* accfull = bars + 2 * STAGES;  // [2]
+  uint64_t* full = bars;                  // [STAGES] rows and factor chunk landed
+  uint64_t* empty = bars + STAGES;        // [STAGES] read by the UMMAs
+  uint64_t* stored = bars + 2 * STAGES;   // [STAGES] read by the bulk stores
+  uint64_t* accfull = bars + 3 * STAGES;  // [2]
   uint64_t* accempty = accfull + 2;       // [2]
   uint64_t* drain = accfull + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accfull + 5);
@@ -577,8 +567,9 @@ __global__ void __launch_bounds__(adp::kThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], kLoadWarps * 32 + 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&stored[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accfull[b], 1);
@@ -588,7 +579,7 @@ __global__ void __launch_bounds__(adp::kThreads)
     ctl->abort = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == kIssueWarp) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
@@ -601,64 +592,96 @@ __global__ void __launch_bounds__(adp::kThreads)
   const int kchunks = (p.R + BK - 1) / BK;
   const uint32_t b_bytes = BK * p.r_pad * 2;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      tma_prefetch_desc(&map_src);
-      tma_prefetch_desc(&map_w);
-    }
-    int s = 0;
-    uint32_t ph = 0, issued = 0, last_par = 0;
+  if (warp < kLoadWarps) {
+    // rows 32 warp + 4 i + lane / 8 of the tile, 16-byte piece lane % 8 of their 128
+    const int c = lane & 7;
+    uint32_t s = 0, ph = 0;
     bool ok = true;
-    const uint32_t base = smem_u32(smem);
     for (int u = blockIdx.x; u < n_tasks && ok; u += gridDim.x) {
       const int4 tk = __ldg(tasks + u);
-      const int row = tk.y + 4 * lane;  // a task's rows start and end at multiples of 16
-      const int4 tok = row < tk.z ? __ldg(reinterpret_cast<const int4*>(p.order + row)) : make_int4(p.T, p.T, p.T, p.T);
+      const uint16_t* src[8];
+      bool live[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = tk.y + 32 * warp + 4 * i + (lane >> 3);
+        const int t = row < tk.z ? __ldg(p.order + row) : p.T;
+        live[i] = t < p.T;
+        src[i] = p.src + (live[i] ? (size_t)t * p.R : 0) + 8 * c;
+      }
       for (int kc = 0; kc < kchunks; ++kc) {
-        if (!(ok = __all_sync(kFull, mbar_wait(&empty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 410)))) break;
-        if (lane == 0) mbar_arrive_expect_tx(&full[s], A_BYTES + b_bytes);
-        __syncwarp();
-        tma_gather4(base + s * STAGE_BYTES + lane * 512, &map_src, &full[s], kc * BK, tok);
-        if (lane == 0) {
-          uint8_t* st = smem + s * STAGE_BYTES + A_BYTES;
-          if (W_MN)
-            tma_load_3d(st, &map_w, &full[s], 0, kc * BK, tk.x);
-          else
-            tma_load_3d(st, &map_w, &full[s], kc * BK, 0, tk.x);
+        if (!(ok = __all_sync(kFull, mbar_wait(&empty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 411)))) break;
+        if (!(ok = __all_sync(kFull, mbar_wait(&stored[s], ph ^ 1, ctl, p.err, p.timeout_ns, 412)))) break;
+        uint8_t* tile = smem + s * STAGE_BYTES;
+        const bool in = kc * BK + 8 * c < p.R;  // the last chunk of a length that is no multiple of 64
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int q = 32 * warp + 4 * i + (lane >> 3);
+          const bool go = live[i] && in;
+          cp_async_16_zfill(tile + (q >> 3) * 1024 + (q & 7) * 128 + ((c ^ (q & 7)) << 4),
+                            go ? src[i] + kc * BK : p.src, go ? 16u : 0u);
         }
-        __syncwarp();
-        issued |= 1u << s;
-        last_par = (last_par & ~(1u << s)) | (ph << s);
+        cp_async_arrive_noinc(&full[s]);
         if (++s == STAGES) {
           s = 0;
           ph ^= 1;
         }
       }
     }
-    if (!ok) let_land(full, STAGES, issued, last_par, p.timeout_ns);
-    __syncwarp();
-  } else if (warp == 1) {
+    asm volatile("cp.async.wait_all;" ::: "memory");  // nothing in flight when the shared memory goes away
+  } else if (warp == kWLoadWarp) {
+    if (lane == 0) {
+      tma_prefetch_desc(&map_w);
+      uint32_t s = 0, ph = 0, issued = 0, last_par = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < n_tasks && ok; u += gridDim.x) {
+        const int a = __ldg(tasks + u).x;
+        for (int kc = 0; kc < kchunks; ++kc) {
+          if (!(ok = mbar_wait(&empty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 413))) break;
+          uint8_t* st = smem + s * STAGE_BYTES + A_BYTES;
+          if (a < p.n) {
+            mbar_arrive_expect_tx(&full[s], b_bytes);
+            if (W_MN)
+              tma_load_3d(st, &map_w, &full[s], 0, kc * BK, a);
+            else
+              tma_load_3d(st, &map_w, &full[s], kc * BK, 0, a);
+          } else {
+            mbar_arrive(&full[s]);  // no adapter: nothing to multiply with
+          }
+          issued |= 1u << s;
+          last_par = (last_par & ~(1u << s)) | (ph << s);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (!ok) let_land(full, STAGES, issued, last_par, p.timeout_ns);
+    }
+  } else if (warp == kIssueWarp) {
     if (lane == 0) {
       const uint32_t idesc = make_idesc_bf16(BM, p.r_pad, false, W_MN);
       const uint32_t wswz = swz_for_row_bytes(2 * p.r_pad);
-      int s = 0;
-      uint32_t ph = 0, ti = 0;
+      uint32_t s = 0, ph = 0, ti = 0;
       bool ok = true;
       for (int u = blockIdx.x; u < n_tasks && ok; u += gridDim.x, ++ti) {
+        const bool project = __ldg(tasks + u).x < p.n;
         const uint32_t b = ti & 1, use = ti >> 1;
         if (!(ok = mbar_wait(&accempty[b], (use & 1) ^ 1, ctl, p.err, p.timeout_ns, 420))) break;
         tc_fence_after();
         const uint32_t acc = tmem + b * kAccCols;
         for (int kc = 0; kc < kchunks; ++kc) {
           if (!(ok = mbar_wait(&full[s], ph, ctl, p.err, p.timeout_ns, 421))) break;
+          fence_proxy_async_smem();  // the rows were written by cp.async
           tc_fence_after();
           const uint32_t a0 = smem_u32(smem + s * STAGE_BYTES), b0 = a0 + A_BYTES;
+          if (project) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = make_sdesc(a0 + 32 * kk, 16, 1024, kSw128);
-            const uint64_t bd = W_MN ? make_sdesc(b0 + 32 * p.r_pad * kk, b_bytes, 16 * p.r_pad, wswz)
-                                     : make_sdesc(b0 + 32 * kk, 16, 1024, kSw128);
-            umma_bf16(acc, ad, bd, idesc, (kc > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < BK / 16; ++kk) {
+              const uint64_t ad = make_sdesc(a0 + 32 * kk, 16, 1024, kSw128);
+              const uint64_t bd = W_MN ? make_sdesc(b0 + 32 * p.r_pad * kk, b_bytes, 16 * p.r_pad, wswz)
+                                       : make_sdesc(b0 + 32 * kk, 16, 1024, kSw128);
+              umma_bf16(acc, ad, bd, idesc, (kc > 0 || kk > 0) ? 1u : 0u);
+            }
           }
           umma_commit(&empty[s]);
           if (++s == STAGES) {
@@ -674,13 +697,44 @@ __global__ void __launch_bounds__(adp::kThreads)
       while (!mbar_try_wait(drain, 0) && (long long)(globaltimer_ns() - t0) < p.timeout_ns) {
       }
     }
+  } else if (warp == kStoreWarp) {
+    // two chunks' stores in flight; a slot is handed back once its stores have read it
+    if (lane == 0) {
+      tma_prefetch_desc(&map_dst);
+      uint32_t s = 0, ph = 0, prev = 0;
+      bool ok = true, pending = false;
+      for (int u = blockIdx.x; u < n_tasks && ok; u += gridDim.x) {
+        const int4 tk = __ldg(tasks + u);
+        const int granules = (min(BM, tk.z - tk.y) + 15) / 16;
+        for (int kc = 0; kc < kchunks; ++kc) {
+          if (!(ok = mbar_wait(&full[s], ph, ctl, p.err, p.timeout_ns, 415))) break;
+          fence_proxy_async_smem();
+          for (int g = 0; g < granules; ++g)
+            tma_store_2d(&map_dst, smem_u32(smem + s * STAGE_BYTES) + g * 2048, kc * BK, tk.y + 16 * g);
+          bulk_commit();
+          if (pending) {
+            bulk_wait_read<1>();
+            mbar_arrive(&stored[prev]);
+          }
+          prev = s;
+          pending = true;
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      bulk_wait<0>();  // reads and writes of every store done
+      if (pending) mbar_arrive(&stored[prev]);
+    }
   } else {
     const int q = ((warp & 3) << 5) | lane;  // TMEM lane of this thread
     uint32_t ti = 0;
     bool ok = true;
     for (int u = blockIdx.x; u < n_tasks && ok; u += gridDim.x, ++ti) {
       const int4 tk = __ldg(tasks + u);
-      const float sc = __ldg(p.scale + tk.x);
+      const bool project = tk.x < p.n;
+      const float sc = project ? __ldg(p.scale + tk.x) : 0.0f;
       const uint32_t b = ti & 1, use = ti >> 1;
       const uint32_t tl = tmem + b * kAccCols + ((uint32_t)(32 * (warp & 3)) << 16);
       const int row = tk.y + q;
@@ -688,7 +742,7 @@ __global__ void __launch_bounds__(adp::kThreads)
       if (!ok) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int j = 0; j < p.r_pad; j += 16) {
+      for (int j = 0; project && j < p.r_pad; j += 16) {
         float v[16];
         tmem_ld16(tl + j, v);
         uint32_t w[8];
@@ -707,7 +761,7 @@ __global__ void __launch_bounds__(adp::kThreads)
   }
   __syncwarp();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == kIssueWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -722,13 +776,16 @@ constexpr int A_BYTES = BK * BM * 2;            // 64 rows x 128 features, MN-ma
 constexpr int B_BYTES = BK * E4B_MAX_RANK * 2;  // 64 rows x r_pad, MN-major
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 1024;
-constexpr int kThreads = 192;
+// warps 0-3 row loaders, 4 low-rank rows, 5 UMMA issuer + TMEM owner, 6-9 epilogue
+constexpr int kLoadWarps = 4, kLowWarp = 4, kIssueWarp = 5;
+constexpr int kThreads = 10 * 32;
 constexpr int kAccCols = 64;
 constexpr int kTmemCols = 2 * kAccCols;
 static_assert(STAGE_BYTES % 1024 == 0, "stage alignment");
 }  // namespace adw
 
 struct AdapterWgradParams {
+  const uint16_t* act[2];  // x [T, K], dY [T, N]
   uint16_t* out[2];  // dA [n, r, K], dB [n, N, r]
   int F[2], n_ft[2];
   const int32_t* order;
@@ -753,9 +810,8 @@ __device__ __forceinline__ AdapterWgradUnit adapter_wgrad_unit(const AdapterWgra
   return w;
 }
 
-__global__ void __launch_bounds__(adw::kThreads)
-    adapter_wgrad_kernel(const __grid_constant__ CUtensorMap act0, const __grid_constant__ CUtensorMap act1,
-                         const __grid_constant__ CUtensorMap low0, const __grid_constant__ CUtensorMap low1,
+__global__ void __launch_bounds__(adw::kThreads, 2)
+    adapter_wgrad_kernel(const __grid_constant__ CUtensorMap low0, const __grid_constant__ CUtensorMap low1,
                          const AdapterWgradParams p) {
   using namespace adw;
   extern __shared__ uint8_t smem_dyn[];
@@ -771,7 +827,7 @@ __global__ void __launch_bounds__(adw::kThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], kLoadWarps * 32 + 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -782,7 +838,7 @@ __global__ void __launch_bounds__(adw::kThreads)
     ctl->abort = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == kIssueWarp) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
@@ -793,37 +849,66 @@ __global__ void __launch_bounds__(adw::kThreads)
   const int n_units = p.n * (p.n_ft[0] + p.n_ft[1]);
   const uint32_t b_bytes = BK * p.r_pad * 2;
 
-  if (warp == 0) {
-    int s = 0;
-    uint32_t ph = 0, issued = 0, last_par = 0;
+  if (warp < kLoadWarps) {
+    // rows 16 warp + 4 (i % 4) + lane / 8 of the chunk, feature half i / 4, 16-byte piece lane % 8
+    const int c = lane & 7;
+    uint32_t s = 0, ph = 0;
     bool ok = true;
-    const uint32_t base = smem_u32(smem);
     for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
       const AdapterWgradUnit w = adapter_wgrad_unit(p, u);
-      const CUtensorMap* act = w.g ? &act1 : &act0;
-      const CUtensorMap* low = w.g ? &low1 : &low0;
-      const int x = w.ft * BM + (lane >> 4) * 64;  // lanes 0-15: features 0-63 of the tile, 16-31: 64-127
+      const uint16_t* act = w.g ? p.act[1] : p.act[0];
+      const int F = w.g ? p.F[1] : p.F[0];
+      const int f = w.ft * BM + 8 * c;
+      auto tokens = [&](int kc, int (&t)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = kc * BK + 16 * warp + 4 * i + (lane >> 3);
+          t[i] = row < w.rows ? __ldg(p.order + w.row0 + row) : p.T;
+        }
+      };
+      int t[4];
+      tokens(0, t);
       for (int kc = 0; kc * BK < w.rows; ++kc) {
-        const int row = kc * BK + 4 * (lane & 15);
-        const int4 tok = row < w.rows ? __ldg(reinterpret_cast<const int4*>(p.order + w.row0 + row))
-                                      : make_int4(p.T, p.T, p.T, p.T);
         if (!(ok = __all_sync(kFull, mbar_wait(&empty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 510)))) break;
-        if (lane == 0) mbar_arrive_expect_tx(&full[s], A_BYTES + b_bytes);
-        __syncwarp();
-        tma_gather4(base + s * STAGE_BYTES + (lane >> 4) * (A_BYTES / 2) + (lane & 15) * 512, act, &full[s], x, tok);
-        if (lane == 0) tma_load_2d(smem + s * STAGE_BYTES + A_BYTES, low, &full[s], 0, w.row0 + kc * BK);
-        __syncwarp();
-        issued |= 1u << s;
-        last_par = (last_par & ~(1u << s)) | (ph << s);
+        uint8_t* tile = smem + s * STAGE_BYTES;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int q = 16 * warp + 4 * (i & 3) + (lane >> 3), col = f + 64 * (i >> 2);
+          const bool go = t[i & 3] < p.T && col < F;
+          cp_async_16_zfill(tile + (i >> 2) * (A_BYTES / 2) + (q >> 3) * 1024 + (q & 7) * 128 + ((c ^ (q & 7)) << 4),
+                            go ? act + (size_t)t[i & 3] * F + col : act, go ? 16u : 0u);
+        }
+        cp_async_arrive_noinc(&full[s]);
+        tokens(kc + 1, t);
         if (++s == STAGES) {
           s = 0;
           ph ^= 1;
         }
       }
     }
-    if (!ok) let_land(full, STAGES, issued, last_par, p.timeout_ns);
-    __syncwarp();
-  } else if (warp == 1) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == kLowWarp) {
+    if (lane == 0) {
+      uint32_t s = 0, ph = 0, issued = 0, last_par = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
+        const AdapterWgradUnit w = adapter_wgrad_unit(p, u);
+        const CUtensorMap* low = w.g ? &low1 : &low0;
+        for (int kc = 0; kc * BK < w.rows; ++kc) {
+          if (!(ok = mbar_wait(&empty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 511))) break;
+          mbar_arrive_expect_tx(&full[s], b_bytes);
+          tma_load_2d(smem + s * STAGE_BYTES + A_BYTES, low, &full[s], 0, w.row0 + kc * BK);
+          issued |= 1u << s;
+          last_par = (last_par & ~(1u << s)) | (ph << s);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (!ok) let_land(full, STAGES, issued, last_par, p.timeout_ns);
+    }
+  } else if (warp == kIssueWarp) {
     if (lane == 0) {
       const uint32_t idesc = make_idesc_bf16(BM, p.r_pad, true, true);
       const uint32_t lswz = swz_for_row_bytes(2 * p.r_pad);
@@ -838,6 +923,7 @@ __global__ void __launch_bounds__(adw::kThreads)
         const uint32_t acc = tmem + b * kAccCols;
         for (int kc = 0; kc * BK < w.rows; ++kc) {
           if (!(ok = mbar_wait(&full[s], ph, ctl, p.err, p.timeout_ns, 521))) break;
+          fence_proxy_async_smem();  // the rows were written by cp.async
           tc_fence_after();
           const uint32_t a0 = smem_u32(smem + s * STAGE_BYTES), b0 = a0 + A_BYTES;
           const int steps = min(BK, w.rows - kc * BK) / 16;  // rows past the adapter's end take no part
@@ -907,7 +993,7 @@ __global__ void __launch_bounds__(adw::kThreads)
   }
   __syncwarp();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == kIssueWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -933,19 +1019,14 @@ cudaError_t map_u8_2d(CUtensorMap* m, const void* base, uint64_t bytes, uint64_t
   return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box,
                            CU_TENSOR_MAP_SWIZZLE_NONE);
 }
-
-// Token rows for gather4: one-row boxes of 64 columns.
-cudaError_t map_gather(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows) {
-  return map_bf16_2d(m, base, cols, rows, 64, 1, CU_TENSOR_MAP_SWIZZLE_128B);
-}
 }  // namespace
 
-cudaError_t launch_adapter_gemm(const AdapterProjHost& h, bool mn, const uint16_t* src, const uint16_t* low,
+cudaError_t launch_adapter_gemm(const AdapterProjHost& h, bool mn, const uint16_t* rows, const uint16_t* low,
                                 const uint16_t* fac, uint16_t* out, int num_sms, cudaStream_t stream) {
   const int R = mn ? h.N : h.K, O = mn ? h.K : h.N, rp = rank_padded(h.r);
   CUtensorMap ma, mraw, mla, mlb;
   cudaError_t err;
-  if ((err = map_gather(&ma, src, R, h.T)) != cudaSuccess) return err;
+  if ((err = map_bf16_2d(&ma, rows, R, h.rows_cap, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return err;
   if ((err = mn ? map_u8_2d(&mraw, h.nf4, h.K / 2, h.N, 64, 64) : map_u8_2d(&mraw, h.nf4, h.K / 2, h.N, 32, 128)) !=
       cudaSuccess)
     return err;
@@ -987,17 +1068,19 @@ cudaError_t launch_adapter_gemm(const AdapterProjHost& h, bool mn, const uint16_
 }
 
 cudaError_t launch_adapter_rows(const AdapterProjHost& h, bool mn, const uint16_t* src, const uint16_t* fac,
-                                uint16_t* out, int num_sms, cudaStream_t stream) {
+                                uint16_t* rows, uint16_t* out, int num_sms, cudaStream_t stream) {
   const int R = mn ? h.N : h.K, rp = rank_padded(h.r);
   CUtensorMap ms, mw;
   cudaError_t err;
-  if ((err = map_gather(&ms, src, R, h.T)) != cudaSuccess) return err;
+  if ((err = map_bf16_2d(&ms, rows, R, h.rows_cap, 64, 16, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return err;
   if (mn)  // B [n, N, r]
     err = map_bf16_3d(&mw, fac, h.r, h.N, h.n, rp, 64, swizzle_for_bytes(2 * rp));
   else  // A [n, r, K]
     err = map_bf16_3d(&mw, fac, h.K, h.r, h.n, 64, rp, CU_TENSOR_MAP_SWIZZLE_128B);
   if (err != cudaSuccess) return err;
   AdapterRowsParams p;
+  p.src = src;
+  p.n = h.n;
   p.order = h.order;
   p.steps = h.steps;
   p.scale = h.scale;
@@ -1009,8 +1092,8 @@ cudaError_t launch_adapter_rows(const AdapterProjHost& h, bool mn, const uint16_
   p.r = h.r;
   p.r_pad = rp;
   p.tasks = adapter_steps_layout(h.rows_cap, h.n).tasks;
-  const int64_t cap = h.rows_cap / kAdapterTaskRows + h.n;
-  const int grid = (int)(cap < num_sms ? cap : num_sms);
+  const int64_t cap = h.rows_cap / kAdapterTaskRows + h.n + 1;
+  const int grid = (int)(cap < 2 * num_sms ? cap : 2 * num_sms);
   LaunchScope scope(mn ? "adapter_proj_dy" : "adapter_proj_x", stream);
   if (mn) {
     if ((err = set_smem(adapter_proj_kernel<true>, adp::SMEM_BYTES)) != cudaSuccess) return err;
@@ -1025,14 +1108,14 @@ cudaError_t launch_adapter_rows(const AdapterProjHost& h, bool mn, const uint16_
 cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, const uint16_t* dY, const uint16_t* p_low,
                                  const uint16_t* q_low, uint16_t* dA, uint16_t* dB, int num_sms, cudaStream_t stream) {
   const int rp = rank_padded(h.r);
-  CUtensorMap mx, md, mq, mp;
+  CUtensorMap mq, mp;
   cudaError_t err;
-  if ((err = map_gather(&mx, x, h.K, h.T)) != cudaSuccess) return err;
-  if ((err = map_gather(&md, dY, h.N, h.T)) != cudaSuccess) return err;
   const CUtensorMapSwizzle rswz = swizzle_for_bytes(2 * rp);
   if ((err = map_bf16_2d(&mq, q_low, h.r, h.rows_cap, rp, 64, rswz)) != cudaSuccess) return err;
   if ((err = map_bf16_2d(&mp, p_low, h.r, h.rows_cap, rp, 64, rswz)) != cudaSuccess) return err;
   AdapterWgradParams p;
+  p.act[0] = x;
+  p.act[1] = dY;
   p.out[0] = dA;
   p.out[1] = dB;
   p.F[0] = h.K;
@@ -1052,7 +1135,7 @@ cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, co
   const int grid = (int)(units < cap ? units : cap);
   if ((err = set_smem(adapter_wgrad_kernel, adw::SMEM_BYTES)) != cudaSuccess) return err;
   LaunchScope scope("adapter_wgrad", stream);
-  adapter_wgrad_kernel<<<grid, adw::kThreads, adw::SMEM_BYTES, stream>>>(mx, md, mq, mp, p);
+  adapter_wgrad_kernel<<<grid, adw::kThreads, adw::SMEM_BYTES, stream>>>(mq, mp, p);
   return cudaGetLastError();
 }
 

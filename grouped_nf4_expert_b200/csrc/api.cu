@@ -126,9 +126,9 @@ e4b_status check_proj_dims(const e4b_proj_dims* d, int32_t T) {
   return E4B_OK;
 }
 
-// Workspace of the serving call: the error word, then the grouping and p.
+// Workspace of the serving call: the error word, then the grouping, p and the rows of x in their order.
 struct ServeProjLayout {
-  size_t order, offsets, steps, low, total;
+  size_t order, offsets, steps, low, rows, total;
 };
 ServeProjLayout serve_proj_layout(const e4b_proj_dims* d, int32_t T) {
   auto up = [](size_t b) { return (b + 255) / 256 * 256; };
@@ -138,8 +138,15 @@ ServeProjLayout serve_proj_layout(const e4b_proj_dims* d, int32_t T) {
   l.offsets = l.order + up((size_t)rows * 4);
   l.steps = l.offsets + up((size_t)(d->n_adapters + 2) * 4);
   l.low = l.steps + up((size_t)adapter_steps_layout(rows, d->n_adapters).total * 4);
-  l.total = l.low + up((size_t)rows * d->r * 2);
+  l.rows = l.low + up((size_t)rows * d->r * 2);
+  l.total = l.rows + up((size_t)rows * d->K * 2);
   return l;
+}
+
+// Workspace of the training calls: the error word, then the rows of x or dY in their order.
+size_t proj_workspace_bytes(const e4b_proj_dims* d, int32_t T) {
+  const int wide = d->K > d->N ? d->K : d->N;
+  return sizeof(DeviceError) + (size_t)adapter_rows_cap(T, d->n_adapters) * wide * 2;
 }
 
 e4b_status check_groups(const e4b_adapter_groups* g) {
@@ -742,7 +749,7 @@ e4b_status e4b_proj_get_sizes(const e4b_proj_dims* dims, int32_t T, e4b_proj_siz
   if (out == nullptr) return E4B_ERR_INVALID_ARG;
   out->rows_cap = adapter_rows_cap(T, dims->n_adapters);
   out->steps_cap = adapter_steps_layout(out->rows_cap, dims->n_adapters).total;
-  out->workspace_bytes = sizeof(DeviceError);
+  out->workspace_bytes = proj_workspace_bytes(dims, T);
   out->serve_workspace_bytes = serve_proj_layout(dims, T).total;
   return E4B_OK;
 }
@@ -774,12 +781,13 @@ e4b_status e4b_multi_lora_serve_fwd(const e4b_proj_dims* dims, int32_t T, const 
   int32_t* offsets = reinterpret_cast<int32_t*>(w + l.offsets);
   int32_t* steps = reinterpret_cast<int32_t*>(w + l.steps);
   uint16_t* low = reinterpret_cast<uint16_t*>(w + l.low);
+  uint16_t* rows = reinterpret_cast<uint16_t*>(w + l.rows);
   int sms = 0;
   E4B_CUDA(device_sms(&sms));
   const AdapterProjHost h = proj_host(dims, T, base, adapters, order, offsets, steps, ws);
   E4B_CUDA(launch_adapter_group(ids, T, dims->n_adapters, order, offsets, steps, st));
-  E4B_CUDA(launch_adapter_rows(h, false, x, adapters->A, low, sms, st));
-  E4B_CUDA(launch_adapter_gemm(h, false, x, low, adapters->B, y, sms, st));
+  E4B_CUDA(launch_adapter_rows(h, false, x, adapters->A, rows, low, sms, st));
+  E4B_CUDA(launch_adapter_gemm(h, false, rows, low, adapters->B, y, sms, st));
   return E4B_OK;
 }
 
@@ -789,16 +797,17 @@ e4b_status e4b_multi_lora_fwd(const e4b_proj_dims* dims, int32_t T, const e4b_ad
   E4B_TRY(check_proj_dims(dims, T));
   if (T == 0) return E4B_OK;
   if (!aligned16(ws)) return E4B_ERR_INVALID_ARG;
-  if (ws_bytes < sizeof(DeviceError)) return E4B_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < proj_workspace_bytes(dims, T)) return E4B_ERR_WORKSPACE_TOO_SMALL;
   E4B_TRY(check_groups(groups));
   E4B_TRY(check_projection(base, adapters));
   if (!aligned16(x) || !aligned16(p) || !aligned16(y)) return E4B_ERR_INVALID_ARG;
   const cudaStream_t st = (cudaStream_t)stream;
+  uint16_t* rows = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + sizeof(DeviceError));
   int sms = 0;
   E4B_CUDA(device_sms(&sms));
   const AdapterProjHost h = proj_host(dims, T, base, adapters, groups->order, groups->offsets, groups->steps, ws);
-  E4B_CUDA(launch_adapter_rows(h, false, x, adapters->A, p, sms, st));
-  E4B_CUDA(launch_adapter_gemm(h, false, x, p, adapters->B, y, sms, st));
+  E4B_CUDA(launch_adapter_rows(h, false, x, adapters->A, rows, p, sms, st));
+  E4B_CUDA(launch_adapter_gemm(h, false, rows, p, adapters->B, y, sms, st));
   return E4B_OK;
 }
 
@@ -808,16 +817,17 @@ e4b_status e4b_multi_lora_dgrad(const e4b_proj_dims* dims, int32_t T, const e4b_
   E4B_TRY(check_proj_dims(dims, T));
   if (T == 0) return E4B_OK;
   if (!aligned16(ws)) return E4B_ERR_INVALID_ARG;
-  if (ws_bytes < sizeof(DeviceError)) return E4B_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < proj_workspace_bytes(dims, T)) return E4B_ERR_WORKSPACE_TOO_SMALL;
   E4B_TRY(check_groups(groups));
   E4B_TRY(check_projection(base, adapters));
   if (!aligned16(dY) || !aligned16(q) || !aligned16(dx)) return E4B_ERR_INVALID_ARG;
   const cudaStream_t st = (cudaStream_t)stream;
+  uint16_t* rows = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + sizeof(DeviceError));
   int sms = 0;
   E4B_CUDA(device_sms(&sms));
   const AdapterProjHost h = proj_host(dims, T, base, adapters, groups->order, groups->offsets, groups->steps, ws);
-  E4B_CUDA(launch_adapter_rows(h, true, dY, adapters->B, q, sms, st));
-  E4B_CUDA(launch_adapter_gemm(h, true, dY, q, adapters->A, dx, sms, st));
+  E4B_CUDA(launch_adapter_rows(h, true, dY, adapters->B, rows, q, sms, st));
+  E4B_CUDA(launch_adapter_gemm(h, true, rows, q, adapters->A, dx, sms, st));
   return E4B_OK;
 }
 

@@ -214,7 +214,7 @@ __host__ __device__ inline AdapterSteps adapter_steps_layout(int64_t rows_cap, i
   a.unit_start = 8;
   a.entries = (int)((8 + units + 1 + 3) / 4 * 4);
   a.tasks = (int)(a.entries + 4 * (units + n + 1));
-  a.total = a.tasks + 4 * (rows_cap / kAdapterTaskRows + n);
+  a.total = a.tasks + 4 * (rows_cap / kAdapterTaskRows + n + 1);
   return a;
 }
 cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int32_t* order, int32_t* offsets, int32_t* steps,
@@ -230,11 +230,11 @@ struct AdapterProjHost {
   DeviceError* err;
   long long timeout_ns;
 };
-// out[row, :r] = bf16(s[a] src[t] . factor[a]): A [n, r, K] over x, or (mn) B [n, N, r] over dY.
+// rows[row] = src[t], out[row, :r] = bf16(s[a] src[t] . factor[a]): A [n, r, K] over x, or (mn) B [n, N, r] over dY.
 cudaError_t launch_adapter_rows(const AdapterProjHost& h, bool mn, const uint16_t* src, const uint16_t* fac,
-                                uint16_t* out, int num_sms, cudaStream_t stream);
-// out[t] = src[t] W^T + low[row] B[a]^T, or (mn) src[t] W + low[row] A[a].
-cudaError_t launch_adapter_gemm(const AdapterProjHost& h, bool mn, const uint16_t* src, const uint16_t* low,
+                                uint16_t* rows, uint16_t* out, int num_sms, cudaStream_t stream);
+// out[t] = rows[row] W^T + low[row] B[a]^T, or (mn) rows[row] W + low[row] A[a].
+cudaError_t launch_adapter_gemm(const AdapterProjHost& h, bool mn, const uint16_t* rows, const uint16_t* low,
                                 const uint16_t* fac, uint16_t* out, int num_sms, cudaStream_t stream);
 cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, const uint16_t* dY, const uint16_t* p,
                                  const uint16_t* q, uint16_t* dA, uint16_t* dB, int num_sms, cudaStream_t stream);
