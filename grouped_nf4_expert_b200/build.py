@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libe4b.so")
 SOURCES = ["api.cu", "route.cu", "gemm.cu", "stream.cu", "serve.cu", "noalloc.cu",
-           "adapters.cu", "adapters_gemm.cu", "balance.cu"]
+           "adapters.cu", "adapters_gemm.cu", "adapters_serve.cu", "balance.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-DNDEBUG"]
