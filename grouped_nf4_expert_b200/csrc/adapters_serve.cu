@@ -32,6 +32,8 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTokenTile = 8;
+constexpr int kProjThreads = 512;
+constexpr int kProjWarps = kProjThreads / 32;
 
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -46,133 +48,98 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// 16 bytes, or zeros where `ok` is false (nothing is read then).  Volatile, so that a batch of loads written
+// ahead of the instructions that use them is issued ahead of them: left to the compiler, they were paired with
+// their uses and few were in flight.
 __device__ __forceinline__ uint4 ldg16(const void* p, bool ok) {
-  return ok ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+  uint4 v;
+  asm volatile(
+      "{\n"
+      ".reg .pred q;\n"
+      "setp.ne.b32 q, %5, 0;\n"
+      "mov.u32 %0, 0;\n"
+      "mov.u32 %1, 0;\n"
+      "mov.u32 %2, 0;\n"
+      "mov.u32 %3, 0;\n"
+      "@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+      "}\n"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "l"(p), "r"((int)ok));
+  return v;
 }
 
 // ----------------------------------------------------------------------------
 // p for up to kAdapterSmallTokens tokens
 // ----------------------------------------------------------------------------
-// A work item is (tile of up to eight tokens of one adapter, 16 of the r
-// ranks): the block's warps split K, lanes read A and x straight from global
-// memory, and the partial sums meet in shared memory.  GROUPED: every block
-// first groups the tokens by adapter, in token order, so that all blocks find
-// the same tiles (warp matches and counts in shared memory), and block 0
-// leaves the tiles to the base product.  Otherwise (few
-// tokens) every token is a tile of its own: grouping would cost its five block
-// barriers to save reads of an adapter that L2 holds anyway.
+// The tokens of an adapter are taken in tiles of up to eight, in token order.
+// Block (t, slice) does the tile that starts with token t -- or nothing, where
+// t is not the first, ninth, ... token of its adapter -- for 16 of the r ranks:
+// its warps split K, lanes read A and x straight from global memory, and the
+// partial sums meet in shared memory.  Each block finds its tile from one look
+// at the ids (a ballot a warp), without a sort ahead of the loads.
 struct SmallProjParams {
   const int32_t* ids;
   const uint16_t* x;
   const uint16_t* A;
   const float* scale;
   uint16_t* p;
-  int32_t* list;  // AdapterTiles, or nullptr
   int T, K, n, r;
 };
 
-template <bool GROUPED>
-__global__ void __launch_bounds__(kThreads) adapter_small_proj_kernel(const SmallProjParams p) {
-  constexpr int kMax = GROUPED ? kAdapterSmallTokens : 1;
-  constexpr int kCols = E4B_MAX_ADAPTERS + 16;
-  static_assert(kAdapterSmallTokens == kThreads && E4B_MAX_ADAPTERS == 4 * kThreads, "one token, four adapters a thread");
-  __shared__ __align__(16) uint8_t wcnt[GROUPED ? kWarps * kCols : 16];  // tokens of an adapter in a warp
-  __shared__ int16_t first[GROUPED ? E4B_MAX_ADAPTERS : 1];              // an adapter's first tile
-  __shared__ int16_t tile_tok[kMax * kTokenTile];          // -1: none
-  __shared__ int16_t tile_ad[kMax];
-  __shared__ float red[kWarps][16][kTokenTile + 1];
-  __shared__ int wsum[kWarps];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+__global__ void __launch_bounds__(kProjThreads) adapter_small_proj_kernel(const SmallProjParams p) {
+  static_assert(kAdapterSmallTokens <= kProjThreads, "a token a thread");
+  __shared__ uint32_t member[kProjWarps];  // tokens of this block's adapter, a bit each
+  __shared__ float red[kProjWarps][16][kTokenTile + 1];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   grid_launch_dependents();
-  int n_tiles = p.T;
-  if constexpr (GROUPED) {
-    for (int i = tid; i < kWarps * kCols / 16; i += kThreads) reinterpret_cast<uint4*>(wcnt)[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    // thread t's token: its rank among its adapter's, in token order (every block finds the same tiles)
-    int ad = -1;
-    if (tid < p.T) {
-      const uint32_t a = (uint32_t)__ldg(p.ids + tid);
-      ad = a < (uint32_t)p.n ? (int)a : p.n;
+  const int slices = (p.r + 15) / 16, first = (int)blockIdx.x / slices, j0 = ((int)blockIdx.x - first * slices) * 16;
+  const int a = __ldg(p.ids + first);
+  if ((uint32_t)a >= (uint32_t)p.n) return;
+  const uint32_t mine = __ballot_sync(kFull, tid < p.T && __ldg(p.ids + tid) == a);
+  if (lane == 0) member[warp] = mine;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w <= first >> 5; ++w)
+    before += __popc(w < first >> 5 ? member[w] : member[w] & ((1u << (first & 31)) - 1));
+  if (before % kTokenTile) return;
+  // the i-th token of the tile (-1: none)
+  auto token = [&](int i) -> int {
+    for (int w = first >> 5; w < kProjWarps; ++w) {
+      uint32_t m = member[w];
+      if (w == first >> 5) m &= kFull << (first & 31);
+      const int c = __popc(m);
+      if (i < c) {
+        for (; i > 0; --i) m &= m - 1;
+        return 32 * w + __ffs(m) - 1;
+      }
+      i -= c;
     }
-    const uint32_t same = __match_any_sync(kFull, ad);
-    int pos = __popc(same & ((1u << lane) - 1));
-    if (ad >= 0 && pos == 0) wcnt[warp * kCols + ad] = (uint8_t)__popc(same);
-    __syncthreads();
-    if (ad >= 0)
-      for (int w = 0; w < warp; ++w) pos += wcnt[w * kCols + ad];
-    // exclusive prefix of the adapters' tiles; thread tid owns adapters 4 tid ..
-    constexpr int kAds = E4B_MAX_ADAPTERS / kThreads;
-    int tiles[kAds] = {}, sum = 0, none = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      const uint32_t c4 = *reinterpret_cast<const uint32_t*>(wcnt + w * kCols + tid * kAds);
-#pragma unroll
-      for (int i = 0; i < kAds; ++i) tiles[i] += (c4 >> (8 * i)) & 0xffu;
-      none += wcnt[w * kCols + p.n];
-    }
-#pragma unroll
-    for (int i = 0; i < kAds; ++i) {
-      tiles[i] = tid * kAds + i < p.n ? (tiles[i] + kTokenTile - 1) / kTokenTile : 0;
-      sum += tiles[i];
-    }
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(kFull, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
-    int base = incl - sum;
-    n_tiles = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) base += wsum[w];
-      n_tiles += wsum[w];
-    }
-#pragma unroll
-    for (int i = 0; i < kAds; ++i) {
-      const int a = tid * kAds + i;
-      if (a < p.n) first[a] = (int16_t)base;
-      for (int j = 0; j < tiles[i]; ++j) tile_ad[base + j] = (int16_t)a;
-      base += tiles[i];
-    }
-    const int all_tiles = n_tiles + (none + kTokenTile - 1) / kTokenTile;
-    for (int i = n_tiles + tid; i < all_tiles; i += kThreads) tile_ad[i] = (int16_t)p.n;
-    for (int i = tid; i < all_tiles * kTokenTile; i += kThreads) tile_tok[i] = -1;
-    __syncthreads();
-    if (ad >= 0) tile_tok[(ad < p.n ? first[ad] : n_tiles) * kTokenTile + pos] = (int16_t)tid;
-    __syncthreads();
-    if (blockIdx.x == 0) {
-      if (tid == 0) p.list[0] = all_tiles;
-      for (int i = tid; i < all_tiles; i += kThreads) p.list[kAdapterListAd + i] = tile_ad[i];
-      for (int i = tid; i < all_tiles * kTokenTile; i += kThreads) p.list[kAdapterListTok + i] = tile_tok[i];
-    }
-  }
-
-  const int g = lane >> 2, q = lane & 3;
-  const int slices = (p.r + 15) / 16;
-  for (int item = blockIdx.x; item < n_tiles * slices; item += gridDim.x) {
-    const int tile = item / slices, j0 = (item - tile * slices) * 16;
-    int a, t;
-    if constexpr (GROUPED) {
-      a = tile_ad[tile];
-      t = tile_tok[tile * kTokenTile + g];
-    } else {
-      a = __ldg(p.ids + tile);
-      t = g == 0 ? tile : -1;
-      if ((uint32_t)a >= (uint32_t)p.n) continue;  // the whole block
-    }
+    return -1;
+  };
+  {
+    const int t = token(g);
     const bool tok = t >= 0, lo = j0 + g < p.r, hi = j0 + g + 8 < p.r;
     const uint16_t* xr = p.x + (tok ? (size_t)t * p.K : 0) + 8 * q;
     const uint16_t* a0 = p.A + ((size_t)a * p.r + (lo ? j0 + g : 0)) * p.K + 8 * q;
     const uint16_t* a1 = p.A + ((size_t)a * p.r + (hi ? j0 + g + 8 : 0)) * p.K + 8 * q;
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    // 32 values of k a step: lane q of a row holds 8 of them, two instructions' worth
-#pragma unroll 8
-    for (int k = warp * 32; k < p.K; k += kWarps * 32) {
-      const uint4 w0 = ldg16(a0 + k, lo), w1 = ldg16(a1 + k, hi), xv = ldg16(xr + k, tok);
-      mma_bf16(acc, w0.x, w1.x, w0.y, w1.y, xv.x, xv.y);
-      mma_bf16(acc, w0.z, w1.z, w0.w, w1.w, xv.z, xv.w);
+    // 32 values of k a step: lane q of a row holds 8 of them, two instructions' worth.  Four steps' loads go
+    // out together.
+    constexpr int kAhead = 4;
+    for (int k0 = warp * 32; k0 < p.K; k0 += kProjWarps * 32 * kAhead) {
+      uint4 w0[kAhead], w1[kAhead], xv[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int k = k0 + i * kProjWarps * 32;
+        w0[i] = ldg16(a0 + k, lo && k < p.K);
+        w1[i] = ldg16(a1 + k, hi && k < p.K);
+        xv[i] = ldg16(xr + k, tok && k < p.K);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        mma_bf16(acc, w0[i].x, w1[i].x, w0[i].y, w1[i].y, xv[i].x, xv[i].y);
+        mma_bf16(acc, w0[i].z, w1[i].z, w0[i].w, w1[i].w, xv[i].z, xv[i].w);
+      }
     }
     red[warp][g][2 * q] = acc[0];
     red[warp][g][2 * q + 1] = acc[1];
@@ -180,17 +147,15 @@ __global__ void __launch_bounds__(kThreads) adapter_small_proj_kernel(const Smal
     red[warp][g + 8][2 * q + 1] = acc[3];
     __syncthreads();
     if (tid < 16 * kTokenTile) {
-      const int j = tid & 15, c = tid >> 4;
-      const int to = GROUPED ? tile_tok[tile * kTokenTile + c] : (c == 0 ? tile : -1);
+      const int j = tid & 15, to = token(tid >> 4);
       if (to >= 0 && j0 + j < p.r) {
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += red[w][j][c];
+        for (int w = 0; w < kProjWarps; ++w) v += red[w][j][tid >> 4];
         const __nv_bfloat16 b = __float2bfloat16_rn(__ldg(p.scale + a) * v);
         p.p[(size_t)to * p.r + j0 + j] = *reinterpret_cast<const uint16_t*>(&b);
       }
     }
-    __syncthreads();
   }
 }
 
@@ -317,23 +282,26 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvPar
 // y for up to 256 tokens: 128 rows of W x all tokens x a share of K per block
 // ----------------------------------------------------------------------------
 // Warp 0 loads x tiles (TMA), warp 1 owns tensor memory and issues the UMMAs,
-// warps 4-15 are three decode teams that take the k-chunks round robin: a
-// thread owns a row of W, reads 32 bytes of codes and a scale a chunk straight
-// into registers two of its chunks ahead, and writes the decoded row to the A
-// buffer in tensor memory.  Then every block's partial sums go to its shared
-// memory (over the x tiles), the cluster's blocks each add up 128 / S rows over
-// the S shares of K, and the adapters' part is added in the fragment layout of
-// the warp instruction, tile by tile of eight tokens of one adapter, so that
-// no adapter's values meet another's tokens.
+// warp 2 sorts the tokens into tiles of eight of one adapter, warps 4-15 are
+// three decode teams that take the k-chunks round robin: a thread owns a row of
+// W, reads 32 bytes of codes and a scale a chunk straight into registers two of
+// its chunks ahead, and writes the decoded row to the A buffer in tensor
+// memory.  Each of the cluster's S blocks then owns 128 / S of the rows: the
+// partial sums are stored into their owners' shared memory (over the x tiles;
+// reading them from there instead took 4.7 us at 256 tokens, one round trip
+// after another), added, and the adapters' part is added in the fragment
+// layout of the warp instruction, tile by tile, so that no adapter's values
+// meet another's tokens.
 namespace ads {
 constexpr int BM = 128, BK = 64;
 constexpr int kXStages = 4, kTeams = 3, kABufs = 2 * kTeams, kACols = BK / 2;
 constexpr int kThreadsSplit = 512;
 constexpr int kAOff = 256;             // TMEM columns: accumulator [0, 256), A buffers behind
-constexpr int kPitch = BM + 4;         // floats of a token's partial sums (no bank conflicts in fragment reads)
 constexpr int kTmemCols = 512;
-inline int ring_bytes(int nt) {
-  const int x = kXStages * nt * BK * 2, part = nt * kPitch * 4;
+constexpr int kBarBytes = 256;
+constexpr int kListBytes = (9 * kAdapterSmallTokens + E4B_MAX_ADAPTERS) * 2;
+inline int ring_bytes(int nt, int S) {  // x tiles, then the S shares of 128 / S rows (4 floats of padding a token)
+  const int x = kXStages * nt * BK * 2, part = nt * (BM + 4 * S) * 4;
   return ((x > part ? x : part) + 1023) / 1024 * 1024;
 }
 static_assert(kAOff + kABufs * kACols <= kTmemCols, "TMEM budget");
@@ -344,20 +312,38 @@ struct SplitParams {
   const float* absmax;
   const uint16_t* B;
   const uint16_t* p;
-  const int32_t* list;
+  const int32_t* ids;
   uint16_t* y;
   DeviceError* err;
   long long timeout_ns;
-  int T, NT, K, N, n, r, S;  // NT: T rounded up to 16
-  int ring;                  // bytes of the x ring / partial sums
+  int T, NT, K, N, n, r;  // NT: T rounded up to 16
+  int ring;               // bytes of the x ring / partial sums
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// As ldg16, from L2: the launch that wrote it may have run beside this one.
+__device__ __forceinline__ uint4 ldcg16(const void* p, bool ok) {
+  uint4 v;
+  asm volatile(
+      "{\n"
+      ".reg .pred q;\n"
+      "setp.ne.b32 q, %5, 0;\n"
+      "mov.u32 %0, 0;\n"
+      "mov.u32 %1, 0;\n"
+      "mov.u32 %2, 0;\n"
+      "mov.u32 %3, 0;\n"
+      "@q ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+      "}\n"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "l"(p), "r"((int)ok)
+      : "memory");
   return v;
 }
 
+template <int S, bool WIDE>  // blocks of a cluster, the shares of K; r > 32
 __global__ void __launch_bounds__(ads::kThreadsSplit, 1)
     adapter_split_kernel(const __grid_constant__ CUtensorMap map_x, const SplitParams p) {
   using namespace ads;
@@ -371,10 +357,14 @@ __global__ void __launch_bounds__(ads::kThreadsSplit, 1)
   uint64_t* accfull = a_empty + kABufs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accfull + 1);
   CtaControl* ctl = reinterpret_cast<CtaControl*>(accfull + 2);
+  int32_t* n_tiles = reinterpret_cast<int32_t*>(accfull + 3);
+  int16_t* tile_ad = reinterpret_cast<int16_t*>(smem + p.ring + kBarBytes);  // [kAdapterSmallTokens]
+  int16_t* tile_tok = tile_ad + kAdapterSmallTokens;                         // eight a tile, -1: none
+  int16_t* count = tile_tok + kTokenTile * kAdapterSmallTokens;              // [n]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = (int)(blockIdx.x % p.S), n0 = (int)(blockIdx.x / p.S) * BM;
+  const int rank = (int)(blockIdx.x % S), n0 = (int)(blockIdx.x / S) * BM;
   const int chunks = p.K / BK;
-  const int k_lo = rank * chunks / p.S, nc = (rank + 1) * chunks / p.S - k_lo;
+  const int k_lo = rank * chunks / S, nc = (rank + 1) * chunks / S - k_lo;
   if (tid == 0) {
     for (int s = 0; s < kXStages; ++s) {
       mbar_init(&x_full[s], 1);
@@ -397,6 +387,7 @@ __global__ void __launch_bounds__(ads::kThreadsSplit, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int x_bytes = p.NT * BK * 2;
+  bool done = false;  // (teams) the accumulator is complete
 
   if (warp == 0) {
     if (lane == 0) {
@@ -444,6 +435,50 @@ __global__ void __launch_bounds__(ads::kThreadsSplit, 1)
       }
     }
     __syncwarp();
+  } else if (warp == 2) {
+    // ---- token tiles: a stable counting sort of the tokens by adapter, in the shadow of the products
+    for (int i = lane; i < p.n; i += 32) count[i] = 0;
+    __syncwarp();
+    constexpr int kRounds = kAdapterSmallTokens / 32;
+    int16_t ad[kRounds], pos[kRounds];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const int t = 32 * i + lane;
+      const uint32_t a = t < p.T ? (uint32_t)__ldg(p.ids + t) : kFull;
+      ad[i] = a < (uint32_t)p.n ? (int16_t)a : (int16_t)-1;
+    }
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const uint32_t same = __match_any_sync(kFull, (int)ad[i]);
+      const int rank_in = __popc(same & ((1u << lane) - 1));
+      pos[i] = ad[i] >= 0 ? (int16_t)(count[ad[i]] + rank_in) : (int16_t)0;
+      __syncwarp();
+      if (ad[i] >= 0 && rank_in == 0) count[ad[i]] += (int16_t)__popc(same);
+      __syncwarp();
+    }
+    // an adapter's first tile; lane l owns adapters l m ..
+    const int m = (p.n + 31) / 32;
+    int sum = 0;
+    for (int i = lane * m; i < min(p.n, lane * m + m); ++i) sum += (count[i] + kTokenTile - 1) / kTokenTile;
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int total = __shfl_sync(kFull, incl, 31);
+    for (int i = lane; i < total * kTokenTile; i += 32) tile_tok[i] = -1;
+    int base = incl - sum;
+    for (int i = lane * m; i < min(p.n, lane * m + m); ++i) {
+      const int tiles = (count[i] + kTokenTile - 1) / kTokenTile;
+      count[i] = (int16_t)base;
+      for (int j = 0; j < tiles; ++j) tile_ad[base++] = (int16_t)i;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i)
+      if (ad[i] >= 0) tile_tok[count[ad[i]] * kTokenTile + pos[i]] = (int16_t)(32 * i + lane);
+    if (lane == 0) *n_tiles = total;
   } else if (warp >= 4) {
     const int team = (warp - 4) >> 2, row = n0 + 32 * (warp & 3) + lane;
     const bool valid = row < p.N;
@@ -481,80 +516,105 @@ __global__ void __launch_bounds__(ads::kThreadsSplit, 1)
       w0 = w1;
       w1 = w2;
     }
-    // partial sums to shared memory, [token][row]; the UMMAs have read the last x tile.  Team by team 16 columns.
-    if (__all_sync(kFull, mbar_wait(accfull, 0, ctl, p.err, p.timeout_ns, 631))) {
-      tc_fence_after();
-      float* part = reinterpret_cast<float*>(smem) + 32 * (warp & 3) + lane;
-      for (int c = 16 * team; c < p.NT; c += 16 * kTeams) {
-        float v[16];
-        tmem_ld16(tmem + c + ((uint32_t)(32 * (warp & 3)) << 16), v);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) part[(c + i) * kPitch] = v[i];
-      }
-      tc_fence_before();
-    }
+    done = __all_sync(kFull, mbar_wait(accfull, 0, ctl, p.err, p.timeout_ns, 631));
   }
   __syncwarp();
-  cluster_sync();  // every block's partial sums are in place
+  cluster_sync();  // no block's UMMAs read its x tiles any more
+  // Partial sums into the shared memory of the block that owns the row, [share][token][row]: a lane holds a row
+  // of the accumulator, so a store writes whole runs of rows.  Team by team 16 columns.
+  constexpr int kRows = BM / S, kPitch = kRows + 4;
+  const int rank0 = rank * kRows;
+  float* part = reinterpret_cast<float*>(smem);
+  if (warp >= 4 && done) {
+    tc_fence_after();
+    const int team = (warp - 4) >> 2, row = 32 * (warp & 3) + lane;
+    const uint32_t to = mapa_shared(smem_u32(part + (size_t)rank * p.NT * kPitch + row % kRows), (uint32_t)(row / kRows));
+    for (int c = 16 * team; c < p.NT; c += 16 * kTeams) {
+      float v[16];
+      tmem_ld16(tmem + c + ((uint32_t)(32 * (warp & 3)) << 16), v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) st_cluster_f32(to + (uint32_t)((c + i) * kPitch * 4), v[i]);
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  cluster_sync();  // every share is in place
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  grid_wait();  // p and the token tiles
-  {
-    // This block's rows: 128 / S of the 128, in groups of 16; item = (group, tile of 8 tokens).
-    const int rows = BM / p.S, groups = rows / 16, g = lane >> 2, q = lane & 3;
-    const int n_tiles = __ldcg(p.list);
-    const uint32_t part_u = smem_u32(smem);
-    for (int item = warp; item < n_tiles * groups; item += kThreadsSplit / 32) {
-      const int tile = item / groups, grp = item - tile * groups;
-      const int lrow = rank * rows + 16 * grp, row = n0 + lrow;
-      if (row >= p.N) continue;  // the whole warp (N is a multiple of 8: the second half may still be outside)
-      const int a = __ldcg(p.list + kAdapterListAd + tile);
-      const int* toks = p.list + kAdapterListTok + tile * kTokenTile;
-      const int tg = __ldcg(toks + g);                                            // fragment B column
-      const int t0 = __ldcg(toks + 2 * q), t1 = __ldcg(toks + 2 * q + 1);         // fragment D columns
-      const bool hi = row + 8 < p.N;
-      uint4 b0[2], b1[2], pv[2];
+  // The shares of K are added in order.
+  if constexpr (S > 1) {
+    for (int i = tid; i < p.T * (kRows / 4); i += kThreadsSplit) {
+      float4* at = reinterpret_cast<float4*>(part + (i / (kRows / 4)) * kPitch + 4 * (i % (kRows / 4)));
+      float4 v = at[0];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int j = 32 * c + 8 * q;
-        const bool go = a < p.n && j < p.r && row + g < p.N;
-        b0[c] = ldg16(p.B + ((size_t)(go ? a : 0) * p.N + (go ? row + g : 0)) * p.r + (go ? j : 0), go);
-        b1[c] = ldg16(p.B + ((size_t)(go ? a : 0) * p.N + (go && hi ? row + g + 8 : 0)) * p.r + (go ? j : 0), go && hi);
-        pv[c] = make_uint4(0, 0, 0, 0);
-        if (go && tg >= 0) pv[c] = __ldcg(reinterpret_cast<const uint4*>(p.p + (size_t)tg * p.r + j));
+      for (int s = 1; s < S; ++s) {
+        const float4 w = at[(size_t)s * p.NT * (kPitch / 4)];
+        v.x += w.x;
+        v.y += w.y;
+        v.z += w.z;
+        v.w += w.w;
       }
-      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      const uint32_t o0 = (uint32_t)(((t0 < 0 ? 0 : t0) * kPitch + lrow + g) * 4);
-      const uint32_t o1 = (uint32_t)(((t1 < 0 ? 0 : t1) * kPitch + lrow + g) * 4);
-      for (int s = 0; s < p.S; ++s) {  // the shares of K, in order
-        const uint32_t base = mapa_shared(part_u, (uint32_t)s);
-        d[0] += ld_cluster_f32(base + o0);
-        d[1] += ld_cluster_f32(base + o1);
-        d[2] += ld_cluster_f32(base + o0 + 32);
-        d[3] += ld_cluster_f32(base + o1 + 32);
-      }
-      if (a < p.n) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          if (32 * c < p.r) {
-            mma_bf16(d, b0[c].x, b1[c].x, b0[c].y, b1[c].y, pv[c].x, pv[c].y);
-            mma_bf16(d, b0[c].z, b1[c].z, b0[c].w, b1[c].w, pv[c].z, pv[c].w);
-          }
-      }
-      auto put = [&](int t, int r, float f) {
-        const __nv_bfloat16 h = __float2bfloat16_rn(f);
-        if (t >= 0 && r < p.N) p.y[(size_t)t * p.N + r] = *reinterpret_cast<const uint16_t*>(&h);
-      };
-      put(t0, row + g, d[0]);
-      put(t1, row + g, d[1]);
-      put(t0, row + g + 8, d[2]);
-      put(t1, row + g + 8, d[3]);
+      at[0] = v;
     }
   }
-  __syncwarp();
-  cluster_sync();  // no block's shared memory goes away while another reads it
+  grid_wait();  // p
+  __syncthreads();
+  // The adapters' part: item = (tile of 8 tokens of one adapter, group of 16 rows), fragments of B and p
+  // fetched two items ahead.
+  {
+    constexpr int kGroupsOf16 = kRows / 16, kItemWarps = kThreadsSplit / 32, kC = WIDE ? 2 : 1;
+    const int g = lane >> 2, q = lane & 3;
+    const int items = *n_tiles * kGroupsOf16;
+    struct Low {
+      uint4 b0[kC], b1[kC], p[kC];
+    };
+    auto fetch = [&](int item) -> Low {
+      Low w;
+      const int tile = item / kGroupsOf16, row = n0 + rank0 + 16 * (item % kGroupsOf16);
+      const bool on = item < items && row < p.N;
+      const int a = on ? tile_ad[tile] : 0, t = on ? tile_tok[tile * kTokenTile + g] : -1;
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        const int j = 32 * c + 8 * q;
+        const bool go = on && j < p.r;
+        const uint16_t* b = p.B + ((size_t)a * p.N + (go ? row + g : 0)) * p.r + (go ? j : 0);
+        w.b0[c] = ldg16(b, go);
+        w.b1[c] = ldg16(b + 8 * p.r, go && row + 8 < p.N);  // N is a multiple of 8
+        w.p[c] = ldcg16(p.p + (size_t)(t >= 0 ? t : 0) * p.r + (go ? j : 0), go && t >= 0);
+      }
+      return w;
+    };
+    Low w0 = fetch(warp), w1 = fetch(warp + kItemWarps);
+    for (int item = warp; item < items; item += kItemWarps) {
+      const Low w2 = fetch(item + 2 * kItemWarps);
+      const int tile = item / kGroupsOf16, lrow = 16 * (item % kGroupsOf16);
+      const int t0 = tile_tok[tile * kTokenTile + 2 * q], t1 = tile_tok[tile * kTokenTile + 2 * q + 1];
+      float* c0 = part + (t0 < 0 ? 0 : t0) * kPitch + lrow + g;
+      float* c1 = part + (t1 < 0 ? 0 : t1) * kPitch + lrow + g;
+      float d[4] = {c0[0], c1[0], c0[8], c1[8]};
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        mma_bf16(d, w0.b0[c].x, w0.b1[c].x, w0.b0[c].y, w0.b1[c].y, w0.p[c].x, w0.p[c].y);
+        mma_bf16(d, w0.b0[c].z, w0.b1[c].z, w0.b0[c].w, w0.b1[c].w, w0.p[c].z, w0.p[c].w);
+      }
+      if (t0 >= 0) c0[0] = d[0], c0[8] = d[2];
+      if (t1 >= 0) c1[0] = d[1], c1[8] = d[3];
+      w0 = w1;
+      w1 = w2;
+    }
+  }
+  __syncthreads();
+  // y, eight rows (16 bytes) of a token a thread; N is a multiple of 8
+  for (int i = tid; i < p.T * (kRows / 8); i += kThreadsSplit) {
+    const int t = i / (kRows / 8), lrow = 8 * (i % (kRows / 8));
+    const float4 u = *reinterpret_cast<const float4*>(part + t * kPitch + lrow);
+    const float4 v = *reinterpret_cast<const float4*>(part + t * kPitch + lrow + 4);
+    if (n0 + rank0 + lrow < p.N)
+      *reinterpret_cast<uint4*>(p.y + (size_t)t * p.N + n0 + rank0 + lrow) =
+          make_uint4(pack_bf16x2(u.x, u.y), pack_bf16x2(u.z, u.w), pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  }
 }
 
 // Launches `kernel` so that it may start before the launch ahead of it in the stream has finished (it calls
@@ -581,20 +641,12 @@ cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int threads, i
 }  // namespace
 
 cudaError_t launch_adapter_small(const AdapterProjHost& h, const int32_t* ids, const uint16_t* x, const uint16_t* A,
-                                 const uint16_t* B, uint16_t* low, int32_t* list, uint16_t* y, int num_sms,
-                                 cudaStream_t stream) {
+                                 const uint16_t* B, uint16_t* low, uint16_t* y, int num_sms, cudaStream_t stream) {
   const bool few = h.T <= kAdapterGemvTokens;
   {
-    const SmallProjParams p{ids, x, A, h.scale, low, list, h.T, h.K, h.n, h.r};
-    // at most T tiles, and at most T / 8 full ones with one more an adapter
-    const int tiles = few || h.T < h.T / kTokenTile + h.n ? h.T : h.T / kTokenTile + h.n;
-    const int items = tiles * ((h.r + 15) / 16);
-    const int grid = items < 4 * num_sms ? items : 4 * num_sms;
+    const SmallProjParams p{ids, x, A, h.scale, low, h.T, h.K, h.n, h.r};
     LaunchScope scope("adapter_small_proj", stream);
-    if (few)
-      adapter_small_proj_kernel<false><<<grid, kThreads, 0, stream>>>(p);
-    else
-      adapter_small_proj_kernel<true><<<grid, kThreads, 0, stream>>>(p);
+    adapter_small_proj_kernel<<<h.T * ((h.r + 15) / 16), kProjThreads, 0, stream>>>(p);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
   }
@@ -612,13 +664,23 @@ cudaError_t launch_adapter_small(const AdapterProjHost& h, const int32_t* ids, c
   CUtensorMap mx;
   cudaError_t err = map_bf16_2d(&mx, x, h.K, h.T, 64, (uint32_t)NT, CU_TENSOR_MAP_SWIZZLE_128B);
   if (err != cudaSuccess) return err;
-  const int ring = ads::ring_bytes(NT), smem = ring + 1024 + 1024;
-  const SplitParams p{h.nf4, h.absmax, B, low, list, y, h.err, h.timeout_ns, h.T, NT, h.K, h.N, h.n, h.r, S, ring};
-  if ((err = cudaFuncSetAttribute(adapter_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) !=
-      cudaSuccess)
-    return err;
+  const int ring = ads::ring_bytes(NT, S), smem = ring + ads::kBarBytes + ads::kListBytes + 1024;
+  const SplitParams p{h.nf4, h.absmax, B, low, ids, y, h.err, h.timeout_ns, h.T, NT, h.K, h.N, h.n, h.r, ring};
   LaunchScope scope("adapter_split", stream);
-  return launch_dependent(adapter_split_kernel, tiles * S, ads::kThreadsSplit, smem, S, stream, mx, p);
+  auto run = [&](auto kernel) -> cudaError_t {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return e != cudaSuccess ? e
+                            : launch_dependent(kernel, tiles * S, ads::kThreadsSplit, smem, S, stream, mx, p);
+  };
+  if (h.r > 32)
+    return S == 1   ? run(adapter_split_kernel<1, true>)
+           : S == 2 ? run(adapter_split_kernel<2, true>)
+           : S == 4 ? run(adapter_split_kernel<4, true>)
+                    : run(adapter_split_kernel<8, true>);
+  return S == 1   ? run(adapter_split_kernel<1, false>)
+         : S == 2 ? run(adapter_split_kernel<2, false>)
+         : S == 4 ? run(adapter_split_kernel<4, false>)
+                  : run(adapter_split_kernel<8, false>);
 }
 
 }  // namespace e4b

@@ -128,7 +128,7 @@ e4b_status check_proj_dims(const e4b_proj_dims* d, int32_t T) {
 
 // Workspace of the serving call: the error word, then the grouping, p and the rows of x in their order.
 struct ServeProjLayout {
-  size_t order, offsets, steps, low, rows, list, total;
+  size_t order, offsets, steps, low, rows, total;
 };
 ServeProjLayout serve_proj_layout(const e4b_proj_dims* d, int32_t T) {
   auto up = [](size_t b) { return (b + 255) / 256 * 256; };
@@ -139,8 +139,7 @@ ServeProjLayout serve_proj_layout(const e4b_proj_dims* d, int32_t T) {
   l.steps = l.offsets + up((size_t)(d->n_adapters + 2) * 4);
   l.low = l.steps + up((size_t)adapter_steps_layout(rows, d->n_adapters).total * 4);
   l.rows = l.low + up((size_t)rows * d->r * 2);
-  l.list = l.rows + up((size_t)rows * d->K * 2);
-  l.total = l.list + up((size_t)kAdapterListInts * 4);
+  l.total = l.rows + up((size_t)rows * d->K * 2);
   return l;
 }
 
@@ -787,8 +786,7 @@ e4b_status e4b_multi_lora_serve_fwd(const e4b_proj_dims* dims, int32_t T, const 
   E4B_CUDA(device_sms(&sms));
   const AdapterProjHost h = proj_host(dims, T, base, adapters, order, offsets, steps, ws);
   if (T <= kAdapterSmallTokens) {
-    E4B_CUDA(launch_adapter_small(h, ids, x, adapters->A, adapters->B, low, reinterpret_cast<int32_t*>(w + l.list), y,
-                                  sms, st));
+    E4B_CUDA(launch_adapter_small(h, ids, x, adapters->A, adapters->B, low, y, sms, st));
     return E4B_OK;
   }
   E4B_CUDA(launch_adapter_group(ids, T, dims->n_adapters, order, offsets, steps, st));

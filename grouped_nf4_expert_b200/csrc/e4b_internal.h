@@ -199,10 +199,6 @@ cudaError_t launch_wgrad(const WgradHost& h, int num_sms, cudaStream_t stream);
 constexpr int kAdapterUnitRows = 256;  // rows of a GEMM unit (a CTA pair)
 constexpr int kAdapterGemvTokens = 16;    // most tokens of the base product on warp instructions
 constexpr int kAdapterSmallTokens = 256;  // most tokens of the small-batch kernels
-// Token tiles of the small-batch kernels (int32): [0] tiles, their adapters, their eight tokens (-1: none).
-constexpr int kAdapterListAd = 8;
-constexpr int kAdapterListTok = kAdapterListAd + kAdapterSmallTokens;
-constexpr int kAdapterListInts = kAdapterListTok + 8 * kAdapterSmallTokens;
 constexpr int kAdapterTaskRows = 128;  // rows of a low-rank projection task (one adapter's)
 inline int64_t adapter_rows_cap(int64_t T, int n) {
   const int64_t groups = T < n + 1 ? T : n + 1;
@@ -245,10 +241,9 @@ cudaError_t launch_adapter_gemm(const AdapterProjHost& h, bool mn, const uint16_
                                 const uint16_t* fac, uint16_t* out, int num_sms, cudaStream_t stream);
 cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, const uint16_t* dY, const uint16_t* p,
                                  const uint16_t* q, uint16_t* dA, uint16_t* dB, int num_sms, cudaStream_t stream);
-// y for up to kAdapterSmallTokens tokens in two launches (scratch: low [T, r], list [kAdapterListInts]).
+// y for up to kAdapterSmallTokens tokens in two launches (scratch: low [T, r]).
 cudaError_t launch_adapter_small(const AdapterProjHost& h, const int32_t* ids, const uint16_t* x, const uint16_t* A,
-                                 const uint16_t* B, uint16_t* low, int32_t* list, uint16_t* y, int num_sms,
-                                 cudaStream_t stream);
+                                 const uint16_t* B, uint16_t* low, uint16_t* y, int num_sms, cudaStream_t stream);
 
 // ---- balance loss (balance.cu)
 struct BalanceHost {
