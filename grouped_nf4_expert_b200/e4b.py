@@ -549,18 +549,42 @@ class _OnDevice:
     """Calls on the object's device, whatever device is current: its current stream by default, or a
     stream of that device (a stream of another device is refused)."""
 
-    def _call(self, name, stream, *args):
+    def _arg(self, t, dtype, numel, name, optional=False):
+        """Device address of ``t`` after the checks of :func:`_dev`; the tests a sound tensor passes come
+        first, since a small batch's call costs the host more than the GPU."""
+        if (type(t) is self._tensor and t.dtype is dtype[1] and t.device == self.device and t.is_contiguous()
+                and t.numel() >= numel > 0):
+            return t.data_ptr()
+        return _dev(t, dtype[0], numel, name, self.device, optional=optional or self.T == 0)
+
+    def _on(self, device):
         import torch
+        self.device = _cuda_device(device)
+        self._tensor = torch.Tensor
+        self._raw_stream = torch._C._cuda_getCurrentRawStream  # the handle, without a Stream object a call
+        self._current_device = torch.cuda.current_device
+        self._bf16, self._f32 = ("bf16", torch.bfloat16), ("f32", torch.float32)
+        self._i32, self._u8 = ("i32", torch.int32), ("u8", torch.uint8)
+        self._fns = {}
+        return self.device
+
+    def _call(self, name, stream, *args):
+        index = self.device.index
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
+            handle = self._raw_stream(index)
         elif stream.device != self.device:
             raise ValueError("stream: on %s, the problem is on %s" % (stream.device, self.device))
-        fn = getattr(lib(), name)
-        if torch.cuda.current_device() == self.device.index:
-            status = fn(*args, stream.cuda_stream)
         else:
+            handle = stream.cuda_stream
+        fn = self._fns.get(name)
+        if fn is None:
+            fn = self._fns[name] = getattr(lib(), name)
+        if self._current_device() == index:
+            status = fn(*args, handle)
+        else:
+            import torch
             with torch.cuda.device(self.device):
-                status = fn(*args, stream.cuda_stream)
+                status = fn(*args, handle)
         if status != E4B_OK:
             raise E4BError(status, name)
 
@@ -591,13 +615,15 @@ class Projection(_OnDevice):
         self.dims, self.T, self.train = dims, T, train
         sz = e4b_proj_get_sizes(dims, T)
         self.sizes = sz
-        self.device = dev = _cuda_device(device)
+        dev = self._on(device)
         n, r, R = dims.n_adapters, dims.r, sz.rows_cap
         bf, i32 = torch.bfloat16, torch.int32
         self.y = _alloc((T, dims.N), bf, dev)
         self.ws = _alloc((int(max(sz.workspace_bytes, sz.serve_workspace_bytes)),), torch.uint8, dev)
         self._dims_c = dims.c()
         self._dims_p = ctypes.byref(self._dims_c)
+        self._base_need = {"nf4": dims.N * dims.K // 2, "absmax": dims.N * dims.K // 64}
+        self._adapters_need = {"A": n * r * dims.K, "B": n * dims.N * r, "scale": n}
         self._y_p, self._ws_p, self._ws_n = _ptr(self.y), _ptr(self.ws), self.ws.numel()
         if train:
             self.order, self.offsets = _alloc((R,), i32, dev), _alloc((n + 2,), i32, dev)
@@ -610,20 +636,17 @@ class Projection(_OnDevice):
             self.dA = self.lora_grads[:na].view(n, r, dims.K)
             self.dB = self.lora_grads[na:].view(n, dims.N, r)
             self._groups = AdapterGroups(_ptr(self.order), _ptr(self.offsets), _ptr(self.steps))
+            self._groups_p = ctypes.byref(self._groups)
+            self._low_p = (_ptr(self.p), _ptr(self.q))
+            self._dx_p, self._grad_p = _ptr(self.dx), (_ptr(self.dA), _ptr(self.dB))
         self._call("e4b_workspace_init", None, self._ws_p, self._ws_n)
 
-    def _tokens(self, t, dtype, cols, name):
-        return _dev(t, dtype, self.T * cols, name, self.device, optional=self.T == 0)
-
     def _base(self, base: Nf4Matrix):
-        d = self.dims
-        _check_struct(base, {"nf4": d.N * d.K // 2, "absmax": d.N * d.K // 64}, self.device, "base")
+        _check_struct(base, self._base_need, self.device, "base")
         return ctypes.byref(base)
 
     def _adapters(self, ad: AdapterFactors):
-        d = self.dims
-        _check_struct(ad, {"A": d.n_adapters * d.r * d.K, "B": d.n_adapters * d.N * d.r, "scale": d.n_adapters},
-                      self.device, "adapters")
+        _check_struct(ad, self._adapters_need, self.device, "adapters")
         return ctypes.byref(ad)
 
     def _training(self):
@@ -632,36 +655,36 @@ class Projection(_OnDevice):
 
     def e4b_multi_lora_serve_fwd(self, ids, x, base: Nf4Matrix, adapters: AdapterFactors, stream=None):
         """Serving forward into ``self.y`` (ids int32 [T], any id outside [0, n) for no adapter)."""
-        pi = self._tokens(ids, "i32", 1, "ids")
-        px = self._tokens(x, "bf16", self.dims.K, "x")
+        pi = self._arg(ids, self._i32, self.T, "ids")
+        px = self._arg(x, self._bf16, self.T * self.dims.K, "x")
         self._call("e4b_multi_lora_serve_fwd", stream, self._dims_p, self.T, pi, px, self._base(base),
                    self._adapters(adapters), self._y_p, self._ws_p, self._ws_n)
 
     def e4b_adapter_group(self, ids, stream=None):
         """Groups the step's tokens by adapter for the training calls."""
         self._training()
-        self._call("e4b_adapter_group", stream, self._dims_p, self.T, self._tokens(ids, "i32", 1, "ids"),
-                   ctypes.byref(self._groups))
+        self._call("e4b_adapter_group", stream, self._dims_p, self.T, self._arg(ids, self._i32, self.T, "ids"),
+                   self._groups_p)
 
     def e4b_multi_lora_fwd(self, x, base: Nf4Matrix, adapters: AdapterFactors, stream=None):
         self._training()
-        px = self._tokens(x, "bf16", self.dims.K, "x")
-        self._call("e4b_multi_lora_fwd", stream, self._dims_p, self.T, ctypes.byref(self._groups), px,
-                   self._base(base), self._adapters(adapters), _ptr(self.p), self._y_p, self._ws_p, self._ws_n)
+        px = self._arg(x, self._bf16, self.T * self.dims.K, "x")
+        self._call("e4b_multi_lora_fwd", stream, self._dims_p, self.T, self._groups_p, px,
+                   self._base(base), self._adapters(adapters), self._low_p[0], self._y_p, self._ws_p, self._ws_n)
 
     def e4b_multi_lora_dgrad(self, dY, base: Nf4Matrix, adapters: AdapterFactors, stream=None):
         self._training()
-        pd = self._tokens(dY, "bf16", self.dims.N, "dY")
-        self._call("e4b_multi_lora_dgrad", stream, self._dims_p, self.T, ctypes.byref(self._groups), pd,
-                   self._base(base), self._adapters(adapters), _ptr(self.q), _ptr(self.dx), self._ws_p, self._ws_n)
+        pd = self._arg(dY, self._bf16, self.T * self.dims.N, "dY")
+        self._call("e4b_multi_lora_dgrad", stream, self._dims_p, self.T, self._groups_p, pd,
+                   self._base(base), self._adapters(adapters), self._low_p[1], self._dx_p, self._ws_p, self._ws_n)
 
     def e4b_multi_lora_wgrad(self, x, dY, stream=None):
         """Adapter gradients from the ``p`` and ``q`` of the forward and the input gradient."""
         self._training()
-        px = self._tokens(x, "bf16", self.dims.K, "x")
-        pd = self._tokens(dY, "bf16", self.dims.N, "dY")
-        self._call("e4b_multi_lora_wgrad", stream, self._dims_p, self.T, ctypes.byref(self._groups), px, pd,
-                   _ptr(self.p), _ptr(self.q), _ptr(self.dA), _ptr(self.dB), self._ws_p, self._ws_n)
+        px = self._arg(x, self._bf16, self.T * self.dims.K, "x")
+        pd = self._arg(dY, self._bf16, self.T * self.dims.N, "dY")
+        self._call("e4b_multi_lora_wgrad", stream, self._dims_p, self.T, self._groups_p, px, pd,
+                   *self._low_p, *self._grad_p, self._ws_p, self._ws_n)
 
     def check_device_error(self, stream=None) -> int:
         import torch
@@ -683,7 +706,7 @@ class RouterBalance(_OnDevice):
         self._dims_c = BalanceDims(E, top_k, S, 0.0, 0.0)
         self._dims_p = ctypes.byref(self._dims_c)
         ws_bytes = e4b_balance_get_sizes(self._dims_c, T)
-        self.device = dev = _cuda_device(device)
+        dev = self._on(device)
         f32, i32 = torch.float32, torch.int32
         self.counts, self.prob_sum = _alloc((S, E), i32, dev), _alloc((S, E), f32, dev)
         self._tokens = _alloc((S + 2,), i32, dev)
@@ -695,11 +718,11 @@ class RouterBalance(_OnDevice):
         self._loss_p, self._ws_p, self._ws_n = _ptr(self.loss), _ptr(self.ws), self.ws.numel()
 
     def _inputs(self, logits, seq_offsets, token_mask):
-        pl = _dev(logits, "f32", self.T * self.E, "logits", self.device, optional=self.T == 0)
+        pl = self._arg(logits, self._f32, self.T * self.E, "logits")
         if seq_offsets is None and self.S != 1:
             raise ValueError("seq_offsets: required for %d sequences" % self.S)
-        ps = _dev(seq_offsets, "i32", self.S + 1, "seq_offsets", self.device, optional=True)
-        pm = _dev(token_mask, "u8", self.T, "token_mask", self.device, optional=True)
+        ps = self._arg(seq_offsets, self._i32, self.S + 1, "seq_offsets", optional=True)
+        pm = self._arg(token_mask, self._u8, self.T, "token_mask", optional=True)
         return pl, ps, pm
 
     def e4b_balance_fwd(self, logits, topk_ids, seq_offsets=None, token_mask=None, balance_coef=1.0, z_coef=0.0,
@@ -707,7 +730,7 @@ class RouterBalance(_OnDevice):
         """Loss and per-expert counts.  seq_offsets: int32 [S + 1] ascending (None: one sequence of all
         tokens); token_mask: uint8 [T], 0 for tokens that take no part."""
         pl, ps, pm = self._inputs(logits, seq_offsets, token_mask)
-        pi = _dev(topk_ids, "i32", self.T * self.top_k, "topk_ids", self.device, optional=self.T == 0)
+        pi = self._arg(topk_ids, self._i32, self.T * self.top_k, "topk_ids")
         self._dims_c.balance_coef, self._dims_c.z_coef = balance_coef, z_coef
         self._call("e4b_balance_fwd", stream, self._dims_p, self.T, pl, pi, ps, pm, self._stats_p, self._loss_p,
                    self._ws_p, self._ws_n)
@@ -716,8 +739,8 @@ class RouterBalance(_OnDevice):
                         dloss=None, accumulate=False, stream=None):
         """d_logits = dloss * dloss/dlogits (dloss: float32 [1], None for 1), or += with ``accumulate``."""
         pl, ps, pm = self._inputs(logits, seq_offsets, token_mask)
-        pd = _dev(d_logits, "f32", self.T * self.E, "d_logits", self.device, optional=self.T == 0)
-        pg = _dev(dloss, "f32", 1, "dloss", self.device, optional=True)
+        pd = self._arg(d_logits, self._f32, self.T * self.E, "d_logits")
+        pg = self._arg(dloss, self._f32, 1, "dloss", optional=True)
         self._dims_c.balance_coef, self._dims_c.z_coef = balance_coef, z_coef
         self._call("e4b_balance_bwd", stream, self._dims_p, self.T, pl, ps, pm, self._stats_p, pg,
                    1 if accumulate else 0, pd)
