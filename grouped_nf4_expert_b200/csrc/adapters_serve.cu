@@ -1,13 +1,16 @@
-// Small batches of the NF4 projection with adapters of many requests.
+// Small batches of the NF4 projection with adapters of many requests, one
+// launch each:
 //
-//   adapter_small_proj_kernel: p[t] = bf16(s[a] A[a] x[t]) for up to 256 tokens;
-//   adapter_gemv_kernel:       y[t] = W x[t] + B[a] p[t] for up to 16 tokens;
-//   adapter_split_kernel:      the same for up to 256 tokens.
+//   adapter_gemv_kernel:  y[t] = W x[t] + B[a] p[t], p[t] = s[a] A[a] x[t], for
+//                         up to 16 tokens;
+//   adapter_split_kernel: the same for up to 256 tokens.
 //
 // What bounds them: reading the matrix (4.5 bits a weight) and each named
-// adapter once, and the latency of two dependent launches.  The second launch
-// starts while the first still runs (programmatic dependent launch), streams
-// the matrix, and waits for p only before its epilogue.
+// adapter once, and latency: two dependent launches cost the host 9 us here and
+// one 4.5 us, more than the GPU needs.  So the first blocks of the grid compute p
+// while the others stream the matrix and wait for p (a counter in the workspace,
+// bounded wait) only in their epilogue.  The blocks of p never wait and come
+// first in the grid.
 //
 // Up to 16 tokens the products run on warp matrix instructions (m16n8k16):
 // there is nothing for a 128-row UMMA tile to amortise its set-up over.  Above,
@@ -17,7 +20,7 @@
 // shared memory.
 //
 // The sum over k may be taken in any order that both operands share, so in the
-// warp products a lane takes 16 (x: 64) consecutive bytes of its row, and the
+// warp products a lane takes 16 (W, x: 64) consecutive values of its row, and the
 // elements it holds are declared to be the ones the instruction expects of it.
 #include <math.h>
 
@@ -32,11 +35,34 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTokenTile = 8;
-constexpr int kProjThreads = 512;
-constexpr int kProjWarps = kProjThreads / 32;
 
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Hand-over of p between the blocks of a launch.  signal_ready: the whole block, after its stores of p.
+// wait_ready: one thread; false where the limit ran out.  leave: one thread, once the block has p.
+__device__ __forceinline__ void signal_ready(DeviceError* err) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    atomicAdd(&err->ready, 1);
+  }
+}
+__device__ __forceinline__ bool wait_ready(DeviceError* err, int blocks, long long timeout_ns, int site) {
+  const long long c0 = clock64(), limit = wait_limit_cycles(timeout_ns);
+  while (true) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(&err->ready) : "memory");
+    if (v >= blocks) return true;
+    if (clock64() - c0 > limit) {
+      record_error(err, E4B_ERR_DEVICE_TIMEOUT, site);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ void leave(DeviceError* err, int blocks) {
+  if (atomicAdd(&err->left, 1) == blocks - 1) {
+    err->ready = 0;
+    err->left = 0;
+  }
+}
 
 // D (16 x 8) += A (16 x 16) B (16 x 8), bf16 inputs, float32 sums.
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -69,207 +95,216 @@ __device__ __forceinline__ uint4 ldg16(const void* p, bool ok) {
 }
 
 // ----------------------------------------------------------------------------
-// p for up to kAdapterSmallTokens tokens
+// 16 ranks of an adapter against up to eight tokens, over [k_lo, k_hi)
 // ----------------------------------------------------------------------------
-// The tokens of an adapter are taken in tiles of up to eight, in token order.
-// Block (t, slice) does the tile that starts with token t -- or nothing, where
-// t is not the first, ninth, ... token of its adapter -- for 16 of the r ranks:
-// its warps split K, lanes read A and x straight from global memory, and the
-// partial sums meet in shared memory.  Each block finds its tile from one look
-// at the ids (a ballot a warp), without a sort ahead of the loads.
-struct SmallProjParams {
-  const int32_t* ids;
-  const uint16_t* x;
-  const uint16_t* A;
-  const float* scale;
-  uint16_t* p;
-  int T, K, n, r;
-};
-
-__global__ void __launch_bounds__(kProjThreads) adapter_small_proj_kernel(const SmallProjParams p) {
-  static_assert(kAdapterSmallTokens <= kProjThreads, "a token a thread");
-  __shared__ uint32_t member[kProjWarps];  // tokens of this block's adapter, a bit each
-  __shared__ float red[kProjWarps][16][kTokenTile + 1];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-  grid_launch_dependents();
-  const int slices = (p.r + 15) / 16, first = (int)blockIdx.x / slices, j0 = ((int)blockIdx.x - first * slices) * 16;
-  const int a = __ldg(p.ids + first);
-  if ((uint32_t)a >= (uint32_t)p.n) return;
-  const uint32_t mine = __ballot_sync(kFull, tid < p.T && __ldg(p.ids + tid) == a);
-  if (lane == 0) member[warp] = mine;
-  __syncthreads();
-  int before = 0;
-  for (int w = 0; w <= first >> 5; ++w)
-    before += __popc(w < first >> 5 ? member[w] : member[w] & ((1u << (first & 31)) - 1));
-  if (before % kTokenTile) return;
-  // the i-th token of the tile (-1: none)
-  auto token = [&](int i) -> int {
-    for (int w = first >> 5; w < kProjWarps; ++w) {
-      uint32_t m = member[w];
-      if (w == first >> 5) m &= kFull << (first & 31);
-      const int c = __popc(m);
-      if (i < c) {
-        for (; i > 0; --i) m &= m - 1;
-        return 32 * w + __ffs(m) - 1;
-      }
-      i -= c;
+// The block's warps split the range, lanes read A and x straight from global
+// memory; every warp leaves its partial sums in red[warp][rank][token].  t: the
+// token of this lane's column (-1: none); k_lo a multiple of 32.
+template <int WARPS>
+__device__ __forceinline__ void low_rank_tile(const uint16_t* x, const uint16_t* A, int K, int r, int a, int t, int j0,
+                                              int k_lo, int k_hi, float (*red)[16][kTokenTile + 1]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const bool tok = t >= 0, lo = j0 + g < r, hi = j0 + g + 8 < r;
+  const uint16_t* xr = x + (tok ? (size_t)t * K : 0) + 8 * q;
+  const uint16_t* a0 = A + ((size_t)a * r + (lo ? j0 + g : 0)) * K + 8 * q;
+  const uint16_t* a1 = A + ((size_t)a * r + (hi ? j0 + g + 8 : 0)) * K + 8 * q;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  // 32 values of k a step: lane q of a row holds 8 of them, two instructions' worth.  Four steps' loads go out
+  // together.
+  constexpr int kAhead = 4;
+  for (int k0 = k_lo + warp * 32; k0 < k_hi; k0 += WARPS * 32 * kAhead) {
+    uint4 w0[kAhead], w1[kAhead], xv[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = k0 + i * WARPS * 32;
+      w0[i] = ldg16(a0 + k, lo && k < k_hi);
+      w1[i] = ldg16(a1 + k, hi && k < k_hi);
+      xv[i] = ldg16(xr + k, tok && k < k_hi);
     }
-    return -1;
-  };
-  {
-    const int t = token(g);
-    const bool tok = t >= 0, lo = j0 + g < p.r, hi = j0 + g + 8 < p.r;
-    const uint16_t* xr = p.x + (tok ? (size_t)t * p.K : 0) + 8 * q;
-    const uint16_t* a0 = p.A + ((size_t)a * p.r + (lo ? j0 + g : 0)) * p.K + 8 * q;
-    const uint16_t* a1 = p.A + ((size_t)a * p.r + (hi ? j0 + g + 8 : 0)) * p.K + 8 * q;
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    // 32 values of k a step: lane q of a row holds 8 of them, two instructions' worth.  Four steps' loads go
-    // out together.
-    constexpr int kAhead = 4;
-    for (int k0 = warp * 32; k0 < p.K; k0 += kProjWarps * 32 * kAhead) {
-      uint4 w0[kAhead], w1[kAhead], xv[kAhead];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int k = k0 + i * kProjWarps * 32;
-        w0[i] = ldg16(a0 + k, lo && k < p.K);
-        w1[i] = ldg16(a1 + k, hi && k < p.K);
-        xv[i] = ldg16(xr + k, tok && k < p.K);
-      }
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        mma_bf16(acc, w0[i].x, w1[i].x, w0[i].y, w1[i].y, xv[i].x, xv[i].y);
-        mma_bf16(acc, w0[i].z, w1[i].z, w0[i].w, w1[i].w, xv[i].z, xv[i].w);
-      }
-    }
-    red[warp][g][2 * q] = acc[0];
-    red[warp][g][2 * q + 1] = acc[1];
-    red[warp][g + 8][2 * q] = acc[2];
-    red[warp][g + 8][2 * q + 1] = acc[3];
-    __syncthreads();
-    if (tid < 16 * kTokenTile) {
-      const int j = tid & 15, to = token(tid >> 4);
-      if (to >= 0 && j0 + j < p.r) {
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kProjWarps; ++w) v += red[w][j][tid >> 4];
-        const __nv_bfloat16 b = __float2bfloat16_rn(__ldg(p.scale + a) * v);
-        p.p[(size_t)to * p.r + j0 + j] = *reinterpret_cast<const uint16_t*>(&b);
-      }
+    for (int i = 0; i < kAhead; ++i) {
+      mma_bf16(acc, w0[i].x, w1[i].x, w0[i].y, w1[i].y, xv[i].x, xv[i].y);
+      mma_bf16(acc, w0[i].z, w1[i].z, w0[i].w, w1[i].w, xv[i].z, xv[i].w);
     }
   }
+  red[warp][g][2 * q] = acc[0];
+  red[warp][g][2 * q + 1] = acc[1];
+  red[warp][g + 8][2 * q] = acc[2];
+  red[warp][g + 8][2 * q + 1] = acc[3];
 }
 
 // ----------------------------------------------------------------------------
 // y for up to 16 tokens: 16 rows of W a block, K split over its warps
 // ----------------------------------------------------------------------------
+// The blocks of p take (token, 16 ranks, share of K) each; with few of them K is
+// split (kq shares, added in order by the readers), since one block's loads
+// would be the longest chain of the launch.
 struct GemvParams {
   const int32_t* ids;
   const uint16_t* x;
   const uint8_t* nf4;
   const float* absmax;
+  const uint16_t* A;
   const uint16_t* B;
-  const uint16_t* p;
+  const float* scale;
+  float* part;  // [kq, T, r] shares of A x
   uint16_t* y;
+  DeviceError* err;
+  long long timeout_ns;
   int T, K, N, n, r;
+  int kq, p_blocks;
 };
 
 template <int NT>  // tiles of 8 tokens
 __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvParams p) {
-  __shared__ float red[kWarps][8 * NT][17];
+  __shared__ float red[kWarps * 16 * 9 > kWarps * 8 * NT * 17 ? kWarps * 16 * 9 : kWarps * 8 * NT * 17];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-  const int n0 = blockIdx.x * 16;
+  if ((int)blockIdx.x < p.p_blocks) {
+    const int slices = (p.r + 15) / 16;
+    const int share = (int)blockIdx.x % p.kq, item = (int)blockIdx.x / p.kq;
+    const int t = item / slices, j0 = (item - t * slices) * 16;
+    const int a = __ldg(p.ids + t);
+    if ((uint32_t)a < (uint32_t)p.n) {
+      float(*tile)[16][kTokenTile + 1] = reinterpret_cast<float(*)[16][kTokenTile + 1]>(red);
+      const int blocks32 = p.K / 32;
+      low_rank_tile<kWarps>(p.x, p.A, p.K, p.r, a, g == 0 ? t : -1, j0, share * blocks32 / p.kq * 32,
+                            (share + 1) * blocks32 / p.kq * 32, tile);
+      __syncthreads();
+      if (tid < 16 && j0 + tid < p.r) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += tile[w][tid][0];
+        p.part[((size_t)share * p.T + t) * p.r + j0 + tid] = v;
+      }
+    }
+    signal_ready(p.err);
+    return;
+  }
+  const int n0 = ((int)blockIdx.x - p.p_blocks) * 16;
   const bool lo = n0 + g < p.N, hi = n0 + g + 8 < p.N;
   const size_t r0 = lo ? n0 + g : 0, r1 = hi ? n0 + g + 8 : 0;
-  const uint8_t* c0 = p.nf4 + r0 * (p.K / 2) + 16 * q;
-  const uint8_t* c1 = p.nf4 + r1 * (p.K / 2) + 16 * q;
-  const float* s0 = p.absmax + r0 * (p.K / 64) + (q >> 1);
-  const float* s1 = p.absmax + r1 * (p.K / 64) + (q >> 1);
+  // A step is 256 values of k, one NF4 block of 64 a lane and row.
+  const uint8_t* c0 = p.nf4 + r0 * (p.K / 2) + 32 * q;
+  const uint8_t* c1 = p.nf4 + r1 * (p.K / 2) + 32 * q;
+  const float* s0 = p.absmax + r0 * (p.K / 64) + q;
+  const float* s1 = p.absmax + r1 * (p.K / 64) + q;
   const uint16_t* xr[NT];
   bool tok[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     tok[i] = 8 * i + g < p.T;
-    xr[i] = p.x + (tok[i] ? (size_t)(8 * i + g) * p.K : 0) + 32 * q;
+    xr[i] = p.x + (tok[i] ? (size_t)(8 * i + g) * p.K : 0) + 64 * q;
   }
   const Nf4Shift ks = nf4_shift_consts();
   float acc[NT][4];
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
-  // A step is 128 values of k: 32 a lane, inside one block of 64.  The codes of four steps are in flight.
-  const int steps = (p.K + 127) / 128;
-  constexpr int kAhead = 4;
-  for (int b0 = warp; b0 < steps; b0 += kWarps * kAhead) {
-    uint4 w0[kAhead], w1[kAhead];
-    float m0[kAhead], m1[kAhead];
+  struct Raw {
+    uint4 a[2], b[2];
+    float ma, mb;
+  };
+  auto load = [&](int k0) -> Raw {
+    Raw w;
+    const bool in = k0 + 64 * q < p.K;  // K is a multiple of 64: the last step may be short of blocks
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int b = b0 + i * kWarps;
-      const bool in = b * 128 + 32 * q < p.K;  // K is a multiple of 64: the last step may be half
-      w0[i] = ldg16(c0 + (size_t)b * 64, in && lo);
-      w1[i] = ldg16(c1 + (size_t)b * 64, in && hi);
-      m0[i] = in && lo ? __ldg(s0 + 2 * b) : 0.0f;
-      m1[i] = in && hi ? __ldg(s1 + 2 * b) : 0.0f;
+    for (int h = 0; h < 2; ++h) {
+      w.a[h] = ldg16(c0 + k0 / 2 + 16 * h, in && lo);
+      w.b[h] = ldg16(c1 + k0 / 2 + 16 * h, in && hi);
     }
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int b = b0 + i * kWarps;
-      if (b >= steps) break;
-      const bool in = b * 128 + 32 * q < p.K;
-      uint4 xv[NT][4];
+    w.ma = in && lo ? __ldg(s0 + k0 / 64) : 0.0f;
+    w.mb = in && hi ? __ldg(s1 + k0 / 64) : 0.0f;
+    return w;
+  };
+  Raw next = load(warp * 256);
+  for (int k0 = warp * 256; k0 < p.K; k0 += kWarps * 256) {
+    const Raw w = next;
+    const bool in = k0 + 64 * q < p.K;
+    uint4 xv[NT][4];
+    auto load_x = [&](int h) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) xv[j][c] = ldg16(xr[j] + b * 128 + 8 * c, in && tok[j]);
-      const Nf4Planes p0 = nf4_block_planes(m0[i]), p1 = nf4_block_planes(m1[i]);
-      const uint32_t cw0[4] = {w0[i].x, w0[i].y, w0[i].z, w0[i].w}, cw1[4] = {w1[i].x, w1[i].y, w1[i].z, w1[i].w};
+        for (int c = 0; c < 4; ++c) xv[j][c] = ldg16(xr[j] + k0 + 32 * h + 8 * c, in && tok[j]);
+    };
+    load_x(0);
+    next = load(k0 + kWarps * 256);
+    const Nf4Planes pa = nf4_block_planes(w.ma), pb = nf4_block_planes(w.mb);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t ca[4] = {w.a[h].x, w.a[h].y, w.a[h].z, w.a[h].w};
+      const uint32_t cb[4] = {w.b[h].x, w.b[h].y, w.b[h].z, w.b[h].w};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t d0[4], d1[4];
-        nf4_decode_word(cw0[c], p0, ks, d0);
-        nf4_decode_word(cw1[c], p1, ks, d1);
+        uint32_t da[4], db[4];
+        nf4_decode_word(ca[c], pa, ks, da);
+        nf4_decode_word(cb[c], pb, ks, db);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          mma_bf16(acc[j], d0[0], d1[0], d0[1], d1[1], xv[j][c].x, xv[j][c].y);
-          mma_bf16(acc[j], d0[2], d1[2], d0[3], d1[3], xv[j][c].z, xv[j][c].w);
+          mma_bf16(acc[j], da[0], db[0], da[1], db[1], xv[j][c].x, xv[j][c].y);
+          mma_bf16(acc[j], da[2], db[2], da[3], db[3], xv[j][c].z, xv[j][c].w);
         }
       }
+      if (h == 0) load_x(1);
     }
   }
+  float(*sums)[8 * NT][17] = reinterpret_cast<float(*)[8 * NT][17]>(red);
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    red[warp][8 * i + 2 * q][g] = acc[i][0];
-    red[warp][8 * i + 2 * q + 1][g] = acc[i][1];
-    red[warp][8 * i + 2 * q][g + 8] = acc[i][2];
-    red[warp][8 * i + 2 * q + 1][g + 8] = acc[i][3];
+    sums[warp][8 * i + 2 * q][g] = acc[i][0];
+    sums[warp][8 * i + 2 * q + 1][g] = acc[i][1];
+    sums[warp][8 * i + 2 * q][g + 8] = acc[i][2];
+    sums[warp][8 * i + 2 * q + 1][g + 8] = acc[i][3];
   }
   // One output a thread: its adapter's row of B is fetched before p is waited for.
   const int t = tid >> 4, row = tid & 15;
   const bool mine = t < p.T && n0 + row < p.N;
   uint32_t a = 0xffffffffu;
+  if (t < p.T) a = (uint32_t)__ldg(p.ids + t);
+  const bool adapted = a < (uint32_t)p.n;
   uint4 bw[E4B_MAX_RANK / 8];
-  if (mine) a = (uint32_t)__ldg(p.ids + t);
-  const bool adapted = mine && a < (uint32_t)p.n;
 #pragma unroll
   for (int j = 0; j < E4B_MAX_RANK / 8; ++j)
-    bw[j] = ldg16(p.B + ((size_t)(adapted ? a : 0) * p.N + (mine ? n0 + row : 0)) * p.r + 8 * j,
-                  adapted && 8 * j < p.r);
+    bw[j] = ldg16(p.B + ((size_t)(adapted ? a : 0) * p.N + (mine ? n0 + row : 0)) * p.r + (8 * j < p.r ? 8 * j : 0),
+                  adapted && mine && 8 * j < p.r);
+  __shared__ float ps[8 * NT][E4B_MAX_RANK + 4];
+  __shared__ int have;
+  if (tid == 0) {
+    have = wait_ready(p.err, p.p_blocks, p.timeout_ns, 640);
+    if (have) leave(p.err, (int)gridDim.x - p.p_blocks);
+  }
   __syncthreads();
-  grid_wait();
+  if (!have) return;
+  // p[t, j] = bf16(s[a] sum of the shares), 16 threads a token
+  if (adapted) {
+    const float sc = __ldg(p.scale + a);
+    for (int j = 4 * row; j < p.r; j += 64) {
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int s = 0; s < p.kq; ++s) {
+        const float4 w = __ldcg(reinterpret_cast<const float4*>(p.part + ((size_t)s * p.T + t) * p.r + j));
+        v.x += w.x;
+        v.y += w.y;
+        v.z += w.z;
+        v.w += w.w;
+      }
+      const uint32_t u0 = pack_bf16x2(sc * v.x, sc * v.y), u1 = pack_bf16x2(sc * v.z, sc * v.w);
+      *reinterpret_cast<float4*>(&ps[t][j]) =
+          make_float4(bf16lo_to_f32(u0), bf16hi_to_f32(u0), bf16lo_to_f32(u1), bf16hi_to_f32(u1));
+    }
+  }
+  __syncwarp();  // a token's 16 threads are of one warp
   if (mine) {
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += red[w][t][row];
+    for (int w = 0; w < kWarps; ++w) v += sums[w][t][row];
     if (adapted) {
-      const uint4* pr = reinterpret_cast<const uint4*>(p.p + (size_t)t * p.r);
 #pragma unroll
       for (int j = 0; j < E4B_MAX_RANK / 8; ++j) {
         if (8 * j >= p.r) break;
-        const uint4 pv = __ldcg(pr + j);
-        const uint32_t b4[4] = {bw[j].x, bw[j].y, bw[j].z, bw[j].w}, p4[4] = {pv.x, pv.y, pv.z, pv.w};
+        const uint32_t b4[4] = {bw[j].x, bw[j].y, bw[j].z, bw[j].w};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          v = fmaf(bf16lo_to_f32(b4[c]), bf16lo_to_f32(p4[c]), v);
-          v = fmaf(bf16hi_to_f32(b4[c]), bf16hi_to_f32(p4[c]), v);
+          v = fmaf(bf16lo_to_f32(b4[c]), ps[t][8 * j + 2 * c], v);
+          v = fmaf(bf16hi_to_f32(b4[c]), ps[t][8 * j + 2 * c + 1], v);
         }
       }
     }
@@ -281,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvPar
 // ----------------------------------------------------------------------------
 // y for up to 256 tokens: 128 rows of W x all tokens x a share of K per block
 // ----------------------------------------------------------------------------
-// Warp 0 loads x tiles (TMA), warp 1 owns tensor memory and issues the UMMAs,
+// After the blocks of p: warp 0 loads x tiles (TMA), warp 1 owns tensor memory and issues the UMMAs,
 // warp 2 sorts the tokens into tiles of eight of one adapter, warps 4-15 are
 // three decode teams that take the k-chunks round robin: a thread owns a row of
 // W, reads 32 bytes of codes and a scale a chunk straight into registers two of
@@ -310,14 +345,18 @@ static_assert(kAOff + kABufs * kACols <= kTmemCols, "TMEM budget");
 struct SplitParams {
   const uint8_t* nf4;
   const float* absmax;
+  const uint16_t* x;
+  const uint16_t* A;
   const uint16_t* B;
-  const uint16_t* p;
+  const float* scale;
+  uint16_t* p;         // [T, r]
   const int32_t* ids;
   uint16_t* y;
   DeviceError* err;
   long long timeout_ns;
   int T, NT, K, N, n, r;  // NT: T rounded up to 16
   int ring;               // bytes of the x ring / partial sums
+  int p_blocks;           // blocks of p, ahead of the others (whole clusters)
 };
 
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
@@ -343,12 +382,85 @@ __device__ __forceinline__ uint4 ldcg16(const void* p, bool ok) {
   return v;
 }
 
+// p for the split kernel: the tokens of an adapter in tiles of up to eight, in token order; an item is (tile, 16
+// ranks), and the blocks of p take the items in turn.
+__device__ void split_low_rank(uint8_t* smem, const SplitParams& p) {
+  constexpr int kW = ads::kThreadsSplit / 32;
+  static_assert(kAdapterSmallTokens <= ads::kThreadsSplit, "a token a thread");
+  float(*red)[16][kTokenTile + 1] = reinterpret_cast<float(*)[16][kTokenTile + 1]>(smem);
+  int16_t* ids = reinterpret_cast<int16_t*>(red + kW);    // [kAdapterSmallTokens] -1: no adapter
+  int16_t* first = ids + kAdapterSmallTokens;             // first tokens of the tiles
+  int16_t* ranks = first + kAdapterSmallTokens;           // and their ranks
+  int16_t* tok = ranks + kAdapterSmallTokens;             // [8] tokens of the item's tile
+  int16_t* warp_tiles = tok + kTokenTile;                 // [kW]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2;
+  int a = -1;
+  if (tid < kAdapterSmallTokens) {
+    const uint32_t id = tid < p.T ? (uint32_t)__ldg(p.ids + tid) : kFull;
+    a = id < (uint32_t)p.n ? (int)id : -1;
+    ids[tid] = (int16_t)a;
+  }
+  __syncthreads();
+  // this token's rank among its adapter's: a warp counts eight earlier tokens a read
+  int rank = 0;
+  if (a >= 0) {
+    const uint32_t want = (uint32_t)a * 0x10001u;
+    for (int i = 0; i < tid / 8; ++i) {
+      const uint4 w = reinterpret_cast<const uint4*>(ids)[i];
+      rank += __popc(__vcmpeq2(w.x, want) & 0x10001u) + __popc(__vcmpeq2(w.y, want) & 0x10001u) +
+              __popc(__vcmpeq2(w.z, want) & 0x10001u) + __popc(__vcmpeq2(w.w, want) & 0x10001u);
+    }
+    for (int i = tid / 8 * 8; i < tid; ++i) rank += ids[i] == a;
+  }
+  const bool opens = a >= 0 && rank % kTokenTile == 0;
+  const uint32_t b = __ballot_sync(kFull, opens);
+  if (lane == 0) warp_tiles[warp] = (int16_t)__popc(b);
+  __syncthreads();
+  int at = __popc(b & ((1u << lane) - 1)), n_tiles = 0;
+  for (int w = 0; w < kW; ++w) {
+    if (w < warp) at += warp_tiles[w];
+    n_tiles += warp_tiles[w];
+  }
+  if (opens) {
+    first[at] = (int16_t)tid;
+    ranks[at] = (int16_t)rank;
+  }
+  const int slices = (p.r + 15) / 16;
+  for (int item = (int)blockIdx.x; item < n_tiles * slices; item += p.p_blocks) {
+    const int tile = item / slices, j0 = (item - tile * slices) * 16;
+    __syncthreads();  // the list; the last item's tokens and sums are read
+    if (tid < kTokenTile) tok[tid] = -1;
+    const int ad = ids[first[tile]];
+    __syncthreads();
+    const int d = rank - ranks[tile];  // the tile's first token and the next seven of its adapter
+    if (a == ad && d >= 0 && d < kTokenTile) tok[d] = (int16_t)tid;
+    __syncthreads();
+    low_rank_tile<kW>(p.x, p.A, p.K, p.r, ad, tok[g], j0, 0, p.K, red);
+    __syncthreads();
+    if (tid < 16 * kTokenTile) {
+      const int j = tid & 15, c = tid >> 4, t = tok[c];
+      if (t >= 0 && j0 + j < p.r) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) v += red[w][j][c];
+        const __nv_bfloat16 h = __float2bfloat16_rn(__ldg(p.scale + ad) * v);
+        p.p[(size_t)t * p.r + j0 + j] = *reinterpret_cast<const uint16_t*>(&h);
+      }
+    }
+  }
+  signal_ready(p.err);
+}
+
 template <int S, bool WIDE>  // blocks of a cluster, the shares of K; r > 32
 __global__ void __launch_bounds__(ads::kThreadsSplit, 1)
     adapter_split_kernel(const __grid_constant__ CUtensorMap map_x, const SplitParams p) {
   using namespace ads;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = align1024(smem_dyn);
+  if ((int)blockIdx.x < p.p_blocks) {
+    split_low_rank(smem, p);
+    return;
+  }
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.ring);
   uint64_t* x_full = bars;                  // [kXStages]
   uint64_t* x_empty = x_full + kXStages;    // [kXStages]
@@ -362,7 +474,7 @@ __global__ void __launch_bounds__(ads::kThreadsSplit, 1)
   int16_t* tile_tok = tile_ad + kAdapterSmallTokens;                         // eight a tile, -1: none
   int16_t* count = tile_tok + kTokenTile * kAdapterSmallTokens;              // [n]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = (int)(blockIdx.x % S), n0 = (int)(blockIdx.x / S) * BM;
+  const int rank = (int)(blockIdx.x % S), n0 = (int)((blockIdx.x - p.p_blocks) / S) * BM;
   const int chunks = p.K / BK;
   const int k_lo = rank * chunks / S, nc = (rank + 1) * chunks / S - k_lo;
   if (tid == 0) {
@@ -559,8 +671,12 @@ __global__ void __launch_bounds__(ads::kThreadsSplit, 1)
       at[0] = v;
     }
   }
-  grid_wait();  // p
+  if (tid == 0) {
+    ctl->pad = wait_ready(p.err, p.p_blocks, p.timeout_ns, 641);
+    if (ctl->pad) leave(p.err, (int)gridDim.x - p.p_blocks);
+  }
   __syncthreads();
+  if (!ctl->pad) return;
   // The adapters' part: item = (tile of 8 tokens of one adapter, group of 16 rows), fragments of B and p
   // fetched two items ahead.
   {
@@ -617,60 +733,60 @@ __global__ void __launch_bounds__(ads::kThreadsSplit, 1)
   }
 }
 
-// Launches `kernel` so that it may start before the launch ahead of it in the stream has finished (it calls
-// griddepcontrol.wait before it reads what that launch wrote).
-template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int threads, int smem, int cluster,
-                             cudaStream_t stream, const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)cluster;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = cluster > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 }  // namespace
 
+// Shares of K of the blocks of p for up to 16 tokens.
+int adapter_gemv_shares(int T, int r) {
+  const int items = T * ((r + 15) / 16);
+  return items <= 16 ? 4 : (items <= 32 ? 2 : 1);
+}
+
 cudaError_t launch_adapter_small(const AdapterProjHost& h, const int32_t* ids, const uint16_t* x, const uint16_t* A,
-                                 const uint16_t* B, uint16_t* low, uint16_t* y, int num_sms, cudaStream_t stream) {
-  const bool few = h.T <= kAdapterGemvTokens;
-  {
-    const SmallProjParams p{ids, x, A, h.scale, low, h.T, h.K, h.n, h.r};
-    LaunchScope scope("adapter_small_proj", stream);
-    adapter_small_proj_kernel<<<h.T * ((h.r + 15) / 16), kProjThreads, 0, stream>>>(p);
-    const cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-  }
-  if (few) {
-    const GemvParams p{ids, x, h.nf4, h.absmax, B, low, y, h.T, h.K, h.N, h.n, h.r};
+                                 const uint16_t* B, void* low, uint16_t* y, int num_sms, cudaStream_t stream) {
+  const int items = h.T * ((h.r + 15) / 16);
+  if (h.T <= kAdapterGemvTokens) {
+    const int kq = adapter_gemv_shares(h.T, h.r);
+    const GemvParams p{ids, x,   h.nf4, h.absmax, A,   B,   h.scale, static_cast<float*>(low), y, h.err, h.timeout_ns,
+                       h.T, h.K, h.N,   h.n,      h.r, kq,  items * kq};
     LaunchScope scope("adapter_gemv", stream);
-    const int grid = (h.N + 15) / 16;
-    return h.T <= kTokenTile ? launch_dependent(adapter_gemv_kernel<1>, grid, kThreads, 0, 0, stream, p)
-                             : launch_dependent(adapter_gemv_kernel<2>, grid, kThreads, 0, 0, stream, p);
+    const int grid = p.p_blocks + (h.N + 15) / 16;
+    if (h.T <= kTokenTile)
+      adapter_gemv_kernel<1><<<grid, kThreads, 0, stream>>>(p);
+    else
+      adapter_gemv_kernel<2><<<grid, kThreads, 0, stream>>>(p);
+    return cudaGetLastError();
   }
   const int NT = (h.T + 15) / 16 * 16, tiles = (h.N + ads::BM - 1) / ads::BM, chunks = h.K / ads::BK;
   // K is split while the blocks fit the GPU at once and every block keeps two chunks.
   int S = 1;
   while (S < 8 && 2 * S * tiles <= num_sms && chunks >= 4 * S) S *= 2;
+  // The blocks of p take the SMs that are left over; where few are, every SM first does a share of p.
+  const int spare = num_sms - tiles * S;
+  int p_blocks = items <= 4 * spare ? spare : num_sms;
+  p_blocks = (p_blocks < items ? p_blocks : items) / S * S;
+  if (p_blocks < S) p_blocks = S;
   CUtensorMap mx;
   cudaError_t err = map_bf16_2d(&mx, x, h.K, h.T, 64, (uint32_t)NT, CU_TENSOR_MAP_SWIZZLE_128B);
   if (err != cudaSuccess) return err;
   const int ring = ads::ring_bytes(NT, S), smem = ring + ads::kBarBytes + ads::kListBytes + 1024;
-  const SplitParams p{h.nf4, h.absmax, B, low, ids, y, h.err, h.timeout_ns, h.T, NT, h.K, h.N, h.n, h.r, ring};
+  const SplitParams p{h.nf4, h.absmax, x,   A,  B,   h.scale, static_cast<uint16_t*>(low), ids, y,    h.err, h.timeout_ns,
+                      h.T,   NT,       h.K, h.N, h.n, h.r,    ring,                        p_blocks};
   LaunchScope scope("adapter_split", stream);
   auto run = [&](auto kernel) -> cudaError_t {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    return e != cudaSuccess ? e
-                            : launch_dependent(kernel, tiles * S, ads::kThreadsSplit, smem, S, stream, mx, p);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p_blocks + tiles * S));
+    cfg.blockDim = dim3(ads::kThreadsSplit);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)S;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, mx, p);
   };
   if (h.r > 32)
     return S == 1   ? run(adapter_split_kernel<1, true>)

@@ -19,7 +19,9 @@ struct DeviceError {
   int code;       // 0 or an e4b_status
   int site;       // which wait gave up (kernel-specific id)
   int block;      // blockIdx.x of the first CTA that gave up
-  int pad[61];    // keeps the rest of the workspace 256-byte aligned
+  int ready;      // (small projection batches) blocks whose p is written; 0 between launches
+  int left;       // blocks that no longer need it; the last one sets both back to 0
+  int pad[59];    // keeps the rest of the workspace 256-byte aligned
 };
 static_assert(sizeof(DeviceError) == 256, "error word block must be 256 bytes");
 

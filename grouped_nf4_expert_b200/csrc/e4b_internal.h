@@ -241,9 +241,11 @@ cudaError_t launch_adapter_gemm(const AdapterProjHost& h, bool mn, const uint16_
                                 const uint16_t* fac, uint16_t* out, int num_sms, cudaStream_t stream);
 cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, const uint16_t* dY, const uint16_t* p,
                                  const uint16_t* q, uint16_t* dA, uint16_t* dB, int num_sms, cudaStream_t stream);
-// y for up to kAdapterSmallTokens tokens in two launches (scratch: low [T, r]).
+// y for up to kAdapterSmallTokens tokens in one launch (scratch: low [T, r] bf16, or for up to kAdapterGemvTokens
+// tokens [adapter_gemv_shares, T, r] float32).
+int adapter_gemv_shares(int T, int r);
 cudaError_t launch_adapter_small(const AdapterProjHost& h, const int32_t* ids, const uint16_t* x, const uint16_t* A,
-                                 const uint16_t* B, uint16_t* low, uint16_t* y, int num_sms, cudaStream_t stream);
+                                 const uint16_t* B, void* low, uint16_t* y, int num_sms, cudaStream_t stream);
 
 // ---- balance loss (balance.cu)
 struct BalanceHost {

@@ -85,7 +85,11 @@ e4b_status e4b_adapter_group(const e4b_proj_dims *dims, int32_t T, const int32_t
 /* Serving forward for any T, from one token up: y (bf16 [T, N]) for x (bf16
  * [T, K]) and ids, with nothing kept for a backward.  Needs no grouping by the
  * caller.  Its scratch lives in ws, so two calls that share a workspace must
- * not overlap on the GPU.  Allocates nothing and never synchronises: it can be
+ * not overlap on the GPU.  Batches of at most 256 tokens keep two counters in
+ * the first 256 bytes of ws, which must be 0 before the first call (as
+ * e4b_workspace_init leaves them) and are 0 again after each; a call that ended
+ * in E4B_ERR_DEVICE_TIMEOUT may leave them otherwise, until the workspace is
+ * initialised again.  Allocates nothing and never synchronises: it can be
  * captured into a CUDA graph. */
 e4b_status e4b_multi_lora_serve_fwd(const e4b_proj_dims *dims, int32_t T, const int32_t *ids, const e4b_bf16 *x,
                                     const e4b_nf4_matrix *base, const e4b_adapter_factors *adapters, e4b_bf16 *y,
