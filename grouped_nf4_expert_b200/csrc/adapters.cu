@@ -16,7 +16,10 @@ constexpr uint32_t kFull = 0xffffffffu;
 // Every warp owns a contiguous run of tokens and a histogram row of its own in
 // shared memory; lanes with equal ids find one another with a warp match, so
 // that there are no shared-memory atomics and the order is fixed.  Two passes
-// over the ids (count, place) around one scan over the adapters.
+// over the ids (count, place) around one scan over the adapters, thread a owning
+// adapter a.  Latency bounds it (one read of the ids and a dozen block-wide
+// steps), so the scan's three sums go through one barrier and the histogram is
+// read once, all warps' rows at a time.
 // ----------------------------------------------------------------------------
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupWarps = kGroupThreads / 32;
@@ -26,136 +29,125 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
                          int32_t* __restrict__ offsets, int32_t* __restrict__ steps) {
   extern __shared__ int32_t table[];  // [kGroupWarps][n + 1]
   __shared__ int32_t wsum[3][kGroupWarps];
+  __shared__ int32_t none_total;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cols = n + 1;
-  for (int i = tid; i < kGroupWarps * cols; i += kGroupThreads) table[i] = 0;
-  __syncthreads();
   const int per = ((T + kGroupWarps - 1) / kGroupWarps + 31) / 32 * 32;
   const int t0 = min(T, warp * per), t1 = min(T, t0 + per);
   int32_t* mine = table + warp * cols;
   auto adapter_of = [&](int t) -> int {
+    if (t >= t1) return -1;
     const uint32_t a = (uint32_t)__ldg(ids + t);
     return a < (uint32_t)n ? (int)a : n;
   };
-  int next = t0 + lane < t1 ? adapter_of(t0 + lane) : -1;
+  int next = adapter_of(t0 + lane);
+  const int first = next;
+  for (int i = lane; i < cols; i += 32) mine[i] = 0;
+  __syncwarp();
   for (int tb = t0; tb < t1; tb += 32) {
     const int a = next;
-    if (tb + 32 + lane < t1)
-      next = adapter_of(tb + 32 + lane);
-    else
-      next = -1;
+    next = adapter_of(tb + 32 + lane);
     const uint32_t same = __match_any_sync(kFull, a);
     if (a >= 0 && (same & ((1u << lane) - 1)) == 0) mine[a] += __popc(same);
     __syncwarp();
   }
   __syncthreads();
-  // Scan over the adapters (thread a owns adapter a): rows padded to 16, the
-  // 256-row units its rows meet, and its 128-row projection tasks.
+  // Adapter tid: its tokens in each warp, its rows padded to 16, the 256-row units they meet and its 128-row
+  // projection tasks.
+  int at[kGroupWarps];
   int count = 0;
-  if (tid < n)
-    for (int w = 0; w < kGroupWarps; ++w) count += table[w * cols + tid];
-  const int padded = (count + 15) / 16 * 16;
-  auto block_scan = [&](int v, int which) -> int {  // exclusive prefix over the block
-    int x = v;
+#pragma unroll
+  for (int w = 0; w < kGroupWarps; ++w) {
+    const int c = tid < n ? table[w * cols + tid] : 0;
+    at[w] = count;
+    count += c;
+  }
+  if (warp == kGroupWarps - 1) {  // the tokens without an adapter: their places, from the end of the adapters' rows
+    const int c = table[lane * cols + n];
+    int x = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(kFull, x, o);
       if (lane >= o) x += y;
     }
-    if (lane == 31) wsum[which][warp] = x;
-    __syncthreads();
-    int base = 0;
-    for (int w = 0; w < warp; ++w) base += wsum[which][w];
-    return base + x - v;
-  };
-  auto block_total = [&](int which) -> int {
-    int s = 0;
-    for (int w = 0; w < kGroupWarps; ++w) s += wsum[which][w];
-    return s;
-  };
-  const int start = block_scan(padded, 0), end = start + padded;
-  const int u0 = start / kAdapterUnitRows, u1 = padded ? (end - 1) / kAdapterUnitRows : u0 - 1;
-  const int entry0 = block_scan(u1 - u0 + 1, 1);
+    table[lane * cols + n] = x - c;
+    if (lane == 31) none_total = x;
+  }
+  const int padded = (count + 15) / 16 * 16;
   const int ntask = (padded + kAdapterTaskRows - 1) / kAdapterTaskRows;
-  const int task0 = block_scan(ntask, 2);
-  const int none0 = block_total(0), entries = block_total(1), adapter_tasks = block_total(2);
-  int nnone = 0;
-  for (int w = 0; w < kGroupWarps; ++w) nnone += table[w * cols + n];
-  const int none_tasks = (nnone + kAdapterTaskRows - 1) / kAdapterTaskRows;
-  const int used = none0 + nnone;
-  const int units = (used + kAdapterUnitRows - 1) / kAdapterUnitRows;
+  auto warp_scan = [&](int v) -> int {  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, v, o);
+      if (lane >= o) v += y;
+    }
+    return v;
+  };
+  const int in_rows = warp_scan(padded), in_tasks = warp_scan(ntask);
+  if (lane == 31) {
+    wsum[0][warp] = in_rows;
+    wsum[1][warp] = in_tasks;
+  }
+  __syncthreads();
+  auto before = [&](int which, int& total) -> int {  // sum of the warps ahead of this one, and of all
+    const int v = wsum[which][lane], x = warp_scan(v);
+    total = __shfl_sync(kFull, x, 31);
+    return __shfl_sync(kFull, x - v, warp);
+  };
+  int none0, adapter_tasks, entries;
+  const int start = before(0, none0) + in_rows - padded, end = start + padded;
+  const int task0 = before(1, adapter_tasks) + in_tasks - ntask;
+  const int u0 = start / kAdapterUnitRows, u1 = padded ? (end - 1) / kAdapterUnitRows : u0 - 1;
+  const int in_entries = warp_scan(u1 - u0 + 1);
+  if (lane == 31) wsum[2][warp] = in_entries;
+  const int nnone = none_total, none_tasks = (nnone + kAdapterTaskRows - 1) / kAdapterTaskRows;
+  const int used = none0 + nnone, units = (used + kAdapterUnitRows - 1) / kAdapterUnitRows;
   const AdapterSteps lay = adapter_steps_layout(rows_cap, n);
   int32_t* unit_start = steps + lay.unit_start;
-  for (int u = tid; u <= rows_cap / kAdapterUnitRows; u += kGroupThreads) unit_start[u] = entries;
+  if (tid < n) {  // where each warp's tokens of this adapter start
+#pragma unroll
+    for (int w = 0; w < kGroupWarps; ++w) table[w * cols + tid] = start + at[w];
+  }
   __syncthreads();
+  const int entry0 = before(2, entries) + in_entries - (u1 - u0 + 1);
   if (tid < n) {
     offsets[tid] = start;
-    for (int u = u0; u <= u1; ++u) {
-      const int i = entry0 + u - u0;
-      int32_t* en = steps + lay.entries + 4 * i;
-      en[0] = tid;
-      en[1] = u;
-      en[2] = start;
-      en[3] = end;
-      if (start <= u * kAdapterUnitRows) unit_start[u] = i;  // the first adapter with rows in unit u
-    }
-    for (int i = 0; i < ntask; ++i) {
-      int32_t* tk = steps + lay.tasks + 4 * (task0 + i);
-      tk[0] = tid;
-      tk[1] = start + i * kAdapterTaskRows;
-      tk[2] = end;
-      tk[3] = 0;
-    }
+    int4* en = reinterpret_cast<int4*>(steps + lay.entries) + entry0;
+    for (int u = u0; u <= u1; ++u) en[u - u0] = make_int4(tid, u, start, end);
+    // a unit's first entry: the adapter with its first row
+    for (int u = (start + kAdapterUnitRows - 1) / kAdapterUnitRows; u <= u1; ++u) unit_start[u] = entry0 + u - u0;
+    int4* tk = reinterpret_cast<int4*>(steps + lay.tasks) + task0;
+    for (int i = 0; i < ntask; ++i) tk[i] = make_int4(tid, start + i * kAdapterTaskRows, end, 0);
     for (int i = start + count; i < end; ++i) order[i] = T;  // padding rows
-    // where each warp's tokens of this adapter start
-    int at = start;
-    for (int w = 0; w < kGroupWarps; ++w) {
-      const int c = table[w * cols + tid];
-      table[w * cols + tid] = at;
-      at += c;
-    }
   }
   if (tid == 0) {
     steps[0] = units;
     steps[1] = used;
     steps[2] = entries;
     steps[3] = adapter_tasks + none_tasks;
-    int32_t* en = steps + lay.entries + 4 * entries;  // sentinel
-    en[0] = -1;
-    en[1] = -1;
-    en[2] = en[3] = 0;
+    reinterpret_cast<int4*>(steps + lay.entries)[entries] = make_int4(-1, -1, 0, 0);  // sentinel
     offsets[n] = none0;
     offsets[n + 1] = used;
-    int at = none0;
-    for (int w = 0; w < kGroupWarps; ++w) {
-      const int c = table[w * cols + n];
-      table[w * cols + n] = at;
-      at += c;
-    }
   }
-  for (int i = tid; i < none_tasks; i += kGroupThreads) {
-    int32_t* tk = steps + lay.tasks + 4 * (adapter_tasks + i);
-    tk[0] = n;
-    tk[1] = none0 + i * kAdapterTaskRows;
-    tk[2] = used;
-    tk[3] = 0;
-  }
+  // units past the adapters' rows have no entries
+  for (int u = (none0 + kAdapterUnitRows - 1) / kAdapterUnitRows + tid; u <= rows_cap / kAdapterUnitRows;
+       u += kGroupThreads)
+    unit_start[u] = entries;
+  for (int i = tid; i < none_tasks; i += kGroupThreads)
+    reinterpret_cast<int4*>(steps + lay.tasks)[adapter_tasks + i] =
+        make_int4(n, none0 + i * kAdapterTaskRows, used, 0);
   for (int i = used + tid; i < rows_cap; i += kGroupThreads) order[i] = T;
-  __syncthreads();
-  next = t0 + lane < t1 ? adapter_of(t0 + lane) : -1;
+  next = first;
   for (int tb = t0; tb < t1; tb += 32) {
     const int a = next;
-    if (tb + 32 + lane < t1)
-      next = adapter_of(tb + 32 + lane);
-    else
-      next = -1;
+    next = adapter_of(tb + 32 + lane);
     const uint32_t same = __match_any_sync(kFull, a);
-    const int before = __popc(same & ((1u << lane) - 1));
+    const int rank = __popc(same & ((1u << lane) - 1));
     const int base = a >= 0 ? mine[a] : 0;
     __syncwarp();
     if (a >= 0) {
-      order[base + before] = tb + lane;
-      if (before == 0) mine[a] = base + __popc(same);
+      order[(a == n ? none0 : 0) + base + rank] = tb + lane;
+      if (rank == 0) mine[a] = base + __popc(same);
     }
     __syncwarp();
   }
