@@ -56,6 +56,45 @@ __device__ __forceinline__ uint32_t rows_off(int lo, int hi, int w) {
   return ~(below_b & ~below_a);
 }
 
+// Shares of a 128 x r_pad accumulator over a cluster of S blocks that split its reduction: block b owns rows
+// [128 b / S, 128 (b + 1) / S).  push_share: an epilogue warp stores its 32 TMEM lanes (zeros unless `live`)
+// into the owners' shared memory, [share][row][column]; sum_share adds four columns of an owned row in share
+// order.
+constexpr int kSharePad = 4;
+constexpr int share_bytes(int r_pad) { return 128 * (r_pad + kSharePad) * 4; }
+__device__ __forceinline__ void push_share(uint8_t* smem, uint32_t tmem, int quarter, int lane, int S, int rank,
+                                           int r_pad, bool live) {
+  const int rows = 128 / S, row = 32 * quarter + lane, pitch = r_pad + kSharePad;
+  const uint32_t to = mapa_shared(smem_u32(smem) + (uint32_t)(((rank * rows + row % rows) * pitch) * 4),
+                                  (uint32_t)(row / rows));
+  for (int j = 0; j < r_pad; j += 16) {
+    float v[16];
+    if (live) {
+      tmem_ld16(tmem + j + ((uint32_t)(32 * quarter) << 16), v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to + (uint32_t)((j + 4 * i) * 4)),
+                   "f"(v[4 * i]), "f"(v[4 * i + 1]), "f"(v[4 * i + 2]), "f"(v[4 * i + 3])
+                   : "memory");
+  }
+}
+__device__ __forceinline__ float4 sum_share(const uint8_t* smem, int S, int row, int j, int r_pad) {
+  const int rows = 128 / S, pitch = r_pad + kSharePad;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int s = 0; s < S; ++s) {
+    const float4 w = *reinterpret_cast<const float4*>(smem + ((s * rows + row) * pitch + j) * 4);
+    v.x += w.x;
+    v.y += w.y;
+    v.z += w.z;
+    v.w += w.w;
+  }
+  return v;
+}
+
 // Waits (with the limit) until the copies this role issued have landed, before its shared memory goes away.
 __device__ __forceinline__ void let_land(uint64_t* bars, int n, uint32_t issued, uint32_t last_par,
                                          long long timeout_ns) {
@@ -533,6 +572,7 @@ constexpr int kThreads = 11 * 32;
 constexpr int kAccCols = 64;
 constexpr int kTmemCols = 2 * kAccCols;
 static_assert(STAGE_BYTES % 1024 == 0, "stage alignment");
+static_assert(share_bytes(E4B_MAX_RANK) <= STAGES * STAGE_BYTES, "the shares fit the stages");
 static_assert(kAdapterTaskRows == BM, "a task is one tile");
 }  // namespace adp
 
@@ -545,9 +585,11 @@ struct AdapterRowsParams {
   DeviceError* err;
   long long timeout_ns;
   int R, T, n, r, r_pad, tasks;  // tasks: place of the task list in `steps`
+  int S;                         // blocks of a cluster, each a share of R
 };
 
-// F = A [n, r, R] (K-major), or B [n, R, r] (W_MN).
+// F = A [n, r, R] (K-major), or B [n, R, r] (W_MN).  With few tasks R is split over the blocks of a cluster: one
+// block's chain of chunks would be the launch's time (13 tasks of R = 2048: 21 us).
 template <bool W_MN>
 __global__ void __launch_bounds__(adp::kThreads, 2)
     adapter_proj_kernel(const __grid_constant__ CUtensorMap map_dst, const __grid_constant__ CUtensorMap map_w,
@@ -589,15 +631,18 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
   const uint32_t tmem = *tmem_slot;
   const int n_tasks = p.steps[3];
   const int4* tasks = reinterpret_cast<const int4*>(p.steps + p.tasks);  // (adapter, first row, end row, 0)
-  const int kchunks = (p.R + BK - 1) / BK;
+  const int chunks = (p.R + BK - 1) / BK, rank = (int)blockIdx.x % p.S;
+  const int k_lo = rank * chunks / p.S, k_hi = (rank + 1) * chunks / p.S;  // this block's chunks of R
+  const int u0 = (int)blockIdx.x / p.S, u_step = (int)gridDim.x / p.S;     // S > 1: one task a cluster
   const uint32_t b_bytes = BK * p.r_pad * 2;
+  bool done = false;  // (epilogue warps, S > 1) the accumulator is complete
 
   if (warp < kLoadWarps) {
     // rows 32 warp + 4 i + lane / 8 of the tile, 16-byte piece lane % 8 of their 128
     const int c = lane & 7;
     uint32_t s = 0, ph = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < n_tasks && ok; u += gridDim.x) {
+    for (int u = u0; u < n_tasks && ok; u += u_step) {
       const int4 tk = __ldg(tasks + u);
       const uint16_t* src[8];
       bool live[8];
@@ -608,7 +653,7 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
         live[i] = t < p.T;
         src[i] = p.src + (live[i] ? (size_t)t * p.R : 0) + 8 * c;
       }
-      for (int kc = 0; kc < kchunks; ++kc) {
+      for (int kc = k_lo; kc < k_hi; ++kc) {
         if (!(ok = __all_sync(kFull, mbar_wait(&empty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 411)))) break;
         if (!(ok = __all_sync(kFull, mbar_wait(&stored[s], ph ^ 1, ctl, p.err, p.timeout_ns, 412)))) break;
         uint8_t* tile = smem + s * STAGE_BYTES;
@@ -633,9 +678,9 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
       tma_prefetch_desc(&map_w);
       uint32_t s = 0, ph = 0, issued = 0, last_par = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < n_tasks && ok; u += gridDim.x) {
+      for (int u = u0; u < n_tasks && ok; u += u_step) {
         const int a = __ldg(tasks + u).x;
-        for (int kc = 0; kc < kchunks; ++kc) {
+        for (int kc = k_lo; kc < k_hi; ++kc) {
           if (!(ok = mbar_wait(&empty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 413))) break;
           uint8_t* st = smem + s * STAGE_BYTES + A_BYTES;
           if (a < p.n) {
@@ -663,13 +708,13 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
       const uint32_t wswz = swz_for_row_bytes(2 * p.r_pad);
       uint32_t s = 0, ph = 0, ti = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < n_tasks && ok; u += gridDim.x, ++ti) {
+      for (int u = u0; u < n_tasks && ok; u += u_step, ++ti) {
         const bool project = __ldg(tasks + u).x < p.n;
         const uint32_t b = ti & 1, use = ti >> 1;
         if (!(ok = mbar_wait(&accempty[b], (use & 1) ^ 1, ctl, p.err, p.timeout_ns, 420))) break;
         tc_fence_after();
         const uint32_t acc = tmem + b * kAccCols;
-        for (int kc = 0; kc < kchunks; ++kc) {
+        for (int kc = k_lo; kc < k_hi; ++kc) {
           if (!(ok = mbar_wait(&full[s], ph, ctl, p.err, p.timeout_ns, 421))) break;
           fence_proxy_async_smem();  // the rows were written by cp.async
           tc_fence_after();
@@ -680,7 +725,7 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
               const uint64_t ad = make_sdesc(a0 + 32 * kk, 16, 1024, kSw128);
               const uint64_t bd = W_MN ? make_sdesc(b0 + 32 * p.r_pad * kk, b_bytes, 16 * p.r_pad, wswz)
                                        : make_sdesc(b0 + 32 * kk, 16, 1024, kSw128);
-              umma_bf16(acc, ad, bd, idesc, (kc > 0 || kk > 0) ? 1u : 0u);
+              umma_bf16(acc, ad, bd, idesc, (kc > k_lo || kk > 0) ? 1u : 0u);
             }
           }
           umma_commit(&empty[s]);
@@ -703,10 +748,10 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
       tma_prefetch_desc(&map_dst);
       uint32_t s = 0, ph = 0, prev = 0;
       bool ok = true, pending = false;
-      for (int u = blockIdx.x; u < n_tasks && ok; u += gridDim.x) {
+      for (int u = u0; u < n_tasks && ok; u += u_step) {
         const int4 tk = __ldg(tasks + u);
         const int granules = (min(BM, tk.z - tk.y) + 15) / 16;
-        for (int kc = 0; kc < kchunks; ++kc) {
+        for (int kc = k_lo; kc < k_hi; ++kc) {
           if (!(ok = mbar_wait(&full[s], ph, ctl, p.err, p.timeout_ns, 415))) break;
           fence_proxy_async_smem();
           for (int g = 0; g < granules; ++g)
@@ -731,7 +776,7 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
     const int q = ((warp & 3) << 5) | lane;  // TMEM lane of this thread
     uint32_t ti = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < n_tasks && ok; u += gridDim.x, ++ti) {
+    for (int u = u0; u < n_tasks && ok; u += u_step, ++ti) {
       const int4 tk = __ldg(tasks + u);
       const bool project = tk.x < p.n;
       const float sc = project ? __ldg(p.scale + tk.x) : 0.0f;
@@ -741,6 +786,10 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
       ok = __all_sync(kFull, mbar_wait(&accfull[b], use & 1, ctl, p.err, p.timeout_ns, 430));
       if (!ok) break;
       tc_fence_after();
+      if (p.S > 1) {
+        done = project;
+        break;
+      }
 #pragma unroll 1
       for (int j = 0; project && j < p.r_pad; j += 16) {
         float v[16];
@@ -760,7 +809,28 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
     }
   }
   __syncwarp();
-  __syncthreads();
+  if (p.S > 1) {
+    cluster_sync();  // no block's copies or UMMAs use its shared memory any more
+    if (done) push_share(smem, tmem, warp & 3, lane, p.S, rank, p.r_pad, true);
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();  // every share is in place
+    const int4 tk = u0 < n_tasks ? __ldg(tasks + u0) : make_int4(p.n, 0, 0, 0);
+    const int rows = BM / p.S;
+    if (tk.x < p.n && !ctl->abort) {
+      const float sc = __ldg(p.scale + tk.x);
+      for (int i = threadIdx.x; i < rows * (p.r / 4); i += kThreads) {
+        const int row = i / (p.r / 4), j = 4 * (i % (p.r / 4)), to = tk.y + rank * rows + row;
+        if (to < tk.z) {
+          const float4 v = sum_share(smem, p.S, row, j, p.r_pad);
+          *reinterpret_cast<uint2*>(p.out + (size_t)to * p.r + j) =
+              make_uint2(pack_bf16x2(sc * v.x, sc * v.y), pack_bf16x2(sc * v.z, sc * v.w));
+        }
+      }
+    }
+  } else {
+    __syncthreads();
+  }
   if (warp == kIssueWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
@@ -793,10 +863,12 @@ struct AdapterWgradParams {
   DeviceError* err;
   long long timeout_ns;
   int T, n, r, r_pad;
+  int S;  // blocks of a cluster, each a share of an adapter's rows
 };
 
 struct AdapterWgradUnit {
-  int g, ft, a, row0, rows;
+  int g, ft, a, row0, rows;  // rows: all of the adapter's
+  int k_lo, k_hi;            // this block's 64-row chunks of them
 };
 __device__ __forceinline__ AdapterWgradUnit adapter_wgrad_unit(const AdapterWgradParams& p, int u) {
   AdapterWgradUnit w;
@@ -807,6 +879,9 @@ __device__ __forceinline__ AdapterWgradUnit adapter_wgrad_unit(const AdapterWgra
   if (w.g) w.ft -= p.n_ft[0];
   w.row0 = __ldg(p.offsets + w.a);
   w.rows = __ldg(p.offsets + w.a + 1) - w.row0;  // a multiple of 16
+  const int chunks = (w.rows + adw::BK - 1) / adw::BK, rank = (int)blockIdx.x % p.S;
+  w.k_lo = rank * chunks / p.S;
+  w.k_hi = (rank + 1) * chunks / p.S;
   return w;
 }
 
@@ -848,13 +923,15 @@ __global__ void __launch_bounds__(adw::kThreads, 2)
   const uint32_t tmem = *tmem_slot;
   const int n_units = p.n * (p.n_ft[0] + p.n_ft[1]);
   const uint32_t b_bytes = BK * p.r_pad * 2;
+  const int u0 = (int)blockIdx.x / p.S, u_step = (int)gridDim.x / p.S;  // S > 1: one unit a cluster
+  bool done = false;  // (epilogue warps, S > 1) the accumulator is complete
 
   if (warp < kLoadWarps) {
     // rows 16 warp + 4 (i % 4) + lane / 8 of the chunk, feature half i / 4, 16-byte piece lane % 8
     const int c = lane & 7;
     uint32_t s = 0, ph = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
+    for (int u = u0; u < n_units && ok; u += u_step) {
       const AdapterWgradUnit w = adapter_wgrad_unit(p, u);
       const uint16_t* act = w.g ? p.act[1] : p.act[0];
       const int F = w.g ? p.F[1] : p.F[0];
@@ -867,8 +944,8 @@ __global__ void __launch_bounds__(adw::kThreads, 2)
         }
       };
       int t[4];
-      tokens(0, t);
-      for (int kc = 0; kc * BK < w.rows; ++kc) {
+      tokens(w.k_lo, t);
+      for (int kc = w.k_lo; kc < w.k_hi; ++kc) {
         if (!(ok = __all_sync(kFull, mbar_wait(&empty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 510)))) break;
         uint8_t* tile = smem + s * STAGE_BYTES;
 #pragma unroll
@@ -891,10 +968,10 @@ __global__ void __launch_bounds__(adw::kThreads, 2)
     if (lane == 0) {
       uint32_t s = 0, ph = 0, issued = 0, last_par = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
+      for (int u = u0; u < n_units && ok; u += u_step) {
         const AdapterWgradUnit w = adapter_wgrad_unit(p, u);
         const CUtensorMap* low = w.g ? &low1 : &low0;
-        for (int kc = 0; kc * BK < w.rows; ++kc) {
+        for (int kc = w.k_lo; kc < w.k_hi; ++kc) {
           if (!(ok = mbar_wait(&empty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 511))) break;
           mbar_arrive_expect_tx(&full[s], b_bytes);
           tma_load_2d(smem + s * STAGE_BYTES + A_BYTES, low, &full[s], 0, w.row0 + kc * BK);
@@ -915,13 +992,13 @@ __global__ void __launch_bounds__(adw::kThreads, 2)
       int s = 0;
       uint32_t ph = 0, ti = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++ti) {
+      for (int u = u0; u < n_units && ok; u += u_step, ++ti) {
         const AdapterWgradUnit w = adapter_wgrad_unit(p, u);
         const uint32_t b = ti & 1, use = ti >> 1;
         if (!(ok = mbar_wait(&accempty[b], (use & 1) ^ 1, ctl, p.err, p.timeout_ns, 520))) break;
         tc_fence_after();
         const uint32_t acc = tmem + b * kAccCols;
-        for (int kc = 0; kc * BK < w.rows; ++kc) {
+        for (int kc = w.k_lo; kc < w.k_hi; ++kc) {
           if (!(ok = mbar_wait(&full[s], ph, ctl, p.err, p.timeout_ns, 521))) break;
           fence_proxy_async_smem();  // the rows were written by cp.async
           tc_fence_after();
@@ -930,7 +1007,7 @@ __global__ void __launch_bounds__(adw::kThreads, 2)
           for (int kk = 0; kk < steps; ++kk) {
             const uint64_t ad = make_sdesc(a0 + 2048 * kk, A_BYTES / 2, 1024, kSw128);
             const uint64_t bd = make_sdesc(b0 + 32 * p.r_pad * kk, b_bytes, 16 * p.r_pad, lswz);
-            umma_bf16(acc, ad, bd, idesc, (kc > 0 || kk > 0) ? 1u : 0u);
+            umma_bf16(acc, ad, bd, idesc, (kc > w.k_lo || kk > 0) ? 1u : 0u);
           }
           umma_commit(&empty[s]);
           if (++s == STAGES) {
@@ -950,13 +1027,17 @@ __global__ void __launch_bounds__(adw::kThreads, 2)
     const int q = ((warp & 3) << 5) | lane;
     uint32_t ti = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++ti) {
+    for (int u = u0; u < n_units && ok; u += u_step, ++ti) {
       const AdapterWgradUnit w = adapter_wgrad_unit(p, u);
       const uint32_t b = ti & 1, use = ti >> 1;
       const uint32_t tl = tmem + b * kAccCols + ((uint32_t)(32 * (warp & 3)) << 16);
       ok = __all_sync(kFull, mbar_wait(&accfull[b], use & 1, ctl, p.err, p.timeout_ns, 530));
       if (!ok) break;
       tc_fence_after();
+      if (p.S > 1) {
+        done = true;
+        break;
+      }
       const int F = p.F[w.g], m = w.ft * BM + q;
       uint16_t* out = p.out[w.g];
 #pragma unroll 1
@@ -992,7 +1073,37 @@ __global__ void __launch_bounds__(adw::kThreads, 2)
     }
   }
   __syncwarp();
-  __syncthreads();
+  if (p.S > 1) {
+    const AdapterWgradUnit w = adapter_wgrad_unit(p, u0);  // the grid holds n_units clusters
+    const int rank = (int)blockIdx.x % p.S, rows = BM / p.S, F = w.g ? p.F[1] : p.F[0];
+    cluster_sync();  // no block's copies or UMMAs use its shared memory any more
+    if (done) push_share(smem, tmem, warp & 3, lane, p.S, rank, p.r_pad, w.k_hi > w.k_lo);
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();  // every share is in place
+    if (!ctl->abort) {
+      const int m0 = w.ft * BM + rank * rows;
+      uint16_t* out = w.g ? p.out[1] : p.out[0];
+      for (int i = threadIdx.x; i < rows * (p.r / 4); i += kThreads) {
+        // neighbouring threads: neighbouring ranks of dB [N, r], neighbouring features of dA [r, K]
+        const int row = w.g ? i / (p.r / 4) : i % rows, j = 4 * (w.g ? i % (p.r / 4) : i / rows), m = m0 + row;
+        if (m >= F) continue;
+        const float4 v = sum_share(smem, p.S, row, j, p.r_pad);
+        const uint32_t lo = pack_bf16x2(v.x, v.y), hi = pack_bf16x2(v.z, v.w);
+        if (w.g) {
+          *reinterpret_cast<uint2*>(out + ((size_t)w.a * F + m) * p.r + j) = make_uint2(lo, hi);
+        } else {
+          uint16_t* d = out + ((size_t)w.a * p.r + j) * F + m;
+          d[0] = (uint16_t)lo;
+          d[F] = (uint16_t)(lo >> 16);
+          d[2 * (size_t)F] = (uint16_t)hi;
+          d[3 * (size_t)F] = (uint16_t)(hi >> 16);
+        }
+      }
+    }
+  } else {
+    __syncthreads();
+  }
   if (warp == kIssueWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
@@ -1008,6 +1119,26 @@ int rank_padded(int r) { return r <= 16 ? 16 : (r <= 32 ? 32 : 64); }
 template <typename K>
 cudaError_t set_smem(K kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// Launches clusters of S blocks.
+template <typename... Params, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(Params...), int grid, int threads, int smem, int S, cudaStream_t stream,
+                            const Args&... args) {
+  const cudaError_t err = set_smem(kernel, smem);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)S;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // 2-D byte matrix [rows, bytes].
@@ -1092,17 +1223,16 @@ cudaError_t launch_adapter_rows(const AdapterProjHost& h, bool mn, const uint16_
   p.r = h.r;
   p.r_pad = rp;
   p.tasks = adapter_steps_layout(h.rows_cap, h.n).tasks;
-  const int64_t cap = h.rows_cap / kAdapterTaskRows + h.n + 1;
-  const int grid = (int)(cap < 2 * num_sms ? cap : 2 * num_sms);
+  // two blocks an SM; R is split while all clusters fit at once and every block keeps two chunks
+  const int64_t cap = h.rows_cap / kAdapterTaskRows + h.n + 1, fit = 2 * (int64_t)num_sms;
+  const int chunks = (R + adp::BK - 1) / adp::BK;
+  p.S = 1;
+  while (p.S < 8 && 2 * p.S * cap <= fit && chunks >= 4 * p.S) p.S *= 2;
+  const int grid = p.S * (int)(cap < fit / p.S ? cap : fit / p.S);
   LaunchScope scope(mn ? "adapter_proj_dy" : "adapter_proj_x", stream);
-  if (mn) {
-    if ((err = set_smem(adapter_proj_kernel<true>, adp::SMEM_BYTES)) != cudaSuccess) return err;
-    adapter_proj_kernel<true><<<grid, adp::kThreads, adp::SMEM_BYTES, stream>>>(ms, mw, p);
-  } else {
-    if ((err = set_smem(adapter_proj_kernel<false>, adp::SMEM_BYTES)) != cudaSuccess) return err;
-    adapter_proj_kernel<false><<<grid, adp::kThreads, adp::SMEM_BYTES, stream>>>(ms, mw, p);
-  }
-  return cudaGetLastError();
+  return mn ? launch_clusters(adapter_proj_kernel<true>, grid, adp::kThreads, adp::SMEM_BYTES, p.S, stream, ms, mw, p)
+            : launch_clusters(adapter_proj_kernel<false>, grid, adp::kThreads, adp::SMEM_BYTES, p.S, stream, ms, mw,
+                              p);
 }
 
 cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, const uint16_t* dY, const uint16_t* p_low,
@@ -1130,13 +1260,14 @@ cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, co
   p.n = h.n;
   p.r = h.r;
   p.r_pad = rp;
-  const int64_t units = (int64_t)h.n * (p.n_ft[0] + p.n_ft[1]);
-  const int64_t cap = (int64_t)num_sms * 2;
-  const int grid = (int)(units < cap ? units : cap);
-  if ((err = set_smem(adapter_wgrad_kernel, adw::SMEM_BYTES)) != cudaSuccess) return err;
+  // Rows are split over clusters where that fills the GPU twice over (adapters have unequal numbers of rows) and
+  // leaves a block four chunks of an even share.
+  const int64_t units = (int64_t)h.n * (p.n_ft[0] + p.n_ft[1]), cap = (int64_t)num_sms * 2;
+  p.S = 1;
+  while (p.S < 8 && 2 * p.S * units <= 2 * cap && h.T / h.n >= 8 * p.S * adw::BK) p.S *= 2;
+  const int grid = (int)(p.S > 1 ? units * p.S : (units < cap ? units : cap));
   LaunchScope scope("adapter_wgrad", stream);
-  adapter_wgrad_kernel<<<grid, adw::kThreads, adw::SMEM_BYTES, stream>>>(mq, mp, p);
-  return cudaGetLastError();
+  return launch_clusters(adapter_wgrad_kernel, grid, adw::kThreads, adw::SMEM_BYTES, p.S, stream, mq, mp, p);
 }
 
 }  // namespace e4b
