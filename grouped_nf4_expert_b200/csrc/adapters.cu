@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
     __syncwarp();
   }
   __syncthreads();
-  // Adapter tid: its tokens in each warp, its rows padded to 16, the 256-row units they meet and its 128-row
+  // Adapter tid: its tokens in each warp, its padded rows, the 256-row units they meet and its 128-row
   // projection tasks.
   int at[kGroupWarps];
   int count = 0;
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
     table[lane * cols + n] = x - c;
     if (lane == 31) none_total = x;
   }
-  const int padded = (count + 15) / 16 * 16;
+  const int padded = (count + kAdapterRowAlign - 1) / kAdapterRowAlign * kAdapterRowAlign;
   const int ntask = (padded + kAdapterTaskRows - 1) / kAdapterTaskRows;
   auto warp_scan = [&](int v) -> int {  // inclusive
 #pragma unroll

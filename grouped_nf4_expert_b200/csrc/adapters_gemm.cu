@@ -1,28 +1,29 @@
 // Large batches of the NF4 projection with adapters of many requests, on the
 // 5th-generation tensor cores:
 //
-//  * adapter_gemm_kernel: persistent CTA pairs, one 256-row x 256-column
-//    output tile per work unit (cta_group::2 UMMAs): base product with the
-//    NF4 matrix decoded into shared memory, then one K = r step per adapter
-//    with rows in the tile, written to that adapter's rows only.
+//  * adapter_fwd_kernel, adapter_dgrad_kernel: persistent CTA pairs, 256 token
+//    rows x 256 outputs per work unit (cta_group::2 UMMAs): the base product with
+//    the NF4 matrix decoded on the way, then one K = r step per adapter with rows
+//    in the tile, written to that adapter's rows only.
 //  * adapter_proj_kernel: p = s x A^T and q = s dY B, 128 rows of one adapter
 //    at a time.
 //  * adapter_wgrad_kernel: dA = q^T x and dB = dY^T p, K = the rows of one
 //    adapter.
 //
 // Rows are the tokens sorted by adapter; every adapter's rows start at a
-// multiple of 16, the K step of one UMMA, so that the gradient products never
-// multiply two adapters' rows.  The projection kernel gathers the token rows
+// multiple of 32: the column granule of a pair UMMA (forward), and two K steps of
+// a UMMA, so that the gradient products never multiply two adapters' rows.  The projection kernel gathers the token rows
 // (cp.async, 16 bytes a lane) and stores them in row order in passing, for the
 // base product to load as plain tiles.  TMA gathers by row index
 // (tile::gather4) were measured instead: about 77 cycles for every four rows
 // of 128 bytes, 5 times the time of the UMMAs they feed (T = 16384, K = 4096,
 // N = 14336: 4204 us against 1960 us with the copy).
 //
-// The adapters of a tile share its accumulator: each K = r step names the
-// TMEM lanes (rows) it must not write (the disable-output-lane operand), so
-// the rows need not be split into tiles by adapter, and nothing an adapter or
-// a token holds reaches another request's rows.
+// The adapters of a tile share its accumulator: each K = r step is issued at the
+// adapter's own accumulator columns (forward) or names the TMEM lanes it must not
+// write (input gradient: the disable-output-lane operand), so the rows need not
+// be split into tiles by adapter, and nothing an adapter or a token holds reaches
+// another request's rows.
 #include <math.h>
 
 #include "e4b_device.cuh"
@@ -45,6 +46,19 @@ __device__ __forceinline__ void umma_bf16_2sm_masked(uint32_t d_tmem, uint64_t a
       "}\n" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]), "r"(off[4]), "r"(off[5]),
       "r"(off[6]), "r"(off[7])
+      : "memory");
+}
+
+// The pair UMMA with the M operand in tensor memory (each CTA's 128 rows in its own).
+__device__ __forceinline__ void umma_bf16_2sm_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                                 uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n"
+      "}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -109,14 +123,481 @@ __device__ __forceinline__ void let_land(uint64_t* bars, int n, uint32_t issued,
 }  // namespace
 
 // =============================================================================
-// Base product with the adapters' steps
+// Forward: y[t] = W x[t] + B[a] p[t], W as the M operand
 // =============================================================================
-// Roles and rings as in the expert block's grouped GEMM: warp 0 codes, warp 1
+// A unit is 256 rows of W (128 a CTA of the pair) x 256 token rows.  A thread of
+// the decode groups owns a row of W: it decodes 64 weights of a k-chunk into
+// registers and writes them to tensor memory, where the UMMAs read their M
+// operand.  Written to shared memory instead (as the expert block's tiles are,
+// and the input gradient's below), the decoded tile costs 16 KB of writes and 16
+// KB of operand reads a chunk on top of the token rows' 32 KB: more
+// shared-memory time than the chunk's 512 tensor cycles.
+//
+// The accumulator is two halves of 128 token rows, in three TMEM slots used in
+// turn: while the epilogue empties a unit's first half, the next unit's first
+// half fills (its first chunks' second-half products follow once the slot is
+// free), so the tensor pipe does not wait for a whole epilogue.  Token rows are
+// accumulator columns, so an adapter's K = r product is issued at its own
+// columns: adapters' rows start at multiples of 32, the column granule of a pair
+// UMMA.
+//
+// Roles per CTA: warp 0 codes, warp 1 TMEM owner and (even CTA) issuer, warp 2
+// relay of operand readiness to the even CTA, warp 3 token rows and low-rank
+// operands, warps 4-19 four decode groups taking the chunks round robin, warps
+// 20-23 epilogue (32 rows of W each).
+namespace adf {
+constexpr int BM = 128, BK = 64;
+constexpr int kHalf = 128;                    // token rows of an accumulator half
+constexpr int X_BYTES = kHalf * BK * 2;       // a CTA's 64 + 64 token rows of a chunk
+constexpr int SA = 8;                         // token-row ring
+constexpr int kGroups = 4, kGroupWarps = 4;
+constexpr int kSlots = 3;                     // accumulator halves
+constexpr int kAOff = kSlots * kHalf;         // TMEM: the halves, then one decoded chunk (32 columns) a group
+constexpr int RAW_STAGES = 2 * kGroups, RAW_BYTES = BM * BK / 2;
+constexpr int RAW_OFF = SA * X_BYTES;
+constexpr int EPI_OFF = RAW_OFF + RAW_STAGES * RAW_BYTES;
+constexpr int kEpiPitch = 80;                 // bytes of a token's 32 outputs of a warp, padded
+constexpr int kEpiWarpBytes = 32 * kEpiPitch;
+constexpr int BAR_OFF = EPI_OFF + 4 * kEpiWarpBytes;
+constexpr int SMEM_BYTES = BAR_OFF + 1024 + 1024;
+constexpr int kEpiWarp0 = 4 + kGroups * kGroupWarps;
+constexpr int kThreads = 32 * (kEpiWarp0 + 4);
+constexpr int kTmemCols = 512;
+static_assert(kAOff + kGroups * BK / 2 <= kTmemCols, "TMEM budget");
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+static_assert(BM * E4B_MAX_RANK * 2 <= X_BYTES && kHalf * E4B_MAX_RANK * 2 <= X_BYTES, "low-rank operands fit a slot");
+static_assert(kAdapterUnitRows == 2 * kHalf && kAdapterRowAlign % 32 == 0, "column granules");
+}  // namespace adf
+
+struct AdapterFwdParams {
+  const float* absmax;
+  const int32_t* order;
+  const int32_t* steps;
+  uint16_t* out;
+  DeviceError* err;
+  long long timeout_ns;
+  int K, N, T, r_pad, n_mt;
+  int unit_start, entries;  // places in `steps`
+};
+
+// An adapter's rows [lo, hi) in half h of unit mu, relative to the half.
+__device__ __forceinline__ int2 half_range(const int4& en, int mu, int h) {
+  const int base = mu * kAdapterUnitRows + h * adf::kHalf;
+  return make_int2(min(max(en.z - base, 0), adf::kHalf), min(max(en.w - base, 0), adf::kHalf));
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
+    adapter_fwd_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_raw,
+                       const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_b,
+                       const AdapterFwdParams p) {
+  using namespace adf;
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = align1024(smem_dyn);
+  uint8_t* rawbuf = smem + RAW_OFF;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_OFF);
+  uint64_t* raw_full = bars;                    // [RAW_STAGES] codes landed
+  uint64_t* raw_empty = raw_full + RAW_STAGES;  // [RAW_STAGES] codes read into registers (group's 4 warps)
+  uint64_t* xfull = raw_empty + RAW_STAGES;     // [SA] ring use landed
+  uint64_t* xempty = xfull + SA;                // [SA] ring slot consumed by the UMMAs
+  uint64_t* full = xempty + SA;                 // [SA] (even CTA) both CTAs' operands of an MMA step in place
+  uint64_t* adone = full + SA;                  // [kGroups] this CTA's decoded chunk is in tensor memory (4 warps)
+  uint64_t* aempty = adone + kGroups;           // [kGroups] decoded chunk consumed by the UMMAs
+  uint64_t* accfull = aempty + kGroups;         // [kSlots] accumulator half complete
+  uint64_t* accempty = accfull + kSlots;        // [kSlots] (even CTA) half drained in both CTAs
+  uint64_t* drain = accempty + kSlots;          // (even CTA) all issued UMMAs finished
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  CtaControl* ctl = reinterpret_cast<CtaControl*>(drain + 2);
+  uint32_t* sig = reinterpret_cast<uint32_t*>(drain + 3);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  if (threadIdx.x == 0) {
+    for (int r = 0; r < RAW_STAGES; ++r) {
+      mbar_init(&raw_full[r], 1);
+      mbar_init(&raw_empty[r], kGroupWarps);
+    }
+    for (int s = 0; s < SA; ++s) {
+      mbar_init(&xfull[s], 1);
+      mbar_init(&xempty[s], 1);
+      mbar_init(&full[s], 1);
+    }
+    for (int g = 0; g < kGroups; ++g) {
+      mbar_init(&adone[g], kGroupWarps);
+      mbar_init(&aempty[g], 1);
+    }
+    for (int b = 0; b < kSlots; ++b) {
+      mbar_init(&accfull[b], 1);
+      mbar_init(&accempty[b], 8);
+    }
+    mbar_init(drain, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_2sm(tmem_slot, kTmemCols);
+    tmem_relinquish_2sm();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int n_units = p.steps[0] * p.n_mt;
+  const int kchunks = p.K / BK;
+  const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  const int32_t* unit_start = p.steps + p.unit_start;
+  const int4* entries = reinterpret_cast<const int4*>(p.steps + p.entries);  // (adapter, unit, first row, end row)
+
+  if (warp == 0) {
+    // ------------------------------------------------ NF4 codes: 128 rows x 32 bytes a chunk (one lane)
+    if (lane == 0) {
+      tma_prefetch_desc(&map_raw);
+      uint32_t j = 0, issued = 0, last_par = 0;
+      bool ok = true;
+      for (int u = pair; u < n_units && ok; u += n_pairs) {
+        const int row0 = (u % p.n_mt) * 256 + (int)rank * BM;
+        for (int kc = 0; kc < kchunks; ++kc, ++j) {
+          const uint32_t r = j % RAW_STAGES, ph = (j / RAW_STAGES) & 1;
+          if (!(ok = mbar_wait_lazy(&raw_empty[r], ph ^ 1, ctl, p.err, p.timeout_ns, 211, 64))) break;
+          mbar_arrive_expect_tx(&raw_full[r], (uint32_t)RAW_BYTES);
+          tma_load_2d(rawbuf + r * RAW_BYTES, &map_raw, &raw_full[r], kc * (BK / 2), row0);
+          issued |= 1u << r;
+          last_par = (last_par & ~(1u << r)) | (ph << r);
+        }
+      }
+      if (!ok) let_land(raw_full, RAW_STAGES, issued, last_par, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------ token rows, then a unit's low-rank operands (one lane)
+    // This CTA's rows of a half: 64 of its 128 (of an adapter's columns: its half of them).  A low-rank use is
+    // two slots: the adapter's 128 rows of B, then its p rows of both halves.
+    if (lane == 0) {
+      tma_prefetch_desc(&map_x);
+      tma_prefetch_desc(&map_p);
+      tma_prefetch_desc(&map_b);
+      uint32_t s = 0, ph = 0, issued = 0, last_par = 0;
+      auto issued_next = [&]() {
+        issued |= 1u << s;
+        last_par = (last_par & ~(1u << s)) | (ph << s);
+        if (++s == SA) {
+          s = 0;
+          ph ^= 1;
+        }
+      };
+      bool ok = true;
+      for (int u = pair; u < n_units && ok; u += n_pairs) {
+        const int mu = u / p.n_mt, w0 = (u % p.n_mt) * 256 + (int)rank * BM, t0 = mu * kAdapterUnitRows;
+        for (int kc = 0; kc < kchunks; ++kc) {
+          if (!(ok = mbar_wait(&xempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 212))) break;
+          uint8_t* x = smem + s * X_BYTES;
+          mbar_arrive_expect_tx(&xfull[s], (uint32_t)X_BYTES);
+          tma_load_2d(x, &map_x, &xfull[s], kc * BK, t0 + 64 * (int)rank);
+          tma_load_2d(x + X_BYTES / 2, &map_x, &xfull[s], kc * BK, t0 + kHalf + 64 * (int)rank);
+          issued_next();
+        }
+        if (!ok) break;
+        for (int i = __ldg(unit_start + mu);; ++i) {
+          const int4 en = __ldg(entries + i);
+          if (en.y != mu) break;
+          const uint32_t s1 = (s + 1 == SA) ? 0 : s + 1, ph1 = (s + 1 == SA) ? ph ^ 1 : ph;
+          if (!(ok = mbar_wait(&xempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 210))) break;
+          if (!(ok = mbar_wait(&xempty[s1], ph1 ^ 1, ctl, p.err, p.timeout_ns, 210))) break;
+          const int2 h0 = half_range(en, mu, 0), h1 = half_range(en, mu, 1);
+          const int n0 = (h0.y - h0.x) / 2, n1 = (h1.y - h1.x) / 2;  // this CTA's p rows, multiples of 16
+          mbar_arrive_expect_tx(&xfull[s], (uint32_t)((BM + n0 + n1) * 2 * p.r_pad));
+          uint8_t* b = smem + s * X_BYTES;
+          tma_load_3d(b, &map_b, &xfull[s], 0, w0, en.x);
+          tma_load_3d(b + 128 * p.r_pad, &map_b, &xfull[s], 0, w0 + 64, en.x);
+          uint8_t* pr = smem + s1 * X_BYTES;
+          for (int k = 0; k < n0; k += 16)
+            tma_load_2d(pr + k * 2 * p.r_pad, &map_p, &xfull[s], 0, t0 + h0.x + n0 * (int)rank + k);
+          pr += 64 * 2 * p.r_pad;
+          for (int k = 0; k < n1; k += 16)
+            tma_load_2d(pr + k * 2 * p.r_pad, &map_p, &xfull[s], 0, t0 + kHalf + h1.x + n1 * (int)rank + k);
+          mbar_arrive(&xfull[s1]);
+          issued_next();
+          issued_next();
+        }
+      }
+      if (!ok) let_land(xfull, SA, issued, last_par, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp == 1 && rank == 0) {
+    // ------------------------------------------------ UMMA issuer (even CTA, one elected lane)
+    if (elect_one_sync()) {
+      const uint32_t idesc = make_idesc_bf16(256, kHalf, false, false);
+      const uint32_t lswz = swz_for_row_bytes(2 * p.r_pad);
+      const uint32_t x_u = smem_u32(smem);
+      const uint64_t xdesc0 = make_sdesc(x_u, 16, 1024, kSw128);
+      uint32_t sx = 0, g = 0, fs = 0, fph = 0, hs = 0;  // ring slot, decode group, MMA step, accumulator halves used
+      bool ok = true;
+      auto next_x = [&]() { sx = (sx + 1 == SA) ? 0 : sx + 1; };
+      auto next_g = [&]() { g = (g + 1) % kGroups; };
+      auto next_f = [&]() {
+        if (++fs == SA) {
+          fs = 0;
+          fph ^= 1;
+        }
+      };
+      auto wait_step = [&]() -> bool {
+        const bool r = mbar_wait_cluster(&full[fs], fph, ctl, p.err, p.timeout_ns, 223);
+        tc_fence_after();
+        return r;
+      };
+      auto wait_slot = [&](uint32_t use) -> bool {  // accumulator half number `use`
+        const bool r =
+            mbar_wait_cluster(&accempty[use % kSlots], ((use / kSlots) & 1) ^ 1, ctl, p.err, p.timeout_ns, 220);
+        tc_fence_after();
+        return r;
+      };
+      // the products of one chunk (ring slot s, decode group gg) into half h
+      auto half = [&](uint32_t d, uint32_t s, uint32_t gg, int h, bool first) {
+        const uint32_t a = tmem + kAOff + gg * (BK / 2);
+        const uint64_t xd = xdesc0 + (uint64_t)((s * X_BYTES + h * (X_BYTES / 2)) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk)
+          umma_bf16_2sm_ta(d, a + 8 * kk, xd + 2 * kk, idesc, (!first || kk > 0) ? 1u : 0u);
+      };
+      auto release = [&](uint32_t s, uint32_t gg) {
+        umma_commit_2sm(&xempty[s], 0x3);
+        umma_commit_2sm(&aempty[gg], 0x3);
+      };
+      for (int u = pair; u < n_units && ok; u += n_pairs, hs += 2) {
+        const int mu = u / p.n_mt;
+        const uint32_t d0 = tmem + (hs % kSlots) * kHalf, d1 = tmem + ((hs + 1) % kSlots) * kHalf;
+        int i = __ldg(unit_start + mu);
+        int4 en = __ldg(entries + i);
+        // First chunks: the first half at once, the second when its slot has been drained.
+        const int lead = min(kGroups, kchunks);
+        const uint32_t sx0 = sx, g0 = g;
+        if (!(ok = wait_slot(hs))) break;
+        for (int kc = 0; kc < lead; ++kc) {
+          if (!(ok = wait_step())) break;
+          half(d0, sx, g, 0, kc == 0);
+          next_x();
+          next_g();
+          next_f();
+        }
+        if (!ok || !(ok = wait_slot(hs + 1))) break;
+        sx = sx0;
+        g = g0;
+        for (int kc = 0; kc < lead; ++kc) {
+          half(d1, sx, g, 1, kc == 0);
+          release(sx, g);
+          next_x();
+          next_g();
+        }
+        bool ready = false;
+        for (int kc = lead; kc < kchunks; ++kc) {
+          if (!ready && !(ok = wait_step())) break;
+          tc_fence_after();
+          next_f();
+          half(d0, sx, g, 0, false);
+          // peek at the next chunk while these products run
+          ready = kc + 1 < kchunks && mbar_test_wait_cluster(&full[fs], fph);
+          half(d1, sx, g, 1, false);
+          release(sx, g);
+          next_x();
+          next_g();
+        }
+        if (!ok) break;
+        // One K = r product per adapter and half, at the adapter's columns.
+        for (; en.y == mu; en = __ldg(entries + ++i)) {
+          if (!(ok = wait_step())) break;
+          const uint32_t sx1 = (sx + 1 == SA) ? 0 : sx + 1;
+          const uint32_t b_u = x_u + sx * X_BYTES, p_u = x_u + sx1 * X_BYTES;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int2 hr = half_range(en, mu, h);
+            if (hr.y > hr.x) {
+              const uint32_t id = make_idesc_bf16(256, hr.y - hr.x, false, false);
+              for (int ks = 0; ks < p.r_pad / 16; ++ks)
+                umma_bf16_2sm((h ? d1 : d0) + hr.x, make_sdesc(b_u + 32 * ks, 16, 16 * p.r_pad, lswz),
+                              make_sdesc(p_u + h * 128 * p.r_pad + 32 * ks, 16, 16 * p.r_pad, lswz), id, 1u);
+            }
+          }
+          umma_commit_2sm(&xempty[sx], 0x3);
+          umma_commit_2sm(&xempty[sx1], 0x3);
+          next_x();
+          next_x();
+          next_f();
+        }
+        if (!ok) break;
+        umma_commit_2sm(&accfull[hs % kSlots], 0x3);
+        umma_commit_2sm(&accfull[(hs + 1) % kSlots], 0x3);
+      }
+      umma_commit_2sm(drain, 0x1);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(drain, 0) && (long long)(globaltimer_ns() - t0) < p.timeout_ns) {
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------ relays: this CTA's operands of a step -> even CTA's full[]
+    const uint32_t full_even = mapa_shared(smem_u32(full), 0);
+    const uint32_t sig_even = mapa_shared(smem_u32(sig), 0);
+    uint32_t sx = 0, phx = 0, j = 0, fs = 0;
+    bool ok = true;
+    auto wait_x = [&]() -> bool {
+      const bool r = __all_sync(kFull, mbar_wait(&xfull[sx], phx, ctl, p.err, p.timeout_ns, 252));
+      if (++sx == SA) {
+        sx = 0;
+        phx ^= 1;
+      }
+      return r;
+    };
+    auto signal = [&]() {
+      if (lane == 0) {
+        if (rank == 0)
+          mbar_arrive_expect_tx(&full[fs], 4);
+        else
+          st_async_signal(sig_even, full_even + 8 * fs, 1u);
+      }
+      fs = (fs + 1 == SA) ? 0 : fs + 1;
+    };
+    for (int u = pair; u < n_units && ok; u += n_pairs) {
+      const int mu = u / p.n_mt;
+      for (int kc = 0; kc < kchunks; ++kc, ++j) {
+        ok = __all_sync(kFull, mbar_wait(&adone[j % kGroups], (j / kGroups) & 1, ctl, p.err, p.timeout_ns, 251));
+        if (!ok || !(ok = wait_x())) break;
+        tc_fence_after();  // the decoded chunk's tensor-memory writes before the signal
+        tc_fence_before();
+        signal();
+      }
+      if (!ok) break;
+      for (int i = __ldg(unit_start + mu); __ldg(entries + i).y == mu; ++i) {
+        if (!(ok = wait_x()) || !(ok = wait_x())) break;
+        signal();
+      }
+    }
+  } else if (warp >= 4 && warp < kEpiWarp0) {
+    // ------------------------------------------------ NF4 decode: a row of W a thread
+    const uint32_t grp = (warp - 4) >> 2;
+    const int t = (threadIdx.x - 128) & 127;
+    const Nf4Shift ks = nf4_shift_consts();
+    const uint32_t a_base = tmem + kAOff + grp * (BK / 2) + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t my_units = pair < n_units ? (uint32_t)((n_units - pair + n_pairs - 1) / n_pairs) : 0;
+    const uint32_t n_chunks = my_units * (uint32_t)kchunks;
+    // A cursor over this group's chunks, one ahead of the decode (for the block scales).
+    int c_kc = (int)grp, c_u = pair;
+    auto wrap = [&]() {
+      while (c_kc >= kchunks) {
+        c_kc -= kchunks;
+        c_u += n_pairs;
+      }
+    };
+    wrap();
+    int c_row = (c_u % p.n_mt) * 256 + (int)rank * BM + t;
+    auto block_scale = [&]() -> float {  // 0 past the end of the matrix: zero weights
+      if (c_u >= n_units || c_row >= p.N) return 0.0f;
+      return __ldg(p.absmax + (size_t)c_row * kchunks + c_kc);
+    };
+    float amax_next = block_scale();
+    bool ok = true;
+    for (uint32_t jj = grp; jj < n_chunks && ok; jj += kGroups) {
+      const float amax = amax_next;
+      const int old = c_u;
+      c_kc += kGroups;
+      wrap();
+      if (c_u != old) c_row = (c_u % p.n_mt) * 256 + (int)rank * BM + t;
+      const uint32_t r = jj % RAW_STAGES, rph = (jj / RAW_STAGES) & 1;
+      ok = __all_sync(kFull, mbar_wait(&raw_full[r], rph, ctl, p.err, p.timeout_ns, 230));
+      if (!ok) break;
+      const uint8_t* slot = rawbuf + r * RAW_BYTES + t * 32;
+      const uint4 q0 = *reinterpret_cast<const uint4*>(slot);
+      const uint4 q1 = *reinterpret_cast<const uint4*>(slot + 16);
+      const uint32_t codes[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+      fence_proxy_async_smem();  // these reads before the next TMA write of the slot
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&raw_empty[r]);
+      amax_next = block_scale();
+      const Nf4Planes pl = nf4_block_planes(amax);
+      uint32_t v[32];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) nf4_decode_word(codes[c], pl, ks, &v[4 * c]);
+      ok = __all_sync(kFull, mbar_wait(&aempty[grp], ((jj / kGroups) & 1) ^ 1, ctl, p.err, p.timeout_ns, 231));
+      if (!ok) break;
+      tc_fence_after();
+      tmem_st32(a_base, v);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&adone[grp]);
+    }
+  } else if (warp >= kEpiWarp0) {
+    // ------------------------------------------------ epilogue: 32 rows of W x the token rows
+    // A lane holds a row of W; 32 token rows at a time pass through shared memory so that a store writes 64
+    // contiguous bytes of each of eight tokens.
+    const int qrt = warp & 3;
+    const uint32_t accempty_even = mapa_shared(smem_u32(accempty), 0);
+    uint8_t* ebuf = smem + EPI_OFF + qrt * kEpiWarpBytes;
+    uint32_t hs = 0;
+    bool ok = true;
+    for (int u = pair; u < n_units && ok; u += n_pairs) {
+      const int mu = u / p.n_mt, w0 = (u % p.n_mt) * 256 + (int)rank * BM + 32 * qrt;
+      const int col = w0 + 8 * (lane & 3);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h, ++hs) {
+        const uint32_t b = hs % kSlots;
+        ok = __all_sync(kFull, mbar_wait(&accfull[b], (hs / kSlots) & 1, ctl, p.err, p.timeout_ns, 240));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tl = tmem + b * kHalf + ((uint32_t)(qrt * 32) << 16);
+#pragma unroll 1
+        for (int jj = 0; jj < kHalf; jj += 32) {
+          const int tok = __ldg(p.order + mu * kAdapterUnitRows + h * kHalf + jj + lane);
+          if (!__any_sync(kFull, tok < p.T)) continue;
+          float v[32];
+          tmem_ld32(tl + jj, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t w = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            *reinterpret_cast<uint16_t*>(ebuf + (2 * i) * kEpiPitch + 2 * lane) = (uint16_t)w;
+            *reinterpret_cast<uint16_t*>(ebuf + (2 * i + 1) * kEpiPitch + 2 * lane) = (uint16_t)(w >> 16);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = 8 * i + (lane >> 2), t = __shfl_sync(kFull, tok, row);
+            if (t < p.T && col < p.N)
+              *reinterpret_cast<uint4*>(p.out + (size_t)t * p.N + col) =
+                  *reinterpret_cast<const uint4*>(ebuf + row * kEpiPitch + 16 * (lane & 3));
+          }
+          __syncwarp();
+        }
+        // The issuer needs this warp's TMEM reads only, not its global stores: a relaxed arrival.
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0)
+            mbar_arrive(&accempty[b]);
+          else
+            mbar_arrive_cluster_relaxed(accempty_even + 8 * b);
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_2sm(tmem, kTmemCols);
+  }
+}
+
+// =============================================================================
+// Input gradient: dx[t] = dY[t] W + q[t] A[a]
+// =============================================================================
+// The stored rows of W are the reduction here, and its 4-bit codes cannot be
+// read along it, so the decoded tile goes to shared memory with the output
+// columns contiguous, as the N operand.  Roles and rings as in the expert block's grouped GEMM: warp 0 codes, warp 1
 // TMEM owner and (even CTA) UMMA issuer, warp 2 relay of operand readiness to
 // the even CTA, warp 3 activation tiles and low-rank operands, warps 4-19 four
 // decode groups taking the k-chunks round robin, warps 20-23 epilogue.  The
 // low-rank steps come after the k-chunks: a unit's two ring slots per adapter
-// hold its 128 p (or q) rows and 128 factor rows.
+// hold its 128 q rows and 128 columns of A.
 namespace adg {
 constexpr int BM = 128, BN = 128, BK = 64;
 constexpr int A_BYTES = BM * BK * 2;
@@ -143,24 +624,21 @@ static_assert(BM * E4B_MAX_RANK * 2 <= A_BYTES && BN * E4B_MAX_RANK * 2 <= A_BYT
 static_assert(RAW_STAGES % kGroups == 0, "code slots are owned by one decode group each");
 }  // namespace adg
 
-struct AdapterGemmParams {
+struct AdapterDgradParams {
   const float* absmax;
   const int32_t* order;
   const int32_t* steps;
   uint16_t* out;
   DeviceError* err;
   long long timeout_ns;
-  int R;        // reduction length (K, or N for the input gradient)
-  int O;        // output columns (N, or K)
   int T, N, K, r_pad, n_nt;
   int unit_start, entries;  // places in `steps`
 };
 
-template <bool kMN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
-    adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_raw,
+    adapter_dgrad_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_raw,
                         const __grid_constant__ CUtensorMap map_la, const __grid_constant__ CUtensorMap map_lb,
-                        const AdapterGemmParams p) {
+                        const AdapterDgradParams p) {
   using namespace adg;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = align1024(smem_dyn);
@@ -216,7 +694,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   const int n_units = p.steps[0] * p.n_nt;
-  const int kchunks = (p.R + BK - 1) / BK;
+  const int kchunks = (p.N + BK - 1) / BK;
   const int blocks_per_row = p.K / 64;
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   const int32_t* unit_start = p.steps + p.unit_start;
@@ -235,10 +713,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
           if (!(ok = mbar_wait_lazy(&raw_empty[r], ph ^ 1, ctl, p.err, p.timeout_ns, 311, 64))) break;
           uint8_t* slot = rawbuf + r * RAW_BYTES;
           mbar_arrive_expect_tx(&raw_full[r], (uint32_t)RAW_BYTES);
-          if (!kMN)
-            tma_load_2d(slot, &map_raw, &raw_full[r], kc * (BK / 2), c0);
-          else
-            tma_load_2d(slot, &map_raw, &raw_full[r], c0 / 2, kc * BK);
+          tma_load_2d(slot, &map_raw, &raw_full[r], c0 / 2, kc * BK);
           issued |= 1u << r;
           last_par = (last_par & ~(1u << r)) | (ph << r);
         }
@@ -281,13 +756,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
           uint8_t* lb = aring + s1 * A_BYTES;
           mbar_arrive_expect_tx(&xfull[s], (uint32_t)(512 * p.r_pad));
           tma_load_2d(la, &map_la, &xfull[s], 0, row0);
-          if (!kMN) {
-            tma_load_3d(lb, &map_lb, &xfull[s], 0, c0, en.x);
-            tma_load_3d(lb + 128 * p.r_pad, &map_lb, &xfull[s], 0, c0 + 64, en.x);
-          } else {
-            tma_load_3d(lb, &map_lb, &xfull[s], c0, 0, en.x);
-            tma_load_3d(lb + 128 * p.r_pad, &map_lb, &xfull[s], c0 + 64, 0, en.x);
-          }
+          tma_load_3d(lb, &map_lb, &xfull[s], c0, 0, en.x);
+          tma_load_3d(lb + 128 * p.r_pad, &map_lb, &xfull[s], c0 + 64, 0, en.x);
           mbar_arrive(&xfull[s1]);
           issued_next();
           issued_next();
@@ -299,12 +769,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
   } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------ UMMA issuer (even CTA, one elected lane)
     if (elect_one_sync()) {
-      const uint32_t idesc = make_idesc_bf16(256, 256, false, kMN);
+      const uint32_t idesc = make_idesc_bf16(256, 256, false, true);
       const uint32_t lswz = swz_for_row_bytes(2 * p.r_pad);
       const uint32_t a_u = smem_u32(aring), b_u = smem_u32(bring);
-      const uint32_t bstep = kMN ? 128u : 2u;
+      const uint32_t bstep = 128u;  // K16 step of the N operand in the descriptor address field
       const uint64_t adesc0 = make_sdesc(a_u, 16, 1024, kSw128);
-      const uint64_t bdesc0 = kMN ? make_sdesc(b_u, 8192, 1024, kSw128) : make_sdesc(b_u, 16, 1024, kSw128);
+      const uint64_t bdesc0 = make_sdesc(b_u, 8192, 1024, kSw128);
       uint32_t ti = 0;
       uint32_t sa = 0, sb = 0;
       uint32_t fs = 0, fph = 0;
@@ -360,8 +830,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
 #pragma unroll
           for (int w = 0; w < 8; ++w) off[w] = rows_off(en.z - mu * 256, en.w - mu * 256, w);
           for (int ks = 0; ks < p.r_pad / 16; ++ks) {
-            const uint64_t bd = kMN ? make_sdesc(lb_u + 2048 * ks, 128 * p.r_pad, 1024, kSw128)
-                                    : make_sdesc(lb_u + 32 * ks, 16, 16 * p.r_pad, lswz);
+            const uint64_t bd = make_sdesc(lb_u + 2048 * ks, 128 * p.r_pad, 1024, kSw128);
             umma_bf16_2sm_masked(d, make_sdesc(la_u + 32 * ks, 16, 16 * p.r_pad, lswz), bd, idesc, off);
           }
           umma_commit_2sm(&aempty[sa], 0x3);
@@ -418,11 +887,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
   } else if (warp >= 4 && warp < kEpiWarp0) {
     // ------------------------------------------------ NF4 decode, groups take the k-chunks round robin
     const uint32_t grp = (warp - 4) >> 2;
-    const int t = (threadIdx.x - 128) & 127;  // weight row (K-major) / code column pair of this thread
+    const int t = (threadIdx.x - 128) & 127;  // stored row t % 64, block of 64 columns t / 64
     const Nf4Shift ks = nf4_shift_consts();
-    const int raw_off = kMN ? (t & 63) * 64 + (t >> 6) * 32 : t * 32;
-    const int drow = kMN ? (t & 63) : t;
-    const uint32_t drow_off = (kMN ? (t >> 6) * 8192 : 0) + (drow >> 3) * 1024 + (drow & 7) * 128;
+    const int raw_off = (t & 63) * 64 + (t >> 6) * 32;
+    const int drow = t & 63;
+    const uint32_t drow_off = (t >> 6) * 8192 + (drow >> 3) * 1024 + (drow & 7) * 128;
     const uint32_t b_u = smem_u32(bring) + grp * B_BYTES;
     // A cursor over this group's chunks, one chunk ahead of the decode (for the block scales).
     const uint32_t my_units = pair < n_units ? (uint32_t)((n_units - pair + n_pairs - 1) / n_pairs) : 0;
@@ -444,14 +913,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
     // Block scale of this thread's row for the cursor's chunk (0 past the ends of the matrix: zero decode).
     auto block_scale = [&]() -> float {
       if (c_u >= n_units) return 0.0f;
-      int row, blk;
-      if (!kMN) {
-        row = c_nt * 256 + (int)rank * 128 + t;
-        blk = c_kc;
-      } else {
-        row = c_kc * BK + (t & 63);
-        blk = c_nt * 4 + (int)rank * 2 + (t >> 6);
-      }
+      const int row = c_kc * BK + (t & 63), blk = c_nt * 4 + (int)rank * 2 + (t >> 6);
       if (row >= p.N || blk >= blocks_per_row) return 0.0f;
       return __ldg(p.absmax + (size_t)row * blocks_per_row + blk);
     };
@@ -506,7 +968,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
       const uint32_t tl = tmem + b * 256 + ((uint32_t)(qrt * 32) << 16);
 #pragma unroll 1
       for (int jj = 0; jj < 256; jj += 64) {
-        if (c0 + jj >= p.O || !any) break;
+        if (c0 + jj >= p.K || !any) break;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float v[32];
@@ -524,8 +986,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
         for (int i = 0; i < 8; ++i) {
           const int row = 4 * i + (lane >> 3);
           const int t = __shfl_sync(kFull, tok, row);
-          if (t < p.T && col < p.O)
-            *reinterpret_cast<uint4*>(p.out + (size_t)t * p.O + col) =
+          if (t < p.T && col < p.K)
+            *reinterpret_cast<uint4*>(p.out + (size_t)t * p.K + col) =
                 *reinterpret_cast<const uint4*>(ebuf + row * kEpiPitch + 16 * (lane & 7));
         }
         __syncwarp();
@@ -878,7 +1340,7 @@ __device__ __forceinline__ AdapterWgradUnit adapter_wgrad_unit(const AdapterWgra
   w.g = w.ft >= p.n_ft[0];
   if (w.g) w.ft -= p.n_ft[0];
   w.row0 = __ldg(p.offsets + w.a);
-  w.rows = __ldg(p.offsets + w.a + 1) - w.row0;  // a multiple of 16
+  w.rows = __ldg(p.offsets + w.a + 1) - w.row0;  // a multiple of 32
   const int chunks = (w.rows + adw::BK - 1) / adw::BK, rank = (int)blockIdx.x % p.S;
   w.k_lo = rank * chunks / p.S;
   w.k_hi = (rank + 1) * chunks / p.S;
@@ -1152,49 +1614,68 @@ cudaError_t map_u8_2d(CUtensorMap* m, const void* base, uint64_t bytes, uint64_t
 }
 }  // namespace
 
-cudaError_t launch_adapter_gemm(const AdapterProjHost& h, bool mn, const uint16_t* rows, const uint16_t* low,
-                                const uint16_t* fac, uint16_t* out, int num_sms, cudaStream_t stream) {
-  const int R = mn ? h.N : h.K, O = mn ? h.K : h.N, rp = rank_padded(h.r);
-  CUtensorMap ma, mraw, mla, mlb;
-  cudaError_t err;
-  if ((err = map_bf16_2d(&ma, rows, R, h.rows_cap, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return err;
-  if ((err = mn ? map_u8_2d(&mraw, h.nf4, h.K / 2, h.N, 64, 64) : map_u8_2d(&mraw, h.nf4, h.K / 2, h.N, 32, 128)) !=
-      cudaSuccess)
-    return err;
+cudaError_t launch_adapter_fwd(const AdapterProjHost& h, const uint16_t* rows, const uint16_t* low, const uint16_t* B,
+                               uint16_t* y, int num_sms, cudaStream_t stream) {
+  const int rp = rank_padded(h.r);
   const CUtensorMapSwizzle rswz = swizzle_for_bytes(2 * rp);
-  if ((err = map_bf16_2d(&mla, low, h.r, h.rows_cap, rp, 128, rswz)) != cudaSuccess) return err;
-  if (!mn)  // B [n, N, r]
-    err = map_bf16_3d(&mlb, fac, h.r, h.N, h.n, rp, 64, rswz);
-  else  // A [n, r, K]
-    err = map_bf16_3d(&mlb, fac, h.K, h.r, h.n, 64, rp, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (err != cudaSuccess) return err;
+  CUtensorMap mx, mraw, mp, mb;
+  cudaError_t err;
+  if ((err = map_bf16_2d(&mx, rows, h.K, h.rows_cap, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return err;
+  if ((err = map_u8_2d(&mraw, h.nf4, h.K / 2, h.N, 32, 128)) != cudaSuccess) return err;
+  if ((err = map_bf16_2d(&mp, low, h.r, h.rows_cap, rp, 16, rswz)) != cudaSuccess) return err;
+  if ((err = map_bf16_3d(&mb, B, h.r, h.N, h.n, rp, 64, rswz)) != cudaSuccess) return err;
   const AdapterSteps lay = adapter_steps_layout(h.rows_cap, h.n);
-  AdapterGemmParams p;
+  AdapterFwdParams p;
   p.absmax = h.absmax;
   p.order = h.order;
   p.steps = h.steps;
-  p.out = out;
+  p.out = y;
   p.err = h.err;
   p.timeout_ns = h.timeout_ns;
-  p.R = R;
-  p.O = O;
+  p.K = h.K;
+  p.N = h.N;
+  p.T = h.T;
+  p.r_pad = rp;
+  p.n_mt = (h.N + 255) / 256;
+  p.unit_start = lay.unit_start;
+  p.entries = lay.entries;
+  const int64_t units = h.rows_cap / kAdapterUnitRows * p.n_mt;
+  const int grid = 2 * (int)(units < num_sms / 2 ? units : num_sms / 2);
+  if ((err = set_smem(adapter_fwd_kernel, adf::SMEM_BYTES)) != cudaSuccess) return err;
+  LaunchScope scope("adapter_fwd", stream);
+  adapter_fwd_kernel<<<grid, adf::kThreads, adf::SMEM_BYTES, stream>>>(mx, mraw, mp, mb, p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_adapter_dgrad(const AdapterProjHost& h, const uint16_t* rows, const uint16_t* low,
+                                 const uint16_t* A, uint16_t* dx, int num_sms, cudaStream_t stream) {
+  const int rp = rank_padded(h.r);
+  CUtensorMap ma, mraw, mla, mlb;
+  cudaError_t err;
+  if ((err = map_bf16_2d(&ma, rows, h.N, h.rows_cap, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return err;
+  if ((err = map_u8_2d(&mraw, h.nf4, h.K / 2, h.N, 64, 64)) != cudaSuccess) return err;
+  if ((err = map_bf16_2d(&mla, low, h.r, h.rows_cap, rp, 128, swizzle_for_bytes(2 * rp))) != cudaSuccess) return err;
+  if ((err = map_bf16_3d(&mlb, A, h.K, h.r, h.n, 64, rp, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return err;
+  const AdapterSteps lay = adapter_steps_layout(h.rows_cap, h.n);
+  AdapterDgradParams p;
+  p.absmax = h.absmax;
+  p.order = h.order;
+  p.steps = h.steps;
+  p.out = dx;
+  p.err = h.err;
+  p.timeout_ns = h.timeout_ns;
   p.T = h.T;
   p.N = h.N;
   p.K = h.K;
   p.r_pad = rp;
-  p.n_nt = (O + 255) / 256;
+  p.n_nt = (h.K + 255) / 256;
   p.unit_start = lay.unit_start;
   p.entries = lay.entries;
   const int64_t units = h.rows_cap / kAdapterUnitRows * p.n_nt;
   const int grid = 2 * (int)(units < num_sms / 2 ? units : num_sms / 2);
-  LaunchScope scope(mn ? "adapter_gemm_dgrad" : "adapter_gemm_fwd", stream);
-  if (mn) {
-    if ((err = set_smem(adapter_gemm_kernel<true>, adg::SMEM_BYTES)) != cudaSuccess) return err;
-    adapter_gemm_kernel<true><<<grid, adg::kThreads, adg::SMEM_BYTES, stream>>>(ma, mraw, mla, mlb, p);
-  } else {
-    if ((err = set_smem(adapter_gemm_kernel<false>, adg::SMEM_BYTES)) != cudaSuccess) return err;
-    adapter_gemm_kernel<false><<<grid, adg::kThreads, adg::SMEM_BYTES, stream>>>(ma, mraw, mla, mlb, p);
-  }
+  if ((err = set_smem(adapter_dgrad_kernel, adg::SMEM_BYTES)) != cudaSuccess) return err;
+  LaunchScope scope("adapter_dgrad", stream);
+  adapter_dgrad_kernel<<<grid, adg::kThreads, adg::SMEM_BYTES, stream>>>(ma, mraw, mla, mlb, p);
   return cudaGetLastError();
 }
 

@@ -793,7 +793,7 @@ e4b_status e4b_multi_lora_serve_fwd(const e4b_proj_dims* dims, int32_t T, const 
   }
   E4B_CUDA(launch_adapter_group(ids, T, dims->n_adapters, order, offsets, steps, st));
   E4B_CUDA(launch_adapter_rows(h, false, x, adapters->A, rows, low, sms, st));
-  E4B_CUDA(launch_adapter_gemm(h, false, rows, low, adapters->B, y, sms, st));
+  E4B_CUDA(launch_adapter_fwd(h, rows, low, adapters->B, y, sms, st));
   return E4B_OK;
 }
 
@@ -813,7 +813,7 @@ e4b_status e4b_multi_lora_fwd(const e4b_proj_dims* dims, int32_t T, const e4b_ad
   E4B_CUDA(device_sms(&sms));
   const AdapterProjHost h = proj_host(dims, T, base, adapters, groups->order, groups->offsets, groups->steps, ws);
   E4B_CUDA(launch_adapter_rows(h, false, x, adapters->A, rows, p, sms, st));
-  E4B_CUDA(launch_adapter_gemm(h, false, rows, p, adapters->B, y, sms, st));
+  E4B_CUDA(launch_adapter_fwd(h, rows, p, adapters->B, y, sms, st));
   return E4B_OK;
 }
 
@@ -833,7 +833,7 @@ e4b_status e4b_multi_lora_dgrad(const e4b_proj_dims* dims, int32_t T, const e4b_
   E4B_CUDA(device_sms(&sms));
   const AdapterProjHost h = proj_host(dims, T, base, adapters, groups->order, groups->offsets, groups->steps, ws);
   E4B_CUDA(launch_adapter_rows(h, true, dY, adapters->B, rows, q, sms, st));
-  E4B_CUDA(launch_adapter_gemm(h, true, rows, q, adapters->A, dx, sms, st));
+  E4B_CUDA(launch_adapter_dgrad(h, rows, q, adapters->A, dx, sms, st));
   return E4B_OK;
 }
 

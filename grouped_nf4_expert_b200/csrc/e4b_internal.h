@@ -200,9 +200,10 @@ constexpr int kAdapterUnitRows = 256;  // rows of a GEMM unit (a CTA pair)
 constexpr int kAdapterGemvTokens = 16;    // most tokens of the base product on warp instructions
 constexpr int kAdapterSmallTokens = 256;  // most tokens of the small-batch kernels
 constexpr int kAdapterTaskRows = 128;  // rows of a low-rank projection task (one adapter's)
+constexpr int kAdapterRowAlign = 32;   // an adapter's first row
 inline int64_t adapter_rows_cap(int64_t T, int n) {
   const int64_t groups = T < n + 1 ? T : n + 1;
-  return (T + 15 * groups + 255) / 256 * 256;
+  return (T + (kAdapterRowAlign - 1) * groups + 255) / 256 * 256;
 }
 // Work list layout (int32): header ([0] units, [1] rows used, [2] entries, [3] tasks), the first entry of
 // each 256-row unit, entries (adapter, unit, first row, end row of the adapter) by unit with a sentinel
@@ -236,9 +237,12 @@ struct AdapterProjHost {
 // rows[row] = src[t], out[row, :r] = bf16(s[a] src[t] . factor[a]): A [n, r, K] over x, or (mn) B [n, N, r] over dY.
 cudaError_t launch_adapter_rows(const AdapterProjHost& h, bool mn, const uint16_t* src, const uint16_t* fac,
                                 uint16_t* rows, uint16_t* out, int num_sms, cudaStream_t stream);
-// out[t] = rows[row] W^T + low[row] B[a]^T, or (mn) rows[row] W + low[row] A[a].
-cudaError_t launch_adapter_gemm(const AdapterProjHost& h, bool mn, const uint16_t* rows, const uint16_t* low,
-                                const uint16_t* fac, uint16_t* out, int num_sms, cudaStream_t stream);
+// y[t] = rows[row] W^T + low[row] B[a]^T.
+cudaError_t launch_adapter_fwd(const AdapterProjHost& h, const uint16_t* rows, const uint16_t* low, const uint16_t* B,
+                               uint16_t* y, int num_sms, cudaStream_t stream);
+// dx[t] = rows[row] W + low[row] A[a].
+cudaError_t launch_adapter_dgrad(const AdapterProjHost& h, const uint16_t* rows, const uint16_t* low,
+                                 const uint16_t* A, uint16_t* dx, int num_sms, cudaStream_t stream);
 cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, const uint16_t* dY, const uint16_t* p,
                                  const uint16_t* q, uint16_t* dA, uint16_t* dB, int num_sms, cudaStream_t stream);
 // y for up to kAdapterSmallTokens tokens in one launch (scratch: low [T, r] bf16, or for up to kAdapterGemvTokens

@@ -58,7 +58,7 @@ typedef struct {
 
 /* Grouping of the tokens by adapter, written by e4b_adapter_group and read by
  * the training calls.  Rows are the tokens sorted by adapter (stable); every
- * adapter's rows start at a multiple of 16, the tokens without an adapter come
+ * adapter's rows start at a multiple of 32, the tokens without an adapter come
  * last. */
 typedef struct {
   int32_t *order;   /* [rows_cap] token of each row; T for padding rows */
@@ -67,7 +67,7 @@ typedef struct {
 } e4b_adapter_groups;
 
 typedef struct {
-  int64_t rows_cap;             /* rows of order, p and q: T + 15 min(n + 1, T), rounded up to 256 */
+  int64_t rows_cap;             /* rows of order, p and q: T + 31 min(n + 1, T), rounded up to 256 */
   int64_t steps_cap;            /* int32 entries of e4b_adapter_groups.steps */
   size_t  workspace_bytes;      /* bytes of `ws` of the training calls */
   size_t  serve_workspace_bytes;/* bytes of `ws` of e4b_multi_lora_serve_fwd */

@@ -43,13 +43,13 @@ def project_backward(x, ids, dY, W, A, B, scale):
 
 def group(ids, n):
     """(rows of each group, padded starts): the tokens sorted by adapter (stable), each adapter's rows at a
-    multiple of 16, the tokens without an adapter (ids outside [0, n)) last."""
+    multiple of 32, the tokens without an adapter (ids outside [0, n)) last."""
     ids = np.asarray(ids)
     members = [np.flatnonzero(ids == a) for a in range(n)]
     members.append(np.flatnonzero((ids < 0) | (ids >= n)))
     starts, at = [], 0
     for a in range(n):
         starts.append(at)
-        at += -(-members[a].size // 16) * 16
+        at += -(-members[a].size // 32) * 32
     starts += [at, at + members[n].size]
     return members, np.array(starts)

@@ -47,7 +47,7 @@ def test_projection_sizes(so):
     assert so.e4b_proj_get_sizes(ref(d), 10, None) == INVALID
     assert so.e4b_proj_get_sizes(None, 10, ref(out)) == INVALID
     assert so.e4b_proj_get_sizes(ref(d), 1000, ref(out)) == 0
-    assert out.rows_cap == 1280 and out.rows_cap % 256 == 0  # 1000 + 15 * 4, rounded up
+    assert out.rows_cap == 1280 and out.rows_cap % 256 == 0  # 1000 + 31 * 4, rounded up
     assert so.e4b_proj_get_sizes(ref(d), 0, ref(out)) == 0 and out.rows_cap == 0
 
 

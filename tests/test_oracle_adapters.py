@@ -48,7 +48,7 @@ def test_projection_gradients_by_differences():
 def test_group_is_stable_and_padded():
     members, starts = oa.group([1, 0, 1, -1, 9, 1], 3)
     assert [m.tolist() for m in members] == [[1], [0, 2, 5], [], [3, 4]]
-    assert starts.tolist() == [0, 16, 32, 32, 34]
+    assert starts.tolist() == [0, 32, 64, 64, 66]
 
 
 def test_balance_closed_values():
