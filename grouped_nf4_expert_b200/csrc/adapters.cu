@@ -18,7 +18,7 @@ constexpr uint32_t kFull = 0xffffffffu;
 // that there are no shared-memory atomics and the order is fixed.  Two passes
 // over the ids (count, place) around one scan over the adapters, thread a owning
 // adapter a.  Latency bounds it (one read of the ids and a dozen block-wide
-// steps), so the scan's three sums go through one barrier and the histogram is
+// steps), so the scan's two sums go through one barrier and the histogram is
 // read once, all warps' rows at a time.
 // ----------------------------------------------------------------------------
 constexpr int kGroupThreads = 1024;
@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
     adapter_group_kernel(const int32_t* __restrict__ ids, int T, int n, int rows_cap, int32_t* __restrict__ order,
                          int32_t* __restrict__ offsets, int32_t* __restrict__ steps) {
   extern __shared__ int32_t table[];  // [kGroupWarps][n + 1]
-  __shared__ int32_t wsum[3][kGroupWarps];
+  __shared__ int32_t wsum[2][kGroupWarps];
   __shared__ int32_t none_total;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cols = n + 1;
@@ -52,8 +52,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
     __syncwarp();
   }
   __syncthreads();
-  // Adapter tid: its tokens in each warp, its padded rows, the 256-row units they meet and its 128-row
-  // projection tasks.
+  // Adapter tid: its tokens in each warp, its padded rows and its 128-row projection tasks.
   int at[kGroupWarps];
   int count = 0;
 #pragma unroll
@@ -94,48 +93,33 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
     total = __shfl_sync(kFull, x, 31);
     return __shfl_sync(kFull, x - v, warp);
   };
-  int none0, adapter_tasks, entries;
+  int none0, adapter_tasks;
   const int start = before(0, none0) + in_rows - padded, end = start + padded;
   const int task0 = before(1, adapter_tasks) + in_tasks - ntask;
-  const int u0 = start / kAdapterUnitRows, u1 = padded ? (end - 1) / kAdapterUnitRows : u0 - 1;
-  const int in_entries = warp_scan(u1 - u0 + 1);
-  if (lane == 31) wsum[2][warp] = in_entries;
   const int nnone = none_total, none_tasks = (nnone + kAdapterTaskRows - 1) / kAdapterTaskRows;
-  const int used = none0 + nnone, units = (used + kAdapterUnitRows - 1) / kAdapterUnitRows;
-  const AdapterSteps lay = adapter_steps_layout(rows_cap, n);
-  int32_t* unit_start = steps + lay.unit_start;
+  const int used = none0 + nnone;
+  int32_t* granules = steps + kAdapterStepsHeader;
+  int4* tasks = reinterpret_cast<int4*>(steps + adapter_tasks_offset(rows_cap));
   if (tid < n) {  // where each warp's tokens of this adapter start
 #pragma unroll
     for (int w = 0; w < kGroupWarps; ++w) table[w * cols + tid] = start + at[w];
   }
   __syncthreads();
-  const int entry0 = before(2, entries) + in_entries - (u1 - u0 + 1);
   if (tid < n) {
     offsets[tid] = start;
-    int4* en = reinterpret_cast<int4*>(steps + lay.entries) + entry0;
-    for (int u = u0; u <= u1; ++u) en[u - u0] = make_int4(tid, u, start, end);
-    // a unit's first entry: the adapter with its first row
-    for (int u = (start + kAdapterUnitRows - 1) / kAdapterUnitRows; u <= u1; ++u) unit_start[u] = entry0 + u - u0;
-    int4* tk = reinterpret_cast<int4*>(steps + lay.tasks) + task0;
-    for (int i = 0; i < ntask; ++i) tk[i] = make_int4(tid, start + i * kAdapterTaskRows, end, 0);
+    for (int i = start / kAdapterRowAlign; i < end / kAdapterRowAlign; ++i) granules[i] = tid;
+    for (int i = 0; i < ntask; ++i) tasks[task0 + i] = make_int4(tid, start + i * kAdapterTaskRows, end, 0);
     for (int i = start + count; i < end; ++i) order[i] = T;  // padding rows
   }
   if (tid == 0) {
-    steps[0] = units;
-    steps[1] = used;
-    steps[2] = entries;
-    steps[3] = adapter_tasks + none_tasks;
-    reinterpret_cast<int4*>(steps + lay.entries)[entries] = make_int4(-1, -1, 0, 0);  // sentinel
+    steps[0] = used;
+    steps[1] = adapter_tasks + none_tasks;
     offsets[n] = none0;
     offsets[n + 1] = used;
   }
-  // units past the adapters' rows have no entries
-  for (int u = (none0 + kAdapterUnitRows - 1) / kAdapterUnitRows + tid; u <= rows_cap / kAdapterUnitRows;
-       u += kGroupThreads)
-    unit_start[u] = entries;
+  for (int i = none0 / kAdapterRowAlign + tid; i < rows_cap / kAdapterRowAlign; i += kGroupThreads) granules[i] = n;
   for (int i = tid; i < none_tasks; i += kGroupThreads)
-    reinterpret_cast<int4*>(steps + lay.tasks)[adapter_tasks + i] =
-        make_int4(n, none0 + i * kAdapterTaskRows, used, 0);
+    tasks[adapter_tasks + i] = make_int4(n, none0 + i * kAdapterTaskRows, used, 0);
   for (int i = used + tid; i < rows_cap; i += kGroupThreads) order[i] = T;
   next = first;
   for (int tb = t0; tb < t1; tb += 32) {

@@ -62,6 +62,26 @@ __device__ __forceinline__ void umma_bf16_2sm_ta(uint32_t d_tmem, uint32_t a_tme
       : "memory");
 }
 
+// The adapters of a unit of `rows` rows from row0 on, one run of rows [lo, hi) (relative to row0) at a time: the
+// adapter of every 32 rows is in `granules` (n for the tokens without one), and every adapter starts such a granule.
+struct AdapterRun {
+  int row0, rows_used, rows, n;
+  int lo = 0, hi = 0, adapter = -1;
+  __device__ AdapterRun(int row0_, int rows_used_, int rows_, int n_)
+      : row0(row0_), rows_used(rows_used_), rows(min(rows_, rows_used_ - row0_)), n(n_) {}
+  __device__ __forceinline__ bool next(const int32_t* granules) {
+    lo = hi;
+    while (lo < rows) {
+      adapter = __ldg(granules + (row0 + lo) / kAdapterRowAlign);
+      if (adapter >= n) return false;  // the rest has none
+      hi = lo + kAdapterRowAlign;
+      while (hi < rows && __ldg(granules + (row0 + hi) / kAdapterRowAlign) == adapter) hi += kAdapterRowAlign;
+      return true;
+    }
+    return false;
+  }
+};
+
 // Mask word w (rows 32 w ..) with the bits outside rows [lo, hi) set.
 __device__ __forceinline__ uint32_t rows_off(int lo, int hi, int w) {
   const int a = min(max(lo - 32 * w, 0), 32), b = min(max(hi - 32 * w, 0), 32);
@@ -125,7 +145,8 @@ __device__ __forceinline__ void let_land(uint64_t* bars, int n, uint32_t issued,
 // =============================================================================
 // Forward: y[t] = W x[t] + B[a] p[t], W as the M operand
 // =============================================================================
-// A unit is 256 rows of W (128 a CTA of the pair) x 256 token rows.  A thread of
+// A unit is 256 rows of W (128 a CTA of the pair) x up to 256 token rows (a
+// multiple of 32, chosen so that the units fill the GPU's pairs evenly).  A thread of
 // the decode groups owns a row of W: it decodes 64 weights of a k-chunk into
 // registers and writes them to tensor memory, where the UMMAs read their M
 // operand.  Written to shared memory instead (as the expert block's tiles are,
@@ -133,7 +154,7 @@ __device__ __forceinline__ void let_land(uint64_t* bars, int n, uint32_t issued,
 // KB of operand reads a chunk on top of the token rows' 32 KB: more
 // shared-memory time than the chunk's 512 tensor cycles.
 //
-// The accumulator is two halves of 128 token rows, in three TMEM slots used in
+// The accumulator is a half of 128 token rows and one of the rest, in three TMEM slots used in
 // turn: while the epilogue empties a unit's first half, the next unit's first
 // half fills (its first chunks' second-half products follow once the slot is
 // free), so the tensor pipe does not wait for a whole epilogue.  Token rows are
@@ -166,7 +187,6 @@ constexpr int kTmemCols = 512;
 static_assert(kAOff + kGroups * BK / 2 <= kTmemCols, "TMEM budget");
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 static_assert(BM * E4B_MAX_RANK * 2 <= X_BYTES && kHalf * E4B_MAX_RANK * 2 <= X_BYTES, "low-rank operands fit a slot");
-static_assert(kAdapterUnitRows == 2 * kHalf && kAdapterRowAlign % 32 == 0, "column granules");
 }  // namespace adf
 
 struct AdapterFwdParams {
@@ -176,20 +196,20 @@ struct AdapterFwdParams {
   uint16_t* out;
   DeviceError* err;
   long long timeout_ns;
-  int K, N, T, r_pad, n_mt;
-  int unit_start, entries;  // places in `steps`
+  int K, N, T, n, r_pad, n_mt;
+  int n0, n1;  // token rows of a unit's halves, multiples of 32 (n1 may be 0)
 };
 
-// An adapter's rows [lo, hi) in half h of unit mu, relative to the half.
-__device__ __forceinline__ int2 half_range(const int4& en, int mu, int h) {
-  const int base = mu * kAdapterUnitRows + h * adf::kHalf;
-  return make_int2(min(max(en.z - base, 0), adf::kHalf), min(max(en.w - base, 0), adf::kHalf));
+// Rows [lo, hi) of a unit in its half h, relative to the half.
+__device__ __forceinline__ int2 half_range(const AdapterRun& run, int h, int n0, int n1) {
+  const int base = h ? n0 : 0, n = h ? n1 : n0;
+  return make_int2(min(max(run.lo - base, 0), n), min(max(run.hi - base, 0), n));
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
-    adapter_fwd_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_raw,
-                       const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_b,
-                       const AdapterFwdParams p) {
+    adapter_fwd_kernel(const __grid_constant__ CUtensorMap map_x0, const __grid_constant__ CUtensorMap map_x1,
+                       const __grid_constant__ CUtensorMap map_raw, const __grid_constant__ CUtensorMap map_p,
+                       const __grid_constant__ CUtensorMap map_b, const AdapterFwdParams p) {
   using namespace adf;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = align1024(smem_dyn);
@@ -242,11 +262,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const int n_units = p.steps[0] * p.n_mt;
+  const int rows_used = p.steps[0], unit_rows = p.n0 + p.n1;
+  const int n_units = (rows_used + unit_rows - 1) / unit_rows * p.n_mt;
   const int kchunks = p.K / BK;
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
-  const int32_t* unit_start = p.steps + p.unit_start;
-  const int4* entries = reinterpret_cast<const int4*>(p.steps + p.entries);  // (adapter, unit, first row, end row)
+  const int32_t* granules = p.steps + kAdapterStepsHeader;
 
   if (warp == 0) {
     // ------------------------------------------------ NF4 codes: 128 rows x 32 bytes a chunk (one lane)
@@ -273,7 +293,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
     // This CTA's rows of a half: 64 of its 128 (of an adapter's columns: its half of them).  A low-rank use is
     // two slots: the adapter's 128 rows of B, then its p rows of both halves.
     if (lane == 0) {
-      tma_prefetch_desc(&map_x);
+      tma_prefetch_desc(&map_x0);
       tma_prefetch_desc(&map_p);
       tma_prefetch_desc(&map_b);
       uint32_t s = 0, ph = 0, issued = 0, last_par = 0;
@@ -287,34 +307,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
       };
       bool ok = true;
       for (int u = pair; u < n_units && ok; u += n_pairs) {
-        const int mu = u / p.n_mt, w0 = (u % p.n_mt) * 256 + (int)rank * BM, t0 = mu * kAdapterUnitRows;
+        const int w0 = (u % p.n_mt) * 256 + (int)rank * BM, t0 = u / p.n_mt * unit_rows;
         for (int kc = 0; kc < kchunks; ++kc) {
           if (!(ok = mbar_wait(&xempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 212))) break;
           uint8_t* x = smem + s * X_BYTES;
-          mbar_arrive_expect_tx(&xfull[s], (uint32_t)X_BYTES);
-          tma_load_2d(x, &map_x, &xfull[s], kc * BK, t0 + 64 * (int)rank);
-          tma_load_2d(x + X_BYTES / 2, &map_x, &xfull[s], kc * BK, t0 + kHalf + 64 * (int)rank);
+          mbar_arrive_expect_tx(&xfull[s], (uint32_t)(unit_rows * BK));
+          tma_load_2d(x, &map_x0, &xfull[s], kc * BK, t0 + p.n0 / 2 * (int)rank);
+          if (p.n1) tma_load_2d(x + X_BYTES / 2, &map_x1, &xfull[s], kc * BK, t0 + p.n0 + p.n1 / 2 * (int)rank);
           issued_next();
         }
         if (!ok) break;
-        for (int i = __ldg(unit_start + mu);; ++i) {
-          const int4 en = __ldg(entries + i);
-          if (en.y != mu) break;
+        AdapterRun run{t0, rows_used, unit_rows, p.n};
+        while (run.next(granules)) {
           const uint32_t s1 = (s + 1 == SA) ? 0 : s + 1, ph1 = (s + 1 == SA) ? ph ^ 1 : ph;
           if (!(ok = mbar_wait(&xempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 210))) break;
           if (!(ok = mbar_wait(&xempty[s1], ph1 ^ 1, ctl, p.err, p.timeout_ns, 210))) break;
-          const int2 h0 = half_range(en, mu, 0), h1 = half_range(en, mu, 1);
+          const int2 h0 = half_range(run, 0, p.n0, p.n1), h1 = half_range(run, 1, p.n0, p.n1);
           const int n0 = (h0.y - h0.x) / 2, n1 = (h1.y - h1.x) / 2;  // this CTA's p rows, multiples of 16
           mbar_arrive_expect_tx(&xfull[s], (uint32_t)((BM + n0 + n1) * 2 * p.r_pad));
           uint8_t* b = smem + s * X_BYTES;
-          tma_load_3d(b, &map_b, &xfull[s], 0, w0, en.x);
-          tma_load_3d(b + 128 * p.r_pad, &map_b, &xfull[s], 0, w0 + 64, en.x);
+          tma_load_3d(b, &map_b, &xfull[s], 0, w0, run.adapter);
+          tma_load_3d(b + 128 * p.r_pad, &map_b, &xfull[s], 0, w0 + 64, run.adapter);
           uint8_t* pr = smem + s1 * X_BYTES;
           for (int k = 0; k < n0; k += 16)
             tma_load_2d(pr + k * 2 * p.r_pad, &map_p, &xfull[s], 0, t0 + h0.x + n0 * (int)rank + k);
           pr += 64 * 2 * p.r_pad;
           for (int k = 0; k < n1; k += 16)
-            tma_load_2d(pr + k * 2 * p.r_pad, &map_p, &xfull[s], 0, t0 + kHalf + h1.x + n1 * (int)rank + k);
+            tma_load_2d(pr + k * 2 * p.r_pad, &map_p, &xfull[s], 0, t0 + p.n0 + h1.x + n1 * (int)rank + k);
           mbar_arrive(&xfull[s1]);
           issued_next();
           issued_next();
@@ -326,11 +345,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
   } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------ UMMA issuer (even CTA, one elected lane)
     if (elect_one_sync()) {
-      const uint32_t idesc = make_idesc_bf16(256, kHalf, false, false);
+      const uint32_t idesc0 = make_idesc_bf16(256, p.n0, false, false), idesc1 = make_idesc_bf16(256, p.n1, false, false);
       const uint32_t lswz = swz_for_row_bytes(2 * p.r_pad);
       const uint32_t x_u = smem_u32(smem);
       const uint64_t xdesc0 = make_sdesc(x_u, 16, 1024, kSw128);
       uint32_t sx = 0, g = 0, fs = 0, fph = 0, hs = 0;  // ring slot, decode group, MMA step, accumulator halves used
+      const uint32_t halves = p.n1 ? 2 : 1;
       bool ok = true;
       auto next_x = [&]() { sx = (sx + 1 == SA) ? 0 : sx + 1; };
       auto next_g = [&]() { g = (g + 1) % kGroups; };
@@ -357,17 +377,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
         const uint64_t xd = xdesc0 + (uint64_t)((s * X_BYTES + h * (X_BYTES / 2)) >> 4);
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk)
-          umma_bf16_2sm_ta(d, a + 8 * kk, xd + 2 * kk, idesc, (!first || kk > 0) ? 1u : 0u);
+          umma_bf16_2sm_ta(d, a + 8 * kk, xd + 2 * kk, h ? idesc1 : idesc0, (!first || kk > 0) ? 1u : 0u);
       };
       auto release = [&](uint32_t s, uint32_t gg) {
         umma_commit_2sm(&xempty[s], 0x3);
         umma_commit_2sm(&aempty[gg], 0x3);
       };
-      for (int u = pair; u < n_units && ok; u += n_pairs, hs += 2) {
-        const int mu = u / p.n_mt;
+      for (int u = pair; u < n_units && ok; u += n_pairs, hs += halves) {
         const uint32_t d0 = tmem + (hs % kSlots) * kHalf, d1 = tmem + ((hs + 1) % kSlots) * kHalf;
-        int i = __ldg(unit_start + mu);
-        int4 en = __ldg(entries + i);
         // First chunks: the first half at once, the second when its slot has been drained.
         const int lead = min(kGroups, kchunks);
         const uint32_t sx0 = sx, g0 = g;
@@ -379,11 +396,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
           next_g();
           next_f();
         }
-        if (!ok || !(ok = wait_slot(hs + 1))) break;
+        if (!ok || (p.n1 && !(ok = wait_slot(hs + 1)))) break;
         sx = sx0;
         g = g0;
         for (int kc = 0; kc < lead; ++kc) {
-          half(d1, sx, g, 1, kc == 0);
+          if (p.n1) half(d1, sx, g, 1, kc == 0);
           release(sx, g);
           next_x();
           next_g();
@@ -396,20 +413,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
           half(d0, sx, g, 0, false);
           // peek at the next chunk while these products run
           ready = kc + 1 < kchunks && mbar_test_wait_cluster(&full[fs], fph);
-          half(d1, sx, g, 1, false);
+          if (p.n1) half(d1, sx, g, 1, false);
           release(sx, g);
           next_x();
           next_g();
         }
         if (!ok) break;
         // One K = r product per adapter and half, at the adapter's columns.
-        for (; en.y == mu; en = __ldg(entries + ++i)) {
+        AdapterRun run{u / p.n_mt * unit_rows, rows_used, unit_rows, p.n};
+        while (run.next(granules)) {
           if (!(ok = wait_step())) break;
           const uint32_t sx1 = (sx + 1 == SA) ? 0 : sx + 1;
           const uint32_t b_u = x_u + sx * X_BYTES, p_u = x_u + sx1 * X_BYTES;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int2 hr = half_range(en, mu, h);
+            const int2 hr = half_range(run, h, p.n0, p.n1);
             if (hr.y > hr.x) {
               const uint32_t id = make_idesc_bf16(256, hr.y - hr.x, false, false);
               for (int ks = 0; ks < p.r_pad / 16; ++ks)
@@ -425,7 +443,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
         }
         if (!ok) break;
         umma_commit_2sm(&accfull[hs % kSlots], 0x3);
-        umma_commit_2sm(&accfull[(hs + 1) % kSlots], 0x3);
+        if (p.n1) umma_commit_2sm(&accfull[(hs + 1) % kSlots], 0x3);
       }
       umma_commit_2sm(drain, 0x1);
       const uint64_t t0 = globaltimer_ns();
@@ -457,7 +475,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
       fs = (fs + 1 == SA) ? 0 : fs + 1;
     };
     for (int u = pair; u < n_units && ok; u += n_pairs) {
-      const int mu = u / p.n_mt;
       for (int kc = 0; kc < kchunks; ++kc, ++j) {
         ok = __all_sync(kFull, mbar_wait(&adone[j % kGroups], (j / kGroups) & 1, ctl, p.err, p.timeout_ns, 251));
         if (!ok || !(ok = wait_x())) break;
@@ -466,7 +483,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
         signal();
       }
       if (!ok) break;
-      for (int i = __ldg(unit_start + mu); __ldg(entries + i).y == mu; ++i) {
+      AdapterRun run{u / p.n_mt * unit_rows, rows_used, unit_rows, p.n};
+      while (run.next(granules)) {
         if (!(ok = wait_x()) || !(ok = wait_x())) break;
         signal();
       }
@@ -534,18 +552,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
     uint32_t hs = 0;
     bool ok = true;
     for (int u = pair; u < n_units && ok; u += n_pairs) {
-      const int mu = u / p.n_mt, w0 = (u % p.n_mt) * 256 + (int)rank * BM + 32 * qrt;
+      const int t0 = u / p.n_mt * unit_rows, w0 = (u % p.n_mt) * 256 + (int)rank * BM + 32 * qrt;
       const int col = w0 + 8 * (lane & 3);
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h, ++hs) {
+      for (int h = 0; h < (p.n1 ? 2 : 1); ++h, ++hs) {
         const uint32_t b = hs % kSlots;
         ok = __all_sync(kFull, mbar_wait(&accfull[b], (hs / kSlots) & 1, ctl, p.err, p.timeout_ns, 240));
         if (!ok) break;
         tc_fence_after();
         const uint32_t tl = tmem + b * kHalf + ((uint32_t)(qrt * 32) << 16);
 #pragma unroll 1
-        for (int jj = 0; jj < kHalf; jj += 32) {
-          const int tok = __ldg(p.order + mu * kAdapterUnitRows + h * kHalf + jj + lane);
+        for (int jj = 0; jj < (h ? p.n1 : p.n0); jj += 32) {
+          const int row0 = t0 + (h ? p.n0 : 0) + jj;
+          const int tok = row0 < rows_used ? __ldg(p.order + row0 + lane) : p.T;
           if (!__any_sync(kFull, tok < p.T)) continue;
           float v[32];
           tmem_ld32(tl + jj, v);
@@ -631,8 +650,7 @@ struct AdapterDgradParams {
   uint16_t* out;
   DeviceError* err;
   long long timeout_ns;
-  int T, N, K, r_pad, n_nt;
-  int unit_start, entries;  // places in `steps`
+  int T, N, K, n, r_pad, n_nt;
 };
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
@@ -693,12 +711,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const int n_units = p.steps[0] * p.n_nt;
+  const int rows_used = p.steps[0];
+  const int n_units = (rows_used + kAdapterUnitRows - 1) / kAdapterUnitRows * p.n_nt;
   const int kchunks = (p.N + BK - 1) / BK;
   const int blocks_per_row = p.K / 64;
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
-  const int32_t* unit_start = p.steps + p.unit_start;
-  const int4* entries = reinterpret_cast<const int4*>(p.steps + p.entries);  // (adapter, unit, first row, end row)
+  const int32_t* granules = p.steps + kAdapterStepsHeader;
 
   if (warp == 0) {
     // ------------------------------------------------ NF4 codes (one lane)
@@ -746,9 +764,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
           issued_next();
         }
         if (!ok) break;
-        for (int i = __ldg(unit_start + mu);; ++i) {
-          const int4 en = __ldg(entries + i);
-          if (en.y != mu) break;
+        AdapterRun run{mu * kAdapterUnitRows, rows_used, kAdapterUnitRows, p.n};
+        while (run.next(granules)) {
           const uint32_t s1 = (s + 1 == SA) ? 0 : s + 1, ph1 = (s + 1 == SA) ? ph ^ 1 : ph;
           if (!(ok = mbar_wait(&aempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 310))) break;
           if (!(ok = mbar_wait(&aempty[s1], ph1 ^ 1, ctl, p.err, p.timeout_ns, 310))) break;
@@ -756,8 +773,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
           uint8_t* lb = aring + s1 * A_BYTES;
           mbar_arrive_expect_tx(&xfull[s], (uint32_t)(512 * p.r_pad));
           tma_load_2d(la, &map_la, &xfull[s], 0, row0);
-          tma_load_3d(lb, &map_lb, &xfull[s], c0, 0, en.x);
-          tma_load_3d(lb + 128 * p.r_pad, &map_lb, &xfull[s], c0 + 64, 0, en.x);
+          tma_load_3d(lb, &map_lb, &xfull[s], c0, 0, run.adapter);
+          tma_load_3d(lb + 128 * p.r_pad, &map_lb, &xfull[s], c0 + 64, 0, run.adapter);
           mbar_arrive(&xfull[s1]);
           issued_next();
           issued_next();
@@ -791,8 +808,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
         const int mu = u / p.n_nt;
         const uint32_t b = ti & 1, use = ti >> 1;
         const uint32_t d = tmem + b * 256;
-        int i = __ldg(unit_start + mu);
-        int4 en = __ldg(entries + i);
         if (!(ok = mbar_wait_cluster(&accempty[b], (use & 1) ^ 1, ctl, p.err, p.timeout_ns, 320))) break;
         tc_fence_after();
         if (!(ok = wait_step())) break;
@@ -821,14 +836,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
         }
         if (!ok) break;
         // One K = r step per adapter of the tile, into its own rows.
-        for (; en.y == mu; en = __ldg(entries + ++i)) {
+        AdapterRun run{mu * kAdapterUnitRows, rows_used, kAdapterUnitRows, p.n};
+        while (run.next(granules)) {
           if (!(ok = wait_step())) break;
           tc_fence_after();
           const uint32_t sa1 = (sa + 1 == SA) ? 0 : sa + 1;
           const uint32_t la_u = a_u + sa * A_BYTES, lb_u = a_u + sa1 * A_BYTES;
           uint32_t off[8];
 #pragma unroll
-          for (int w = 0; w < 8; ++w) off[w] = rows_off(en.z - mu * 256, en.w - mu * 256, w);
+          for (int w = 0; w < 8; ++w) off[w] = rows_off(run.lo, run.hi, w);
           for (int ks = 0; ks < p.r_pad / 16; ++ks) {
             const uint64_t bd = make_sdesc(lb_u + 2048 * ks, 128 * p.r_pad, 1024, kSw128);
             umma_bf16_2sm_masked(d, make_sdesc(la_u + 32 * ks, 16, 16 * p.r_pad, lswz), bd, idesc, off);
@@ -879,7 +895,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
         signal();
       }
       if (!ok) break;
-      for (int i = __ldg(unit_start + mu); __ldg(entries + i).y == mu; ++i) {
+      AdapterRun run{mu * kAdapterUnitRows, rows_used, kAdapterUnitRows, p.n};
+      while (run.next(granules)) {
         if (!(ok = wait_a()) || !(ok = wait_a())) break;
         signal();
       }
@@ -1091,7 +1108,7 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int n_tasks = p.steps[3];
+  const int n_tasks = p.steps[1];
   const int4* tasks = reinterpret_cast<const int4*>(p.steps + p.tasks);  // (adapter, first row, end row, 0)
   const int chunks = (p.R + BK - 1) / BK, rank = (int)blockIdx.x % p.S;
   const int k_lo = rank * chunks / p.S, k_hi = (rank + 1) * chunks / p.S;  // this block's chunks of R
@@ -1614,18 +1631,42 @@ cudaError_t map_u8_2d(CUtensorMap* m, const void* base, uint64_t bytes, uint64_t
 }
 }  // namespace
 
+// Token rows of a forward unit: the ones that take the pairs the fewest turns, a turn's time being the larger of
+// decoding a chunk (about 400 cycles whatever the rows) and its products.
+static int fwd_unit_rows(const AdapterProjHost& h, int n_mt, int pairs) {
+  const int64_t rows = h.T + 16 * (int64_t)(h.T < h.n + 1 ? h.T : h.n + 1);  // with an average of padding
+  int best = 256;
+  int64_t best_cost = INT64_MAX;
+  for (int nt = 256; nt >= 96; nt -= 32) {
+    const int64_t turns = ((rows + nt - 1) / nt * n_mt + pairs - 1) / pairs;
+    const int64_t cost = turns * (nt > 128 ? 180 + 2 * nt : 440);
+    if (cost < best_cost) {
+      best = nt;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
 cudaError_t launch_adapter_fwd(const AdapterProjHost& h, const uint16_t* rows, const uint16_t* low, const uint16_t* B,
                                uint16_t* y, int num_sms, cudaStream_t stream) {
   const int rp = rank_padded(h.r);
   const CUtensorMapSwizzle rswz = swizzle_for_bytes(2 * rp);
-  CUtensorMap mx, mraw, mp, mb;
+  const int n_mt = (h.N + 255) / 256, unit_rows = fwd_unit_rows(h, n_mt, num_sms / 2);
+  AdapterFwdParams p;
+  p.n0 = unit_rows < adf::kHalf ? unit_rows : adf::kHalf;
+  p.n1 = unit_rows - p.n0;
+  CUtensorMap mx0, mx1, mraw, mp, mb;
   cudaError_t err;
-  if ((err = map_bf16_2d(&mx, rows, h.K, h.rows_cap, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return err;
+  if ((err = map_bf16_2d(&mx0, rows, h.K, h.rows_cap, 64, p.n0 / 2, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess)
+    return err;
+  mx1 = mx0;
+  if (p.n1 &&
+      (err = map_bf16_2d(&mx1, rows, h.K, h.rows_cap, 64, p.n1 / 2, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess)
+    return err;
   if ((err = map_u8_2d(&mraw, h.nf4, h.K / 2, h.N, 32, 128)) != cudaSuccess) return err;
   if ((err = map_bf16_2d(&mp, low, h.r, h.rows_cap, rp, 16, rswz)) != cudaSuccess) return err;
   if ((err = map_bf16_3d(&mb, B, h.r, h.N, h.n, rp, 64, rswz)) != cudaSuccess) return err;
-  const AdapterSteps lay = adapter_steps_layout(h.rows_cap, h.n);
-  AdapterFwdParams p;
   p.absmax = h.absmax;
   p.order = h.order;
   p.steps = h.steps;
@@ -1636,14 +1677,13 @@ cudaError_t launch_adapter_fwd(const AdapterProjHost& h, const uint16_t* rows, c
   p.N = h.N;
   p.T = h.T;
   p.r_pad = rp;
-  p.n_mt = (h.N + 255) / 256;
-  p.unit_start = lay.unit_start;
-  p.entries = lay.entries;
-  const int64_t units = h.rows_cap / kAdapterUnitRows * p.n_mt;
+  p.n = h.n;
+  p.n_mt = n_mt;
+  const int64_t units = (h.rows_cap + unit_rows - 1) / unit_rows * n_mt;
   const int grid = 2 * (int)(units < num_sms / 2 ? units : num_sms / 2);
   if ((err = set_smem(adapter_fwd_kernel, adf::SMEM_BYTES)) != cudaSuccess) return err;
   LaunchScope scope("adapter_fwd", stream);
-  adapter_fwd_kernel<<<grid, adf::kThreads, adf::SMEM_BYTES, stream>>>(mx, mraw, mp, mb, p);
+  adapter_fwd_kernel<<<grid, adf::kThreads, adf::SMEM_BYTES, stream>>>(mx0, mx1, mraw, mp, mb, p);
   return cudaGetLastError();
 }
 
@@ -1656,7 +1696,6 @@ cudaError_t launch_adapter_dgrad(const AdapterProjHost& h, const uint16_t* rows,
   if ((err = map_u8_2d(&mraw, h.nf4, h.K / 2, h.N, 64, 64)) != cudaSuccess) return err;
   if ((err = map_bf16_2d(&mla, low, h.r, h.rows_cap, rp, 128, swizzle_for_bytes(2 * rp))) != cudaSuccess) return err;
   if ((err = map_bf16_3d(&mlb, A, h.K, h.r, h.n, 64, rp, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return err;
-  const AdapterSteps lay = adapter_steps_layout(h.rows_cap, h.n);
   AdapterDgradParams p;
   p.absmax = h.absmax;
   p.order = h.order;
@@ -1668,9 +1707,8 @@ cudaError_t launch_adapter_dgrad(const AdapterProjHost& h, const uint16_t* rows,
   p.N = h.N;
   p.K = h.K;
   p.r_pad = rp;
+  p.n = h.n;
   p.n_nt = (h.K + 255) / 256;
-  p.unit_start = lay.unit_start;
-  p.entries = lay.entries;
   const int64_t units = h.rows_cap / kAdapterUnitRows * p.n_nt;
   const int grid = 2 * (int)(units < num_sms / 2 ? units : num_sms / 2);
   if ((err = set_smem(adapter_dgrad_kernel, adg::SMEM_BYTES)) != cudaSuccess) return err;
@@ -1703,7 +1741,7 @@ cudaError_t launch_adapter_rows(const AdapterProjHost& h, bool mn, const uint16_
   p.T = h.T;
   p.r = h.r;
   p.r_pad = rp;
-  p.tasks = adapter_steps_layout(h.rows_cap, h.n).tasks;
+  p.tasks = (int)adapter_tasks_offset(h.rows_cap);
   // two blocks an SM; R is split while all clusters fit at once and every block keeps two chunks
   const int64_t cap = h.rows_cap / kAdapterTaskRows + h.n + 1, fit = 2 * (int64_t)num_sms;
   const int chunks = (R + adp::BK - 1) / adp::BK;

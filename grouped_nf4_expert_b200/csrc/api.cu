@@ -137,7 +137,7 @@ ServeProjLayout serve_proj_layout(const e4b_proj_dims* d, int32_t T) {
   l.order = sizeof(DeviceError);
   l.offsets = l.order + up((size_t)rows * 4);
   l.steps = l.offsets + up((size_t)(d->n_adapters + 2) * 4);
-  l.low = l.steps + up((size_t)adapter_steps_layout(rows, d->n_adapters).total * 4);
+  l.low = l.steps + up((size_t)adapter_steps_cap(rows, d->n_adapters) * 4);
   size_t low = (size_t)rows * d->r * 2;
   if (T <= kAdapterGemvTokens) low = (size_t)adapter_gemv_shares(T, d->r) * T * d->r * 4;
   l.rows = l.low + up(low);
@@ -750,7 +750,7 @@ e4b_status e4b_proj_get_sizes(const e4b_proj_dims* dims, int32_t T, e4b_proj_siz
   E4B_TRY(check_proj_dims(dims, T));
   if (out == nullptr) return E4B_ERR_INVALID_ARG;
   out->rows_cap = adapter_rows_cap(T, dims->n_adapters);
-  out->steps_cap = adapter_steps_layout(out->rows_cap, dims->n_adapters).total;
+  out->steps_cap = adapter_steps_cap(out->rows_cap, dims->n_adapters);
   out->workspace_bytes = proj_workspace_bytes(dims, T);
   out->serve_workspace_bytes = serve_proj_layout(dims, T).total;
   return E4B_OK;

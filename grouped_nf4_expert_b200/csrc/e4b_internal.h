@@ -196,7 +196,7 @@ cudaError_t launch_wgrad(const WgradHost& h, int num_sms, cudaStream_t stream);
 
 // ---- adapters beside a shared projection (adapters.cu, adapters_gemm.cu,
 // adapters_serve.cu)
-constexpr int kAdapterUnitRows = 256;  // rows of a GEMM unit (a CTA pair)
+constexpr int kAdapterUnitRows = 256;  // rows of an input-gradient unit (a CTA pair)
 constexpr int kAdapterGemvTokens = 16;    // most tokens of the base product on warp instructions
 constexpr int kAdapterSmallTokens = 256;  // most tokens of the small-batch kernels
 constexpr int kAdapterTaskRows = 128;  // rows of a low-rank projection task (one adapter's)
@@ -205,21 +205,14 @@ inline int64_t adapter_rows_cap(int64_t T, int n) {
   const int64_t groups = T < n + 1 ? T : n + 1;
   return (T + (kAdapterRowAlign - 1) * groups + 255) / 256 * 256;
 }
-// Work list layout (int32): header ([0] units, [1] rows used, [2] entries, [3] tasks), the first entry of
-// each 256-row unit, entries (adapter, unit, first row, end row of the adapter) by unit with a sentinel
-// (unit -1), tasks (adapter, first row, end row of the adapter, 0).
-struct AdapterSteps {
-  int unit_start, entries, tasks;
-  int64_t total;
-};
-__host__ __device__ inline AdapterSteps adapter_steps_layout(int64_t rows_cap, int n) {
-  const int64_t units = rows_cap / kAdapterUnitRows;
-  AdapterSteps a;
-  a.unit_start = 8;
-  a.entries = (int)((8 + units + 1 + 3) / 4 * 4);
-  a.tasks = (int)(a.entries + 4 * (units + n + 1));
-  a.total = a.tasks + 4 * (rows_cap / kAdapterTaskRows + n + 1);
-  return a;
+// Work list layout (int32): header ([0] rows used, [1] tasks), the adapter of every 32 rows (n: none), tasks
+// (adapter, first row, end row of the adapter, 0).
+constexpr int kAdapterStepsHeader = 8;
+__host__ __device__ inline int64_t adapter_tasks_offset(int64_t rows_cap) {
+  return kAdapterStepsHeader + rows_cap / kAdapterRowAlign;  // rows_cap / 32 is a multiple of 8
+}
+inline int64_t adapter_steps_cap(int64_t rows_cap, int n) {
+  return adapter_tasks_offset(rows_cap) + 4 * (rows_cap / kAdapterTaskRows + n + 1);
 }
 cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int32_t* order, int32_t* offsets, int32_t* steps,
                                  cudaStream_t stream);
