@@ -154,18 +154,21 @@ __device__ __forceinline__ void let_land(uint64_t* bars, int n, uint32_t issued,
 // KB of operand reads a chunk on top of the token rows' 32 KB: more
 // shared-memory time than the chunk's 512 tensor cycles.
 //
-// The accumulator is a half of 128 token rows and one of the rest, in three TMEM slots used in
-// turn: while the epilogue empties a unit's first half, the next unit's first
-// half fills (its first chunks' second-half products follow once the slot is
-// free), so the tensor pipe does not wait for a whole epilogue.  Token rows are
+// The accumulator is a half of 128 token rows and one of the rest, in three TMEM
+// slots used in turn, and each half has an issuing warp of its own: while the
+// epilogue empties a unit's first half, the next unit's first half fills, and the
+// second follows once its slot is free.  (One warp handing in both halves'
+// products took 720 cycles a chunk, against 512 in the tensor pipe: its
+// instruction stream, not the operands, was the limit.)  Token rows are
 // accumulator columns, so an adapter's K = r product is issued at its own
 // columns: adapters' rows start at multiples of 32, the column granule of a pair
 // UMMA.
 //
-// Roles per CTA: warp 0 codes, warp 1 TMEM owner and (even CTA) issuer, warp 2
-// relay of operand readiness to the even CTA, warp 3 token rows and low-rank
-// operands, warps 4-19 four decode groups taking the chunks round robin, warps
-// 20-23 epilogue (32 rows of W each).
+// Roles per CTA: warp 0 codes, warp 1 TMEM owner and (even CTA) issuer of the
+// first halves, warp 2 relay of operand readiness to the even CTA, warp 3 token
+// rows and low-rank operands, warps 4-19 four decode groups taking the chunks
+// round robin, warps 20-23 epilogue (32 rows of W each), warp 24 (even CTA)
+// issuer of the second halves.
 namespace adf {
 constexpr int BM = 128, BK = 64;
 constexpr int kHalf = 128;                    // token rows of an accumulator half
@@ -182,7 +185,8 @@ constexpr int kEpiWarpBytes = 32 * kEpiPitch;
 constexpr int BAR_OFF = EPI_OFF + 4 * kEpiWarpBytes;
 constexpr int SMEM_BYTES = BAR_OFF + 1024 + 1024;
 constexpr int kEpiWarp0 = 4 + kGroups * kGroupWarps;
-constexpr int kThreads = 32 * (kEpiWarp0 + 4);
+constexpr int kIssuer1 = kEpiWarp0 + 4;
+constexpr int kThreads = 32 * (kIssuer1 + 1);
 constexpr int kTmemCols = 512;
 static_assert(kAOff + kGroups * BK / 2 <= kTmemCols, "TMEM budget");
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -224,13 +228,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
   uint64_t* aempty = adone + kGroups;           // [kGroups] decoded chunk consumed by the UMMAs
   uint64_t* accfull = aempty + kGroups;         // [kSlots] accumulator half complete
   uint64_t* accempty = accfull + kSlots;        // [kSlots] (even CTA) half drained in both CTAs
-  uint64_t* drain = accempty + kSlots;          // (even CTA) all issued UMMAs finished
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  CtaControl* ctl = reinterpret_cast<CtaControl*>(drain + 2);
-  uint32_t* sig = reinterpret_cast<uint32_t*>(drain + 3);
+  uint64_t* drain = accempty + kSlots;          // [2] (even CTA) all of an issuer's UMMAs finished
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+  CtaControl* ctl = reinterpret_cast<CtaControl*>(drain + 3);
+  uint32_t* sig = reinterpret_cast<uint32_t*>(drain + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
+  const int halves = p.n1 ? 2 : 1;
   if (threadIdx.x == 0) {
     for (int r = 0; r < RAW_STAGES; ++r) {
       mbar_init(&raw_full[r], 1);
@@ -238,18 +243,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
     }
     for (int s = 0; s < SA; ++s) {
       mbar_init(&xfull[s], 1);
-      mbar_init(&xempty[s], 1);
+      mbar_init(&xempty[s], halves);
       mbar_init(&full[s], 1);
     }
     for (int g = 0; g < kGroups; ++g) {
       mbar_init(&adone[g], kGroupWarps);
-      mbar_init(&aempty[g], 1);
+      mbar_init(&aempty[g], halves);
     }
     for (int b = 0; b < kSlots; ++b) {
       mbar_init(&accfull[b], 1);
       mbar_init(&accempty[b], 8);
     }
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     ctl->abort = 0;
     fence_mbar_init();
   }
@@ -342,98 +348,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
       if (!ok) let_land(xfull, SA, issued, last_par, p.timeout_ns);
     }
     __syncwarp();
-  } else if (warp == 1 && rank == 0) {
-    // ------------------------------------------------ UMMA issuer (even CTA, one elected lane)
-    if (elect_one_sync()) {
-      const uint32_t idesc0 = make_idesc_bf16(256, p.n0, false, false), idesc1 = make_idesc_bf16(256, p.n1, false, false);
+  } else if (warp == 1 || warp == kIssuer1) {
+    // ------------------------------------------------ UMMA issuers (even CTA, one elected lane each)
+    const int h = warp == 1 ? 0 : 1;
+    if (rank == 0 && h < halves && elect_one_sync()) {
+      const uint32_t idesc = make_idesc_bf16(256, h ? p.n1 : p.n0, false, false);
       const uint32_t lswz = swz_for_row_bytes(2 * p.r_pad);
       const uint32_t x_u = smem_u32(smem);
-      const uint64_t xdesc0 = make_sdesc(x_u, 16, 1024, kSw128);
-      uint32_t sx = 0, g = 0, fs = 0, fph = 0, hs = 0;  // ring slot, decode group, MMA step, accumulator halves used
-      const uint32_t halves = p.n1 ? 2 : 1;
+      const uint64_t xdesc0 = make_sdesc(x_u + h * (X_BYTES / 2), 16, 1024, kSw128);
+      uint32_t sx = 0, g = 0, fs = 0, fph = 0, hs = h;  // ring slot, decode group, MMA step, accumulator half used
       bool ok = true;
       auto next_x = [&]() { sx = (sx + 1 == SA) ? 0 : sx + 1; };
-      auto next_g = [&]() { g = (g + 1) % kGroups; };
       auto next_f = [&]() {
         if (++fs == SA) {
           fs = 0;
           fph ^= 1;
         }
       };
-      auto wait_step = [&]() -> bool {
-        const bool r = mbar_wait_cluster(&full[fs], fph, ctl, p.err, p.timeout_ns, 223);
-        tc_fence_after();
-        return r;
-      };
-      auto wait_slot = [&](uint32_t use) -> bool {  // accumulator half number `use`
-        const bool r =
-            mbar_wait_cluster(&accempty[use % kSlots], ((use / kSlots) & 1) ^ 1, ctl, p.err, p.timeout_ns, 220);
-        tc_fence_after();
-        return r;
-      };
-      // the products of one chunk (ring slot s, decode group gg) into half h
-      auto half = [&](uint32_t d, uint32_t s, uint32_t gg, int h, bool first) {
-        const uint32_t a = tmem + kAOff + gg * (BK / 2);
-        const uint64_t xd = xdesc0 + (uint64_t)((s * X_BYTES + h * (X_BYTES / 2)) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk)
-          umma_bf16_2sm_ta(d, a + 8 * kk, xd + 2 * kk, h ? idesc1 : idesc0, (!first || kk > 0) ? 1u : 0u);
-      };
-      auto release = [&](uint32_t s, uint32_t gg) {
-        umma_commit_2sm(&xempty[s], 0x3);
-        umma_commit_2sm(&aempty[gg], 0x3);
-      };
+      auto wait_step = [&]() -> bool { return mbar_wait_cluster(&full[fs], fph, ctl, p.err, p.timeout_ns, 223); };
       for (int u = pair; u < n_units && ok; u += n_pairs, hs += halves) {
-        const uint32_t d0 = tmem + (hs % kSlots) * kHalf, d1 = tmem + ((hs + 1) % kSlots) * kHalf;
-        // First chunks: the first half at once, the second when its slot has been drained.
-        const int lead = min(kGroups, kchunks);
-        const uint32_t sx0 = sx, g0 = g;
-        if (!(ok = wait_slot(hs))) break;
-        for (int kc = 0; kc < lead; ++kc) {
-          if (!(ok = wait_step())) break;
-          half(d0, sx, g, 0, kc == 0);
-          next_x();
-          next_g();
-          next_f();
-        }
-        if (!ok || (p.n1 && !(ok = wait_slot(hs + 1)))) break;
-        sx = sx0;
-        g = g0;
-        for (int kc = 0; kc < lead; ++kc) {
-          if (p.n1) half(d1, sx, g, 1, kc == 0);
-          release(sx, g);
-          next_x();
-          next_g();
-        }
+        const uint32_t slot = hs % kSlots, d = tmem + slot * kHalf;
+        if (!(ok = mbar_wait_cluster(&accempty[slot], ((hs / kSlots) & 1) ^ 1, ctl, p.err, p.timeout_ns, 220))) break;
+        tc_fence_after();
         bool ready = false;
-        for (int kc = lead; kc < kchunks; ++kc) {
+        for (int kc = 0; kc < kchunks; ++kc) {
           if (!ready && !(ok = wait_step())) break;
           tc_fence_after();
           next_f();
-          half(d0, sx, g, 0, false);
-          // peek at the next chunk while these products run
-          ready = kc + 1 < kchunks && mbar_test_wait_cluster(&full[fs], fph);
-          if (p.n1) half(d1, sx, g, 1, false);
-          release(sx, g);
+          const uint32_t a = tmem + kAOff + g * (BK / 2);
+          const uint64_t xd = xdesc0 + (uint64_t)(sx * (X_BYTES >> 4));
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            umma_bf16_2sm_ta(d, a + 8 * kk, xd + 2 * kk, idesc, (kc > 0 || kk > 0) ? 1u : 0u);
+            // peek at the next chunk while these products run
+            if (kk == 1) ready = kc + 1 < kchunks && mbar_test_wait_cluster(&full[fs], fph);
+          }
+          umma_commit_2sm(&xempty[sx], 0x3);
+          umma_commit_2sm(&aempty[g], 0x3);
           next_x();
-          next_g();
+          g = (g + 1) % kGroups;
         }
         if (!ok) break;
-        // One K = r product per adapter and half, at the adapter's columns.
+        // One K = r product per adapter, at the adapter's columns of this half.
         AdapterRun run{u / p.n_mt * unit_rows, rows_used, unit_rows, p.n};
         while (run.next(granules)) {
           if (!(ok = wait_step())) break;
+          tc_fence_after();
           const uint32_t sx1 = (sx + 1 == SA) ? 0 : sx + 1;
-          const uint32_t b_u = x_u + sx * X_BYTES, p_u = x_u + sx1 * X_BYTES;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int2 hr = half_range(run, h, p.n0, p.n1);
-            if (hr.y > hr.x) {
-              const uint32_t id = make_idesc_bf16(256, hr.y - hr.x, false, false);
-              for (int ks = 0; ks < p.r_pad / 16; ++ks)
-                umma_bf16_2sm((h ? d1 : d0) + hr.x, make_sdesc(b_u + 32 * ks, 16, 16 * p.r_pad, lswz),
-                              make_sdesc(p_u + h * 128 * p.r_pad + 32 * ks, 16, 16 * p.r_pad, lswz), id, 1u);
-            }
+          const uint32_t b_u = x_u + sx * X_BYTES, p_u = x_u + sx1 * X_BYTES + h * 128 * p.r_pad;
+          const int2 hr = half_range(run, h, p.n0, p.n1);
+          if (hr.y > hr.x) {
+            const uint32_t id = make_idesc_bf16(256, hr.y - hr.x, false, false);
+            for (int ks = 0; ks < p.r_pad / 16; ++ks)
+              umma_bf16_2sm(d + hr.x, make_sdesc(b_u + 32 * ks, 16, 16 * p.r_pad, lswz),
+                            make_sdesc(p_u + 32 * ks, 16, 16 * p.r_pad, lswz), id, 1u);
           }
           umma_commit_2sm(&xempty[sx], 0x3);
           umma_commit_2sm(&xempty[sx1], 0x3);
@@ -442,12 +410,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
           next_f();
         }
         if (!ok) break;
-        umma_commit_2sm(&accfull[hs % kSlots], 0x3);
-        if (p.n1) umma_commit_2sm(&accfull[(hs + 1) % kSlots], 0x3);
+        umma_commit_2sm(&accfull[slot], 0x3);
       }
-      umma_commit_2sm(drain, 0x1);
+      umma_commit_2sm(&drain[h], 0x1);
       const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(drain, 0) && (long long)(globaltimer_ns() - t0) < p.timeout_ns) {
+      while (!mbar_try_wait(&drain[h], 0) && (long long)(globaltimer_ns() - t0) < p.timeout_ns) {
       }
     }
     __syncwarp();
@@ -542,7 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&adone[grp]);
     }
-  } else if (warp >= kEpiWarp0) {
+  } else if (warp >= kEpiWarp0 && warp < kIssuer1) {
     // ------------------------------------------------ epilogue: 32 rows of W x the token rows
     // A lane holds a row of W; 32 token rows at a time pass through shared memory so that a store writes 64
     // contiguous bytes of each of eight tokens.
@@ -555,7 +522,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
       const int t0 = u / p.n_mt * unit_rows, w0 = (u % p.n_mt) * 256 + (int)rank * BM + 32 * qrt;
       const int col = w0 + 8 * (lane & 3);
 #pragma unroll 1
-      for (int h = 0; h < (p.n1 ? 2 : 1); ++h, ++hs) {
+      for (int h = 0; h < halves; ++h, ++hs) {
         const uint32_t b = hs % kSlots;
         ok = __all_sync(kFull, mbar_wait(&accfull[b], (hs / kSlots) & 1, ctl, p.err, p.timeout_ns, 240));
         if (!ok) break;
