@@ -62,6 +62,9 @@ __device__ __forceinline__ void umma_bf16_2sm_ta(uint32_t d_tmem, uint32_t a_tme
       : "memory");
 }
 
+// After a wait ran out, time for copies in flight to land before the shared memory goes away.
+constexpr uint64_t kLandNs = 1000000;
+
 // The adapters of a unit of `rows` rows from row0 on, one run of rows [lo, hi) (relative to row0) at a time: the
 // adapter of every 32 rows is in `granules` (n for the tokens without one), and every adapter starts such a granule.
 struct AdapterRun {
@@ -81,6 +84,23 @@ struct AdapterRun {
     return false;
   }
 };
+
+// TMA loads whose completion is counted on a barrier of either CTA of the pair (a cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+      "%4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y,
+                                                 int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+      "%4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
 
 // Mask word w (rows 32 w ..) with the bits outside rows [lo, hi) set.
 __device__ __forceinline__ uint32_t rows_off(int lo, int hi, int w) {
@@ -164,11 +184,16 @@ __device__ __forceinline__ void let_land(uint64_t* bars, int n, uint32_t issued,
 // columns: adapters' rows start at multiples of 32, the column granule of a pair
 // UMMA.
 //
+// The issuers see both CTAs' operands on barriers of the even CTA: the odd CTA's
+// TMA loads count their bytes there, and its decode warps signal with a 4-byte
+// st.async each.  (A relay warp that waited for a CTA's operands and passed one
+// signal on took about 690 cycles a chunk: beside four decode warps on its
+// scheduler, every instruction of it waits for a turn.)
+//
 // Roles per CTA: warp 0 codes, warp 1 TMEM owner and (even CTA) issuer of the
-// first halves, warp 2 relay of operand readiness to the even CTA, warp 3 token
-// rows and low-rank operands, warps 4-19 four decode groups taking the chunks
-// round robin, warps 20-23 epilogue (32 rows of W each), warp 24 (even CTA)
-// issuer of the second halves.
+// first halves, warp 2 (even CTA) issuer of the second halves, warp 3 token rows
+// and low-rank operands, warps 4-19 four decode groups taking the chunks round
+// robin, warps 20-23 epilogue (32 rows of W each).
 namespace adf {
 constexpr int BM = 128, BK = 64;
 constexpr int kHalf = 128;                    // token rows of an accumulator half
@@ -185,8 +210,7 @@ constexpr int kEpiWarpBytes = 32 * kEpiPitch;
 constexpr int BAR_OFF = EPI_OFF + 4 * kEpiWarpBytes;
 constexpr int SMEM_BYTES = BAR_OFF + 1024 + 1024;
 constexpr int kEpiWarp0 = 4 + kGroups * kGroupWarps;
-constexpr int kIssuer1 = kEpiWarp0 + 4;
-constexpr int kThreads = 32 * (kIssuer1 + 1);
+constexpr int kThreads = 32 * (kEpiWarp0 + 4);
 constexpr int kTmemCols = 512;
 static_assert(kAOff + kGroups * BK / 2 <= kTmemCols, "TMEM budget");
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -221,10 +245,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_OFF);
   uint64_t* raw_full = bars;                    // [RAW_STAGES] codes landed
   uint64_t* raw_empty = raw_full + RAW_STAGES;  // [RAW_STAGES] codes read into registers (group's 4 warps)
-  uint64_t* xfull = raw_empty + RAW_STAGES;     // [SA] ring use landed
+  uint64_t* xfull = raw_empty + RAW_STAGES;     // [SA] (even CTA) ring use landed in both CTAs
   uint64_t* xempty = xfull + SA;                // [SA] ring slot consumed by the UMMAs
-  uint64_t* full = xempty + SA;                 // [SA] (even CTA) both CTAs' operands of an MMA step in place
-  uint64_t* adone = full + SA;                  // [kGroups] this CTA's decoded chunk is in tensor memory (4 warps)
+  uint64_t* adone = xempty + SA;                // [kGroups] (even CTA) both CTAs' decoded chunk is in tensor memory
   uint64_t* aempty = adone + kGroups;           // [kGroups] decoded chunk consumed by the UMMAs
   uint64_t* accfull = aempty + kGroups;         // [kSlots] accumulator half complete
   uint64_t* accempty = accfull + kSlots;        // [kSlots] (even CTA) half drained in both CTAs
@@ -244,7 +267,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
     for (int s = 0; s < SA; ++s) {
       mbar_init(&xfull[s], 1);
       mbar_init(&xempty[s], halves);
-      mbar_init(&full[s], 1);
     }
     for (int g = 0; g < kGroups; ++g) {
       mbar_init(&adone[g], kGroupWarps);
@@ -302,10 +324,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
       tma_prefetch_desc(&map_x0);
       tma_prefetch_desc(&map_p);
       tma_prefetch_desc(&map_b);
-      uint32_t s = 0, ph = 0, issued = 0, last_par = 0;
+      // Completions are counted on the even CTA's xfull, which its loader arms for both CTAs' (equal) bytes.
+      const uint32_t xfull_even = mapa_shared(smem_u32(xfull), 0);
+      uint32_t s = 0, ph = 0;
       auto issued_next = [&]() {
-        issued |= 1u << s;
-        last_par = (last_par & ~(1u << s)) | (ph << s);
         if (++s == SA) {
           s = 0;
           ph ^= 1;
@@ -317,9 +339,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
         for (int kc = 0; kc < kchunks; ++kc) {
           if (!(ok = mbar_wait(&xempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 212))) break;
           uint8_t* x = smem + s * X_BYTES;
-          mbar_arrive_expect_tx(&xfull[s], (uint32_t)(unit_rows * BK));
-          tma_load_2d(x, &map_x0, &xfull[s], kc * BK, t0 + p.n0 / 2 * (int)rank);
-          if (p.n1) tma_load_2d(x + X_BYTES / 2, &map_x1, &xfull[s], kc * BK, t0 + p.n0 + p.n1 / 2 * (int)rank);
+          const uint32_t bar = xfull_even + 8 * s;
+          if (rank == 0) mbar_arrive_expect_tx(&xfull[s], (uint32_t)(2 * unit_rows * BK));
+          tma_load_2d_pair(x, &map_x0, bar, kc * BK, t0 + p.n0 / 2 * (int)rank);
+          if (p.n1) tma_load_2d_pair(x + X_BYTES / 2, &map_x1, bar, kc * BK, t0 + p.n0 + p.n1 / 2 * (int)rank);
           issued_next();
         }
         if (!ok) break;
@@ -330,25 +353,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
           if (!(ok = mbar_wait(&xempty[s1], ph1 ^ 1, ctl, p.err, p.timeout_ns, 210))) break;
           const int2 h0 = half_range(run, 0, p.n0, p.n1), h1 = half_range(run, 1, p.n0, p.n1);
           const int n0 = (h0.y - h0.x) / 2, n1 = (h1.y - h1.x) / 2;  // this CTA's p rows, multiples of 16
-          mbar_arrive_expect_tx(&xfull[s], (uint32_t)((BM + n0 + n1) * 2 * p.r_pad));
+          const uint32_t bar = xfull_even + 8 * s;
+          if (rank == 0) {
+            mbar_arrive_expect_tx(&xfull[s], (uint32_t)((BM + n0 + n1) * 4 * p.r_pad));
+            mbar_arrive(&xfull[s1]);
+          }
           uint8_t* b = smem + s * X_BYTES;
-          tma_load_3d(b, &map_b, &xfull[s], 0, w0, run.adapter);
-          tma_load_3d(b + 128 * p.r_pad, &map_b, &xfull[s], 0, w0 + 64, run.adapter);
+          tma_load_3d_pair(b, &map_b, bar, 0, w0, run.adapter);
+          tma_load_3d_pair(b + 128 * p.r_pad, &map_b, bar, 0, w0 + 64, run.adapter);
           uint8_t* pr = smem + s1 * X_BYTES;
           for (int k = 0; k < n0; k += 16)
-            tma_load_2d(pr + k * 2 * p.r_pad, &map_p, &xfull[s], 0, t0 + h0.x + n0 * (int)rank + k);
+            tma_load_2d_pair(pr + k * 2 * p.r_pad, &map_p, bar, 0, t0 + h0.x + n0 * (int)rank + k);
           pr += 64 * 2 * p.r_pad;
           for (int k = 0; k < n1; k += 16)
-            tma_load_2d(pr + k * 2 * p.r_pad, &map_p, &xfull[s], 0, t0 + p.n0 + h1.x + n1 * (int)rank + k);
-          mbar_arrive(&xfull[s1]);
+            tma_load_2d_pair(pr + k * 2 * p.r_pad, &map_p, bar, 0, t0 + p.n0 + h1.x + n1 * (int)rank + k);
           issued_next();
           issued_next();
         }
       }
-      if (!ok) let_land(xfull, SA, issued, last_par, p.timeout_ns);
+      // (After a wait ran out: copies of either CTA may be in flight; they are given time to land.)
+      if (!ok) {
+        const uint64_t c0 = globaltimer_ns();
+        while (globaltimer_ns() - c0 < kLandNs) {
+        }
+      }
     }
     __syncwarp();
-  } else if (warp == 1 || warp == kIssuer1) {
+  } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------ UMMA issuers (even CTA, one elected lane each)
     const int h = warp == 1 ? 0 : 1;
     if (rank == 0 && h < halves && elect_one_sync()) {
@@ -356,43 +387,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
       const uint32_t lswz = swz_for_row_bytes(2 * p.r_pad);
       const uint32_t x_u = smem_u32(smem);
       const uint64_t xdesc0 = make_sdesc(x_u + h * (X_BYTES / 2), 16, 1024, kSw128);
-      uint32_t sx = 0, g = 0, fs = 0, fph = 0, hs = h;  // ring slot, decode group, MMA step, accumulator half used
+      uint32_t sx = 0, phx = 0, g = 0, pha = 0, hs = h;  // ring slot, decode group, accumulator half used
       bool ok = true;
-      auto next_x = [&]() { sx = (sx + 1 == SA) ? 0 : sx + 1; };
-      auto next_f = [&]() {
-        if (++fs == SA) {
-          fs = 0;
-          fph ^= 1;
+      auto next_x = [&]() {
+        if (++sx == SA) {
+          sx = 0;
+          phx ^= 1;
         }
       };
-      auto wait_step = [&]() -> bool { return mbar_wait_cluster(&full[fs], fph, ctl, p.err, p.timeout_ns, 223); };
+      auto wait_x = [&]() -> bool { return mbar_wait_cluster(&xfull[sx], phx, ctl, p.err, p.timeout_ns, 223); };
       for (int u = pair; u < n_units && ok; u += n_pairs, hs += halves) {
         const uint32_t slot = hs % kSlots, d = tmem + slot * kHalf;
         if (!(ok = mbar_wait_cluster(&accempty[slot], ((hs / kSlots) & 1) ^ 1, ctl, p.err, p.timeout_ns, 220))) break;
         tc_fence_after();
-        bool ready = false;
         for (int kc = 0; kc < kchunks; ++kc) {
-          if (!ready && !(ok = wait_step())) break;
+          if (!(ok = wait_x())) break;
+          if (!(ok = mbar_wait_cluster(&adone[g], pha, ctl, p.err, p.timeout_ns, 224))) break;
           tc_fence_after();
-          next_f();
           const uint32_t a = tmem + kAOff + g * (BK / 2);
           const uint64_t xd = xdesc0 + (uint64_t)(sx * (X_BYTES >> 4));
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
+          for (int kk = 0; kk < BK / 16; ++kk)
             umma_bf16_2sm_ta(d, a + 8 * kk, xd + 2 * kk, idesc, (kc > 0 || kk > 0) ? 1u : 0u);
-            // peek at the next chunk while these products run
-            if (kk == 1) ready = kc + 1 < kchunks && mbar_test_wait_cluster(&full[fs], fph);
-          }
           umma_commit_2sm(&xempty[sx], 0x3);
           umma_commit_2sm(&aempty[g], 0x3);
           next_x();
-          g = (g + 1) % kGroups;
+          if (++g == kGroups) {
+            g = 0;
+            pha ^= 1;
+          }
         }
         if (!ok) break;
         // One K = r product per adapter, at the adapter's columns of this half.
         AdapterRun run{u / p.n_mt * unit_rows, rows_used, unit_rows, p.n};
         while (run.next(granules)) {
-          if (!(ok = wait_step())) break;
+          if (!(ok = wait_x())) break;
           tc_fence_after();
           const uint32_t sx1 = (sx + 1 == SA) ? 0 : sx + 1;
           const uint32_t b_u = x_u + sx * X_BYTES, p_u = x_u + sx1 * X_BYTES + h * 128 * p.r_pad;
@@ -407,7 +436,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
           umma_commit_2sm(&xempty[sx1], 0x3);
           next_x();
           next_x();
-          next_f();
         }
         if (!ok) break;
         umma_commit_2sm(&accfull[slot], 0x3);
@@ -418,47 +446,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 2) {
-    // ------------------------------------------------ relays: this CTA's operands of a step -> even CTA's full[]
-    const uint32_t full_even = mapa_shared(smem_u32(full), 0);
-    const uint32_t sig_even = mapa_shared(smem_u32(sig), 0);
-    uint32_t sx = 0, phx = 0, j = 0, fs = 0;
-    bool ok = true;
-    auto wait_x = [&]() -> bool {
-      const bool r = __all_sync(kFull, mbar_wait(&xfull[sx], phx, ctl, p.err, p.timeout_ns, 252));
-      if (++sx == SA) {
-        sx = 0;
-        phx ^= 1;
-      }
-      return r;
-    };
-    auto signal = [&]() {
-      if (lane == 0) {
-        if (rank == 0)
-          mbar_arrive_expect_tx(&full[fs], 4);
-        else
-          st_async_signal(sig_even, full_even + 8 * fs, 1u);
-      }
-      fs = (fs + 1 == SA) ? 0 : fs + 1;
-    };
-    for (int u = pair; u < n_units && ok; u += n_pairs) {
-      for (int kc = 0; kc < kchunks; ++kc, ++j) {
-        ok = __all_sync(kFull, mbar_wait(&adone[j % kGroups], (j / kGroups) & 1, ctl, p.err, p.timeout_ns, 251));
-        if (!ok || !(ok = wait_x())) break;
-        tc_fence_after();  // the decoded chunk's tensor-memory writes before the signal
-        tc_fence_before();
-        signal();
-      }
-      if (!ok) break;
-      AdapterRun run{u / p.n_mt * unit_rows, rows_used, unit_rows, p.n};
-      while (run.next(granules)) {
-        if (!(ok = wait_x()) || !(ok = wait_x())) break;
-        signal();
-      }
-    }
   } else if (warp >= 4 && warp < kEpiWarp0) {
     // ------------------------------------------------ NF4 decode: a row of W a thread
     const uint32_t grp = (warp - 4) >> 2;
+    const uint32_t adone_even = mapa_shared(smem_u32(adone + grp), 0), sig_even = mapa_shared(smem_u32(sig), 0);
     const int t = (threadIdx.x - 128) & 127;
     const Nf4Shift ks = nf4_shift_consts();
     const uint32_t a_base = tmem + kAOff + grp * (BK / 2) + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -507,9 +498,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
       tmem_st32(a_base, v);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&adone[grp]);
+      if (lane == 0) {
+        if (rank)
+          st_async_signal(sig_even, adone_even, 1u);
+        else if ((warp & 3) == 0)
+          mbar_arrive_expect_tx(&adone[grp], 4 * kGroupWarps);  // and the odd CTA's four signals
+        else
+          mbar_arrive(&adone[grp]);
+      }
     }
-  } else if (warp >= kEpiWarp0 && warp < kIssuer1) {
+  } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------ epilogue: 32 rows of W x the token rows
     // A lane holds a row of W; 32 token rows at a time pass through shared memory so that a store writes 64
     // contiguous bytes of each of eight tokens.
