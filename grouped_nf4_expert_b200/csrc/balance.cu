@@ -7,16 +7,21 @@
 // S' sequences and n tokens are the ones that take part.  Forward: one pass
 // over the logits (maximum, sum of exponentials and probabilities of a row
 // from one set of registers), the probabilities of a token range summed per
-// expert in registers, one partial record per (range, sequence) piece; then
-// one launch that joins a sequence's records in range order (so the sums do
-// not depend on which block ran first) and, in its last block, the loss.
-// Backward: one pass over the logits with lse given.
+// expert in registers, one partial record per (range, sequence) piece; the
+// grid's last blocks wait for the records (a counter in the workspace, bounded
+// wait; the blocks they wait for come first in the grid and never wait), add a
+// sequence's records in range order, so that the sums do not depend on which
+// block ran first, and the last of them forms the loss.  A second launch in
+// their place cost the host 4.5 us and the GPU 10 to 15.  Backward: one pass
+// over the logits with lse given.
 //
 // What bounds them: HBM reads of the logits (forward) and reads plus writes
-// of T x E float32 (backward); for small batches the two launches' latency.
-// A group of G lanes owns a token, each lane four or more neighbouring
-// columns (16-byte loads), G the smallest power of two with 4 G >= E, so that
-// no lane idles at few experts and a row needs log2(G) shuffles.
+// of T x E float32 (backward); for small batches the launch.
+// A group of G lanes owns a token, each lane 16 columns in runs of four
+// (16-byte loads), G the smallest power of two with 16 G >= E: with four columns
+// a lane the shuffles and the other work per token and lane were the limit, not
+// memory (131072 tokens of 64 experts: forward 46 us, backward 23 us).  A group
+// takes two tokens at a time, their loads together.
 #include <math.h>
 
 #include "e4b_device.cuh"
@@ -29,17 +34,23 @@ namespace {
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSlice = 32;  // experts of one block of the joining launch
+constexpr int kSlice = 8;  // experts of a joining item: 8 lanes, so that 32 records are read at a time
 
-// First sequence whose end lies beyond token t (S: none); ends ascending.
+// Tokens of a group at a time.
+constexpr int tokens_at_once(int V) { return V <= 2 ? 4 : (V == 4 ? 2 : 1); }
+
+// First sequence whose end lies beyond token t (S: none); ends ascending.  Whole warp: 32 ends a round trip, where
+// a binary search would wait for memory log2(S) times.
 __device__ __forceinline__ int sequence_of(const int32_t* offsets, int S, int t) {
-  int lo = 0, hi = S;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(offsets + mid + 1) > t)
-      hi = mid;
-    else
-      lo = mid + 1;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = S;  // the answer lies in [lo, hi]
+  while (hi > lo) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const bool past = at < hi && __ldg(offsets + at + 1) <= t;  // sequence `at` ends at or before t
+    const int n = __popc(__ballot_sync(kFull, past));
+    if (n == 0) return lo;
+    lo += (n - 1) * step + 1;
+    hi = min(hi, lo + step - 1);
   }
   return lo;
 }
@@ -58,7 +69,8 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 
 // The columns of lane g of a group: 4 (v G + g) + 0..3 for v < V.  Rows start
-// 16-byte aligned only when E is a multiple of 4; columns past E read as -inf.
+// 16-byte aligned only when E is a multiple of 4; columns past E, and rows that
+// are not there, read as -inf.
 template <int G, int V, bool ALIGNED>
 __device__ __forceinline__ void load_row(const float* row, int g, int E, bool live, float (&l)[4 * V]) {
 #pragma unroll
@@ -78,244 +90,145 @@ __device__ __forceinline__ void load_row(const float* row, int g, int E, bool li
   }
 }
 
+// Counters at the front of the workspace, 0 between launches, then the records.
+struct Counters {
+  int ready;   // blocks whose records are written
+  int joined;  // blocks that are done joining
+};
+
 struct FwdParams {
   const float* logits;
   const int32_t* ids;
   const int32_t* offsets;  // [S + 1] or nullptr
   const uint8_t* mask;     // [T] or nullptr
-  float* lse;
-  float* part_p;      // [slots, E] partial probability sums
-  int32_t* part_c;    // [slots, E] partial counts
-  float* part_z;      // [slots]
-  int32_t* part_n;    // [slots] tokens
-  int32_t* ticket;
-  int T, E, k, S, per_block;
-};
-
-// Block b owns tokens [b C, (b + 1) C); every sequence that meets the range
-// gives one piece, recorded in slot b + s (distinct along the staircase of
-// pieces, which moves right in b or s at every step).
-template <int G, int V, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const FwdParams p) {
-  extern __shared__ uint8_t smem[];
-  float* sp = reinterpret_cast<float*>(smem);                  // [kWarps][E]
-  int32_t* sc = reinterpret_cast<int32_t*>(sp + kWarps * p.E);  // [E]
-  float* sz = reinterpret_cast<float*>(sc + p.E);               // [kWarps]
-  int32_t* sn = reinterpret_cast<int32_t*>(sz + kWarps);        // [kWarps]
-  constexpr int kTok = 32 / G;  // tokens of a warp at a time
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane % G, sub = lane / G;
-  const int E = p.E;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
-  const int64_t r0 = (int64_t)blockIdx.x * p.per_block;
-  const int t_end = (int)min((int64_t)p.T, r0 + p.per_block);
-  int t0 = (int)min((int64_t)p.T, r0);
-  int s = p.offsets ? sequence_of(p.offsets, p.S, t0) : 0;
-  // tokens outside every sequence: lse = 0 like masked ones
-  while (t0 < t_end) {
-    int lo = 0, hi = p.T;
-    if (p.offsets) {
-      if (s >= p.S) {
-        lo = hi = t_end;
-      } else {
-        lo = min(max(__ldg(p.offsets + s), t0), t_end);
-        hi = min(max(__ldg(p.offsets + s + 1), lo), t_end);
-      }
-    }
-    lo = max(lo, t0);
-    hi = min(hi, t_end);
-    for (int t = t0 + threadIdx.x; t < lo; t += kThreads) p.lse[t] = 0.0f;
-    if (hi <= lo) {  // nothing of sequence s here
-      t0 = lo;
-      ++s;
-      continue;
-    }
-    for (int e = threadIdx.x; e < E; e += kThreads) sc[e] = 0;
-    float acc[4 * V];
-#pragma unroll
-    for (int i = 0; i < 4 * V; ++i) acc[i] = 0.0f;
-    float zsum = 0.0f;
-    int n = 0;
-    for (int tb = lo + warp * kTok; tb < hi; tb += kWarps * kTok) {
-      const int t = tb + sub;
-      const bool in = t < hi;
-      const bool live = in && (p.mask == nullptr || __ldg(p.mask + t) != 0);
-      float l[4 * V];
-      load_row<G, V, ALIGNED>(p.logits + (size_t)(in ? t : lo) * E, g, E, live, l);
-      float m = l[0];
-#pragma unroll
-      for (int i = 1; i < 4 * V; ++i) m = fmaxf(m, l[i]);
-      m = group_max<G>(m);
-      // a row of -inf alone (a masked token too) has no probabilities
-      const float ms = (m == -INFINITY) ? 0.0f : m;
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4 * V; ++i) {
-        l[i] = expf(l[i] - ms);
-        sum += l[i];
-      }
-      sum = group_sum<G>(sum);
-      const float inv = (sum == 0.0f) ? 0.0f : 1.0f / sum;
-#pragma unroll
-      for (int i = 0; i < 4 * V; ++i) acc[i] = fmaf(l[i], inv, acc[i]);
-      if (g == 0 && in) {
-        const float lse = (sum == 0.0f) ? (live ? -INFINITY : 0.0f) : ms + logf(sum);
-        p.lse[t] = lse;
-        if (live) {
-          if (sum != 0.0f) zsum = fmaf(lse, lse, zsum);
-          ++n;
-        }
-      }
-    }
-    // this warp's tokens of one column: over the groups of the warp, then the warps in order
-#pragma unroll
-    for (int i = 0; i < 4 * V; ++i) {
-#pragma unroll
-      for (int o = G; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(kFull, acc[i], o);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      zsum += __shfl_xor_sync(kFull, zsum, o);
-      n += __shfl_xor_sync(kFull, n, o);
-    }
-    if (sub == 0) {
-#pragma unroll
-      for (int i = 0; i < 4 * V; ++i) {
-        const int c = 4 * ((i >> 2) * G + g) + (i & 3);
-        if (c < E) sp[warp * E + c] = acc[i];
-      }
-    }
-    if (lane == 0) {
-      sz[warp] = zsum;
-      sn[warp] = n;
-    }
-    __syncthreads();
-    // counts of the piece's slots (integer sums: any order)
-    for (int64_t i = (int64_t)lo * p.k + threadIdx.x; i < (int64_t)hi * p.k; i += kThreads) {
-      const uint32_t e = (uint32_t)__ldg(p.ids + i);
-      if (e < (uint32_t)E && (p.mask == nullptr || __ldg(p.mask + (int)(i / p.k)) != 0)) atomicAdd(&sc[e], 1);
-    }
-    __syncthreads();
-    const size_t slot = (size_t)blockIdx.x + s;
-    for (int e = threadIdx.x; e < E; e += kThreads) {
-      float v = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += sp[w * E + e];
-      p.part_p[slot * E + e] = v;
-      p.part_c[slot * E + e] = sc[e];
-    }
-    if (threadIdx.x == 0) {
-      float z = 0.0f;
-      int c = 0;
-      for (int w = 0; w < kWarps; ++w) {
-        z += sz[w];
-        c += sn[w];
-      }
-      p.part_z[slot] = z;
-      p.part_n[slot] = c;
-    }
-    __syncthreads();  // the shared sums are read before the next piece
-    t0 = hi;
-    ++s;
-  }
-}
-
-struct JoinParams {
-  const int32_t* offsets;
-  const float* part_p;
-  const int32_t* part_c;
-  const float* part_z;
-  const int32_t* part_n;
-  float* seq_dot;    // [S, slices] sum over a slice's experts of counts * probability sums
-  float* seq_z;      // [S]
-  int32_t* ticket;
+  Counters* counters;
+  float2* part;       // [slots, E] (probability sum, count as an int's bits)
+  float2* part_zn;    // [slots] (sum of lse^2, tokens as an int's bits)
+  float* seq_dot;     // [S, slices] sum over a slice's experts of counts * probability sums
+  float* seq_z;       // [S]
   int32_t* counts;
   float* prob_sum;
   int32_t* tokens;
+  float* lse;
   float* loss;
-  int T, E, k, S, per_block, slices;
+  int T, E, k, S, per_block, slices, join_blocks;
   float c_b, c_z;
 };
 
-// Block (s, slice): the records of sequence s in range order, one expert a
-// lane and every eighth record a warp.  The last block to finish adds up the
-// loss, in sequence order.
-__global__ void __launch_bounds__(kThreads) balance_join_kernel(const JoinParams p) {
+__device__ __forceinline__ int2 sequence_range(const FwdParams& p, int s) {
+  if (p.offsets == nullptr) return make_int2(0, p.T);
+  const int lo = min(max(__ldg(p.offsets + s), 0), p.T);
+  return make_int2(lo, min(max(__ldg(p.offsets + s + 1), lo), p.T));
+}
+
+// The join: item (s, slice) adds the records of sequence s in range order: W warps take every W-th 4-record group, a
+// lane one expert of every fourth record.  A block an item (W = 8) while there are blocks enough, else a warp.
+template <int W>
+__device__ void join_items(const FwdParams& p, int first, int step, int2 range) {
   __shared__ float sp[kWarps][kSlice];
   __shared__ int32_t sc[kWarps][kSlice];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = lane & (kSlice - 1), row = lane / kSlice;
+  const int part_of = W == 1 ? 0 : warp;
+  for (int item = first; item < p.S * p.slices; item += step) {
+    const int s = item / p.slices, slice = item - s * p.slices, e = slice * kSlice + col;
+    if (item != first) range = sequence_range(p, s);
+    const int lo = range.x, hi = range.y;
+    const int b0 = lo / p.per_block, b1 = hi > lo ? (hi - 1) / p.per_block : b0 - 1;
+    float a = 0.0f, z = 0.0f;
+    int c = 0, n = 0;
+    constexpr int kAhead = 4, kStep = W * 4;
+    for (int b = b0 + 4 * part_of + row; b <= b1; b += kStep * kAhead) {
+      float2 v[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int at = b + i * kStep;
+        v[i] = (at <= b1 && e < p.E) ? __ldcg(p.part + ((size_t)at + s) * p.E + e) : make_float2(0.0f, 0.0f);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        a += v[i].x;
+        c += __float_as_int(v[i].y);
+      }
+    }
+    if (slice == 0 && part_of == 0) {
+      for (int b = b0 + lane; b <= b1; b += 32) {
+        const float2 v = __ldcg(p.part_zn + (size_t)b + s);
+        z += v.x;
+        n += __float_as_int(v.y);
+      }
+    }
+#pragma unroll
+    for (int o = kSlice; o < 32; o <<= 1) {
+      a += __shfl_xor_sync(kFull, a, o);
+      c += __shfl_xor_sync(kFull, c, o);
+    }
+    if constexpr (W > 1) {
+      if (row == 0) {
+        sp[warp][col] = a;
+        sc[warp][col] = c;
+      }
+      __syncthreads();
+      a = 0.0f;
+      c = 0;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        a += sp[w][col];
+        c += sc[w][col];
+      }
+    }
+    if (part_of == 0) {
+      if (row == 0 && e < p.E) {
+        p.counts[(size_t)s * p.E + e] = c;
+        p.prob_sum[(size_t)s * p.E + e] = a;
+      }
+      float dot = (row == 0 && e < p.E) ? (float)c * a : 0.0f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        dot += __shfl_xor_sync(kFull, dot, o);
+        z += __shfl_xor_sync(kFull, z, o);
+        n += __shfl_xor_sync(kFull, n, o);
+      }
+      if (lane == 0) {
+        p.seq_dot[item] = dot;
+        if (slice == 0) {
+          p.seq_z[s] = z;
+          p.tokens[s] = n;
+        }
+      }
+    }
+    if constexpr (W > 1) __syncthreads();
+  }
+}
+
+__device__ __forceinline__ void write_loss(const FwdParams& p, float bal, float zz, int nt, int ns) {
+  bal = ns > 0 ? bal / (float)ns : 0.0f;
+  zz = nt > 0 ? zz / (float)nt : 0.0f;
+  p.tokens[p.S] = nt;
+  p.tokens[p.S + 1] = ns;
+  p.loss[0] = p.c_b * bal + p.c_z * zz;
+  p.loss[1] = bal;
+  p.loss[2] = zz;
+}
+
+// balance = (1 / S') sum_s (E / (k n_s^2)) sum_e counts psum;  z = sum_s seq_z / n
+__device__ void form_loss(const FwdParams& p) {
   __shared__ float red_a[kWarps], red_b[kWarps];
   __shared__ int red_n[kWarps], red_s[kWarps];
-  __shared__ int last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int s = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
-  const int e = slice * kSlice + lane;
-  int lo = p.offsets ? __ldg(p.offsets + s) : 0, hi = p.offsets ? __ldg(p.offsets + s + 1) : p.T;
-  lo = min(max(lo, 0), p.T);
-  hi = min(max(hi, lo), p.T);
-  float a = 0.0f, z = 0.0f;
-  int c = 0, n = 0;
-  if (hi > lo) {
-    const int b0 = lo / p.per_block, b1 = (hi - 1) / p.per_block;
-    for (int b = b0 + warp; b <= b1; b += kWarps) {
-      const size_t slot = (size_t)b + s;
-      if (e < p.E) {
-        a += p.part_p[slot * p.E + e];
-        c += p.part_c[slot * p.E + e];
-      }
-    }
-    if (warp == 0) {
-      for (int b = b0 + lane; b <= b1; b += 32) {
-        z += p.part_z[(size_t)b + s];
-        n += p.part_n[(size_t)b + s];
-      }
-    }
-  }
-  sp[warp][lane] = a;
-  sc[warp][lane] = c;
-  __syncthreads();
-  if (warp == 0) {
-    a = 0.0f;
-    c = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      a += sp[w][lane];
-      c += sc[w][lane];
-    }
-    if (e < p.E) {
-      p.counts[(size_t)s * p.E + e] = c;
-      p.prob_sum[(size_t)s * p.E + e] = a;
-    }
-    float dot = (e < p.E) ? (float)c * a : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      dot += __shfl_xor_sync(kFull, dot, o);
-      z += __shfl_xor_sync(kFull, z, o);
-      n += __shfl_xor_sync(kFull, n, o);
-    }
-    if (lane == 0) {
-      p.seq_dot[(size_t)s * p.slices + slice] = dot;
-      if (slice == 0) {
-        p.seq_z[s] = z;
-        p.tokens[s] = n;
-      }
-      __threadfence();
-      last = atomicAdd(p.ticket, 1) == (int)gridDim.x - 1;
-    }
-  }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  // balance = (1 / S') sum_s (E / (k n_s^2)) sum_e counts psum;  z = sum_s seq_z / n
   float bal = 0.0f, zz = 0.0f;
   int nt = 0, ns = 0;
-  for (int q = threadIdx.x; q < p.S; q += kThreads) {
+#pragma unroll 4
+  for (int i = threadIdx.x; i < p.S * p.slices; i += kThreads) {
+    const int q = i / p.slices;
+    const float d = __ldcg(p.seq_dot + i), zq = __ldcg(p.seq_z + q);
     const int m = __ldcg(p.tokens + q);
     if (m > 0) {
-      float d = 0.0f;
-      for (int i = 0; i < p.slices; ++i) d += __ldcg(p.seq_dot + (size_t)q * p.slices + i);
       bal += d * ((float)p.E / ((float)p.k * (float)m)) / (float)m;
-      zz += __ldcg(p.seq_z + q);
-      nt += m;
-      ++ns;
+      if (i - q * p.slices == 0) {
+        zz += zq;
+        nt += m;
+        ++ns;
+      }
     }
   }
 #pragma unroll
@@ -341,14 +254,227 @@ __global__ void __launch_bounds__(kThreads) balance_join_kernel(const JoinParams
       nt += red_n[w];
       ns += red_s[w];
     }
-    bal = ns > 0 ? bal / (float)ns : 0.0f;
-    zz = nt > 0 ? zz / (float)nt : 0.0f;
-    p.tokens[p.S] = nt;
-    p.tokens[p.S + 1] = ns;
-    p.loss[0] = p.c_b * bal + p.c_z * zz;
-    p.loss[1] = bal;
-    p.loss[2] = zz;
+    write_loss(p, bal, zz, nt, ns);
   }
+}
+
+__device__ __forceinline__ void empty_sequence(const FwdParams& p, int s) {
+  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+    p.counts[(size_t)s * p.E + e] = 0;
+    p.prob_sum[(size_t)s * p.E + e] = 0.0f;
+  }
+  if (threadIdx.x == 0) p.tokens[s] = 0;
+}
+
+// Block b owns tokens [b C, (b + 1) C); every sequence that meets the range
+// gives one piece, recorded in slot b + s (distinct along the staircase of
+// pieces, which moves right in b or s at every step).  ONE: a single block
+// covers the batch; its pieces are the sequences and need no records.
+template <int G, int V, bool ALIGNED, bool ONE>
+__global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const FwdParams p) {
+  extern __shared__ uint8_t smem[];
+  float* sp = reinterpret_cast<float*>(smem);                  // [kWarps][E]
+  int32_t* sc = reinterpret_cast<int32_t*>(sp + kWarps * p.E);  // [E]
+  float* sz = reinterpret_cast<float*>(sc + p.E);               // [kWarps]
+  int32_t* sn = reinterpret_cast<int32_t*>(sz + kWarps);        // [kWarps]
+  constexpr int kTok = 32 / G;  // tokens of a warp at a time, and of its groups one after another
+  constexpr int U = tokens_at_once(V);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane % G, sub = lane / G;
+  const int E = p.E;
+  const int64_t r0 = (int64_t)blockIdx.x * p.per_block;
+  const int t_end = (int)min((int64_t)p.T, r0 + p.per_block);
+  int t0 = (int)min((int64_t)p.T, r0);
+  int s = p.offsets && !ONE ? sequence_of(p.offsets, p.S, t0) : 0;
+  float bal = 0.0f, zz = 0.0f;  // (ONE, thread 0) the loss so far
+  int nt = 0, ns = 0;
+  while (t0 < t_end) {
+    int lo = t0, hi = t_end;
+    if (p.offsets) {
+      if (s >= p.S) {
+        lo = hi = t_end;
+      } else {
+        lo = min(max(__ldg(p.offsets + s), t0), t_end);
+        hi = min(max(__ldg(p.offsets + s + 1), lo), t_end);
+      }
+    }
+    for (int t = t0 + threadIdx.x; t < lo; t += kThreads) p.lse[t] = 0.0f;  // tokens of no sequence
+    if (hi <= lo) {  // nothing of sequence s here
+      if (ONE && s < p.S) empty_sequence(p, s);
+      t0 = lo;
+      ++s;
+      continue;
+    }
+    for (int e = threadIdx.x; e < E; e += kThreads) sc[e] = 0;
+    __syncthreads();
+    float acc[4 * V];
+#pragma unroll
+    for (int i = 0; i < 4 * V; ++i) acc[i] = 0.0f;
+    float zsum = 0.0f;
+    int n = 0;
+    for (int tb = lo + warp * kTok + sub; tb - sub < hi; tb += kWarps * kTok * U) {
+      float l[U][4 * V];
+      int id[U];
+      bool live[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = tb + u * kWarps * kTok;
+        const bool in = t < hi;
+        load_row<G, V, ALIGNED>(p.logits + (size_t)(in ? t : lo) * E, g, E, in, l[u]);
+        id[u] = in && g < p.k ? __ldg(p.ids + (size_t)t * p.k + g) : -1;
+        live[u] = in && (p.mask == nullptr || __ldg(p.mask + t) != 0);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = tb + u * kWarps * kTok;
+        if (!live[u]) {  // a masked token's values are not looked at
+#pragma unroll
+          for (int i = 0; i < 4 * V; ++i) l[u][i] = -INFINITY;
+          id[u] = -1;
+        }
+        float m = l[u][0];
+#pragma unroll
+        for (int i = 1; i < 4 * V; ++i) m = fmaxf(m, l[u][i]);
+        m = group_max<G>(m);
+        // a row of -inf alone (a masked token too) has no probabilities
+        const float ms = (m == -INFINITY) ? 0.0f : m;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4 * V; ++i) {
+          l[u][i] = expf(l[u][i] - ms);
+          sum += l[u][i];
+        }
+        sum = group_sum<G>(sum);
+        const float inv = (sum == 0.0f) ? 0.0f : 1.0f / sum;
+#pragma unroll
+        for (int i = 0; i < 4 * V; ++i) acc[i] = fmaf(l[u][i], inv, acc[i]);
+        if (g == 0 && t < hi) {
+          const float lse = (sum == 0.0f) ? (live[u] ? -INFINITY : 0.0f) : ms + logf(sum);
+          p.lse[t] = lse;
+          if (live[u]) {
+            if (sum != 0.0f) zsum = fmaf(lse, lse, zsum);
+            ++n;
+          }
+        }
+        // the token's slots (integer sums: any order)
+        if ((uint32_t)id[u] < (uint32_t)E) atomicAdd(&sc[id[u]], 1);
+        if (live[u])
+          for (int j = g + G; j < p.k; j += G) {
+            const uint32_t e = (uint32_t)__ldg(p.ids + (size_t)t * p.k + j);
+            if (e < (uint32_t)E) atomicAdd(&sc[e], 1);
+          }
+      }
+    }
+    // this warp's tokens of one column: over the groups of the warp, then the warps in order
+#pragma unroll
+    for (int i = 0; i < 4 * V; ++i) {
+#pragma unroll
+      for (int o = G; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(kFull, acc[i], o);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      zsum += __shfl_xor_sync(kFull, zsum, o);
+      n += __shfl_xor_sync(kFull, n, o);
+    }
+    if (sub == 0) {
+#pragma unroll
+      for (int i = 0; i < 4 * V; ++i) {
+        const int c = 4 * ((i >> 2) * G + g) + (i & 3);
+        if (c < E) sp[warp * E + c] = acc[i];
+      }
+    }
+    if (lane == 0) {
+      sz[warp] = zsum;
+      sn[warp] = n;
+    }
+    __syncthreads();
+    const size_t slot = (size_t)blockIdx.x + s;
+    float dot = 0.0f;
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) v += sp[w * E + e];
+      if constexpr (ONE) {
+        p.counts[(size_t)s * E + e] = sc[e];
+        p.prob_sum[(size_t)s * E + e] = v;
+        dot = fmaf((float)sc[e], v, dot);
+      } else {
+        p.part[slot * E + e] = make_float2(v, __int_as_float(sc[e]));
+      }
+    }
+    if constexpr (ONE) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+      __syncthreads();  // the probability sums are read
+      if (lane == 0) sp[warp] = dot;
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+      float z = 0.0f;
+      int c = 0;
+      for (int w = 0; w < kWarps; ++w) {
+        z += sz[w];
+        c += sn[w];
+      }
+      if constexpr (ONE) {
+        p.tokens[s] = c;
+        if (c > 0) {
+          float d = 0.0f;
+          for (int w = 0; w < kWarps; ++w) d += sp[w];
+          bal += d * ((float)E / ((float)p.k * (float)c)) / (float)c;
+          zz += z;
+          nt += c;
+          ++ns;
+        }
+      } else {
+        p.part_zn[slot] = make_float2(z, __int_as_float(c));
+      }
+    }
+    __syncthreads();  // the shared sums are read before the next piece
+    t0 = hi;
+    ++s;
+  }
+  if constexpr (ONE) {
+    for (; s < p.S; ++s) empty_sequence(p, s);
+    if (threadIdx.x == 0) write_loss(p, bal, zz, nt, ns);
+    return;
+  }
+  // The last join_blocks blocks join.
+  __shared__ int flag;
+  const int joiner = (int)blockIdx.x - ((int)gridDim.x - p.join_blocks);
+  const bool wide = p.S * p.slices <= p.join_blocks;
+  const int first = wide ? joiner : joiner * kWarps + warp;
+  int2 range = make_int2(0, 0);
+  if (joiner >= 0 && first < p.S * p.slices) range = sequence_range(p, first / p.slices);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    atomicAdd(&p.counters->ready, 1);
+    flag = 0;
+    if (joiner >= 0) {
+      const long long c0 = clock64(), limit = wait_limit_cycles(kDefaultTimeoutNs);
+      int v;
+      do {
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(&p.counters->ready) : "memory");
+      } while (v < (int)gridDim.x && clock64() - c0 < limit);
+      flag = v >= (int)gridDim.x;
+    }
+  }
+  __syncthreads();
+  if (!flag) return;
+  if (wide)
+    join_items<kWarps>(p, first, p.join_blocks, range);
+  else
+    join_items<1>(p, first, p.join_blocks * kWarps, range);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    flag = atomicAdd(&p.counters->joined, 1) == p.join_blocks - 1;
+  }
+  __syncthreads();
+  if (!flag) return;
+  __threadfence();
+  form_loss(p);
+  if (threadIdx.x == 0) p.counters->ready = p.counters->joined = 0;
 }
 
 struct BwdParams {
@@ -368,7 +494,7 @@ struct BwdParams {
 // registers and is read again where the sequence changes.
 template <int G, int V, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(const BwdParams p) {
-  constexpr int kTok = 32 / G;
+  constexpr int kTok = 32 / G, U = tokens_at_once(V);
   const int lane = threadIdx.x & 31, g = lane % G, sub = lane / G;
   const int64_t w0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.per_warp;
   if (w0 >= p.T) return;
@@ -407,41 +533,58 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(const BwdParams p
       const float fc = n_s > 0 ? (float)E / ((float)p.k * (float)n_s) : 0.0f;
       bc = n_s > 0 ? up * p.c_b / ((float)n_seq * (float)n_s) : 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4 * V; ++i) {
-        const int c = 4 * ((i >> 2) * G + g) + (i & 3);
-        f[i] = c < E ? fc * (float)__ldg(p.counts + (size_t)s * E + c) : 0.0f;
+      for (int v = 0; v < V; ++v) {
+        const int c = 4 * (v * G + g);
+        const int32_t* at = p.counts + (size_t)s * E + c;
+        if (ALIGNED) {
+          const int4 q = c < E ? __ldg(reinterpret_cast<const int4*>(at)) : make_int4(0, 0, 0, 0);
+          f[4 * v] = fc * (float)q.x;
+          f[4 * v + 1] = fc * (float)q.y;
+          f[4 * v + 2] = fc * (float)q.z;
+          f[4 * v + 3] = fc * (float)q.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[4 * v + i] = c + i < E ? fc * (float)__ldg(at + i) : 0.0f;
+        }
       }
     }
-    for (int tb = t0; tb < hi; tb += kTok) {
-      const int t = tb + sub;
-      const bool in = t < hi;
-      const bool live = in && inside && (p.mask == nullptr || __ldg(p.mask + t) != 0);
-      float l[4 * V];
-      load_row<G, V, ALIGNED>(p.logits + (size_t)(in ? t : t0) * E, g, E, live, l);
-      const float lse = live ? __ldg(p.lse + t) : 0.0f;
-      const bool some = lse != -INFINITY;  // a row of -inf alone has no probabilities
-      float dot = 0.0f;
+    for (int tb = t0 + sub; tb - sub < hi; tb += kTok * U) {
+      float l[U][4 * V], lse[U];
+      bool live[U];
 #pragma unroll
-      for (int i = 0; i < 4 * V; ++i) {
-        l[i] = some ? expf(l[i] - lse) : 0.0f;
-        dot = fmaf(l[i], live ? f[i] : 0.0f, dot);
+      for (int u = 0; u < U; ++u) {
+        const int t = tb + u * kTok;
+        const bool in = t < hi;
+        load_row<G, V, ALIGNED>(p.logits + (size_t)(in ? t : t0) * E, g, E, in && inside, l[u]);
+        lse[u] = in ? __ldg(p.lse + t) : 0.0f;
+        live[u] = in && inside && (p.mask == nullptr || __ldg(p.mask + t) != 0);
       }
-      dot = group_sum<G>(dot);
-      const float zt = some ? zc * lse : 0.0f;
-      if (in) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = tb + u * kTok;
+        const bool some = lse[u] != -INFINITY;  // a row of -inf alone has no probabilities
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4 * V; ++i) {
+          l[u][i] = some && live[u] ? expf(l[u][i] - lse[u]) : 0.0f;
+          dot = fmaf(l[u][i], live[u] ? f[i] : 0.0f, dot);
+        }
+        dot = group_sum<G>(dot);
+        const float zt = some ? zc * lse[u] : 0.0f;
+        if (t >= hi) continue;
         float* row = p.d_logits + (size_t)t * E;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const int c = 4 * (v * G + g);
           float d[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) d[i] = live ? l[4 * v + i] * fmaf(bc, f[4 * v + i] - dot, zt) : 0.0f;
+          for (int i = 0; i < 4; ++i) d[i] = live[u] ? l[u][4 * v + i] * fmaf(bc, f[4 * v + i] - dot, zt) : 0.0f;
           if (ALIGNED) {
             if (c < E) {
               float4* q = reinterpret_cast<float4*>(row + c);
               float4 o = make_float4(d[0], d[1], d[2], d[3]);
               if (p.accumulate) {
-                if (!live) continue;
+                if (!live[u]) continue;
                 const float4 w = *q;
                 o = make_float4(w.x + d[0], w.y + d[1], w.z + d[2], w.w + d[3]);
               }
@@ -453,7 +596,7 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(const BwdParams p
               if (c + i < E) {
                 if (!p.accumulate)
                   row[c + i] = d[i];
-                else if (live)
+                else if (live[u])
                   row[c + i] += d[i];
               }
           }
@@ -470,12 +613,12 @@ cudaError_t dispatch_columns(int E, Args... args) {
   const bool al = (E & 3) == 0;
 #define E4B_BAL(G, V) return al ? F<G, V, true>::run(args...) : F<G, V, false>::run(args...)
   if (E <= 4) E4B_BAL(1, 1);
-  if (E <= 8) E4B_BAL(2, 1);
-  if (E <= 16) E4B_BAL(4, 1);
-  if (E <= 32) E4B_BAL(8, 1);
-  if (E <= 64) E4B_BAL(16, 1);
-  if (E <= 128) E4B_BAL(32, 1);
-  if (E <= 256) E4B_BAL(32, 2);
+  if (E <= 8) E4B_BAL(1, 2);
+  if (E <= 16) E4B_BAL(1, 4);
+  if (E <= 32) E4B_BAL(2, 4);
+  if (E <= 64) E4B_BAL(4, 4);
+  if (E <= 128) E4B_BAL(8, 4);
+  if (E <= 256) E4B_BAL(16, 4);
   if (E <= 512) E4B_BAL(32, 4);
   E4B_BAL(32, 8);
 #undef E4B_BAL
@@ -485,7 +628,10 @@ template <int G, int V, bool ALIGNED>
 struct RunFwd {
   static cudaError_t run(FwdParams p, int grid, cudaStream_t stream) {
     const int smem = (kWarps * p.E + p.E + 2 * kWarps) * 4;
-    balance_fwd_kernel<G, V, ALIGNED><<<grid, kThreads, smem, stream>>>(p);
+    if (grid == 1)
+      balance_fwd_kernel<G, V, ALIGNED, true><<<grid, kThreads, smem, stream>>>(p);
+    else
+      balance_fwd_kernel<G, V, ALIGNED, false><<<grid, kThreads, smem, stream>>>(p);
     return cudaGetLastError();
   }
 };
@@ -497,81 +643,73 @@ struct RunBwd {
   }
 };
 
+// Tokens that a warp's groups hold at a time.
+int warp_tokens(int E) {
+  if (E <= 4) return 32 * tokens_at_once(1);
+  if (E <= 8) return 32 * tokens_at_once(2);
+  int g = 1;
+  while (g < 32 && 16 * g < E) g *= 2;
+  return 32 / g * tokens_at_once(E <= 512 ? 4 : 8);
+}
+// Token ranges: at least the tokens that a block's warps hold at a time, at most two blocks an SM (all resident at
+// once).
 constexpr int kMaxBlocks = 2 * 148;
+int balance_blocks(int T, int E) {
+  const int at_once = kWarps * warp_tokens(E), b = (T + at_once - 1) / at_once;
+  return b < kMaxBlocks ? b : kMaxBlocks;
+}
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
-int balance_blocks(int T) {
-  // at least a token for every warp of a block, at most kMaxBlocks ranges
-  const int b = (T + kWarps - 1) / kWarps;
-  return b < 1 ? 1 : (b < kMaxBlocks ? b : kMaxBlocks);
+struct BalanceLayout {
+  size_t part, part_zn, seq_dot, seq_z, total;
+};
+BalanceLayout balance_layout(int T, int E, int S) {
+  const size_t slots = (size_t)balance_blocks(T, E) + S, slices = (E + kSlice - 1) / kSlice;
+  BalanceLayout l;
+  l.part = 256;
+  l.part_zn = l.part + align256(slots * E * 8);
+  l.seq_dot = l.part_zn + align256(slots * 8);
+  l.seq_z = l.seq_dot + align256((size_t)S * slices * 4);
+  l.total = l.seq_z + align256((size_t)S * 4);
+  return l;
 }
 
 }  // namespace
 
-size_t balance_workspace_bytes(int T, int E, int S) {
-  const size_t slots = (size_t)balance_blocks(T) + S;
-  const size_t slices = (E + kSlice - 1) / kSlice;
-  return 256 + 2 * align256(slots * E * 4) + 2 * align256(slots * 4) + align256((size_t)S * slices * 4) +
-         align256((size_t)S * 4);
-}
+size_t balance_workspace_bytes(int T, int E, int S) { return balance_layout(T, E, S).total; }
 
 cudaError_t launch_balance_fwd(const BalanceHost& h, void* ws, cudaStream_t stream) {
-  const int want = balance_blocks(h.T);
-  const int per = (h.T + want - 1) / want;
-  const int grid = (h.T + per - 1) / per;
-  const size_t slots = (size_t)want + h.S;
-  const int slices = (h.E + kSlice - 1) / kSlice;
+  const int want = balance_blocks(h.T, h.E);
+  const BalanceLayout l = balance_layout(h.T, h.E, h.S);
   uint8_t* w = static_cast<uint8_t*>(ws);
-  auto take = [&](size_t bytes) {
-    uint8_t* at = w;
-    w += align256(bytes);
-    return at;
-  };
   FwdParams p;
-  p.ticket = reinterpret_cast<int32_t*>(take(256));
-  p.part_p = reinterpret_cast<float*>(take(slots * h.E * 4));
-  p.part_c = reinterpret_cast<int32_t*>(take(slots * h.E * 4));
-  p.part_z = reinterpret_cast<float*>(take(slots * 4));
-  p.part_n = reinterpret_cast<int32_t*>(take(slots * 4));
-  JoinParams j;
-  j.seq_dot = reinterpret_cast<float*>(take((size_t)h.S * slices * 4));
-  j.seq_z = reinterpret_cast<float*>(take((size_t)h.S * 4));
+  p.per_block = (h.T + want - 1) / want;
+  const int grid = (h.T + p.per_block - 1) / p.per_block;
   p.logits = h.logits;
   p.ids = h.ids;
   p.offsets = h.offsets;
   p.mask = h.mask;
+  p.counters = reinterpret_cast<Counters*>(w);
+  p.part = reinterpret_cast<float2*>(w + l.part);
+  p.part_zn = reinterpret_cast<float2*>(w + l.part_zn);
+  p.seq_dot = reinterpret_cast<float*>(w + l.seq_dot);
+  p.seq_z = reinterpret_cast<float*>(w + l.seq_z);
+  p.counts = h.counts;
+  p.prob_sum = h.prob_sum;
+  p.tokens = h.tokens;
   p.lse = h.lse;
+  p.loss = h.loss;
   p.T = h.T;
   p.E = h.E;
   p.k = h.k;
   p.S = h.S;
-  p.per_block = per;
-  {
-    LaunchScope scope("balance_fwd", stream);
-    const cudaError_t err = dispatch_columns<RunFwd>(h.E, p, grid, stream);
-    if (err != cudaSuccess) return err;
-  }
-  j.offsets = h.offsets;
-  j.part_p = p.part_p;
-  j.part_c = p.part_c;
-  j.part_z = p.part_z;
-  j.part_n = p.part_n;
-  j.ticket = p.ticket;
-  j.counts = h.counts;
-  j.prob_sum = h.prob_sum;
-  j.tokens = h.tokens;
-  j.loss = h.loss;
-  j.T = h.T;
-  j.E = h.E;
-  j.k = h.k;
-  j.S = h.S;
-  j.per_block = per;
-  j.slices = slices;
-  j.c_b = h.c_b;
-  j.c_z = h.c_z;
-  LaunchScope scope("balance_join", stream);
-  balance_join_kernel<<<h.S * slices, kThreads, 0, stream>>>(j);
-  return cudaGetLastError();
+  p.slices = (h.E + kSlice - 1) / kSlice;
+  const int64_t items = (int64_t)h.S * p.slices;
+  p.join_blocks = (int)(items < grid ? items : grid);
+  p.c_b = h.c_b;
+  p.c_z = h.c_z;
+  LaunchScope scope("balance_fwd", stream);
+  return dispatch_columns<RunFwd>(h.E, p, grid, stream);
 }
 
 cudaError_t launch_balance_bwd(const BalanceHost& h, const float* dloss, bool accumulate, float* d_logits,
@@ -592,9 +730,12 @@ cudaError_t launch_balance_bwd(const BalanceHost& h, const float* dloss, bool ac
   p.accumulate = accumulate ? 1 : 0;
   p.c_b = h.c_b;
   p.c_z = h.c_z;
-  // runs of tokens: every warp of eight blocks an SM takes one
-  const int64_t warps = (int64_t)num_sms * 8 * kWarps;
+  // runs of tokens: every warp of three blocks an SM (what the registers hold) takes one, at least the tokens it
+  // holds at a time
+  const int64_t warps = (int64_t)num_sms * 3 * kWarps;
   p.per_warp = (int)((h.T + warps - 1) / warps);
+  const int at_once = warp_tokens(h.E);
+  p.per_warp = (p.per_warp + at_once - 1) / at_once * at_once;
   const int64_t used = ((int64_t)h.T + p.per_warp - 1) / p.per_warp;
   const int grid = (int)((used + kWarps - 1) / kWarps);
   LaunchScope scope("balance_bwd", stream);

@@ -152,7 +152,10 @@ typedef struct {
   float   *lse;      /* [T] logsumexp of each token (0 for a masked one) */
 } e4b_balance_stats;
 
-/* Workspace bytes of e4b_balance_fwd.  Host only; no CUDA call. */
+/* Workspace bytes of e4b_balance_fwd.  Host only; no CUDA call.  The first 256
+ * bytes of the workspace hold two counters, which must be 0 before the first
+ * call and are 0 again after each; calls that share a workspace must not
+ * overlap on the GPU. */
 e4b_status e4b_balance_get_sizes(const e4b_balance_dims *dims, int32_t T, size_t *workspace_bytes);
 
 /* logits: float32 [T, E]; topk_ids: int32 [T, top_k], as e4b_route_permute

@@ -41,7 +41,7 @@ def make(T, E, k, S, keep, seed=0):
 def run(E, k, logits, ids, seq, mask, cb=0.7, cz=0.3, dloss=None, d=None):
     T, S = logits.shape[0], (1 if seq is None else seq.numel() - 1)
     b = e4b.RouterBalance(E, k, T, S)
-    for t in (b.counts, b._tokens, b.lse, b.loss, b.prob_sum, b.ws):
+    for t in (b.counts, b._tokens, b.lse, b.loss, b.prob_sum, b.ws[256:]):
         t.fill_(85)
     b.e4b_balance_fwd(logits, ids, seq, mask, balance_coef=cb, z_coef=cz)
     out = torch.full((T, E), float("nan"), device="cuda") if d is None else d
