@@ -65,23 +65,36 @@ __device__ __forceinline__ void umma_bf16_2sm_ta(uint32_t d_tmem, uint32_t a_tme
 // After a wait ran out, time for copies in flight to land before the shared memory goes away.
 constexpr uint64_t kLandNs = 1000000;
 
-// The adapters of a unit of `rows` rows from row0 on, one run of rows [lo, hi) (relative to row0) at a time: the
+// The adapters of a unit of up to 256 rows from row0 on, one run of rows [lo, hi) (relative to row0) at a time: the
 // adapter of every 32 rows is in `granules` (n for the tokens without one), and every adapter starts such a granule.
+// All eight are read at once, when the unit starts.
 struct AdapterRun {
-  int row0, rows_used, rows, n;
+  static constexpr int kMost = 256 / kAdapterRowAlign;
+  int id[kMost];
+  int n, granule = 0;
   int lo = 0, hi = 0, adapter = -1;
-  __device__ AdapterRun(int row0_, int rows_used_, int rows_, int n_)
-      : row0(row0_), rows_used(rows_used_), rows(min(rows_, rows_used_ - row0_)), n(n_) {}
-  __device__ __forceinline__ bool next(const int32_t* granules) {
-    lo = hi;
-    while (lo < rows) {
-      adapter = __ldg(granules + (row0 + lo) / kAdapterRowAlign);
-      if (adapter >= n) return false;  // the rest has none
-      hi = lo + kAdapterRowAlign;
-      while (hi < rows && __ldg(granules + (row0 + hi) / kAdapterRowAlign) == adapter) hi += kAdapterRowAlign;
-      return true;
-    }
-    return false;
+  __device__ __forceinline__ AdapterRun(const int32_t* granules, int row0, int rows_used, int rows, int n_) : n(n_) {
+    rows = min(rows, rows_used - row0);
+#pragma unroll
+    for (int i = 0; i < kMost; ++i)
+      id[i] = i * kAdapterRowAlign < rows ? __ldg(granules + row0 / kAdapterRowAlign + i) : n;
+  }
+  __device__ __forceinline__ int at(int i) const {
+    int a = n;
+#pragma unroll
+    for (int j = 0; j < kMost; ++j)
+      if (j == i) a = id[j];
+    return a;
+  }
+  __device__ __forceinline__ bool next() {
+    adapter = at(granule);
+    if (adapter >= n) return false;  // the rest has none
+    lo = granule * kAdapterRowAlign;
+    do {
+      ++granule;
+    } while (at(granule) == adapter);
+    hi = granule * kAdapterRowAlign;
+    return true;
   }
 };
 
@@ -336,6 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
       bool ok = true;
       for (int u = pair; u < n_units && ok; u += n_pairs) {
         const int w0 = (u % p.n_mt) * 256 + (int)rank * BM, t0 = u / p.n_mt * unit_rows;
+        AdapterRun run(granules, t0, rows_used, unit_rows, p.n);
         for (int kc = 0; kc < kchunks; ++kc) {
           if (!(ok = mbar_wait(&xempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 212))) break;
           uint8_t* x = smem + s * X_BYTES;
@@ -346,8 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
           issued_next();
         }
         if (!ok) break;
-        AdapterRun run{t0, rows_used, unit_rows, p.n};
-        while (run.next(granules)) {
+        while (run.next()) {
           const uint32_t s1 = (s + 1 == SA) ? 0 : s + 1, ph1 = (s + 1 == SA) ? ph ^ 1 : ph;
           if (!(ok = mbar_wait(&xempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 210))) break;
           if (!(ok = mbar_wait(&xempty[s1], ph1 ^ 1, ctl, p.err, p.timeout_ns, 210))) break;
@@ -398,6 +411,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
       auto wait_x = [&]() -> bool { return mbar_wait_cluster(&xfull[sx], phx, ctl, p.err, p.timeout_ns, 223); };
       for (int u = pair; u < n_units && ok; u += n_pairs, hs += halves) {
         const uint32_t slot = hs % kSlots, d = tmem + slot * kHalf;
+        AdapterRun run(granules, u / p.n_mt * unit_rows, rows_used, unit_rows, p.n);
         if (!(ok = mbar_wait_cluster(&accempty[slot], ((hs / kSlots) & 1) ^ 1, ctl, p.err, p.timeout_ns, 220))) break;
         tc_fence_after();
         for (int kc = 0; kc < kchunks; ++kc) {
@@ -419,8 +433,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
         }
         if (!ok) break;
         // One K = r product per adapter, at the adapter's columns of this half.
-        AdapterRun run{u / p.n_mt * unit_rows, rows_used, unit_rows, p.n};
-        while (run.next(granules)) {
+        while (run.next()) {
           if (!(ok = wait_x())) break;
           tc_fence_after();
           const uint32_t sx1 = (sx + 1 == SA) ? 0 : sx + 1;
@@ -519,17 +532,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
     for (int u = pair; u < n_units && ok; u += n_pairs) {
       const int t0 = u / p.n_mt * unit_rows, w0 = (u % p.n_mt) * 256 + (int)rank * BM + 32 * qrt;
       const int col = w0 + 8 * (lane & 3);
-#pragma unroll 1
-      for (int h = 0; h < halves; ++h, ++hs) {
+      // the tokens of the unit's rows, 32 in a register across the warp
+      int toks[AdapterRun::kMost];
+#pragma unroll
+      for (int i = 0; i < AdapterRun::kMost; ++i) {
+        const int row = t0 + 32 * i;
+        toks[i] = 32 * i < unit_rows && row < rows_used ? __ldg(p.order + row + lane) : p.T;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h == halves) break;
         const uint32_t b = hs % kSlots;
         ok = __all_sync(kFull, mbar_wait(&accfull[b], (hs / kSlots) & 1, ctl, p.err, p.timeout_ns, 240));
         if (!ok) break;
         tc_fence_after();
         const uint32_t tl = tmem + b * kHalf + ((uint32_t)(qrt * 32) << 16);
-#pragma unroll 1
-        for (int jj = 0; jj < (h ? p.n1 : p.n0); jj += 32) {
-          const int row0 = t0 + (h ? p.n0 : 0) + jj;
-          const int tok = row0 < rows_used ? __ldg(p.order + row0 + lane) : p.T;
+#pragma unroll
+        for (int j = 0; j < kHalf / 32; ++j) {
+          // (a second half follows a full first one)
+          const int jj = 32 * j, tok = toks[h * (kHalf / 32) + j];
+          if (jj >= (h ? p.n1 : p.n0)) break;
           if (!__any_sync(kFull, tok < p.T)) continue;
           float v[32];
           tmem_ld32(tl + jj, v);
@@ -558,6 +580,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
           else
             mbar_arrive_cluster_relaxed(accempty_even + 8 * b);
         }
+        ++hs;
       }
     }
   }
@@ -576,12 +599,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
 // =============================================================================
 // The stored rows of W are the reduction here, and its 4-bit codes cannot be
 // read along it, so the decoded tile goes to shared memory with the output
-// columns contiguous, as the N operand.  Roles and rings as in the expert block's grouped GEMM: warp 0 codes, warp 1
-// TMEM owner and (even CTA) UMMA issuer, warp 2 relay of operand readiness to
-// the even CTA, warp 3 activation tiles and low-rank operands, warps 4-19 four
-// decode groups taking the k-chunks round robin, warps 20-23 epilogue.  The
-// low-rank steps come after the k-chunks: a unit's two ring slots per adapter
-// hold its 128 q rows and 128 columns of A.
+// columns contiguous, as the N operand; token rows are the M operand.  Roles per
+// CTA: warp 0 codes, warp 1 TMEM owner and (even CTA) UMMA issuer, warp 3
+// activation tiles and low-rank operands, warps 4-19 four decode groups taking
+// the k-chunks round robin, warps 20-23 epilogue; operands of both CTAs are
+// counted on the even CTA's barriers, as in the forward.  The low-rank steps
+// come after the k-chunks: a unit's two ring slots per adapter hold its 128 q
+// rows and 128 columns of A.
 namespace adg {
 constexpr int BM = 128, BN = 128, BK = 64;
 constexpr int A_BYTES = BM * BK * 2;
@@ -631,10 +655,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_OFF);
   uint64_t* raw_full = bars;                    // [RAW_STAGES] codes landed
   uint64_t* raw_empty = raw_full + RAW_STAGES;  // [RAW_STAGES] codes read into registers (group's 4 warps)
-  uint64_t* xfull = raw_empty + RAW_STAGES;     // [SA] activation use landed
+  uint64_t* xfull = raw_empty + RAW_STAGES;     // [SA] (even CTA) ring use landed in both CTAs
   uint64_t* aempty = xfull + SA;                // [SA] activation slot consumed by the UMMAs
-  uint64_t* full = aempty + SA;                 // [SA] (even CTA) both CTAs' operands of an MMA step in place
-  uint64_t* bdone = full + SA;                  // [SB] this CTA's decoded tile written (group's 4 warps)
+  uint64_t* bdone = aempty + SA;                // [SB] (even CTA) both CTAs' decoded tile written
   uint64_t* bempty = bdone + SB;                // [SB] decoded-tile slot consumed by the UMMAs
   uint64_t* accfull = bempty + SB;              // [2] accumulator complete
   uint64_t* accempty = accfull + 2;             // [2] (even CTA) accumulator drained in both CTAs
@@ -653,7 +676,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
     for (int s = 0; s < SA; ++s) {
       mbar_init(&xfull[s], 1);
       mbar_init(&aempty[s], 1);
-      mbar_init(&full[s], 1);
     }
     for (int s = 0; s < SB; ++s) {
       mbar_init(&bdone[s], kGroupWarps);
@@ -710,10 +732,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
       tma_prefetch_desc(&map_a);
       tma_prefetch_desc(&map_la);
       tma_prefetch_desc(&map_lb);
-      uint32_t s = 0, ph = 0, issued = 0, last_par = 0;
+      const uint32_t xfull_even = mapa_shared(smem_u32(xfull), 0);  // armed there for both CTAs' bytes
+      uint32_t s = 0, ph = 0;
       auto issued_next = [&]() {
-        issued |= 1u << s;
-        last_par = (last_par & ~(1u << s)) | (ph << s);
         if (++s == SA) {
           s = 0;
           ph ^= 1;
@@ -722,30 +743,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
       bool ok = true;
       for (int u = pair; u < n_units && ok; u += n_pairs) {
         const int mu = u / p.n_nt, c0 = (u % p.n_nt) * 256 + (int)rank * 128, row0 = mu * 256 + (int)rank * 128;
+        AdapterRun run(granules, mu * kAdapterUnitRows, rows_used, kAdapterUnitRows, p.n);
         for (int kc = 0; kc < kchunks; ++kc) {
           if (!(ok = mbar_wait(&aempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 312))) break;
-          mbar_arrive_expect_tx(&xfull[s], (uint32_t)A_BYTES);
-          tma_load_2d(aring + s * A_BYTES, &map_a, &xfull[s], kc * BK, row0);
+          if (rank == 0) mbar_arrive_expect_tx(&xfull[s], (uint32_t)(2 * A_BYTES));
+          tma_load_2d_pair(aring + s * A_BYTES, &map_a, xfull_even + 8 * s, kc * BK, row0);
           issued_next();
         }
         if (!ok) break;
-        AdapterRun run{mu * kAdapterUnitRows, rows_used, kAdapterUnitRows, p.n};
-        while (run.next(granules)) {
+        while (run.next()) {
           const uint32_t s1 = (s + 1 == SA) ? 0 : s + 1, ph1 = (s + 1 == SA) ? ph ^ 1 : ph;
           if (!(ok = mbar_wait(&aempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 310))) break;
           if (!(ok = mbar_wait(&aempty[s1], ph1 ^ 1, ctl, p.err, p.timeout_ns, 310))) break;
           uint8_t* la = aring + s * A_BYTES;
           uint8_t* lb = aring + s1 * A_BYTES;
-          mbar_arrive_expect_tx(&xfull[s], (uint32_t)(512 * p.r_pad));
-          tma_load_2d(la, &map_la, &xfull[s], 0, row0);
-          tma_load_3d(lb, &map_lb, &xfull[s], c0, 0, run.adapter);
-          tma_load_3d(lb + 128 * p.r_pad, &map_lb, &xfull[s], c0 + 64, 0, run.adapter);
-          mbar_arrive(&xfull[s1]);
+          const uint32_t bar = xfull_even + 8 * s;
+          if (rank == 0) {
+            mbar_arrive_expect_tx(&xfull[s], (uint32_t)(1024 * p.r_pad));
+            mbar_arrive(&xfull[s1]);
+          }
+          tma_load_2d_pair(la, &map_la, bar, 0, row0);
+          tma_load_3d_pair(lb, &map_lb, bar, c0, 0, run.adapter);
+          tma_load_3d_pair(lb + 128 * p.r_pad, &map_lb, bar, c0 + 64, 0, run.adapter);
           issued_next();
           issued_next();
         }
       }
-      if (!ok) let_land(xfull, SA, issued, last_par, p.timeout_ns);
+      // (After a wait ran out: copies of either CTA may be in flight; they are given time to land.)
+      if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < kLandNs) {
+        }
+      }
     }
     __syncwarp();
   } else if (warp == 1 && rank == 0) {
@@ -758,52 +787,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
       const uint64_t adesc0 = make_sdesc(a_u, 16, 1024, kSw128);
       const uint64_t bdesc0 = make_sdesc(b_u, 8192, 1024, kSw128);
       uint32_t ti = 0;
-      uint32_t sa = 0, sb = 0;
-      uint32_t fs = 0, fph = 0;
+      uint32_t sa = 0, pha = 0, sb = 0, phb = 0;
       bool ok = true;
-      auto next_a = [&]() { sa = (sa + 1 == SA) ? 0 : sa + 1; };
-      auto next_f = [&]() {
-        if (++fs == SA) {
-          fs = 0;
-          fph ^= 1;
+      auto next_a = [&]() {
+        if (++sa == SA) {
+          sa = 0;
+          pha ^= 1;
         }
       };
-      auto wait_step = [&]() -> bool { return mbar_wait_cluster(&full[fs], fph, ctl, p.err, p.timeout_ns, 323); };
+      auto wait_a = [&]() -> bool { return mbar_wait_cluster(&xfull[sa], pha, ctl, p.err, p.timeout_ns, 323); };
       for (int u = pair; u < n_units && ok; u += n_pairs, ++ti) {
         const int mu = u / p.n_nt;
+        AdapterRun run(granules, mu * kAdapterUnitRows, rows_used, kAdapterUnitRows, p.n);
         const uint32_t b = ti & 1, use = ti >> 1;
         const uint32_t d = tmem + b * 256;
         if (!(ok = mbar_wait_cluster(&accempty[b], (use & 1) ^ 1, ctl, p.err, p.timeout_ns, 320))) break;
         tc_fence_after();
-        if (!(ok = wait_step())) break;
-        tc_fence_after();
         for (int kc = 0; kc < kchunks; ++kc) {
+          if (!(ok = wait_a())) break;
+          if (!(ok = mbar_wait_cluster(&bdone[sb], phb, ctl, p.err, p.timeout_ns, 324))) break;
+          tc_fence_after();
           const uint64_t adesc = adesc0 + (uint64_t)(sa * (A_BYTES >> 4));
           const uint64_t bdesc = bdesc0 + (uint64_t)(sb * (B_BYTES >> 4));
-          const uint32_t fs1 = (fs + 1 == SA) ? 0 : fs + 1, fph1 = (fs + 1 == SA) ? fph ^ 1 : fph;
-          const bool more = kc + 1 < kchunks;
 #pragma unroll
-          for (int kk = 0; kk < BK / 16 - 1; ++kk)
+          for (int kk = 0; kk < BK / 16; ++kk)
             umma_bf16_2sm(d, adesc + 2 * kk, bdesc + bstep * kk, idesc, (kc > 0 || kk > 0) ? 1u : 0u);
-          // Peek at the next k-chunk while the UMMAs above execute.
-          const bool next_ready = more && mbar_test_wait_cluster(&full[fs1], fph1);
-          umma_bf16_2sm(d, adesc + 2 * (BK / 16 - 1), bdesc + bstep * (BK / 16 - 1), idesc, 1u);
           umma_commit_2sm(&aempty[sa], 0x3);
           umma_commit_2sm(&bempty[sb], 0x3);
           next_a();
-          sb = (sb + 1 == SB) ? 0 : sb + 1;
-          fs = fs1;
-          fph = fph1;
-          if (more) {
-            if (!next_ready && !(ok = wait_step())) break;
-            tc_fence_after();
+          if (++sb == SB) {
+            sb = 0;
+            phb ^= 1;
           }
         }
         if (!ok) break;
         // One K = r step per adapter of the tile, into its own rows.
-        AdapterRun run{mu * kAdapterUnitRows, rows_used, kAdapterUnitRows, p.n};
-        while (run.next(granules)) {
-          if (!(ok = wait_step())) break;
+        while (run.next()) {
+          if (!(ok = wait_a())) break;
           tc_fence_after();
           const uint32_t sa1 = (sa + 1 == SA) ? 0 : sa + 1;
           const uint32_t la_u = a_u + sa * A_BYTES, lb_u = a_u + sa1 * A_BYTES;
@@ -818,7 +838,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
           umma_commit_2sm(&aempty[sa1], 0x3);
           next_a();
           next_a();
-          next_f();
         }
         if (!ok) break;
         umma_commit_2sm(&accfull[b], 0x3);
@@ -829,46 +848,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 2) {
-    // ------------------------------------------------ relays: this CTA's operands of a step -> even CTA's full[]
-    const uint32_t full_even = mapa_shared(smem_u32(full), 0);
-    const uint32_t sig_even = mapa_shared(smem_u32(sig), 0);
-    uint32_t sa = 0, pha = 0, jb = 0, fs = 0;
-    bool ok = true;
-    auto wait_a = [&]() -> bool {
-      const bool r = __all_sync(kFull, mbar_wait(&xfull[sa], pha, ctl, p.err, p.timeout_ns, 352));
-      if (++sa == SA) {
-        sa = 0;
-        pha ^= 1;
-      }
-      return r;
-    };
-    auto signal = [&]() {
-      if (lane == 0) {
-        if (rank == 0)
-          mbar_arrive_expect_tx(&full[fs], 4);
-        else
-          st_async_signal(sig_even, full_even + 8 * fs, 1u);
-      }
-      fs = (fs + 1 == SA) ? 0 : fs + 1;
-    };
-    for (int u = pair; u < n_units && ok; u += n_pairs) {
-      const int mu = u / p.n_nt;
-      for (int kc = 0; kc < kchunks; ++kc, ++jb) {
-        ok = __all_sync(kFull, mbar_wait(&bdone[jb % SB], (jb / SB) & 1, ctl, p.err, p.timeout_ns, 351));
-        if (!ok || !(ok = wait_a())) break;
-        signal();
-      }
-      if (!ok) break;
-      AdapterRun run{mu * kAdapterUnitRows, rows_used, kAdapterUnitRows, p.n};
-      while (run.next(granules)) {
-        if (!(ok = wait_a()) || !(ok = wait_a())) break;
-        signal();
-      }
-    }
   } else if (warp >= 4 && warp < kEpiWarp0) {
     // ------------------------------------------------ NF4 decode, groups take the k-chunks round robin
     const uint32_t grp = (warp - 4) >> 2;
+    const uint32_t bdone_even = mapa_shared(smem_u32(bdone + grp), 0), sig_even = mapa_shared(smem_u32(sig), 0);
     const int t = (threadIdx.x - 128) & 127;  // stored row t % 64, block of 64 columns t / 64
     const Nf4Shift ks = nf4_shift_consts();
     const int raw_off = (t & 63) * 64 + (t >> 6) * 32;
@@ -927,7 +910,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
         st_shared_v4(dbase + ((c ^ (drow & 7)) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
       fence_proxy_async_smem();  // the tile stores before the UMMA reads them
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bdone[grp]);
+      if (lane == 0) {
+        if (rank)
+          st_async_signal(sig_even, bdone_even, 1u);
+        else if ((warp & 3) == 0)
+          mbar_arrive_expect_tx(&bdone[grp], 4 * kGroupWarps);  // and the odd CTA's four signals
+        else
+          mbar_arrive(&bdone[grp]);
+      }
     }
   } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------ epilogue: 32 rows of this warp to their tokens
