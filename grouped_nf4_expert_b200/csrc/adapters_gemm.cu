@@ -62,6 +62,11 @@ __device__ __forceinline__ void umma_bf16_2sm_ta(uint32_t d_tmem, uint32_t a_tme
       : "memory");
 }
 
+// The launches of a step follow one another closely: each may start while the one before it still runs, sets up its
+// barriers and tensor memory, and waits for the other's end before it touches memory.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // After a wait ran out, time for copies in flight to land before the shared memory goes away.
 constexpr uint64_t kLandNs = 1000000;
 
@@ -302,6 +307,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_wait();
+  grid_launch_dependents();
 
   const int rows_used = p.steps[0], unit_rows = p.n0 + p.n1;
   const int n_units = (rows_used + unit_rows - 1) / unit_rows * p.n_mt;
@@ -697,6 +704,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_wait();
+  grid_launch_dependents();
 
   const int rows_used = p.steps[0];
   const int n_units = (rows_used + kAdapterUnitRows - 1) / kAdapterUnitRows * p.n_nt;
@@ -1063,6 +1072,8 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_wait();
+  grid_launch_dependents();
   const int n_tasks = p.steps[1];
   const int4* tasks = reinterpret_cast<const int4*>(p.steps + p.tasks);  // (adapter, first row, end row, 0)
   const int chunks = (p.R + BK - 1) / BK, rank = (int)blockIdx.x % p.S;
@@ -1355,6 +1366,8 @@ __global__ void __launch_bounds__(adw::kThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_wait();
+  grid_launch_dependents();
   const int n_units = p.n * (p.n_ft[0] + p.n_ft[1]);
   const uint32_t b_bytes = BK * p.r_pad * 2;
   const int u0 = (int)blockIdx.x / p.S, u_step = (int)gridDim.x / p.S;  // S > 1: one unit a cluster
@@ -1555,10 +1568,11 @@ cudaError_t set_smem(K kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-// Launches clusters of S blocks.
+// Launches `kernel` so that it may start before the launch ahead of it has ended (it calls grid_wait); S > 0: in
+// clusters of S blocks.
 template <typename... Params, typename... Args>
-cudaError_t launch_clusters(void (*kernel)(Params...), int grid, int threads, int smem, int S, cudaStream_t stream,
-                            const Args&... args) {
+cudaError_t launch_following(void (*kernel)(Params...), int grid, int threads, int smem, int S, cudaStream_t stream,
+                             const Args&... args) {
   const cudaError_t err = set_smem(kernel, smem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
@@ -1566,12 +1580,14 @@ cudaError_t launch_clusters(void (*kernel)(Params...), int grid, int threads, in
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)S;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)S;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = S > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -1636,10 +1652,9 @@ cudaError_t launch_adapter_fwd(const AdapterProjHost& h, const uint16_t* rows, c
   p.n_mt = n_mt;
   const int64_t units = (h.rows_cap + unit_rows - 1) / unit_rows * n_mt;
   const int grid = 2 * (int)(units < num_sms / 2 ? units : num_sms / 2);
-  if ((err = set_smem(adapter_fwd_kernel, adf::SMEM_BYTES)) != cudaSuccess) return err;
   LaunchScope scope("adapter_fwd", stream);
-  adapter_fwd_kernel<<<grid, adf::kThreads, adf::SMEM_BYTES, stream>>>(mx0, mx1, mraw, mp, mb, p);
-  return cudaGetLastError();
+  return launch_following(adapter_fwd_kernel, grid, adf::kThreads, adf::SMEM_BYTES, 0, stream, mx0, mx1, mraw, mp, mb,
+                          p);
 }
 
 cudaError_t launch_adapter_dgrad(const AdapterProjHost& h, const uint16_t* rows, const uint16_t* low,
@@ -1666,10 +1681,9 @@ cudaError_t launch_adapter_dgrad(const AdapterProjHost& h, const uint16_t* rows,
   p.n_nt = (h.K + 255) / 256;
   const int64_t units = h.rows_cap / kAdapterUnitRows * p.n_nt;
   const int grid = 2 * (int)(units < num_sms / 2 ? units : num_sms / 2);
-  if ((err = set_smem(adapter_dgrad_kernel, adg::SMEM_BYTES)) != cudaSuccess) return err;
   LaunchScope scope("adapter_dgrad", stream);
-  adapter_dgrad_kernel<<<grid, adg::kThreads, adg::SMEM_BYTES, stream>>>(ma, mraw, mla, mlb, p);
-  return cudaGetLastError();
+  return launch_following(adapter_dgrad_kernel, grid, adg::kThreads, adg::SMEM_BYTES, 0, stream, ma, mraw, mla, mlb,
+                          p);
 }
 
 cudaError_t launch_adapter_rows(const AdapterProjHost& h, bool mn, const uint16_t* src, const uint16_t* fac,
@@ -1704,8 +1718,8 @@ cudaError_t launch_adapter_rows(const AdapterProjHost& h, bool mn, const uint16_
   while (p.S < 8 && 2 * p.S * cap <= fit && chunks >= 4 * p.S) p.S *= 2;
   const int grid = p.S * (int)(cap < fit / p.S ? cap : fit / p.S);
   LaunchScope scope(mn ? "adapter_proj_dy" : "adapter_proj_x", stream);
-  return mn ? launch_clusters(adapter_proj_kernel<true>, grid, adp::kThreads, adp::SMEM_BYTES, p.S, stream, ms, mw, p)
-            : launch_clusters(adapter_proj_kernel<false>, grid, adp::kThreads, adp::SMEM_BYTES, p.S, stream, ms, mw,
+  return mn ? launch_following(adapter_proj_kernel<true>, grid, adp::kThreads, adp::SMEM_BYTES, p.S, stream, ms, mw, p)
+            : launch_following(adapter_proj_kernel<false>, grid, adp::kThreads, adp::SMEM_BYTES, p.S, stream, ms, mw,
                               p);
 }
 
@@ -1741,7 +1755,7 @@ cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, co
   while (p.S < 8 && 2 * p.S * units <= 2 * cap && h.T / h.n >= 8 * p.S * adw::BK) p.S *= 2;
   const int grid = (int)(p.S > 1 ? units * p.S : (units < cap ? units : cap));
   LaunchScope scope("adapter_wgrad", stream);
-  return launch_clusters(adapter_wgrad_kernel, grid, adw::kThreads, adw::SMEM_BYTES, p.S, stream, mq, mp, p);
+  return launch_following(adapter_wgrad_kernel, grid, adw::kThreads, adw::SMEM_BYTES, p.S, stream, mq, mp, p);
 }
 
 }  // namespace e4b
