@@ -281,6 +281,7 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const FwdParams p
   constexpr int U = tokens_at_once(V);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane % G, sub = lane / G;
   const int E = p.E;
+  const bool few_ids = p.k <= 2 * G;
   const int64_t r0 = (int64_t)blockIdx.x * p.per_block;
   const int t_end = (int)min((int64_t)p.T, r0 + p.per_block);
   int t0 = (int)min((int64_t)p.T, r0);
@@ -313,14 +314,16 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const FwdParams p
     int n = 0;
     for (int tb = lo + warp * kTok + sub; tb - sub < hi; tb += kWarps * kTok * U) {
       float l[U][4 * V];
-      int id[U];
+      int id[U][2];
       bool live[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int t = tb + u * kWarps * kTok;
         const bool in = t < hi;
         load_row<G, V, ALIGNED>(p.logits + (size_t)(in ? t : lo) * E, g, E, in, l[u]);
-        id[u] = in && g < p.k ? __ldg(p.ids + (size_t)t * p.k + g) : -1;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          id[u][j] = in && few_ids && g + j * G < p.k ? __ldg(p.ids + (size_t)t * p.k + g + j * G) : -1;
         live[u] = in && (p.mask == nullptr || __ldg(p.mask + t) != 0);
       }
 #pragma unroll
@@ -329,7 +332,7 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const FwdParams p
         if (!live[u]) {  // a masked token's values are not looked at
 #pragma unroll
           for (int i = 0; i < 4 * V; ++i) l[u][i] = -INFINITY;
-          id[u] = -1;
+          id[u][0] = id[u][1] = -1;
         }
         float m = l[u][0];
 #pragma unroll
@@ -356,12 +359,28 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const FwdParams p
           }
         }
         // the token's slots (integer sums: any order)
-        if ((uint32_t)id[u] < (uint32_t)E) atomicAdd(&sc[id[u]], 1);
-        if (live[u])
-          for (int j = g + G; j < p.k; j += G) {
-            const uint32_t e = (uint32_t)__ldg(p.ids + (size_t)t * p.k + j);
-            if (e < (uint32_t)E) atomicAdd(&sc[e], 1);
-          }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if ((uint32_t)id[u][j] < (uint32_t)E) atomicAdd(&sc[id[u][j]], 1);
+      }
+    }
+    if (!few_ids) {  // more slots than two a lane: the piece's ids in a pass of their own
+      const uint32_t n_ids = (uint32_t)(hi - lo) * p.k;
+      const int32_t* at = p.ids + (size_t)lo * p.k;
+      constexpr int kAhead = 8;
+      for (uint32_t i0 = threadIdx.x; i0 < n_ids; i0 += kThreads * kAhead) {
+        uint32_t e[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const uint32_t i = i0 + j * kThreads;
+          e[j] = i < n_ids ? (uint32_t)__ldg(at + i) : kFull;
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const uint32_t i = i0 + j * kThreads;
+          if (e[j] < (uint32_t)E && (p.mask == nullptr || __ldg(p.mask + lo + i / (uint32_t)p.k) != 0))
+            atomicAdd(&sc[e[j]], 1);
+        }
       }
     }
     // this warp's tokens of one column: over the groups of the warp, then the warps in order
