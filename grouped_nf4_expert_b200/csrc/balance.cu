@@ -509,10 +509,14 @@ struct BwdParams {
   float c_b, c_z;
 };
 
+// Resident blocks of the backward on an SM: the grid is one wave of them (with a third of the blocks left for a
+// second wave, 131072 tokens of 64 experts took 22 us).
+constexpr int bwd_blocks(int V) { return V == 8 ? 2 : 3; }
+
 // A warp owns a run of tokens; the f of the sequence at hand stays in
 // registers and is read again where the sequence changes.
 template <int G, int V, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads) balance_bwd_kernel(const BwdParams p) {
+__global__ void __launch_bounds__(kThreads, bwd_blocks(V)) balance_bwd_kernel(const BwdParams p) {
   constexpr int kTok = 32 / G, U = tokens_at_once(V);
   const int lane = threadIdx.x & 31, g = lane % G, sub = lane / G;
   const int64_t w0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.per_warp;
@@ -749,9 +753,8 @@ cudaError_t launch_balance_bwd(const BalanceHost& h, const float* dloss, bool ac
   p.accumulate = accumulate ? 1 : 0;
   p.c_b = h.c_b;
   p.c_z = h.c_z;
-  // runs of tokens: every warp of three blocks an SM (what the registers hold) takes one, at least the tokens it
-  // holds at a time
-  const int64_t warps = (int64_t)num_sms * 3 * kWarps;
+  // runs of tokens: every resident warp takes one, at least the tokens it holds at a time
+  const int64_t warps = (int64_t)num_sms * bwd_blocks(h.E > 512 ? 8 : 4) * kWarps;
   p.per_warp = (int)((h.T + warps - 1) / warps);
   const int at_once = warp_tokens(h.E);
   p.per_warp = (p.per_warp + at_once - 1) / at_once * at_once;
