@@ -612,16 +612,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
 // the k-chunks round robin, warps 20-23 epilogue; operands of both CTAs are
 // counted on the even CTA's barriers, as in the forward.  The low-rank steps
 // come after the k-chunks: a unit's two ring slots per adapter hold its 128 q
-// rows and 128 columns of A.
+// rows and 64 NB columns of A.
+// A unit is 256 rows x 128 NB columns.  NB = 1 where NB = 2 would leave half the
+// pairs without one: a unit's chunks are a chain whose step is a decode (777
+// rows of 512 columns over 2048: 22 us with NB = 2).
 namespace adg {
-constexpr int BM = 128, BN = 128, BK = 64;
+constexpr int BM = 128, BK = 64;
 constexpr int A_BYTES = BM * BK * 2;
-constexpr int B_BYTES = BN * BK * 2;
-constexpr int kGroups = 4, kGroupWarps = 4;
+constexpr int B_BYTES = 128 * BK * 2;  // 64 stored rows x 64 NB columns, NB = 2 at most
+constexpr int kGroups = 4, kGroupWarps = 4;  // 2 NB of a group's warps decode
 constexpr int SA = 6;         // activation ring
 constexpr int SB = kGroups;   // decoded-tile ring: group g's chunks use slot g
 constexpr int RAW_STAGES = 2 * kGroups;
-constexpr int RAW_BYTES = BN * BK / 2;
+constexpr int RAW_BYTES = 128 * BK / 2;
 constexpr int B_OFF = SA * A_BYTES;
 constexpr int RAW_OFF = B_OFF + SB * B_BYTES;
 constexpr int EPI_OFF = RAW_OFF + RAW_STAGES * RAW_BYTES;
@@ -635,7 +638,7 @@ constexpr int kEpiWarp0 = 4 + kGroups * kGroupWarps;
 constexpr int kThreads = 32 * (kEpiWarp0 + 4);
 constexpr int kTmemCols = 512;
 static_assert(BAR_OFF % 16 == 0 && SMEM_BYTES <= 232448, "shared memory budget");
-static_assert(BM * E4B_MAX_RANK * 2 <= A_BYTES && BN * E4B_MAX_RANK * 2 <= A_BYTES, "low-rank operands fit a slot");
+static_assert(BM * E4B_MAX_RANK * 2 <= A_BYTES, "low-rank operands fit a slot");
 static_assert(RAW_STAGES % kGroups == 0, "code slots are owned by one decode group each");
 }  // namespace adg
 
@@ -649,11 +652,13 @@ struct AdapterDgradParams {
   int T, N, K, n, r_pad, n_nt;
 };
 
+template <int NB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
     adapter_dgrad_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_raw,
                         const __grid_constant__ CUtensorMap map_la, const __grid_constant__ CUtensorMap map_lb,
                         const AdapterDgradParams p) {
   using namespace adg;
+  constexpr int kCols = 128 * NB;  // output columns of a unit, 64 NB of them decoded by each CTA
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = align1024(smem_dyn);
   uint8_t* aring = smem;
@@ -678,14 +683,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int r = 0; r < RAW_STAGES; ++r) {
       mbar_init(&raw_full[r], 1);
-      mbar_init(&raw_empty[r], kGroupWarps);
+      mbar_init(&raw_empty[r], 2 * NB);
     }
     for (int s = 0; s < SA; ++s) {
       mbar_init(&xfull[s], 1);
       mbar_init(&aempty[s], 1);
     }
     for (int s = 0; s < SB; ++s) {
-      mbar_init(&bdone[s], kGroupWarps);
+      mbar_init(&bdone[s], 2 * NB);
       mbar_init(&bempty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -721,12 +726,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
       uint32_t j = 0, issued = 0, last_par = 0;
       bool ok = true;
       for (int u = pair; u < n_units && ok; u += n_pairs) {
-        const int c0 = (u % p.n_nt) * 256 + (int)rank * 128;  // this CTA's 128 output columns
+        const int c0 = (u % p.n_nt) * kCols + (int)rank * 64 * NB;  // this CTA's output columns
         for (int kc = 0; kc < kchunks; ++kc, ++j) {
           const uint32_t r = j % RAW_STAGES, ph = (j / RAW_STAGES) & 1;
           if (!(ok = mbar_wait_lazy(&raw_empty[r], ph ^ 1, ctl, p.err, p.timeout_ns, 311, 64))) break;
           uint8_t* slot = rawbuf + r * RAW_BYTES;
-          mbar_arrive_expect_tx(&raw_full[r], (uint32_t)RAW_BYTES);
+          mbar_arrive_expect_tx(&raw_full[r], (uint32_t)(2048 * NB));
           tma_load_2d(slot, &map_raw, &raw_full[r], c0 / 2, kc * BK);
           issued |= 1u << r;
           last_par = (last_par & ~(1u << r)) | (ph << r);
@@ -751,7 +756,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
       };
       bool ok = true;
       for (int u = pair; u < n_units && ok; u += n_pairs) {
-        const int mu = u / p.n_nt, c0 = (u % p.n_nt) * 256 + (int)rank * 128, row0 = mu * 256 + (int)rank * 128;
+        const int mu = u / p.n_nt, c0 = (u % p.n_nt) * kCols + (int)rank * 64 * NB;
+        const int row0 = mu * kAdapterUnitRows + (int)rank * BM;
         AdapterRun run(granules, mu * kAdapterUnitRows, rows_used, kAdapterUnitRows, p.n);
         for (int kc = 0; kc < kchunks; ++kc) {
           if (!(ok = mbar_wait(&aempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 312))) break;
@@ -768,12 +774,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
           uint8_t* lb = aring + s1 * A_BYTES;
           const uint32_t bar = xfull_even + 8 * s;
           if (rank == 0) {
-            mbar_arrive_expect_tx(&xfull[s], (uint32_t)(1024 * p.r_pad));
+            mbar_arrive_expect_tx(&xfull[s], (uint32_t)((512 + 256 * NB) * p.r_pad));
             mbar_arrive(&xfull[s1]);
           }
           tma_load_2d_pair(la, &map_la, bar, 0, row0);
           tma_load_3d_pair(lb, &map_lb, bar, c0, 0, run.adapter);
-          tma_load_3d_pair(lb + 128 * p.r_pad, &map_lb, bar, c0 + 64, 0, run.adapter);
+          if (NB == 2) tma_load_3d_pair(lb + 128 * p.r_pad, &map_lb, bar, c0 + 64, 0, run.adapter);
           issued_next();
           issued_next();
         }
@@ -789,7 +795,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
   } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------ UMMA issuer (even CTA, one elected lane)
     if (elect_one_sync()) {
-      const uint32_t idesc = make_idesc_bf16(256, 256, false, true);
+      const uint32_t idesc = make_idesc_bf16(256, kCols, false, true);
       const uint32_t lswz = swz_for_row_bytes(2 * p.r_pad);
       const uint32_t a_u = smem_u32(aring), b_u = smem_u32(bring);
       const uint32_t bstep = 128u;  // K16 step of the N operand in the descriptor address field
@@ -863,13 +869,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
     const uint32_t bdone_even = mapa_shared(smem_u32(bdone + grp), 0), sig_even = mapa_shared(smem_u32(sig), 0);
     const int t = (threadIdx.x - 128) & 127;  // stored row t % 64, block of 64 columns t / 64
     const Nf4Shift ks = nf4_shift_consts();
-    const int raw_off = (t & 63) * 64 + (t >> 6) * 32;
+    const int raw_off = (t & 63) * 32 * NB + (t >> 6) * 32;
     const int drow = t & 63;
     const uint32_t drow_off = (t >> 6) * 8192 + (drow >> 3) * 1024 + (drow & 7) * 128;
     const uint32_t b_u = smem_u32(bring) + grp * B_BYTES;
     // A cursor over this group's chunks, one chunk ahead of the decode (for the block scales).
     const uint32_t my_units = pair < n_units ? (uint32_t)((n_units - pair + n_pairs - 1) / n_pairs) : 0;
-    const uint32_t n_chunks = my_units * (uint32_t)kchunks;
+    // (NB = 1: a group's second pair of warps has nothing to do)
+    const uint32_t n_chunks = (t >> 6) < NB ? my_units * (uint32_t)kchunks : 0;
     int c_kc = (int)grp, c_u = pair;
     while (c_kc >= kchunks) {
       c_kc -= kchunks;
@@ -887,7 +894,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
     // Block scale of this thread's row for the cursor's chunk (0 past the ends of the matrix: zero decode).
     auto block_scale = [&]() -> float {
       if (c_u >= n_units) return 0.0f;
-      const int row = c_kc * BK + (t & 63), blk = c_nt * 4 + (int)rank * 2 + (t >> 6);
+      const int row = c_kc * BK + (t & 63), blk = (c_nt * 2 + (int)rank) * NB + (t >> 6);
       if (row >= p.N || blk >= blocks_per_row) return 0.0f;
       return __ldg(p.absmax + (size_t)row * blocks_per_row + blk);
     };
@@ -923,7 +930,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
         if (rank)
           st_async_signal(sig_even, bdone_even, 1u);
         else if ((warp & 3) == 0)
-          mbar_arrive_expect_tx(&bdone[grp], 4 * kGroupWarps);  // and the odd CTA's four signals
+          mbar_arrive_expect_tx(&bdone[grp], 8 * NB);  // and the odd CTA's 2 NB signals of 4 bytes
         else
           mbar_arrive(&bdone[grp]);
       }
@@ -939,7 +946,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
     uint32_t ti = 0;
     bool ok = true;
     for (int u = pair; u < n_units && ok; u += n_pairs, ++ti) {
-      const int mu = u / p.n_nt, c0 = (u % p.n_nt) * 256;
+      const int mu = u / p.n_nt, c0 = (u % p.n_nt) * kCols;
       const int tok = __ldg(p.order + mu * 256 + (int)rank * 128 + qrt * 32 + lane);
       const uint32_t b = ti & 1, use = ti >> 1;
       ok = __all_sync(kFull, mbar_wait(&accfull[b], use & 1, ctl, p.err, p.timeout_ns, 340));
@@ -948,7 +955,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
       const bool any = __any_sync(kFull, tok < p.T);
       const uint32_t tl = tmem + b * 256 + ((uint32_t)(qrt * 32) << 16);
 #pragma unroll 1
-      for (int jj = 0; jj < 256; jj += 64) {
+      for (int jj = 0; jj < kCols; jj += 64) {
         if (c0 + jj >= p.K || !any) break;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -1663,7 +1670,9 @@ cudaError_t launch_adapter_dgrad(const AdapterProjHost& h, const uint16_t* rows,
   CUtensorMap ma, mraw, mla, mlb;
   cudaError_t err;
   if ((err = map_bf16_2d(&ma, rows, h.N, h.rows_cap, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return err;
-  if ((err = map_u8_2d(&mraw, h.nf4, h.K / 2, h.N, 64, 64)) != cudaSuccess) return err;
+  const int64_t row_units = h.rows_cap / kAdapterUnitRows;
+  const int nb = 2 * row_units * ((h.K + 255) / 256) <= num_sms / 2 ? 1 : 2;
+  if ((err = map_u8_2d(&mraw, h.nf4, h.K / 2, h.N, 32 * nb, 64)) != cudaSuccess) return err;
   if ((err = map_bf16_2d(&mla, low, h.r, h.rows_cap, rp, 128, swizzle_for_bytes(2 * rp))) != cudaSuccess) return err;
   if ((err = map_bf16_3d(&mlb, A, h.K, h.r, h.n, 64, rp, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return err;
   AdapterDgradParams p;
@@ -1678,12 +1687,12 @@ cudaError_t launch_adapter_dgrad(const AdapterProjHost& h, const uint16_t* rows,
   p.K = h.K;
   p.r_pad = rp;
   p.n = h.n;
-  p.n_nt = (h.K + 255) / 256;
-  const int64_t units = h.rows_cap / kAdapterUnitRows * p.n_nt;
+  p.n_nt = (h.K + 128 * nb - 1) / (128 * nb);
+  const int64_t units = row_units * p.n_nt;
   const int grid = 2 * (int)(units < num_sms / 2 ? units : num_sms / 2);
   LaunchScope scope("adapter_dgrad", stream);
-  return launch_following(adapter_dgrad_kernel, grid, adg::kThreads, adg::SMEM_BYTES, 0, stream, ma, mraw, mla, mlb,
-                          p);
+  return launch_following(nb == 1 ? adapter_dgrad_kernel<1> : adapter_dgrad_kernel<2>, grid, adg::kThreads,
+                          adg::SMEM_BYTES, 0, stream, ma, mraw, mla, mlb, p);
 }
 
 cudaError_t launch_adapter_rows(const AdapterProjHost& h, bool mn, const uint16_t* src, const uint16_t* fac,
