@@ -130,15 +130,16 @@ __device__ __forceinline__ uint32_t rows_off(int lo, int hi, int w) {
 
 // Shares of a 128 x r_pad accumulator over a cluster of S blocks that split its reduction: block b owns rows
 // [128 b / S, 128 (b + 1) / S).  push_share: an epilogue warp stores its 32 TMEM lanes (zeros unless `live`)
-// into the owners' shared memory, [share][row][column]; sum_share adds four columns of an owned row in share
-// order.
+// into the owners' shared memory, [share][column][row]: a warp's store is one run of rows.  (Rows first, its 32
+// lanes' stores went out as 32 packets, 8 us a block of 64 columns.)  sum_share adds four columns of an owned row
+// in share order.
 constexpr int kSharePad = 4;
-constexpr int share_bytes(int r_pad) { return 128 * (r_pad + kSharePad) * 4; }
+constexpr int share_bytes(int r_pad, int S) { return r_pad * (128 + S * kSharePad) * 4; }
 __device__ __forceinline__ void push_share(uint8_t* smem, uint32_t tmem, int quarter, int lane, int S, int rank,
                                            int r_pad, bool live) {
-  const int rows = 128 / S, row = 32 * quarter + lane, pitch = r_pad + kSharePad;
-  const uint32_t to = mapa_shared(smem_u32(smem) + (uint32_t)(((rank * rows + row % rows) * pitch) * 4),
-                                  (uint32_t)(row / rows));
+  const int rows = 128 / S, row = 32 * quarter + lane, pitch = rows + kSharePad;
+  const uint32_t to =
+      mapa_shared(smem_u32(smem) + (uint32_t)((rank * r_pad * pitch + row % rows) * 4), (uint32_t)(row / rows));
   for (int j = 0; j < r_pad; j += 16) {
     float v[16];
     if (live) {
@@ -148,23 +149,20 @@ __device__ __forceinline__ void push_share(uint8_t* smem, uint32_t tmem, int qua
       for (int i = 0; i < 16; ++i) v[i] = 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to + (uint32_t)((j + 4 * i) * 4)),
-                   "f"(v[4 * i]), "f"(v[4 * i + 1]), "f"(v[4 * i + 2]), "f"(v[4 * i + 3])
+    for (int i = 0; i < 16; ++i)
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + (uint32_t)((j + i) * pitch * 4)), "f"(v[i])
                    : "memory");
   }
 }
 __device__ __forceinline__ float4 sum_share(const uint8_t* smem, int S, int row, int j, int r_pad) {
-  const int rows = 128 / S, pitch = r_pad + kSharePad;
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int pitch = 128 / S + kSharePad;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int s = 0; s < S; ++s) {
-    const float4 w = *reinterpret_cast<const float4*>(smem + ((s * rows + row) * pitch + j) * 4);
-    v.x += w.x;
-    v.y += w.y;
-    v.z += w.z;
-    v.w += w.w;
+    const float* at = reinterpret_cast<const float*>(smem) + (s * r_pad + j) * pitch + row;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += at[i * pitch];
   }
-  return v;
+  return make_float4(v[0], v[1], v[2], v[3]);
 }
 
 // Waits (with the limit) until the copies this role issued have landed, before its shared memory goes away.
@@ -1022,7 +1020,7 @@ constexpr int kThreads = 11 * 32;
 constexpr int kAccCols = 64;
 constexpr int kTmemCols = 2 * kAccCols;
 static_assert(STAGE_BYTES % 1024 == 0, "stage alignment");
-static_assert(share_bytes(E4B_MAX_RANK) <= STAGES * STAGE_BYTES, "the shares fit the stages");
+static_assert(share_bytes(E4B_MAX_RANK, 8) <= STAGES * STAGE_BYTES, "the shares fit the stages");
 static_assert(kAdapterTaskRows == BM, "a task is one tile");
 }  // namespace adp
 
@@ -1272,7 +1270,7 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
     if (tk.x < p.n && !ctl->abort) {
       const float sc = __ldg(p.scale + tk.x);
       for (int i = threadIdx.x; i < rows * (p.r / 4); i += kThreads) {
-        const int row = i / (p.r / 4), j = 4 * (i % (p.r / 4)), to = tk.y + rank * rows + row;
+        const int row = i % rows, j = 4 * (i / rows), to = tk.y + rank * rows + row;
         if (to < tk.z) {
           const float4 v = sum_share(smem, p.S, row, j, p.r_pad);
           *reinterpret_cast<uint2*>(p.out + (size_t)to * p.r + j) =
@@ -1397,8 +1395,9 @@ __global__ void __launch_bounds__(adw::kThreads, 2)
           t[i] = row < w.rows ? __ldg(p.order + w.row0 + row) : p.T;
         }
       };
-      int t[4];
+      int t[4], t1[4];  // of this chunk and the next: their loads have a chunk's time
       tokens(w.k_lo, t);
+      tokens(w.k_lo + 1, t1);
       for (int kc = w.k_lo; kc < w.k_hi; ++kc) {
         if (!(ok = __all_sync(kFull, mbar_wait(&empty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 510)))) break;
         uint8_t* tile = smem + s * STAGE_BYTES;
@@ -1410,7 +1409,9 @@ __global__ void __launch_bounds__(adw::kThreads, 2)
                             go ? act + (size_t)t[i & 3] * F + col : act, go ? 16u : 0u);
         }
         cp_async_arrive_noinc(&full[s]);
-        tokens(kc + 1, t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = t1[i];
+        tokens(kc + 2, t1);
         if (++s == STAGES) {
           s = 0;
           ph ^= 1;
@@ -1539,8 +1540,7 @@ __global__ void __launch_bounds__(adw::kThreads, 2)
       const int m0 = w.ft * BM + rank * rows;
       uint16_t* out = w.g ? p.out[1] : p.out[0];
       for (int i = threadIdx.x; i < rows * (p.r / 4); i += kThreads) {
-        // neighbouring threads: neighbouring ranks of dB [N, r], neighbouring features of dA [r, K]
-        const int row = w.g ? i / (p.r / 4) : i % rows, j = 4 * (w.g ? i % (p.r / 4) : i / rows), m = m0 + row;
+        const int row = i % rows, j = 4 * (i / rows), m = m0 + row;  // neighbouring threads: neighbouring features
         if (m >= F) continue;
         const float4 v = sum_share(smem, p.S, row, j, p.r_pad);
         const uint32_t lo = pack_bf16x2(v.x, v.y), hi = pack_bf16x2(v.z, v.w);
