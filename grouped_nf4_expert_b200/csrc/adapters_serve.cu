@@ -219,14 +219,18 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvPar
   for (int k0 = warp * 256; k0 < p.K; k0 += kWarps * 256) {
     const Raw w = next;
     const bool in = k0 + 64 * q < p.K;
-    uint4 xv[NT][4];
+    // x of both halves of the block at once, or (two tiles: the registers) one after the other
+    constexpr int kXHalves = NT == 1 ? 2 : 1;
+    uint4 xv[NT][4 * kXHalves];
     auto load_x = [&](int h) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) xv[j][c] = ldg16(xr[j] + k0 + 32 * h + 8 * c, in && tok[j]);
+        for (int c = 0; c < 4; ++c)
+          xv[j][4 * (h % kXHalves) + c] = ldg16(xr[j] + k0 + 32 * h + 8 * c, in && tok[j]);
     };
     load_x(0);
+    if (kXHalves == 2) load_x(1);
     next = load(k0 + kWarps * 256);
     const Nf4Planes pa = nf4_block_planes(w.ma), pb = nf4_block_planes(w.mb);
 #pragma unroll
@@ -240,11 +244,11 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvPar
         nf4_decode_word(cb[c], pb, ks, db);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          mma_bf16(acc[j], da[0], db[0], da[1], db[1], xv[j][c].x, xv[j][c].y);
-          mma_bf16(acc[j], da[2], db[2], da[3], db[3], xv[j][c].z, xv[j][c].w);
+          mma_bf16(acc[j], da[0], db[0], da[1], db[1], xv[j][4 * (h % kXHalves) + c].x, xv[j][4 * (h % kXHalves) + c].y);
+          mma_bf16(acc[j], da[2], db[2], da[3], db[3], xv[j][4 * (h % kXHalves) + c].z, xv[j][4 * (h % kXHalves) + c].w);
         }
       }
-      if (h == 0) load_x(1);
+      if (h == 0 && kXHalves == 1) load_x(1);
     }
   }
   float(*sums)[8 * NT][17] = reinterpret_cast<float(*)[8 * NT][17]>(red);
@@ -270,10 +274,10 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvPar
   __shared__ int have;
   if (tid == 0) {
     have = wait_ready(p.err, p.p_blocks, p.timeout_ns, 640);
-    if (have) leave(p.err, (int)gridDim.x - p.p_blocks);
   }
   __syncthreads();
   if (!have) return;
+  if (tid == 0) leave(p.err, (int)gridDim.x - p.p_blocks);
   // p[t, j] = bf16(s[a] sum of the shares), 16 threads a token
   if (adapted) {
     const float sc = __ldg(p.scale + a);
@@ -673,10 +677,10 @@ __global__ void __launch_bounds__(ads::kThreadsSplit, 1)
   }
   if (tid == 0) {
     ctl->pad = wait_ready(p.err, p.p_blocks, p.timeout_ns, 641);
-    if (ctl->pad) leave(p.err, (int)gridDim.x - p.p_blocks);
   }
   __syncthreads();
   if (!ctl->pad) return;
+  if (tid == 0) leave(p.err, (int)gridDim.x - p.p_blocks);
   // The adapters' part: item = (tile of 8 tokens of one adapter, group of 16 rows), fragments of B and p
   // fetched two items ahead.
   {
@@ -735,17 +739,59 @@ __global__ void __launch_bounds__(ads::kThreadsSplit, 1)
 
 }  // namespace
 
-// Shares of K of the blocks of p for up to 16 tokens.
-int adapter_gemv_shares(int T, int r) {
-  const int items = T * ((r + 15) / 16);
-  return items <= 16 ? 4 : (items <= 32 ? 2 : 1);
+// Shares of K of the blocks of p for up to 16 tokens: as many as leave every block of the launch a place (two an
+// SM; with 24 of 320 blocks in a second wave, 16 tokens at 2048 -> 4096 took 8.7 us, not 7.5).
+int adapter_gemv_shares(int T, int r, int N) {
+  const int items = T * ((r + 15) / 16), places = 2 * 148 - (N + 15) / 16;
+  return 4 * items <= places ? 4 : (2 * items <= places ? 2 : 1);
+}
+
+// The shares S of K and the blocks of p, by an estimate in microseconds of what bounds each part: a block reads A
+// at 90 KB/us and needs 1.7 us an item; a chunk of the product costs 0.3 us of decoding or its x tile at 80 KB/us;
+// shares travel at 27 KB/us a block; one SM holds one block, and clusters of 2, 4, 8 find 74, 33, 15 places.
+// Either p has places of its own beside the products, or every SM works on p first.  Measured both ways: 128
+// tokens at 2048 -> 2048, S = 8 (16 clusters in 15 places) 26.7 us, S = 4 14.4 us; 57 tokens of 64 adapters of
+// rank 64 at 2048 -> 512, p beside 16.4 us, before 20.5 us; 32 tokens of 32 such at 4096 -> 4096 28.7 and 24.7 us.
+struct SplitPlan {
+  int S, p_blocks;
+};
+static SplitPlan split_plan(const AdapterProjHost& h, int NT, int tiles, int chunks) {
+  const int slices = (h.r + 15) / 16, named = h.T < h.n ? h.T : h.n;
+  const int items = (h.T / kTokenTile + named < h.T ? h.T / kTokenTile + named : h.T) * slices;
+  const float a_kb = (float)named * h.r * h.K * 2e-3f;
+  auto p_time = [&](int blocks) {
+    const float read = a_kb / (90.0f * blocks), turns = 1.7f * ((items + blocks - 1) / blocks);
+    return 1.5f + (read > turns ? read : turns);
+  };
+  SplitPlan best{1, 1};
+  float best_time = 1e30f;
+  const int places[4] = {148, 74, 33, 15};
+  for (int i = 0; i < 4 && (i == 0 || chunks >= (2 << i)); ++i) {
+    const int S = 1 << i;
+    const float x_time = NT * 0.128f / 80.0f, step = x_time > 0.3f ? x_time : 0.3f;
+    const float product = 2.5f + step * ((chunks + S - 1) / S) + NT * 0.512f * (S - 1) / S / 27.0f;
+    const int turns = (tiles + places[i] - 1) / places[i];
+    for (int beside = 0; beside < 2; ++beside) {
+      int blocks = (beside ? places[i] - tiles : places[i]) * S;
+      const int most = (items + S - 1) / S * S;
+      if (blocks > most) blocks = most;
+      if (blocks <= 0) continue;
+      const float pt = p_time(blocks);
+      const float time = beside ? (pt > product ? pt : product) : pt + turns * product;
+      if (time < best_time) {
+        best_time = time;
+        best = SplitPlan{S, blocks};
+      }
+    }
+  }
+  return best;
 }
 
 cudaError_t launch_adapter_small(const AdapterProjHost& h, const int32_t* ids, const uint16_t* x, const uint16_t* A,
                                  const uint16_t* B, void* low, uint16_t* y, int num_sms, cudaStream_t stream) {
   const int items = h.T * ((h.r + 15) / 16);
   if (h.T <= kAdapterGemvTokens) {
-    const int kq = adapter_gemv_shares(h.T, h.r);
+    const int kq = adapter_gemv_shares(h.T, h.r, h.N);
     const GemvParams p{ids, x,   h.nf4, h.absmax, A,   B,   h.scale, static_cast<float*>(low), y, h.err, h.timeout_ns,
                        h.T, h.K, h.N,   h.n,      h.r, kq,  items * kq};
     LaunchScope scope("adapter_gemv", stream);
@@ -757,14 +803,8 @@ cudaError_t launch_adapter_small(const AdapterProjHost& h, const int32_t* ids, c
     return cudaGetLastError();
   }
   const int NT = (h.T + 15) / 16 * 16, tiles = (h.N + ads::BM - 1) / ads::BM, chunks = h.K / ads::BK;
-  // K is split while the blocks fit the GPU at once and every block keeps two chunks.
-  int S = 1;
-  while (S < 8 && 2 * S * tiles <= num_sms && chunks >= 4 * S) S *= 2;
-  // The blocks of p take the SMs that are left over; where few are, every SM first does a share of p.
-  const int spare = num_sms - tiles * S;
-  int p_blocks = items <= 4 * spare ? spare : num_sms;
-  p_blocks = (p_blocks < items ? p_blocks : items) / S * S;
-  if (p_blocks < S) p_blocks = S;
+  const SplitPlan plan = split_plan(h, NT, tiles, chunks);
+  const int S = plan.S, p_blocks = plan.p_blocks;
   CUtensorMap mx;
   cudaError_t err = map_bf16_2d(&mx, x, h.K, h.T, 64, (uint32_t)NT, CU_TENSOR_MAP_SWIZZLE_128B);
   if (err != cudaSuccess) return err;

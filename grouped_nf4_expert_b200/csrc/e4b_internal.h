@@ -240,7 +240,7 @@ cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, co
                                  const uint16_t* q, uint16_t* dA, uint16_t* dB, int num_sms, cudaStream_t stream);
 // y for up to kAdapterSmallTokens tokens in one launch (scratch: low [T, r] bf16, or for up to kAdapterGemvTokens
 // tokens [adapter_gemv_shares, T, r] float32).
-int adapter_gemv_shares(int T, int r);
+int adapter_gemv_shares(int T, int r, int N);
 cudaError_t launch_adapter_small(const AdapterProjHost& h, const int32_t* ids, const uint16_t* x, const uint16_t* A,
                                  const uint16_t* B, void* low, uint16_t* y, int num_sms, cudaStream_t stream);
 
