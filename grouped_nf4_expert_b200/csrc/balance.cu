@@ -7,9 +7,9 @@
 // S' sequences and n tokens are the ones that take part.  Forward: one pass
 // over the logits (maximum, sum of exponentials and probabilities of a row
 // from one set of registers), the probabilities of a token range summed per
-// expert in registers, one partial record per (range, sequence) piece; the
-// grid's last blocks wait for the records (a counter in the workspace, bounded
-// wait; the blocks they wait for come first in the grid and never wait), add a
+// expert in registers, one partial record per (range, sequence) piece; more
+// blocks at the end of the grid wait for the records (a counter in the workspace,
+// bounded wait; the blocks they wait for come first and never wait), add a
 // sequence's records in range order, so that the sums do not depend on which
 // block ran first, and the last of them forms the loss.  A second launch in
 // their place cost the host 4.5 us and the GPU 10 to 15.  Backward: one pass
@@ -90,18 +90,12 @@ __device__ __forceinline__ void load_row(const float* row, int g, int E, bool li
   }
 }
 
-// Counters at the front of the workspace, 0 between launches, then the records.
-struct Counters {
-  int ready;   // blocks whose records are written
-  int joined;  // blocks that are done joining
-};
-
 struct FwdParams {
   const float* logits;
   const int32_t* ids;
   const int32_t* offsets;  // [S + 1] or nullptr
   const uint8_t* mask;     // [T] or nullptr
-  Counters* counters;
+  DeviceError* err;   // the workspace's front: `ready` record blocks done, `left` joining blocks done
   float2* part;       // [slots, E] (probability sum, count as an int's bits)
   float2* part_zn;    // [slots] (sum of lse^2, tokens as an int's bits)
   float* seq_dot;     // [S, slices] sum over a slice's experts of counts * probability sums
@@ -111,7 +105,7 @@ struct FwdParams {
   int32_t* tokens;
   float* lse;
   float* loss;
-  int T, E, k, S, per_block, slices, join_blocks;
+  int T, E, k, S, per_block, slices, blocks, join_blocks;  // record blocks, then joining blocks
   float c_b, c_z;
 };
 
@@ -266,12 +260,51 @@ __device__ __forceinline__ void empty_sequence(const FwdParams& p, int s) {
   if (threadIdx.x == 0) p.tokens[s] = 0;
 }
 
+// A block behind the record blocks.
+__device__ void join_block(const FwdParams& p) {
+  __shared__ int flag;
+  const int joiner = (int)blockIdx.x - p.blocks, items = p.S * p.slices;
+  const bool wide = items <= p.join_blocks;
+  const int first = wide ? joiner : joiner * kWarps + (threadIdx.x >> 5);
+  int2 range = make_int2(0, 0);
+  if (first < items) range = sequence_range(p, first / p.slices);
+  if (threadIdx.x == 0) {
+    const long long c0 = clock64(), limit = wait_limit_cycles(kDefaultTimeoutNs);
+    int v;
+    do {
+      asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(&p.err->ready) : "memory");
+    } while (v < p.blocks && clock64() - c0 < limit);
+    flag = v >= p.blocks;
+    if (!flag) record_error(p.err, E4B_ERR_DEVICE_TIMEOUT, 700);
+  }
+  __syncthreads();
+  if (!flag) return;
+  if (wide)
+    join_items<kWarps>(p, first, p.join_blocks, range);
+  else
+    join_items<1>(p, first, p.join_blocks * kWarps, range);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    flag = atomicAdd(&p.err->left, 1) == p.join_blocks - 1;
+  }
+  __syncthreads();
+  if (!flag) return;
+  __threadfence();
+  form_loss(p);
+  if (threadIdx.x == 0) p.err->ready = p.err->left = 0;
+}
+
 // Block b owns tokens [b C, (b + 1) C); every sequence that meets the range
 // gives one piece, recorded in slot b + s (distinct along the staircase of
 // pieces, which moves right in b or s at every step).  ONE: a single block
 // covers the batch; its pieces are the sequences and need no records.
 template <int G, int V, bool ALIGNED, bool ONE>
 __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const FwdParams p) {
+  if (!ONE && (int)blockIdx.x >= p.blocks) {
+    join_block(p);
+    return;
+  }
   extern __shared__ uint8_t smem[];
   float* sp = reinterpret_cast<float*>(smem);                  // [kWarps][E]
   int32_t* sc = reinterpret_cast<int32_t*>(sp + kWarps * p.E);  // [E]
@@ -457,43 +490,11 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const FwdParams p
     if (threadIdx.x == 0) write_loss(p, bal, zz, nt, ns);
     return;
   }
-  // The last join_blocks blocks join.
-  __shared__ int flag;
-  const int joiner = (int)blockIdx.x - ((int)gridDim.x - p.join_blocks);
-  const bool wide = p.S * p.slices <= p.join_blocks;
-  const int first = wide ? joiner : joiner * kWarps + warp;
-  int2 range = make_int2(0, 0);
-  if (joiner >= 0 && first < p.S * p.slices) range = sequence_range(p, first / p.slices);
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
-    atomicAdd(&p.counters->ready, 1);
-    flag = 0;
-    if (joiner >= 0) {
-      const long long c0 = clock64(), limit = wait_limit_cycles(kDefaultTimeoutNs);
-      int v;
-      do {
-        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(&p.counters->ready) : "memory");
-      } while (v < (int)gridDim.x && clock64() - c0 < limit);
-      flag = v >= (int)gridDim.x;
-    }
+    atomicAdd(&p.err->ready, 1);
   }
-  __syncthreads();
-  if (!flag) return;
-  if (wide)
-    join_items<kWarps>(p, first, p.join_blocks, range);
-  else
-    join_items<1>(p, first, p.join_blocks * kWarps, range);
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    flag = atomicAdd(&p.counters->joined, 1) == p.join_blocks - 1;
-  }
-  __syncthreads();
-  if (!flag) return;
-  __threadfence();
-  form_loss(p);
-  if (threadIdx.x == 0) p.counters->ready = p.counters->joined = 0;
 }
 
 struct BwdParams {
@@ -651,7 +652,7 @@ template <int G, int V, bool ALIGNED>
 struct RunFwd {
   static cudaError_t run(FwdParams p, int grid, cudaStream_t stream) {
     const int smem = (kWarps * p.E + p.E + 2 * kWarps) * 4;
-    if (grid == 1)
+    if (p.blocks == 1)
       balance_fwd_kernel<G, V, ALIGNED, true><<<grid, kThreads, smem, stream>>>(p);
     else
       balance_fwd_kernel<G, V, ALIGNED, false><<<grid, kThreads, smem, stream>>>(p);
@@ -674,9 +675,10 @@ int warp_tokens(int E) {
   while (g < 32 && 16 * g < E) g *= 2;
   return 32 / g * tokens_at_once(E <= 512 ? 4 : 8);
 }
-// Token ranges: at least the tokens that a block's warps hold at a time, at most two blocks an SM (all resident at
-// once).
-constexpr int kMaxBlocks = 2 * 148;
+// Token ranges: at least the tokens that a block's warps hold at a time; with the joining blocks at most two blocks
+// an SM (all resident at once).
+constexpr int kJoinBlocks = 64;
+constexpr int kMaxBlocks = 2 * 148 - kJoinBlocks;
 int balance_blocks(int T, int E) {
   const int at_once = kWarps * warp_tokens(E), b = (T + at_once - 1) / at_once;
   return b < kMaxBlocks ? b : kMaxBlocks;
@@ -689,7 +691,7 @@ struct BalanceLayout {
 BalanceLayout balance_layout(int T, int E, int S) {
   const size_t slots = (size_t)balance_blocks(T, E) + S, slices = (E + kSlice - 1) / kSlice;
   BalanceLayout l;
-  l.part = 256;
+  l.part = sizeof(DeviceError);
   l.part_zn = l.part + align256(slots * E * 8);
   l.seq_dot = l.part_zn + align256(slots * 8);
   l.seq_z = l.seq_dot + align256((size_t)S * slices * 4);
@@ -707,12 +709,12 @@ cudaError_t launch_balance_fwd(const BalanceHost& h, void* ws, cudaStream_t stre
   uint8_t* w = static_cast<uint8_t*>(ws);
   FwdParams p;
   p.per_block = (h.T + want - 1) / want;
-  const int grid = (h.T + p.per_block - 1) / p.per_block;
+  p.blocks = (h.T + p.per_block - 1) / p.per_block;
   p.logits = h.logits;
   p.ids = h.ids;
   p.offsets = h.offsets;
   p.mask = h.mask;
-  p.counters = reinterpret_cast<Counters*>(w);
+  p.err = reinterpret_cast<DeviceError*>(w);
   p.part = reinterpret_cast<float2*>(w + l.part);
   p.part_zn = reinterpret_cast<float2*>(w + l.part_zn);
   p.seq_dot = reinterpret_cast<float*>(w + l.seq_dot);
@@ -728,11 +730,11 @@ cudaError_t launch_balance_fwd(const BalanceHost& h, void* ws, cudaStream_t stre
   p.S = h.S;
   p.slices = (h.E + kSlice - 1) / kSlice;
   const int64_t items = (int64_t)h.S * p.slices;
-  p.join_blocks = (int)(items < grid ? items : grid);
+  p.join_blocks = p.blocks == 1 ? 0 : (int)(items < kJoinBlocks ? items : kJoinBlocks);
   p.c_b = h.c_b;
   p.c_z = h.c_z;
   LaunchScope scope("balance_fwd", stream);
-  return dispatch_columns<RunFwd>(h.E, p, grid, stream);
+  return dispatch_columns<RunFwd>(h.E, p, p.blocks + p.join_blocks, stream);
 }
 
 cudaError_t launch_balance_bwd(const BalanceHost& h, const float* dloss, bool accumulate, float* d_logits,

@@ -588,6 +588,12 @@ class _OnDevice:
         if status != E4B_OK:
             raise E4BError(status, name)
 
+    def check_device_error(self, stream=None) -> int:
+        """Synchronises the stream; the status of the object's calls so far (does not raise)."""
+        import torch
+        with torch.cuda.device(self.device):
+            return e4b_check_device_error(self.ws, stream)
+
 
 @dataclass(frozen=True)
 class ProjDims:
@@ -686,11 +692,6 @@ class Projection(_OnDevice):
         self._call("e4b_multi_lora_wgrad", stream, self._dims_p, self.T, self._groups_p, px, pd,
                    *self._low_p, *self._grad_p, self._ws_p, self._ws_n)
 
-    def check_device_error(self, stream=None) -> int:
-        import torch
-        with torch.cuda.device(self.device):
-            return e4b_check_device_error(self.ws, stream)
-
 
 class RouterBalance(_OnDevice):
     """Device buffers of the router's balance loss: ``E`` experts, ``top_k``, ``T`` tokens in ``S`` sequences.
@@ -716,6 +717,7 @@ class RouterBalance(_OnDevice):
         self._stats = BalanceStats(*(_ptr(t) for t in (self.counts, self.prob_sum, self._tokens, self.lse)))
         self._stats_p = ctypes.byref(self._stats)
         self._loss_p, self._ws_p, self._ws_n = _ptr(self.loss), _ptr(self.ws), self.ws.numel()
+        self._call("e4b_workspace_init", None, self._ws_p, self._ws_n)
 
     def _inputs(self, logits, seq_offsets, token_mask):
         pl = self._arg(logits, self._f32, self.T * self.E, "logits")

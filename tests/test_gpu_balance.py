@@ -46,6 +46,7 @@ def run(E, k, logits, ids, seq, mask, cb=0.7, cz=0.3, dloss=None, d=None):
     b.e4b_balance_fwd(logits, ids, seq, mask, balance_coef=cb, z_coef=cz)
     out = torch.full((T, E), float("nan"), device="cuda") if d is None else d
     b.e4b_balance_bwd(logits, out, seq, mask, balance_coef=cb, z_coef=cz, dloss=dloss, accumulate=d is not None)
+    assert b.check_device_error() == e4b.E4B_OK
     return b, out
 
 
