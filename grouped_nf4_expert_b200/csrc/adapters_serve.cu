@@ -2,7 +2,7 @@
 // launch each:
 //
 //   adapter_gemv_kernel:  y[t] = W x[t] + B[a] p[t], p[t] = s[a] A[a] x[t], for
-//                         up to 16 tokens;
+//                         up to 16 tokens (8 of a large matrix);
 //   adapter_split_kernel: the same for up to 256 tokens.
 //
 // What bounds them: reading the matrix (4.5 bits a weight) and each named
@@ -12,8 +12,7 @@
 // bounded wait) only in their epilogue.  The blocks of p never wait and come
 // first in the grid.
 //
-// Up to 16 tokens the products run on warp matrix instructions (m16n8k16):
-// there is nothing for a 128-row UMMA tile to amortise its set-up over.  Above,
+// For few tokens the products run on warp matrix instructions (m16n8k16): there is nothing for a 128-row UMMA tile to amortise its set-up over.  Above,
 // reading x again for every 16 rows of W would cost more than W itself, and a
 // UMMA takes 128 rows of W (decoded into tensor memory) against all tokens at
 // once, K split over a cluster whose partial sums meet through distributed
@@ -739,7 +738,15 @@ __global__ void __launch_bounds__(ads::kThreadsSplit, 1)
 
 }  // namespace
 
-// Shares of K of the blocks of p for up to 16 tokens: as many as leave every block of the launch a place (two an
+// Warp products for up to eight tokens, and for up to 16 of a matrix below 2^24 weights: with two token tiles their
+// reads of x and their decoding for every 16 rows cost more than the UMMA kernel's set-up (16 tokens, warp products
+// and UMMAs: 2048 -> 4096 10.3 and 14.4 us, 4096 -> 4096 16.4 and 16.4 us, 4096 -> 14336 46.6 and 30.7 us; 8 tokens
+// at 4096 -> 14336 29.5 and 28.7 us).
+bool adapter_gemv_serves(int T, int K, int N) {
+  return T <= kTokenTile || (T <= 2 * kTokenTile && (int64_t)K * N < (1 << 24));
+}
+
+// Shares of K of the blocks of p of the warp products: as many as leave every block of the launch a place (two an
 // SM; with 24 of 320 blocks in a second wave, 16 tokens at 2048 -> 4096 took 8.7 us, not 7.5).
 int adapter_gemv_shares(int T, int r, int N) {
   const int items = T * ((r + 15) / 16), places = 2 * 148 - (N + 15) / 16;
@@ -790,7 +797,7 @@ static SplitPlan split_plan(const AdapterProjHost& h, int NT, int tiles, int chu
 cudaError_t launch_adapter_small(const AdapterProjHost& h, const int32_t* ids, const uint16_t* x, const uint16_t* A,
                                  const uint16_t* B, void* low, uint16_t* y, int num_sms, cudaStream_t stream) {
   const int items = h.T * ((h.r + 15) / 16);
-  if (h.T <= kAdapterGemvTokens) {
+  if (adapter_gemv_serves(h.T, h.K, h.N)) {
     const int kq = adapter_gemv_shares(h.T, h.r, h.N);
     const GemvParams p{ids, x,   h.nf4, h.absmax, A,   B,   h.scale, static_cast<float*>(low), y, h.err, h.timeout_ns,
                        h.T, h.K, h.N,   h.n,      h.r, kq,  items * kq};

@@ -139,7 +139,7 @@ ServeProjLayout serve_proj_layout(const e4b_proj_dims* d, int32_t T) {
   l.steps = l.offsets + up((size_t)(d->n_adapters + 2) * 4);
   l.low = l.steps + up((size_t)adapter_steps_cap(rows, d->n_adapters) * 4);
   size_t low = (size_t)rows * d->r * 2;
-  if (T <= kAdapterGemvTokens) low = (size_t)adapter_gemv_shares(T, d->r, d->N) * T * d->r * 4;
+  if (adapter_gemv_serves(T, d->K, d->N)) low = (size_t)adapter_gemv_shares(T, d->r, d->N) * T * d->r * 4;
   l.rows = l.low + up(low);
   l.total = l.rows + up((size_t)rows * d->K * 2);
   return l;

@@ -197,7 +197,6 @@ cudaError_t launch_wgrad(const WgradHost& h, int num_sms, cudaStream_t stream);
 // ---- adapters beside a shared projection (adapters.cu, adapters_gemm.cu,
 // adapters_serve.cu)
 constexpr int kAdapterUnitRows = 256;  // rows of an input-gradient unit (a CTA pair)
-constexpr int kAdapterGemvTokens = 16;    // most tokens of the base product on warp instructions
 constexpr int kAdapterSmallTokens = 256;  // most tokens of the small-batch kernels
 constexpr int kAdapterTaskRows = 128;  // rows of a low-rank projection task (one adapter's)
 constexpr int kAdapterRowAlign = 32;   // an adapter's first row
@@ -238,8 +237,9 @@ cudaError_t launch_adapter_dgrad(const AdapterProjHost& h, const uint16_t* rows,
                                  const uint16_t* A, uint16_t* dx, int num_sms, cudaStream_t stream);
 cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, const uint16_t* dY, const uint16_t* p,
                                  const uint16_t* q, uint16_t* dA, uint16_t* dB, int num_sms, cudaStream_t stream);
-// y for up to kAdapterSmallTokens tokens in one launch (scratch: low [T, r] bf16, or for up to kAdapterGemvTokens
-// tokens [adapter_gemv_shares, T, r] float32).
+// y for up to kAdapterSmallTokens tokens in one launch (scratch: low [T, r] bf16, or, where adapter_gemv_serves,
+// [adapter_gemv_shares, T, r] float32).
+bool adapter_gemv_serves(int T, int K, int N);
 int adapter_gemv_shares(int T, int r, int N);
 cudaError_t launch_adapter_small(const AdapterProjHost& h, const int32_t* ids, const uint16_t* x, const uint16_t* A,
                                  const uint16_t* B, void* low, uint16_t* y, int num_sms, cudaStream_t stream);

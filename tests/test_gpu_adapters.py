@@ -160,6 +160,7 @@ TRAIN = [
     (1, 64, 8, 1, 8, "one"), (2, 128, 72, 3, 16, "each"), (16, 64, 64, 4, 8, "each"), (40, 192, 136, 5, 24, "zipf"),
     (100, 256, 128, 100, 8, "each"), (129, 320, 264, 4, 64, "runs"), (255, 128, 512, 6, 40, "zipf"),
     (300, 256, 200, 2, 16, "none"), (777, 512, 256, 16, 24, "zipf"), (1500, 128, 136, 1, 48, "one"),
+    (600, 1024, 1032, 2, 64, "runs"), (2500, 1024, 520, 1, 32, "one"), (1300, 2048, 264, 3, 16, "zipf"),
 ]
 
 
@@ -262,6 +263,125 @@ def test_training_step_captured():
     g.replay()
     for name in ("y", "dx", "dA", "dB"):
         assert torch.equal(getattr(pj, name), getattr(want, name)), name
+
+
+def test_graphs_that_share_a_workspace():
+    # a serving and a training graph over one object's buffers, replayed in turn
+    c = Case(150, 256, 136, 5, 24, "zipf", seed=9)
+    want, want_t = serve(c).y.clone(), train(c)
+    pj = e4b.Projection(c.dims, c.T)
+    base, ad = c.base(), c.adapters()
+    gs, gt = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gs):
+        pj.e4b_multi_lora_serve_fwd(c.ids, c.x, base, ad)
+    with torch.cuda.graph(gt):
+        pj.e4b_adapter_group(c.ids)
+        pj.e4b_multi_lora_fwd(c.x, base, ad)
+        pj.e4b_multi_lora_dgrad(c.dY, base, ad)
+    for _ in range(3):
+        gt.replay()
+        assert torch.equal(pj.y, want_t.y) and torch.equal(pj.dx, want_t.dx)
+        gs.replay()
+        assert torch.equal(pj.y, want)
+    assert pj.check_device_error() == e4b.E4B_OK
+
+
+def test_calls_on_several_streams_at_once():
+    # each with an object of its own: blocks that wait inside one launch wait only for earlier blocks of it
+    cases = [Case(T, 1024, 2048, 8, 16, "zipf", seed=20 + i) for i, T in enumerate((3, 16, 60, 200, 256, 300))]
+    want = [serve(c).y.clone() for c in cases]
+    objs = [(e4b.Projection(c.dims, c.T, train=False), c.base(), c.adapters(), torch.cuda.Stream()) for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, (pj, base, ad, st) in zip(cases, objs):
+            pj.e4b_multi_lora_serve_fwd(c.ids, c.x, base, ad, stream=st)
+    torch.cuda.synchronize()
+    for w, (pj, *_rest) in zip(want, objs):
+        assert torch.equal(pj.y, w) and pj.check_device_error() == e4b.E4B_OK
+
+
+def test_offsets_past_32_bits():
+    # y holds 2^31 elements and more: the last tokens' rows against the formula in 64 bits
+    T, N = 16400, 131080
+    c = Case(1, 64, N, 3, 8, "one", seed=30)
+    g = torch.Generator().manual_seed(4)
+    c.T, c.ids = T, torch.randint(-1, 3, (T,), generator=g).to(torch.int32).cuda()
+    c.x = torch.randn((T, 64), generator=g).to(torch.bfloat16).cuda()
+    y = serve(c).y
+    rows = [0, 7, 16000, 16384, T - 2, T - 1]
+    m = c.ref()
+    m["x"], m["ids"] = m["x"][rows], m["ids"][rows]
+    want, p = oa.project(**m)
+    ab = {k: (np.abs(v) if k != "ids" else v) for k, v in m.items()}
+    want_abs, p_abs = oa.project(**ab)
+    e_p = U * np.abs(p) + (64 + 4) * F * p_abs
+    prop = np.stack([e_p[i] @ ab["B"][a].T if 0 <= a < 3 else np.zeros(N) for i, a in enumerate(m["ids"])])
+    check(y[torch.tensor(rows).cuda()], want, (1 + U) * (prop + (64 + 8 + 4) * F * want_abs) + U * np.abs(want), "y")
+
+
+def test_gradient_offsets_past_32_bits():
+    # x, dx and the rows of the weight gradients' inputs, likewise
+    T, K = 16400, 131136
+    c = Case(1, K, 8, 3, 8, "one", seed=31)
+    g = torch.Generator().manual_seed(5)
+    c.T, c.ids = T, torch.randint(-1, 3, (T,), generator=g).to(torch.int32).cuda()
+    c.x = torch.randint(-3, 4, (T, K), dtype=torch.int8, device="cuda").to(torch.bfloat16)
+    c.dY = torch.randn((T, 8), generator=g).to(torch.bfloat16).cuda()
+    pj = train(c)
+    rows, cols = [0, 7, 16000, 16384, T - 2, T - 1], [0, 1, 63, 65536, K - 2, K - 1]
+    m, ids = c.ref(), c.ids.cpu().numpy()
+    dY = f64(c.dY)
+    q = np.zeros((T, c.r))
+    q_abs = np.zeros((T, c.r))
+    for a in range(c.n):
+        q[ids == a] = m["scale"][a] * dY[ids == a] @ m["B"][a]
+        q_abs[ids == a] = m["scale"][a] * np.abs(dY[ids == a]) @ np.abs(m["B"][a])
+    e_q = U * np.abs(q) + (8 + 4) * F * q_abs
+    xc = f64(c.x[:, torch.tensor(cols).cuda()])
+    for a in range(c.n):
+        of = ids == a
+        want = q[of].T @ xc[of]
+        tol = ((1 + U) * (e_q[of].T @ np.abs(xc[of]) + (T + 4 + 8) * F * (q_abs[of].T @ np.abs(xc[of])))
+               + U * np.abs(want))
+        check(pj.dA[a][:, torch.tensor(cols).cuda()], want, tol, "dA")
+    A = np.stack([m["A"][a] if 0 <= a < 3 else np.zeros_like(m["A"][0]) for a in ids[rows]])
+    dx = dY[rows] @ m["W"] + np.einsum("tr,trk->tk", q[rows], A)
+    dx_abs = np.abs(dY[rows]) @ np.abs(m["W"]) + np.einsum("tr,trk->tk", q_abs[rows], np.abs(A))
+    e = np.einsum("tr,trk->tk", e_q[rows], np.abs(A)) + (8 + 8 + 4) * F * dx_abs
+    check(pj.dx[torch.tensor(rows).cuda()], dx, (1 + U) * e + U * np.abs(dx), "dx")
+
+
+@pytest.mark.parametrize("shape,kernels", [
+    ((1, 256, 136, 3, 8, "one"), {"adapter_gemv": 1}),
+    ((16, 256, 136, 3, 8, "zipf"), {"adapter_gemv": 1}),
+    ((9, 4096, 4096, 3, 8, "zipf"), {"adapter_split": 1}),
+    ((17, 256, 136, 3, 8, "zipf"), {"adapter_split": 1}),
+    ((256, 256, 136, 3, 8, "zipf"), {"adapter_split": 1}),
+    ((257, 256, 136, 3, 8, "zipf"), {"adapter_group": 1, "adapter_proj_x": 1, "adapter_fwd": 1}),
+])
+def test_what_a_serving_call_launches(shape, kernels):
+    c = Case(*shape)
+    pj = e4b.Projection(c.dims, c.T, train=False)
+    e4b.e4b_profiler_read()
+    e4b.e4b_profiler_enable(True)
+    try:
+        pj.e4b_multi_lora_serve_fwd(c.ids, c.x, c.base(), c.adapters())
+    finally:
+        e4b.e4b_profiler_enable(False)
+    assert {k: n for k, (n, _) in e4b.e4b_profiler_read().items()} == kernels
+
+
+@pytest.mark.parametrize("shape", [
+    # one share of K and more, the blocks of p before the products and beside them, two token tiles of the warp
+    # products over several row blocks, forward units of 96 to 256 rows, both widths of the input gradient
+    (9, 4096, 4096, 3, 24, "zipf"), (30, 512, 8200, 5, 16, "zipf"), (30, 2048, 1024, 30, 64, "each"),
+    (250, 1024, 2056, 40, 64, "zipf"), (120, 4096, 264, 3, 32, "runs"), (12, 1024, 4104, 12, 40, "each"),
+    (400, 2048, 4096, 4, 16, "runs"), (700, 512, 12800, 6, 8, "zipf"),
+], ids=lambda s: "-".join(map(str, s)))
+def test_serve_wide(shape):
+    c = Case(*shape)
+    y, tol, _ = bounds(c)
+    check(serve(c).y, y, tol, "y")
 
 
 def test_rows_behind_the_last_token_stay():

@@ -249,3 +249,33 @@ def test_as_used_in_a_training_step():
     # the sum is rounded once more, by half a last place of the router's gradient
     assert np.all(np.abs(got - want[-1]) <= 2 * H * np.abs(total.double().cpu().numpy()) + 1e-4 * np.abs(want[-1]).max())
     assert blk.check_device_error() == e4b.E4B_OK
+
+
+def test_calls_on_several_streams_at_once():
+    # the joining blocks of a launch wait only for blocks of it that come before them
+    cases = [make(T, E, 4, S, 0.9, seed=T) + [E] for T, E, S in ((5000, 64, 3), (3000, 512, 40), (20000, 16, 1),
+                                                                 (2000, 1000, 200))]
+    want = [run(c[4], 4, *c[:4]) for c in cases]
+    objs = [(e4b.RouterBalance(c[4], 4, c[0].shape[0], c[2].numel() - 1), torch.empty_like(c[0]), torch.cuda.Stream())
+            for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (logits, ids, seq, mask, _E), (b, d, st) in zip(cases, objs):
+            b.e4b_balance_fwd(logits, ids, seq, mask, 0.7, 0.3, stream=st)
+            b.e4b_balance_bwd(logits, d, seq, mask, 0.7, 0.3, stream=st)
+    torch.cuda.synchronize()
+    for (w, wd), (b, d, _st) in zip(want, objs):
+        assert torch.equal(b.loss, w.loss) and torch.equal(d, wd) and b.check_device_error() == e4b.E4B_OK
+
+
+def test_what_a_call_launches():
+    logits, ids, seq, mask = make(500, 64, 4, 3, 1.0)
+    b, d = e4b.RouterBalance(64, 4, 500, 3), torch.empty_like(logits)
+    e4b.e4b_profiler_read()
+    e4b.e4b_profiler_enable(True)
+    try:
+        b.e4b_balance_fwd(logits, ids, seq, mask)
+        b.e4b_balance_bwd(logits, d, seq, mask)
+    finally:
+        e4b.e4b_profiler_enable(False)
+    assert {k: n for k, (n, _) in e4b.e4b_profiler_read().items()} == {"balance_fwd": 1, "balance_bwd": 1}
