@@ -11,17 +11,18 @@
 // blocks at the end of the grid wait for the records (a counter in the workspace,
 // bounded wait; the blocks they wait for come first and never wait), add a
 // sequence's records in range order, so that the sums do not depend on which
-// block ran first, and the last of them forms the loss.  A second launch in
-// their place cost the host 4.5 us and the GPU 10 to 15.  Backward: one pass
-// over the logits with lse given.
+// block ran first, and the last of them adds up their shares of the loss.  A
+// second launch in their place cost the host 4.5 us and the GPU 10 to 15.
+// Backward: one pass over the logits with lse given.
 //
 // What bounds them: HBM reads of the logits (forward) and reads plus writes
-// of T x E float32 (backward); for small batches the launch.
+// of T x E float32 (backward); for small batches the launch.  131072 tokens of
+// 64 experts: backward 11 us, 6.1 TB/s; forward 18.5 us, of which the pass over
+// the logits takes 10 and the records, their counter and the join the rest.
 // A group of G lanes owns a token, each lane 16 columns in runs of four
 // (16-byte loads), G the smallest power of two with 16 G >= E: with four columns
 // a lane the shuffles and the other work per token and lane were the limit, not
-// memory (131072 tokens of 64 experts: forward 46 us, backward 23 us).  A group
-// takes two tokens at a time, their loads together.
+// memory (forward 46 us).
 #include <math.h>
 
 #include "e4b_device.cuh"
@@ -35,9 +36,6 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSlice = 8;  // experts of a joining item: 8 lanes, so that 32 records are read at a time
-
-// Tokens of a group at a time.
-constexpr int tokens_at_once(int V) { return V <= 2 ? 4 : (V == 4 ? 2 : 1); }
 
 // First sequence whose end lies beyond token t (S: none); ends ascending.  Whole warp: 32 ends a round trip, where
 // a binary search would wait for memory log2(S) times.
@@ -66,6 +64,15 @@ __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
   for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   return v;
+}
+
+// exp(x) for x up to 0: the exponential of 2 of x log2(e), three operations a value where expf has about nine (131072
+// tokens of 64 experts, both directions: expf 34.9 us, this 29.5 us).  Relative error (1.3 |x| + 4) 2^-24: the product's rounding and the
+// constant's, and the instruction's.  -inf gives 0; probabilities below 2^-126 are 0.
+__device__ __forceinline__ float exp_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
 }
 
 // The columns of lane g of a group: 4 (v G + g) + 0..3 for v < V.  Rows start
@@ -98,8 +105,7 @@ struct FwdParams {
   DeviceError* err;   // the workspace's front: `ready` record blocks done, `left` joining blocks done
   float2* part;       // [slots, E] (probability sum, count as an int's bits)
   float2* part_zn;    // [slots] (sum of lse^2, tokens as an int's bits)
-  float* seq_dot;     // [S, slices] sum over a slice's experts of counts * probability sums
-  float* seq_z;       // [S]
+  float4* joined;     // [joining blocks] its items' balance, sum of lse^2, tokens and sequences as ints' bits
   int32_t* counts;
   float* prob_sum;
   int32_t* tokens;
@@ -115,14 +121,28 @@ __device__ __forceinline__ int2 sequence_range(const FwdParams& p, int s) {
   return make_int2(lo, min(max(__ldg(p.offsets + s + 1), lo), p.T));
 }
 
+// Balance terms, sums of lse^2, tokens and sequences with tokens.
+struct Joined {
+  float bal, z;
+  int n, s;
+};
+__device__ __forceinline__ void add(Joined& a, const Joined& b) {
+  a.bal += b.bal;
+  a.z += b.z;
+  a.n += b.n;
+  a.s += b.s;
+}
+
 // The join: item (s, slice) adds the records of sequence s in range order: W warps take every W-th 4-record group, a
-// lane one expert of every fourth record.  A block an item (W = 8) while there are blocks enough, else a warp.
+// lane one expert of every fourth record.  A block an item (W = 8) while there are blocks enough, else a warp.  A
+// sequence's term of the balance is E / (k n_s^2) sum_e counts * probability sums.  Lane 0's result counts.
 template <int W>
-__device__ void join_items(const FwdParams& p, int first, int step, int2 range) {
+__device__ Joined join_items(const FwdParams& p, int first, int step, int2 range) {
   __shared__ float sp[kWarps][kSlice];
   __shared__ int32_t sc[kWarps][kSlice];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = lane & (kSlice - 1), row = lane / kSlice;
   const int part_of = W == 1 ? 0 : warp;
+  Joined sum = {0.0f, 0.0f, 0, 0};
   for (int item = first; item < p.S * p.slices; item += step) {
     const int s = item / p.slices, slice = item - s * p.slices, e = slice * kSlice + col;
     if (item != first) range = sequence_range(p, s);
@@ -130,7 +150,15 @@ __device__ void join_items(const FwdParams& p, int first, int step, int2 range) 
     const int b0 = lo / p.per_block, b1 = hi > lo ? (hi - 1) / p.per_block : b0 - 1;
     float a = 0.0f, z = 0.0f;
     int c = 0, n = 0;
-    constexpr int kAhead = 4, kStep = W * 4;
+    constexpr int kAhead = 8, kStep = W * 4;
+    if (part_of == 0) {
+#pragma unroll 2
+      for (int b = b0 + lane; b <= b1; b += 32) {
+        const float2 v = __ldcg(p.part_zn + (size_t)b + s);
+        z += v.x;
+        n += __float_as_int(v.y);
+      }
+    }
     for (int b = b0 + 4 * part_of + row; b <= b1; b += kStep * kAhead) {
       float2 v[kAhead];
 #pragma unroll
@@ -142,13 +170,6 @@ __device__ void join_items(const FwdParams& p, int first, int step, int2 range) 
       for (int i = 0; i < kAhead; ++i) {
         a += v[i].x;
         c += __float_as_int(v[i].y);
-      }
-    }
-    if (slice == 0 && part_of == 0) {
-      for (int b = b0 + lane; b <= b1; b += 32) {
-        const float2 v = __ldcg(p.part_zn + (size_t)b + s);
-        z += v.x;
-        n += __float_as_int(v.y);
       }
     }
 #pragma unroll
@@ -182,74 +203,29 @@ __device__ void join_items(const FwdParams& p, int first, int step, int2 range) 
         z += __shfl_xor_sync(kFull, z, o);
         n += __shfl_xor_sync(kFull, n, o);
       }
-      if (lane == 0) {
-        p.seq_dot[item] = dot;
-        if (slice == 0) {
-          p.seq_z[s] = z;
-          p.tokens[s] = n;
+      if (n > 0) sum.bal += dot * ((float)p.E / ((float)p.k * (float)n)) / (float)n;
+      if (slice == 0) {
+        if (lane == 0) p.tokens[s] = n;
+        if (n > 0) {
+          sum.z += z;
+          sum.n += n;
+          ++sum.s;
         }
       }
     }
     if constexpr (W > 1) __syncthreads();
   }
+  return sum;
 }
 
-__device__ __forceinline__ void write_loss(const FwdParams& p, float bal, float zz, int nt, int ns) {
-  bal = ns > 0 ? bal / (float)ns : 0.0f;
-  zz = nt > 0 ? zz / (float)nt : 0.0f;
-  p.tokens[p.S] = nt;
-  p.tokens[p.S + 1] = ns;
+__device__ __forceinline__ void write_loss(const FwdParams& p, const Joined& v) {
+  const float bal = v.s > 0 ? v.bal / (float)v.s : 0.0f;
+  const float zz = v.n > 0 ? v.z / (float)v.n : 0.0f;
+  p.tokens[p.S] = v.n;
+  p.tokens[p.S + 1] = v.s;
   p.loss[0] = p.c_b * bal + p.c_z * zz;
   p.loss[1] = bal;
   p.loss[2] = zz;
-}
-
-// balance = (1 / S') sum_s (E / (k n_s^2)) sum_e counts psum;  z = sum_s seq_z / n
-__device__ void form_loss(const FwdParams& p) {
-  __shared__ float red_a[kWarps], red_b[kWarps];
-  __shared__ int red_n[kWarps], red_s[kWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float bal = 0.0f, zz = 0.0f;
-  int nt = 0, ns = 0;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < p.S * p.slices; i += kThreads) {
-    const int q = i / p.slices;
-    const float d = __ldcg(p.seq_dot + i), zq = __ldcg(p.seq_z + q);
-    const int m = __ldcg(p.tokens + q);
-    if (m > 0) {
-      bal += d * ((float)p.E / ((float)p.k * (float)m)) / (float)m;
-      if (i - q * p.slices == 0) {
-        zz += zq;
-        nt += m;
-        ++ns;
-      }
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    bal += __shfl_xor_sync(kFull, bal, o);
-    zz += __shfl_xor_sync(kFull, zz, o);
-    nt += __shfl_xor_sync(kFull, nt, o);
-    ns += __shfl_xor_sync(kFull, ns, o);
-  }
-  if (lane == 0) {
-    red_a[warp] = bal;
-    red_b[warp] = zz;
-    red_n[warp] = nt;
-    red_s[warp] = ns;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    bal = zz = 0.0f;
-    nt = ns = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      bal += red_a[w];
-      zz += red_b[w];
-      nt += red_n[w];
-      ns += red_s[w];
-    }
-    write_loss(p, bal, zz, nt, ns);
-  }
 }
 
 __device__ __forceinline__ void empty_sequence(const FwdParams& p, int s) {
@@ -279,28 +255,46 @@ __device__ void join_block(const FwdParams& p) {
   }
   __syncthreads();
   if (!flag) return;
-  if (wide)
-    join_items<kWarps>(p, first, p.join_blocks, range);
-  else
-    join_items<1>(p, first, p.join_blocks * kWarps, range);
+  __shared__ Joined warps[kWarps];
+  const Joined mine = wide ? join_items<kWarps>(p, first, p.join_blocks, range)
+                           : join_items<1>(p, first, p.join_blocks * kWarps, range);
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = mine;
   __syncthreads();
   if (threadIdx.x == 0) {
+    Joined v = {0.0f, 0.0f, 0, 0};
+    for (int w = 0; w < kWarps; ++w) add(v, warps[w]);
+    p.joined[joiner] = make_float4(v.bal, v.z, __int_as_float(v.n), __int_as_float(v.s));
     __threadfence();
     flag = atomicAdd(&p.err->left, 1) == p.join_blocks - 1;
   }
   __syncthreads();
-  if (!flag) return;
+  if (!flag || threadIdx.x >= 32) return;
   __threadfence();
-  form_loss(p);
-  if (threadIdx.x == 0) p.err->ready = p.err->left = 0;
+  Joined v = {0.0f, 0.0f, 0, 0};
+  for (int b = threadIdx.x; b < p.join_blocks; b += 32) {
+    const float4 q = __ldcg(p.joined + b);
+    add(v, {q.x, q.y, __float_as_int(q.z), __float_as_int(q.w)});
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    add(v, {__shfl_xor_sync(kFull, v.bal, o), __shfl_xor_sync(kFull, v.z, o), __shfl_xor_sync(kFull, v.n, o),
+            __shfl_xor_sync(kFull, v.s, o)});
+  if (threadIdx.x == 0) {
+    write_loss(p, v);
+    p.err->ready = p.err->left = 0;
+  }
 }
+
+// Resident blocks of the forward on an SM, so that one's loads meet another's arithmetic (131072 tokens of 64 experts:
+// two 20.5 us, four 18.6 us).
+constexpr int fwd_blocks(int V) { return V == 8 ? 2 : 4; }
 
 // Block b owns tokens [b C, (b + 1) C); every sequence that meets the range
 // gives one piece, recorded in slot b + s (distinct along the staircase of
 // pieces, which moves right in b or s at every step).  ONE: a single block
 // covers the batch; its pieces are the sequences and need no records.
 template <int G, int V, bool ALIGNED, bool ONE>
-__global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const FwdParams p) {
+__global__ void __launch_bounds__(kThreads, fwd_blocks(V)) balance_fwd_kernel(const FwdParams p) {
   if (!ONE && (int)blockIdx.x >= p.blocks) {
     join_block(p);
     return;
@@ -310,8 +304,7 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const FwdParams p
   int32_t* sc = reinterpret_cast<int32_t*>(sp + kWarps * p.E);  // [E]
   float* sz = reinterpret_cast<float*>(sc + p.E);               // [kWarps]
   int32_t* sn = reinterpret_cast<int32_t*>(sz + kWarps);        // [kWarps]
-  constexpr int kTok = 32 / G;  // tokens of a warp at a time, and of its groups one after another
-  constexpr int U = tokens_at_once(V);
+  constexpr int kTok = 32 / G;  // tokens of a warp at a time
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane % G, sub = lane / G;
   const int E = p.E;
   const bool few_ids = p.k <= 2 * G;
@@ -319,8 +312,7 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const FwdParams p
   const int t_end = (int)min((int64_t)p.T, r0 + p.per_block);
   int t0 = (int)min((int64_t)p.T, r0);
   int s = p.offsets && !ONE ? sequence_of(p.offsets, p.S, t0) : 0;
-  float bal = 0.0f, zz = 0.0f;  // (ONE, thread 0) the loss so far
-  int nt = 0, ns = 0;
+  Joined total = {0.0f, 0.0f, 0, 0};  // (ONE, thread 0) the sequences so far
   while (t0 < t_end) {
     int lo = t0, hi = t_end;
     if (p.offsets) {
@@ -345,57 +337,48 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const FwdParams p
     for (int i = 0; i < 4 * V; ++i) acc[i] = 0.0f;
     float zsum = 0.0f;
     int n = 0;
-    for (int tb = lo + warp * kTok + sub; tb - sub < hi; tb += kWarps * kTok * U) {
-      float l[U][4 * V];
-      int id[U][2];
-      bool live[U];
+    for (int t = lo + warp * kTok + sub; t - sub < hi; t += kWarps * kTok) {
+      float l[4 * V];
+      int id[2];
+      const bool in = t < hi;
+      load_row<G, V, ALIGNED>(p.logits + (size_t)(in ? t : lo) * E, g, E, in, l);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = tb + u * kWarps * kTok;
-        const bool in = t < hi;
-        load_row<G, V, ALIGNED>(p.logits + (size_t)(in ? t : lo) * E, g, E, in, l[u]);
+      for (int j = 0; j < 2; ++j)
+        id[j] = in && few_ids && g + j * G < p.k ? __ldg(p.ids + (size_t)t * p.k + g + j * G) : -1;
+      const bool live = in && (p.mask == nullptr || __ldg(p.mask + t) != 0);
+      if (!live) {  // a masked token's values are not looked at
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          id[u][j] = in && few_ids && g + j * G < p.k ? __ldg(p.ids + (size_t)t * p.k + g + j * G) : -1;
-        live[u] = in && (p.mask == nullptr || __ldg(p.mask + t) != 0);
+        for (int i = 0; i < 4 * V; ++i) l[i] = -INFINITY;
+        id[0] = id[1] = -1;
       }
+      float m = l[0];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = tb + u * kWarps * kTok;
-        if (!live[u]) {  // a masked token's values are not looked at
+      for (int i = 1; i < 4 * V; ++i) m = fmaxf(m, l[i]);
+      m = group_max<G>(m);
+      // a row of -inf alone (a masked token too) has no probabilities
+      const float ms = (m == -INFINITY) ? 0.0f : m;
+      float sum = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 4 * V; ++i) l[u][i] = -INFINITY;
-          id[u][0] = id[u][1] = -1;
-        }
-        float m = l[u][0];
-#pragma unroll
-        for (int i = 1; i < 4 * V; ++i) m = fmaxf(m, l[u][i]);
-        m = group_max<G>(m);
-        // a row of -inf alone (a masked token too) has no probabilities
-        const float ms = (m == -INFINITY) ? 0.0f : m;
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4 * V; ++i) {
-          l[u][i] = expf(l[u][i] - ms);
-          sum += l[u][i];
-        }
-        sum = group_sum<G>(sum);
-        const float inv = (sum == 0.0f) ? 0.0f : 1.0f / sum;
-#pragma unroll
-        for (int i = 0; i < 4 * V; ++i) acc[i] = fmaf(l[u][i], inv, acc[i]);
-        if (g == 0 && t < hi) {
-          const float lse = (sum == 0.0f) ? (live[u] ? -INFINITY : 0.0f) : ms + logf(sum);
-          p.lse[t] = lse;
-          if (live[u]) {
-            if (sum != 0.0f) zsum = fmaf(lse, lse, zsum);
-            ++n;
-          }
-        }
-        // the token's slots (integer sums: any order)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if ((uint32_t)id[u][j] < (uint32_t)E) atomicAdd(&sc[id[u][j]], 1);
+      for (int i = 0; i < 4 * V; ++i) {
+        l[i] = exp_of(l[i] - ms);
+        sum += l[i];
       }
+      sum = group_sum<G>(sum);
+      const float inv = (sum == 0.0f) ? 0.0f : 1.0f / sum;
+#pragma unroll
+      for (int i = 0; i < 4 * V; ++i) acc[i] = fmaf(l[i], inv, acc[i]);
+      if (g == 0 && in) {
+        const float lse = (sum == 0.0f) ? (live ? -INFINITY : 0.0f) : ms + logf(sum);
+        p.lse[t] = lse;
+        if (live) {
+          if (sum != 0.0f) zsum = fmaf(lse, lse, zsum);
+          ++n;
+        }
+      }
+      // the token's slots (integer sums: any order)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if ((uint32_t)id[j] < (uint32_t)E) atomicAdd(&sc[id[j]], 1);
     }
     if (!few_ids) {  // more slots than two a lane: the piece's ids in a pass of their own
       const uint32_t n_ids = (uint32_t)(hi - lo) * p.k;
@@ -408,12 +391,18 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const FwdParams p
           const uint32_t i = i0 + j * kThreads;
           e[j] = i < n_ids ? (uint32_t)__ldg(at + i) : kFull;
         }
+        if (p.mask != nullptr) {  // loads of their own, all eight in flight
+          uint8_t on[kAhead];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          const uint32_t i = i0 + j * kThreads;
-          if (e[j] < (uint32_t)E && (p.mask == nullptr || __ldg(p.mask + lo + i / (uint32_t)p.k) != 0))
-            atomicAdd(&sc[e[j]], 1);
+          for (int j = 0; j < kAhead; ++j)
+            on[j] = __ldg(p.mask + lo + min(i0 + j * kThreads, n_ids - 1) / (uint32_t)p.k);
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j)
+            if (on[j] == 0) e[j] = kFull;
         }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (e[j] < (uint32_t)E) atomicAdd(&sc[e[j]], 1);
       }
     }
     // this warp's tokens of one column: over the groups of the warp, then the warps in order
@@ -472,10 +461,7 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const FwdParams p
         if (c > 0) {
           float d = 0.0f;
           for (int w = 0; w < kWarps; ++w) d += sp[w];
-          bal += d * ((float)E / ((float)p.k * (float)c)) / (float)c;
-          zz += z;
-          nt += c;
-          ++ns;
+          add(total, {d * ((float)E / ((float)p.k * (float)c)) / (float)c, z, c, 1});
         }
       } else {
         p.part_zn[slot] = make_float2(z, __int_as_float(c));
@@ -487,7 +473,7 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const FwdParams p
   }
   if constexpr (ONE) {
     for (; s < p.S; ++s) empty_sequence(p, s);
-    if (threadIdx.x == 0) write_loss(p, bal, zz, nt, ns);
+    if (threadIdx.x == 0) write_loss(p, total);
     return;
   }
   __syncthreads();
@@ -518,7 +504,7 @@ constexpr int bwd_blocks(int V) { return V == 8 ? 2 : 3; }
 // registers and is read again where the sequence changes.
 template <int G, int V, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, bwd_blocks(V)) balance_bwd_kernel(const BwdParams p) {
-  constexpr int kTok = 32 / G, U = tokens_at_once(V);
+  constexpr int kTok = 32 / G;
   const int lane = threadIdx.x & 31, g = lane % G, sub = lane / G;
   const int64_t w0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.per_warp;
   if (w0 >= p.T) return;
@@ -572,58 +558,49 @@ __global__ void __launch_bounds__(kThreads, bwd_blocks(V)) balance_bwd_kernel(co
         }
       }
     }
-    for (int tb = t0 + sub; tb - sub < hi; tb += kTok * U) {
-      float l[U][4 * V], lse[U];
-      bool live[U];
+    for (int t = t0 + sub; t - sub < hi; t += kTok) {
+      float l[4 * V];
+      const bool in = t < hi;
+      load_row<G, V, ALIGNED>(p.logits + (size_t)(in ? t : t0) * E, g, E, in && inside, l);
+      const float lse = in ? __ldg(p.lse + t) : 0.0f;
+      const bool live = in && inside && (p.mask == nullptr || __ldg(p.mask + t) != 0);
+      const bool some = lse != -INFINITY;  // a row of -inf alone has no probabilities
+      float dot = 0.0f;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = tb + u * kTok;
-        const bool in = t < hi;
-        load_row<G, V, ALIGNED>(p.logits + (size_t)(in ? t : t0) * E, g, E, in && inside, l[u]);
-        lse[u] = in ? __ldg(p.lse + t) : 0.0f;
-        live[u] = in && inside && (p.mask == nullptr || __ldg(p.mask + t) != 0);
+      for (int i = 0; i < 4 * V; ++i) {
+        l[i] = some && live ? exp_of(l[i] - lse) : 0.0f;
+        dot = fmaf(l[i], live ? f[i] : 0.0f, dot);
       }
+      dot = group_sum<G>(dot);
+      const float zt = some ? zc * lse : 0.0f;
+      if (!in) continue;
+      float* row = p.d_logits + (size_t)t * E;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = tb + u * kTok;
-        const bool some = lse[u] != -INFINITY;  // a row of -inf alone has no probabilities
-        float dot = 0.0f;
+      for (int v = 0; v < V; ++v) {
+        const int c = 4 * (v * G + g);
+        float d[4];
 #pragma unroll
-        for (int i = 0; i < 4 * V; ++i) {
-          l[u][i] = some && live[u] ? expf(l[u][i] - lse[u]) : 0.0f;
-          dot = fmaf(l[u][i], live[u] ? f[i] : 0.0f, dot);
-        }
-        dot = group_sum<G>(dot);
-        const float zt = some ? zc * lse[u] : 0.0f;
-        if (t >= hi) continue;
-        float* row = p.d_logits + (size_t)t * E;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int c = 4 * (v * G + g);
-          float d[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) d[i] = live[u] ? l[u][4 * v + i] * fmaf(bc, f[4 * v + i] - dot, zt) : 0.0f;
-          if (ALIGNED) {
-            if (c < E) {
-              float4* q = reinterpret_cast<float4*>(row + c);
-              float4 o = make_float4(d[0], d[1], d[2], d[3]);
-              if (p.accumulate) {
-                if (!live[u]) continue;
-                const float4 w = *q;
-                o = make_float4(w.x + d[0], w.y + d[1], w.z + d[2], w.w + d[3]);
-              }
-              *q = o;
+        for (int i = 0; i < 4; ++i) d[i] = live ? l[4 * v + i] * fmaf(bc, f[4 * v + i] - dot, zt) : 0.0f;
+        if (ALIGNED) {
+          if (c < E) {
+            float4* q = reinterpret_cast<float4*>(row + c);
+            float4 o = make_float4(d[0], d[1], d[2], d[3]);
+            if (p.accumulate) {
+              if (!live) continue;
+              const float4 w = *q;
+              o = make_float4(w.x + d[0], w.y + d[1], w.z + d[2], w.w + d[3]);
             }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (c + i < E) {
-                if (!p.accumulate)
-                  row[c + i] = d[i];
-                else if (live[u])
-                  row[c + i] += d[i];
-              }
+            *q = o;
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c + i < E) {
+              if (!p.accumulate)
+                row[c + i] = d[i];
+              else if (live)
+                row[c + i] += d[i];
+            }
         }
       }
     }
@@ -669,33 +646,32 @@ struct RunBwd {
 
 // Tokens that a warp's groups hold at a time.
 int warp_tokens(int E) {
-  if (E <= 4) return 32 * tokens_at_once(1);
-  if (E <= 8) return 32 * tokens_at_once(2);
   int g = 1;
   while (g < 32 && 16 * g < E) g *= 2;
-  return 32 / g * tokens_at_once(E <= 512 ? 4 : 8);
+  return 32 / g;
 }
-// Token ranges: at least the tokens that a block's warps hold at a time; with the joining blocks at most two blocks
-// an SM (all resident at once).
-constexpr int kJoinBlocks = 64;
-constexpr int kMaxBlocks = 2 * 148 - kJoinBlocks;
+// Token ranges: at least the tokens that a block's warps hold at a time, at most one wave of resident blocks.  (8192
+// tokens of 128 experts, forward: 256 blocks of one round 10.3 us, 147 of two 12.4 us.)  Joining blocks: one an SM
+// (30011 tokens of 256 experts in 37 sequences, forward: 64 20.6 us, 148 17.9 us).
+constexpr int kJoinBlocks = 148;
+constexpr int max_blocks(int E) { return 148 * fwd_blocks(E <= 512 ? 4 : 8); }
 int balance_blocks(int T, int E) {
-  const int at_once = kWarps * warp_tokens(E), b = (T + at_once - 1) / at_once;
-  return b < kMaxBlocks ? b : kMaxBlocks;
+  const int at_once = kWarps * warp_tokens(E);
+  const int b = (T + at_once - 1) / at_once;
+  return b < max_blocks(E) ? b : max_blocks(E);
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 struct BalanceLayout {
-  size_t part, part_zn, seq_dot, seq_z, total;
+  size_t part, part_zn, joined, total;
 };
 BalanceLayout balance_layout(int T, int E, int S) {
-  const size_t slots = (size_t)balance_blocks(T, E) + S, slices = (E + kSlice - 1) / kSlice;
+  const size_t slots = (size_t)balance_blocks(T, E) + S;
   BalanceLayout l;
   l.part = sizeof(DeviceError);
   l.part_zn = l.part + align256(slots * E * 8);
-  l.seq_dot = l.part_zn + align256(slots * 8);
-  l.seq_z = l.seq_dot + align256((size_t)S * slices * 4);
-  l.total = l.seq_z + align256((size_t)S * 4);
+  l.joined = l.part_zn + align256(slots * 8);
+  l.total = l.joined + align256(kJoinBlocks * sizeof(float4));
   return l;
 }
 
@@ -717,8 +693,7 @@ cudaError_t launch_balance_fwd(const BalanceHost& h, void* ws, cudaStream_t stre
   p.err = reinterpret_cast<DeviceError*>(w);
   p.part = reinterpret_cast<float2*>(w + l.part);
   p.part_zn = reinterpret_cast<float2*>(w + l.part_zn);
-  p.seq_dot = reinterpret_cast<float*>(w + l.seq_dot);
-  p.seq_z = reinterpret_cast<float*>(w + l.seq_z);
+  p.joined = reinterpret_cast<float4*>(w + l.joined);
   p.counts = h.counts;
   p.prob_sum = h.prob_sum;
   p.tokens = h.tokens;
