@@ -140,6 +140,8 @@ template <int W>
 __device__ Joined join_items(const FwdParams& p, int first, int step, int2 range) {
   __shared__ float sp[kWarps][kSlice];
   __shared__ int32_t sc[kWarps][kSlice];
+  __shared__ float sz[kWarps];
+  __shared__ int32_t sn[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = lane & (kSlice - 1), row = lane / kSlice;
   const int part_of = W == 1 ? 0 : warp;
   Joined sum = {0.0f, 0.0f, 0, 0};
@@ -151,13 +153,11 @@ __device__ Joined join_items(const FwdParams& p, int first, int step, int2 range
     float a = 0.0f, z = 0.0f;
     int c = 0, n = 0;
     constexpr int kAhead = 8, kStep = W * 4;
-    if (part_of == 0) {
 #pragma unroll 2
-      for (int b = b0 + lane; b <= b1; b += 32) {
-        const float2 v = __ldcg(p.part_zn + (size_t)b + s);
-        z += v.x;
-        n += __float_as_int(v.y);
-      }
+    for (int b = b0 + 32 * part_of + lane; b <= b1; b += 32 * W) {
+      const float2 v = __ldcg(p.part_zn + (size_t)b + s);
+      z += v.x;
+      n += __float_as_int(v.y);
     }
     for (int b = b0 + 4 * part_of + row; b <= b1; b += kStep * kAhead) {
       float2 v[kAhead];
@@ -177,18 +177,29 @@ __device__ Joined join_items(const FwdParams& p, int first, int step, int2 range
       a += __shfl_xor_sync(kFull, a, o);
       c += __shfl_xor_sync(kFull, c, o);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      z += __shfl_xor_sync(kFull, z, o);
+      n += __shfl_xor_sync(kFull, n, o);
+    }
     if constexpr (W > 1) {
       if (row == 0) {
         sp[warp][col] = a;
         sc[warp][col] = c;
       }
+      if (lane == 0) {
+        sz[warp] = z;
+        sn[warp] = n;
+      }
       __syncthreads();
-      a = 0.0f;
-      c = 0;
+      a = z = 0.0f;
+      c = n = 0;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         a += sp[w][col];
         c += sc[w][col];
+        z += sz[w];
+        n += sn[w];
       }
     }
     if (part_of == 0) {
@@ -198,11 +209,7 @@ __device__ Joined join_items(const FwdParams& p, int first, int step, int2 range
       }
       float dot = (row == 0 && e < p.E) ? (float)c * a : 0.0f;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        dot += __shfl_xor_sync(kFull, dot, o);
-        z += __shfl_xor_sync(kFull, z, o);
-        n += __shfl_xor_sync(kFull, n, o);
-      }
+      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
       if (n > 0) sum.bal += dot * ((float)p.E / ((float)p.k * (float)n)) / (float)n;
       if (slice == 0) {
         if (lane == 0) p.tokens[s] = n;
