@@ -12,11 +12,11 @@
 // bounded wait) only in their epilogue.  The blocks of p never wait and come
 // first in the grid.
 //
-// For few tokens the products run on warp matrix instructions (m16n8k16): there is nothing for a 128-row UMMA tile to amortise its set-up over.  Above,
-// reading x again for every 16 rows of W would cost more than W itself, and a
-// UMMA takes 128 rows of W (decoded into tensor memory) against all tokens at
-// once, K split over a cluster whose partial sums meet through distributed
-// shared memory.
+// For few tokens the products run on warp matrix instructions (m16n8k16): there is
+// nothing for a 128-row UMMA tile to amortise its set-up over.  Above, reading x
+// again for every 16 rows of W would cost more than W itself, and a UMMA takes 128
+// rows of W (decoded into tensor memory) against all tokens at once, K split over a
+// cluster whose partial sums meet through distributed shared memory.
 //
 // The sum over k may be taken in any order that both operands share, so in the
 // warp products a lane takes 16 (W, x: 64) consecutive values of its row, and the
@@ -34,6 +34,7 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTokenTile = 8;
+constexpr int kPlaces = 2 * 148;  // blocks of adapter_gemv_kernel at once
 
 // Hand-over of p between the blocks of a launch.  signal_ready: the whole block, after its stores of p.
 // wait_ready: one thread; false where the limit ran out.  leave: one thread, once the block has p.
@@ -133,8 +134,15 @@ __device__ __forceinline__ void low_rank_tile(const uint16_t* x, const uint16_t*
 }
 
 // ----------------------------------------------------------------------------
-// y for up to 16 tokens: 16 rows of W a block, K split over its warps
+// y for up to 16 tokens: 16 rows of W at a time, K split over the block's warps
 // ----------------------------------------------------------------------------
+// Blocks stay for several units of rows, the next unit's codes in flight while one
+// ends and p read once: 4096 -> 14336, 1 token 22.6 us (a block a unit: 24.6 us), 8
+// tokens 26.7 us (30.2 us).  1 token at 2048 -> 4096 takes 8.2 us, the chain of
+// loads and waits; on the large matrix the byte permutes of the decoding fill their
+// pipe for 13 us and what is left is between the steps.  Decoding by a table of byte
+// pairs in shared memory instead: 20.4 us at 1 token, but 32.8 us at 8, whose rows
+// of x come through the same pipe.
 // The blocks of p take (token, 16 ranks, share of K) each; with few of them K is
 // split (kq shares, added in order by the readers), since one block's loads
 // would be the longest chain of the launch.
@@ -156,7 +164,8 @@ struct GemvParams {
 
 template <int NT>  // tiles of 8 tokens
 __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvParams p) {
-  __shared__ float red[kWarps * 16 * 9 > kWarps * 8 * NT * 17 ? kWarps * 16 * 9 : kWarps * 8 * NT * 17];
+  __shared__ float red[2][kWarps * 8 * NT * 17];  // a unit's partial sums, in turn; a block of p: [warp][16][9]
+  static_assert(2 * 8 * NT * 17 >= 16 * 9, "a block of p fits");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   if ((int)blockIdx.x < p.p_blocks) {
     const int slices = (p.r + 15) / 16;
@@ -164,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvPar
     const int t = item / slices, j0 = (item - t * slices) * 16;
     const int a = __ldg(p.ids + t);
     if ((uint32_t)a < (uint32_t)p.n) {
-      float(*tile)[16][kTokenTile + 1] = reinterpret_cast<float(*)[16][kTokenTile + 1]>(red);
+      float(*tile)[16][kTokenTile + 1] = reinterpret_cast<float(*)[16][kTokenTile + 1]>(red[0]);
       const int blocks32 = p.K / 32;
       low_rank_tile<kWarps>(p.x, p.A, p.K, p.r, a, g == 0 ? t : -1, j0, share * blocks32 / p.kq * 32,
                             (share + 1) * blocks32 / p.kq * 32, tile);
@@ -179,14 +188,8 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvPar
     signal_ready(p.err);
     return;
   }
-  const int n0 = ((int)blockIdx.x - p.p_blocks) * 16;
-  const bool lo = n0 + g < p.N, hi = n0 + g + 8 < p.N;
-  const size_t r0 = lo ? n0 + g : 0, r1 = hi ? n0 + g + 8 : 0;
-  // A step is 256 values of k, one NF4 block of 64 a lane and row.
-  const uint8_t* c0 = p.nf4 + r0 * (p.K / 2) + 32 * q;
-  const uint8_t* c1 = p.nf4 + r1 * (p.K / 2) + 32 * q;
-  const float* s0 = p.absmax + r0 * (p.K / 64) + q;
-  const float* s1 = p.absmax + r1 * (p.K / 64) + q;
+  // A unit is 16 rows of W; a step of a warp is 256 values of k, one NF4 block of 64 a lane and row.
+  const int units = (p.N + 15) / 16, step = (int)gridDim.x - p.p_blocks;
   const uint16_t* xr[NT];
   bool tok[NT];
 #pragma unroll
@@ -195,124 +198,137 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvPar
     xr[i] = p.x + (tok[i] ? (size_t)(8 * i + g) * p.K : 0) + 64 * q;
   }
   const Nf4Shift ks = nf4_shift_consts();
-  float acc[NT][4];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
   struct Raw {
     uint4 a[2], b[2];
     float ma, mb;
   };
-  auto load = [&](int k0) -> Raw {
+  auto load = [&](int unit, int k0) -> Raw {
     Raw w;
     const bool in = k0 + 64 * q < p.K;  // K is a multiple of 64: the last step may be short of blocks
+    const int ra = 16 * unit + g, rb = ra + 8;
+    const bool lo = in && ra < p.N, hi = in && rb < p.N;
+    const size_t at = (size_t)(k0 / 2 + 32 * q), sat = (size_t)(k0 / 64 + q);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      w.a[h] = ldg16(c0 + k0 / 2 + 16 * h, in && lo);
-      w.b[h] = ldg16(c1 + k0 / 2 + 16 * h, in && hi);
+      w.a[h] = ldg16(p.nf4 + (lo ? (size_t)ra * (p.K / 2) + at + 16 * h : 0), lo);
+      w.b[h] = ldg16(p.nf4 + (hi ? (size_t)rb * (p.K / 2) + at + 16 * h : 0), hi);
     }
-    w.ma = in && lo ? __ldg(s0 + k0 / 64) : 0.0f;
-    w.mb = in && hi ? __ldg(s1 + k0 / 64) : 0.0f;
+    w.ma = lo ? __ldg(p.absmax + (size_t)ra * (p.K / 64) + sat) : 0.0f;
+    w.mb = hi ? __ldg(p.absmax + (size_t)rb * (p.K / 64) + sat) : 0.0f;
     return w;
   };
-  Raw next = load(warp * 256);
-  for (int k0 = warp * 256; k0 < p.K; k0 += kWarps * 256) {
-    const Raw w = next;
-    const bool in = k0 + 64 * q < p.K;
-    // x of both halves of the block at once, or (two tiles: the registers) one after the other
-    constexpr int kXHalves = NT == 1 ? 2 : 1;
-    uint4 xv[NT][4 * kXHalves];
-    auto load_x = [&](int h) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          xv[j][4 * (h % kXHalves) + c] = ldg16(xr[j] + k0 + 32 * h + 8 * c, in && tok[j]);
-    };
-    load_x(0);
-    if (kXHalves == 2) load_x(1);
-    next = load(k0 + kWarps * 256);
-    const Nf4Planes pa = nf4_block_planes(w.ma), pb = nf4_block_planes(w.mb);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t ca[4] = {w.a[h].x, w.a[h].y, w.a[h].z, w.a[h].w};
-      const uint32_t cb[4] = {w.b[h].x, w.b[h].y, w.b[h].z, w.b[h].w};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t da[4], db[4];
-        nf4_decode_word(ca[c], pa, ks, da);
-        nf4_decode_word(cb[c], pb, ks, db);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          mma_bf16(acc[j], da[0], db[0], da[1], db[1], xv[j][4 * (h % kXHalves) + c].x, xv[j][4 * (h % kXHalves) + c].y);
-          mma_bf16(acc[j], da[2], db[2], da[3], db[3], xv[j][4 * (h % kXHalves) + c].z, xv[j][4 * (h % kXHalves) + c].w);
-        }
-      }
-      if (h == 0 && kXHalves == 1) load_x(1);
-    }
-  }
-  float(*sums)[8 * NT][17] = reinterpret_cast<float(*)[8 * NT][17]>(red);
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    sums[warp][8 * i + 2 * q][g] = acc[i][0];
-    sums[warp][8 * i + 2 * q + 1][g] = acc[i][1];
-    sums[warp][8 * i + 2 * q][g + 8] = acc[i][2];
-    sums[warp][8 * i + 2 * q + 1][g + 8] = acc[i][3];
-  }
-  // One output a thread: its adapter's row of B is fetched before p is waited for.
-  const int t = tid >> 4, row = tid & 15;
-  const bool mine = t < p.T && n0 + row < p.N;
+  const int t = tid >> 4, row = tid & 15;  // this thread's output of a unit
   uint32_t a = 0xffffffffu;
   if (t < p.T) a = (uint32_t)__ldg(p.ids + t);
   const bool adapted = a < (uint32_t)p.n;
-  uint4 bw[E4B_MAX_RANK / 8];
-#pragma unroll
-  for (int j = 0; j < E4B_MAX_RANK / 8; ++j)
-    bw[j] = ldg16(p.B + ((size_t)(adapted ? a : 0) * p.N + (mine ? n0 + row : 0)) * p.r + (8 * j < p.r ? 8 * j : 0),
-                  adapted && mine && 8 * j < p.r);
   __shared__ float ps[8 * NT][E4B_MAX_RANK + 4];
   __shared__ int have;
-  if (tid == 0) {
-    have = wait_ready(p.err, p.p_blocks, p.timeout_ns, 640);
-  }
-  __syncthreads();
-  if (!have) return;
-  if (tid == 0) leave(p.err, (int)gridDim.x - p.p_blocks);
-  // p[t, j] = bf16(s[a] sum of the shares), 16 threads a token
-  if (adapted) {
-    const float sc = __ldg(p.scale + a);
-    for (int j = 4 * row; j < p.r; j += 64) {
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int s = 0; s < p.kq; ++s) {
-        const float4 w = __ldcg(reinterpret_cast<const float4*>(p.part + ((size_t)s * p.T + t) * p.r + j));
-        v.x += w.x;
-        v.y += w.y;
-        v.z += w.z;
-        v.w += w.w;
-      }
-      const uint32_t u0 = pack_bf16x2(sc * v.x, sc * v.y), u1 = pack_bf16x2(sc * v.z, sc * v.w);
-      *reinterpret_cast<float4*>(&ps[t][j]) =
-          make_float4(bf16lo_to_f32(u0), bf16hi_to_f32(u0), bf16lo_to_f32(u1), bf16hi_to_f32(u1));
-    }
-  }
-  __syncwarp();  // a token's 16 threads are of one warp
-  if (mine) {
-    float v = 0.0f;
+  bool first = true;
+  int buf = 0;
+  int unit = (int)blockIdx.x - p.p_blocks;
+  Raw next = load(unit, warp * 256);
+  for (; unit < units; unit += step, buf ^= 1) {
+    float acc[NT][4];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += sums[w][t][row];
-    if (adapted) {
+    for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+    for (int k0 = warp * 256; k0 < p.K; k0 += kWarps * 256) {
+      const Raw w = next;
+      const bool in = k0 + 64 * q < p.K;
+      // x of both halves of the block at once, or (two tiles: the registers) one after the other
+      constexpr int kXHalves = NT == 1 ? 2 : 1;
+      uint4 xv[NT][4 * kXHalves];
+      auto load_x = [&](int h) {
 #pragma unroll
-      for (int j = 0; j < E4B_MAX_RANK / 8; ++j) {
-        if (8 * j >= p.r) break;
-        const uint32_t b4[4] = {bw[j].x, bw[j].y, bw[j].z, bw[j].w};
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            xv[j][4 * (h % kXHalves) + c] = ldg16(xr[j] + k0 + 32 * h + 8 * c, in && tok[j]);
+      };
+      load_x(0);
+      if (kXHalves == 2) load_x(1);
+      // the next step's codes, or the next unit's first (rows past N read as zeros)
+      const bool more = k0 + kWarps * 256 < p.K;
+      next = load(more ? unit : unit + step, more ? k0 + kWarps * 256 : warp * 256);
+      const Nf4Planes pa = nf4_block_planes(w.ma), pb = nf4_block_planes(w.mb);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t ca[4] = {w.a[h].x, w.a[h].y, w.a[h].z, w.a[h].w};
+        const uint32_t cb[4] = {w.b[h].x, w.b[h].y, w.b[h].z, w.b[h].w};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          v = fmaf(bf16lo_to_f32(b4[c]), ps[t][8 * j + 2 * c], v);
-          v = fmaf(bf16hi_to_f32(b4[c]), ps[t][8 * j + 2 * c + 1], v);
+          uint32_t da[4], db[4];
+          nf4_decode_word(ca[c], pa, ks, da);
+          nf4_decode_word(cb[c], pb, ks, db);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const uint4 v = xv[j][4 * (h % kXHalves) + c];
+            mma_bf16(acc[j], da[0], db[0], da[1], db[1], v.x, v.y);
+            mma_bf16(acc[j], da[2], db[2], da[3], db[3], v.z, v.w);
+          }
         }
+        if (h == 0 && kXHalves == 1) load_x(1);
       }
     }
-    const __nv_bfloat16 h = __float2bfloat16_rn(v);
-    p.y[(size_t)t * p.N + n0 + row] = *reinterpret_cast<const uint16_t*>(&h);
+    float(*sums)[8 * NT][17] = reinterpret_cast<float(*)[8 * NT][17]>(red[buf]);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      sums[warp][8 * i + 2 * q][g] = acc[i][0];
+      sums[warp][8 * i + 2 * q + 1][g] = acc[i][1];
+      sums[warp][8 * i + 2 * q][g + 8] = acc[i][2];
+      sums[warp][8 * i + 2 * q + 1][g + 8] = acc[i][3];
+    }
+    // One output a thread: its adapter's row of B is fetched before p is waited for.
+    const int n = 16 * unit + row;
+    const bool mine = t < p.T && n < p.N;
+    uint4 bw[E4B_MAX_RANK / 8];
+#pragma unroll
+    for (int j = 0; j < E4B_MAX_RANK / 8; ++j)
+      bw[j] = ldg16(p.B + ((size_t)(adapted ? a : 0) * p.N + (mine ? n : 0)) * p.r + (8 * j < p.r ? 8 * j : 0),
+                    adapted && mine && 8 * j < p.r);
+    if (first && tid == 0) have = wait_ready(p.err, p.p_blocks, p.timeout_ns, 640);
+    __syncthreads();
+    if (first) {
+      if (!have) return;
+      first = false;
+      if (tid == 0) leave(p.err, step);
+      // p[t, j] = bf16(s[a] sum of the shares), 16 threads a token
+      if (adapted) {
+        const float sc = __ldg(p.scale + a);
+        for (int j = 4 * row; j < p.r; j += 64) {
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int s = 0; s < p.kq; ++s) {
+            const float4 w = __ldcg(reinterpret_cast<const float4*>(p.part + ((size_t)s * p.T + t) * p.r + j));
+            v.x += w.x;
+            v.y += w.y;
+            v.z += w.z;
+            v.w += w.w;
+          }
+          const uint32_t u0 = pack_bf16x2(sc * v.x, sc * v.y), u1 = pack_bf16x2(sc * v.z, sc * v.w);
+          *reinterpret_cast<float4*>(&ps[t][j]) =
+              make_float4(bf16lo_to_f32(u0), bf16hi_to_f32(u0), bf16lo_to_f32(u1), bf16hi_to_f32(u1));
+        }
+      }
+      __syncwarp();  // a token's 16 threads are of one warp
+    }
+    if (mine) {
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) v += sums[w][t][row];
+      if (adapted) {
+#pragma unroll
+        for (int j = 0; j < E4B_MAX_RANK / 8; ++j) {
+          if (8 * j >= p.r) break;
+          const uint32_t b4[4] = {bw[j].x, bw[j].y, bw[j].z, bw[j].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            v = fmaf(bf16lo_to_f32(b4[c]), ps[t][8 * j + 2 * c], v);
+            v = fmaf(bf16hi_to_f32(b4[c]), ps[t][8 * j + 2 * c + 1], v);
+          }
+        }
+      }
+      const __nv_bfloat16 h = __float2bfloat16_rn(v);
+      p.y[(size_t)t * p.N + n] = *reinterpret_cast<const uint16_t*>(&h);
+    }
   }
 }
 
@@ -741,7 +757,7 @@ __global__ void __launch_bounds__(ads::kThreadsSplit, 1)
 // Warp products for up to eight tokens, and for up to 16 of a matrix below 2^24 weights: with two token tiles their
 // reads of x and their decoding for every 16 rows cost more than the UMMA kernel's set-up (16 tokens, warp products
 // and UMMAs: 2048 -> 4096 10.3 and 14.4 us, 4096 -> 4096 16.4 and 16.4 us, 4096 -> 14336 46.6 and 30.7 us; 8 tokens
-// at 4096 -> 14336 29.5 and 28.7 us).
+// at 4096 -> 14336 26.7 and 28.7 us).
 bool adapter_gemv_serves(int T, int K, int N) {
   return T <= kTokenTile || (T <= 2 * kTokenTile && (int64_t)K * N < (1 << 24));
 }
@@ -749,7 +765,7 @@ bool adapter_gemv_serves(int T, int K, int N) {
 // Shares of K of the blocks of p of the warp products: as many as leave every block of the launch a place (two an
 // SM; with 24 of 320 blocks in a second wave, 16 tokens at 2048 -> 4096 took 8.7 us, not 7.5).
 int adapter_gemv_shares(int T, int r, int N) {
-  const int items = T * ((r + 15) / 16), places = 2 * 148 - (N + 15) / 16;
+  const int items = T * ((r + 15) / 16), places = kPlaces - (N + 15) / 16;
   return 4 * items <= places ? 4 : (2 * items <= places ? 2 : 1);
 }
 
@@ -802,7 +818,7 @@ cudaError_t launch_adapter_small(const AdapterProjHost& h, const int32_t* ids, c
     const GemvParams p{ids, x,   h.nf4, h.absmax, A,   B,   h.scale, static_cast<float*>(low), y, h.err, h.timeout_ns,
                        h.T, h.K, h.N,   h.n,      h.r, kq,  items * kq};
     LaunchScope scope("adapter_gemv", stream);
-    const int grid = p.p_blocks + (h.N + 15) / 16;
+    const int units = (h.N + 15) / 16, grid = p.p_blocks + (units < kPlaces ? units : kPlaces);
     if (h.T <= kTokenTile)
       adapter_gemv_kernel<1><<<grid, kThreads, 0, stream>>>(p);
     else
