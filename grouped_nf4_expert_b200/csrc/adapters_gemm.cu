@@ -12,12 +12,13 @@
 //
 // Rows are the tokens sorted by adapter; every adapter's rows start at a
 // multiple of 32: the column granule of a pair UMMA (forward), and two K steps of
-// a UMMA, so that the gradient products never multiply two adapters' rows.  The projection kernel gathers the token rows
-// (cp.async, 16 bytes a lane) and stores them in row order in passing, for the
-// base product to load as plain tiles.  TMA gathers by row index
-// (tile::gather4) were measured instead: about 77 cycles for every four rows
-// of 128 bytes, 5 times the time of the UMMAs they feed (T = 16384, K = 4096,
-// N = 14336: 4204 us against 1960 us with the copy).
+// a UMMA, so that the gradient products never multiply two adapters' rows.  The
+// projection kernel gathers the token rows (cp.async, 16 bytes a lane) and stores
+// them in row order in passing, for the base product to load as plain tiles.  TMA
+// gathers by row index (tile::gather4) were measured instead: about 77 cycles for
+// every four rows of 128 bytes, 5 times the time of the UMMAs they feed (T =
+// 16384, K = 4096, N = 14336, both with one issuing warp and relays: 4204 us
+// against 1960 us with the copy).
 //
 // The adapters of a tile share its accumulator: each K = r step is issued at the
 // adapter's own accumulator columns (forward) or names the TMEM lanes it must not
@@ -205,6 +206,10 @@ __device__ __forceinline__ void let_land(uint64_t* bars, int n, uint32_t issued,
 // st.async each.  (A relay warp that waited for a CTA's operands and passed one
 // signal on took about 690 cycles a chunk: beside four decode warps on its
 // scheduler, every instruction of it waits for a turn.)
+//
+// The tensor pipe bounds it, with the decode beside it: 840 cycles a chunk of 256
+// rows, 680 of 128 and less.  8192 tokens, 2048 -> 2048: 71 us, 970 TFLOP/s, tensor
+// pipe 53% active (3.5 turns of units); 16384 tokens, 4096 -> 14336: 1.15 PFLOP/s.
 //
 // Roles per CTA: warp 0 codes, warp 1 TMEM owner and (even CTA) issuer of the
 // first halves, warp 2 (even CTA) issuer of the second halves, warp 3 token rows
@@ -613,7 +618,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
 // rows and 64 NB columns of A.
 // A unit is 256 rows x 128 NB columns.  NB = 1 where NB = 2 would leave half the
 // pairs without one: a unit's chunks are a chain whose step is a decode (777
-// rows of 512 columns over 2048: 22 us with NB = 2).
+// rows of 512 columns over 2048: 22 us with NB = 2, 20 us with 1).  8192 rows of
+// 2048 columns over 2048: 77 us, 890 TFLOP/s, tensor pipe 47% active.
 namespace adg {
 constexpr int BM = 128, BK = 64;
 constexpr int A_BYTES = BM * BK * 2;
@@ -1037,7 +1043,8 @@ struct AdapterRowsParams {
 };
 
 // F = A [n, r, R] (K-major), or B [n, R, r] (W_MN).  With few tasks R is split over the blocks of a cluster: one
-// block's chain of chunks would be the launch's time (13 tasks of R = 2048: 21 us).
+// block's chain of chunks would be the launch's time (13 tasks of R = 2048: 21 us, split 8 us).  Reading the rows and
+// writing them in their order bounds it: 8192 rows of 2048 columns, 19 us, 3.5 TB/s.
 template <bool W_MN>
 __global__ void __launch_bounds__(adp::kThreads, 2)
     adapter_proj_kernel(const __grid_constant__ CUtensorMap map_dst, const __grid_constant__ CUtensorMap map_w,
@@ -1290,6 +1297,9 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
 // =============================================================================
 // Adapter gradients: dA[a] = q^T x (stored transposed), dB[a] = dY^T p
 // =============================================================================
+// Reading x and dY bounds them.  8192 tokens of 4 adapters, 2048 + 2048 features:
+// 41 us, 1.8 TB/s of their 69 MB: 512 blocks of 8 chunks in two waves, and a join of
+// 6 us a cluster.
 namespace adw {
 constexpr int BM = 128, BK = 64, STAGES = 4;
 constexpr int A_BYTES = BK * BM * 2;            // 64 rows x 128 features, MN-major SW128
@@ -1609,15 +1619,15 @@ cudaError_t map_u8_2d(CUtensorMap* m, const void* base, uint64_t bytes, uint64_t
 }
 }  // namespace
 
-// Token rows of a forward unit: the ones that take the pairs the fewest turns, a turn's time being the larger of
-// decoding a chunk (about 400 cycles whatever the rows) and its products.
+// Token rows of a forward unit: the ones that take the pairs the least time.  Measured cycles a 64-wide chunk: 680 up
+// to 128 rows (decoding it), 790 with 160, 840 with 256.
 static int fwd_unit_rows(const AdapterProjHost& h, int n_mt, int pairs) {
   const int64_t rows = h.T + 16 * (int64_t)(h.T < h.n + 1 ? h.T : h.n + 1);  // with an average of padding
   int best = 256;
   int64_t best_cost = INT64_MAX;
   for (int nt = 256; nt >= 96; nt -= 32) {
     const int64_t turns = ((rows + nt - 1) / nt * n_mt + pairs - 1) / pairs;
-    const int64_t cost = turns * (nt > 128 ? 180 + 2 * nt : 440);
+    const int64_t cost = turns * (nt > 128 ? 707 + 13 * nt / 25 : 680);
     if (cost < best_cost) {
       best = nt;
       best_cost = cost;

@@ -345,7 +345,10 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvPar
 // reading them from there instead took 4.7 us at 256 tokens, one round trip
 // after another), added, and the adapters' part is added in the fragment
 // layout of the warp instruction, tile by tile, so that no adapter's values
-// meet another's tokens.
+// meet another's tokens.  256 tokens, 4096 -> 4096, 32 adapters of rank 32: 29 us,
+// bound by the L2 reads of x (64 KB/us a block; all of x for every 128 rows of W,
+// 64 MB) and the exchange of shares; 57 tokens, 2048 -> 512: 14.3 us, the chain p,
+// hand-over, join.
 namespace ads {
 constexpr int BM = 128, BK = 64;
 constexpr int kXStages = 4, kTeams = 3, kABufs = 2 * kTeams, kACols = BK / 2;
