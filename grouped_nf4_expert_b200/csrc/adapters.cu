@@ -153,8 +153,9 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
 cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int32_t* order, int32_t* offsets, int32_t* steps,
                                  cudaStream_t stream) {
   const int smem = kGroupWarps * (n + 1) * 4;
-  const cudaError_t err =
-      cudaFuncSetAttribute(adapter_group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the same limit in every call: calls of several host threads may meet here
+  const cudaError_t err = cudaFuncSetAttribute(adapter_group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kGroupWarps * (E4B_MAX_ADAPTERS + 1) * 4);
   if (err != cudaSuccess) return err;
   LaunchScope scope("adapter_group", stream);
   adapter_group_kernel<<<1, kGroupThreads, smem, stream>>>(ids, T, n, (int)adapter_rows_cap(T, n), order, offsets,

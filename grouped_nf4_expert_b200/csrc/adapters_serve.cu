@@ -361,6 +361,7 @@ inline int ring_bytes(int nt, int S) {  // x tiles, then the S shares of 128 / S
   const int x = kXStages * nt * BK * 2, part = nt * (BM + 4 * S) * 4;
   return ((x > part ? x : part) + 1023) / 1024 * 1024;
 }
+constexpr int kMaxSmem = 232448;
 static_assert(kAOff + kABufs * kACols <= kTmemCols, "TMEM budget");
 }  // namespace ads
 
@@ -839,7 +840,8 @@ cudaError_t launch_adapter_small(const AdapterProjHost& h, const int32_t* ids, c
                       h.T,   NT,       h.K, h.N, h.n, h.r,    ring,                        p_blocks};
   LaunchScope scope("adapter_split", stream);
   auto run = [&](auto kernel) -> cudaError_t {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // the same limit in every call: calls of several host threads may meet here
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ads::kMaxSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p_blocks + tiles * S));

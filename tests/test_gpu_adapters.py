@@ -300,6 +300,34 @@ def test_calls_on_several_streams_at_once():
         assert torch.equal(pj.y, w) and pj.check_device_error() == e4b.E4B_OK
 
 
+def test_calls_of_several_host_threads():
+    # sizes that need different amounts of shared memory, launched from threads of their own
+    import threading
+    cases = [Case(300, 128, 72, n, 8, "zipf", seed=40 + i) for i, n in enumerate((3, 900, 40, 600))]
+    cases += [Case(T, 256, 264, 5, 8, "zipf", seed=50 + i) for i, T in enumerate((20, 250, 130, 256))]
+    want = [serve(c).y.clone() for c in cases]
+    bad = []
+
+    def work(c, w):
+        try:
+            pj, base, ad, st = e4b.Projection(c.dims, c.T, train=False), c.base(), c.adapters(), torch.cuda.Stream()
+            torch.cuda.synchronize()
+            for _ in range(200):
+                pj.e4b_multi_lora_serve_fwd(c.ids, c.x, base, ad, stream=st)
+            st.synchronize()
+            if not torch.equal(pj.y, w):
+                bad.append((c.T, c.n))
+        except Exception as e:  # noqa: BLE001 (told below, with its case)
+            bad.append((c.T, c.n, repr(e)))
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(cases, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
+
+
 def test_offsets_past_32_bits():
     # y holds 2^31 elements and more: the last tokens' rows against the formula in 64 bits
     T, N = 16400, 131080
