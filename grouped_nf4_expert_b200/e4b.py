@@ -613,12 +613,14 @@ class Projection(_OnDevice):
     Serving: :meth:`e4b_multi_lora_serve_fwd` into ``y``.  Training (``train=True``, the default):
     :meth:`e4b_adapter_group`, then :meth:`e4b_multi_lora_fwd` (``y``), :meth:`e4b_multi_lora_dgrad`
     (``dx``) and :meth:`e4b_multi_lora_wgrad` (``dA``, ``dB``).  Calls on one object share its buffers
-    and workspace, so they must not overlap on the GPU.
+    and workspace, so they must not overlap on the GPU; the buffers are filled on the current stream, which
+    another stream has to wait for before its first call.
     """
 
     def __init__(self, dims: ProjDims, T: int, device="cuda", train: bool = True):
         import torch
         self.dims, self.T, self.train = dims, T, train
+        self._done = 0
         sz = e4b_proj_get_sizes(dims, T)
         self.sizes = sz
         dev = self._on(device)
@@ -659,6 +661,15 @@ class Projection(_OnDevice):
         if not self.train:
             raise ValueError("made with train=False: no training buffers")
 
+    def _after(self, needs):
+        """Refuses a training call ahead of those whose results it reads (1: the grouping, 2: the forward, 4: the
+        input gradient)."""
+        missing = needs & ~self._done
+        if missing and self.T:
+            raise ValueError("call %s first" % ", ".join(
+                name for bit, name in ((1, "e4b_adapter_group"), (2, "e4b_multi_lora_fwd"),
+                                       (4, "e4b_multi_lora_dgrad")) if missing & bit))
+
     def e4b_multi_lora_serve_fwd(self, ids, x, base: Nf4Matrix, adapters: AdapterFactors, stream=None):
         """Serving forward into ``self.y`` (ids int32 [T], any id outside [0, n) for no adapter)."""
         pi = self._arg(ids, self._i32, self.T, "ids")
@@ -671,24 +682,34 @@ class Projection(_OnDevice):
         self._training()
         self._call("e4b_adapter_group", stream, self._dims_p, self.T, self._arg(ids, self._i32, self.T, "ids"),
                    self._groups_p)
+        self._done = 1
 
     def e4b_multi_lora_fwd(self, x, base: Nf4Matrix, adapters: AdapterFactors, stream=None):
+        """``y`` of the grouped tokens; keeps ``p`` for the adapter gradients."""
         self._training()
         px = self._arg(x, self._bf16, self.T * self.dims.K, "x")
-        self._call("e4b_multi_lora_fwd", stream, self._dims_p, self.T, self._groups_p, px,
-                   self._base(base), self._adapters(adapters), self._low_p[0], self._y_p, self._ws_p, self._ws_n)
+        pb, pa = self._base(base), self._adapters(adapters)
+        self._after(1)
+        self._call("e4b_multi_lora_fwd", stream, self._dims_p, self.T, self._groups_p, px, pb, pa,
+                   self._low_p[0], self._y_p, self._ws_p, self._ws_n)
+        self._done |= 2
 
     def e4b_multi_lora_dgrad(self, dY, base: Nf4Matrix, adapters: AdapterFactors, stream=None):
+        """``dx``; keeps ``q`` for the adapter gradients."""
         self._training()
         pd = self._arg(dY, self._bf16, self.T * self.dims.N, "dY")
-        self._call("e4b_multi_lora_dgrad", stream, self._dims_p, self.T, self._groups_p, pd,
-                   self._base(base), self._adapters(adapters), self._low_p[1], self._dx_p, self._ws_p, self._ws_n)
+        pb, pa = self._base(base), self._adapters(adapters)
+        self._after(1)
+        self._call("e4b_multi_lora_dgrad", stream, self._dims_p, self.T, self._groups_p, pd, pb, pa,
+                   self._low_p[1], self._dx_p, self._ws_p, self._ws_n)
+        self._done |= 4
 
     def e4b_multi_lora_wgrad(self, x, dY, stream=None):
         """Adapter gradients from the ``p`` and ``q`` of the forward and the input gradient."""
         self._training()
         px = self._arg(x, self._bf16, self.T * self.dims.K, "x")
         pd = self._arg(dY, self._bf16, self.T * self.dims.N, "dY")
+        self._after(7)
         self._call("e4b_multi_lora_wgrad", stream, self._dims_p, self.T, self._groups_p, px, pd,
                    *self._low_p, *self._grad_p, self._ws_p, self._ws_n)
 
@@ -698,7 +719,8 @@ class RouterBalance(_OnDevice):
 
     :meth:`e4b_balance_fwd` writes ``loss`` (float32 [3]: loss, balance, z), ``counts`` (int32 [S, E]),
     ``prob_sum`` (float32 [S, E]), ``tokens`` (int32 [S]) and ``lse``; :meth:`e4b_balance_bwd` the gradient
-    of the logits.  Calls on one object share its buffers, so they must not overlap on the GPU.
+    of the logits.  Calls on one object share its buffers, so they must not overlap on the GPU; the
+    buffers are filled on the current stream, which another stream has to wait for before its first call.
     """
 
     def __init__(self, E: int, top_k: int, T: int, S: int = 1, device="cuda"):

@@ -155,7 +155,8 @@ typedef struct {
 /* Workspace bytes of e4b_balance_fwd.  Host only; no CUDA call.  The first 256
  * bytes of the workspace hold the error word and two counters, which must be 0
  * before the first call (as e4b_workspace_init leaves them) and are 0 again
- * after each; calls that share a workspace must not overlap on the GPU. */
+ * after each (after E4B_ERR_DEVICE_TIMEOUT: once it is initialised again); calls
+ * that share a workspace must not overlap on the GPU. */
 e4b_status e4b_balance_get_sizes(const e4b_balance_dims *dims, int32_t T, size_t *workspace_bytes);
 
 /* logits: float32 [T, E]; topk_ids: int32 [T, top_k], as e4b_route_permute

@@ -487,3 +487,24 @@ def test_as_used_with_the_expert_block():
     want = oracle.moe_forward(f(prob.x), prob.logits, ex, cfg.top_k, cfg.alpha)["y"]
     got = f64(blk.y)
     assert np.abs(got - want).max() <= 1e-2 * np.abs(want).max()
+
+
+def test_training_calls_out_of_order_are_refused():
+    c = Case(40, 64, 72, 3, 8)
+    pj, n0 = e4b.Projection(c.dims, c.T), e4b.e4b_launch_count()
+    with pytest.raises(ValueError, match="call e4b_adapter_group first"):
+        pj.e4b_multi_lora_fwd(c.x, c.base(), c.adapters())
+    with pytest.raises(ValueError, match="call e4b_adapter_group first"):
+        pj.e4b_multi_lora_dgrad(c.dY, c.base(), c.adapters())
+    assert e4b.e4b_launch_count() == n0
+    pj.e4b_adapter_group(c.ids)
+    pj.e4b_multi_lora_fwd(c.x, c.base(), c.adapters())
+    with pytest.raises(ValueError, match="call e4b_multi_lora_dgrad first"):
+        pj.e4b_multi_lora_wgrad(c.x, c.dY)
+    pj.e4b_multi_lora_dgrad(c.dY, c.base(), c.adapters())
+    pj.e4b_multi_lora_wgrad(c.x, c.dY)
+    pj.e4b_adapter_group(c.ids)  # another step: its forward and input gradient come first again
+    with pytest.raises(ValueError, match="call e4b_multi_lora_fwd, e4b_multi_lora_dgrad first"):
+        pj.e4b_multi_lora_wgrad(c.x, c.dY)
+    with pytest.raises(ValueError, match="train=False"):
+        e4b.Projection(c.dims, c.T, train=False).e4b_adapter_group(c.ids)
