@@ -611,23 +611,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
 // read along it, so the decoded tile goes to shared memory with the output
 // columns contiguous, as the N operand; token rows are the M operand.  Roles per
 // CTA: warp 0 codes, warp 1 TMEM owner and (even CTA) UMMA issuer, warp 3
-// activation tiles and low-rank operands, warps 4-19 four decode groups taking
-// the k-chunks round robin, warps 20-23 epilogue; operands of both CTAs are
+// activation tiles and low-rank operands, warps 4-19 decode groups taking the
+// k-chunks round robin, warps 20-23 epilogue; operands of both CTAs are
 // counted on the even CTA's barriers, as in the forward.  The low-rank steps
 // come after the k-chunks: a unit's two ring slots per adapter hold its 128 q
 // rows and 64 NB columns of A.
 // A unit is 256 rows x 128 NB columns.  NB = 1 where NB = 2 would leave half the
 // pairs without one: a unit's chunks are a chain whose step is a decode (777
-// rows of 512 columns over 2048: 22 us with NB = 2, 20 us with 1).  8192 rows of
+// rows of 512 columns over 2048: 22 us with NB = 2, 14 us with 1).  8192 rows of
 // 2048 columns over 2048: 77 us, 890 TFLOP/s, tensor pipe 47% active.
 namespace adg {
 constexpr int BM = 128, BK = 64;
 constexpr int A_BYTES = BM * BK * 2;
 constexpr int B_BYTES = 128 * BK * 2;  // 64 stored rows x 64 NB columns, NB = 2 at most
-constexpr int kGroups = 4, kGroupWarps = 4;  // 2 NB of a group's warps decode
-constexpr int SA = 6;         // activation ring
-constexpr int SB = kGroups;   // decoded-tile ring: group g's chunks use slot g
-constexpr int RAW_STAGES = 2 * kGroups;
+constexpr int kDecodeWarps = 16;  // in groups of 2 NB, a group's threads a stored row and 64 columns each
+constexpr int groups(int nb) { return kDecodeWarps / (2 * nb); }
+constexpr int SA = 6;             // activation ring
+// Decoded-tile ring: group g's chunks use slot g; codes: two slots a group.  NB = 1 has twice the slots of half the
+// bytes.
+constexpr int SB = groups(2), RAW_STAGES = 2 * groups(2);
 constexpr int RAW_BYTES = 128 * BK / 2;
 constexpr int B_OFF = SA * A_BYTES;
 constexpr int RAW_OFF = B_OFF + SB * B_BYTES;
@@ -638,12 +640,11 @@ constexpr int kEpiPitch = 144;
 constexpr int kEpiWarpBytes = 32 * kEpiPitch;
 constexpr int BAR_OFF = EPI_OFF + 4 * kEpiWarpBytes;
 constexpr int SMEM_BYTES = BAR_OFF + 1024 + 1024;
-constexpr int kEpiWarp0 = 4 + kGroups * kGroupWarps;
+constexpr int kEpiWarp0 = 4 + kDecodeWarps;
 constexpr int kThreads = 32 * (kEpiWarp0 + 4);
 constexpr int kTmemCols = 512;
 static_assert(BAR_OFF % 16 == 0 && SMEM_BYTES <= 232448, "shared memory budget");
 static_assert(BM * E4B_MAX_RANK * 2 <= A_BYTES, "low-rank operands fit a slot");
-static_assert(RAW_STAGES % kGroups == 0, "code slots are owned by one decode group each");
 }  // namespace adg
 
 struct AdapterDgradParams {
@@ -662,6 +663,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
                         const __grid_constant__ CUtensorMap map_la, const __grid_constant__ CUtensorMap map_lb,
                         const AdapterDgradParams p) {
   using namespace adg;
+  constexpr int G = groups(NB), RS = 2 * G, kTileSlot = B_BYTES / 2 * NB, kRawSlot = RAW_BYTES / 2 * NB;
   constexpr int kCols = 128 * NB;  // output columns of a unit, 64 NB of them decoded by each CTA
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = align1024(smem_dyn);
@@ -669,13 +671,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
   uint8_t* bring = smem + B_OFF;
   uint8_t* rawbuf = smem + RAW_OFF;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_OFF);
-  uint64_t* raw_full = bars;                    // [RAW_STAGES] codes landed
-  uint64_t* raw_empty = raw_full + RAW_STAGES;  // [RAW_STAGES] codes read into registers (group's 4 warps)
-  uint64_t* xfull = raw_empty + RAW_STAGES;     // [SA] (even CTA) ring use landed in both CTAs
+  uint64_t* raw_full = bars;                    // [RS] codes landed
+  uint64_t* raw_empty = raw_full + RS;          // [RS] codes read into registers (group's warps)
+  uint64_t* xfull = raw_empty + RS;             // [SA] (even CTA) ring use landed in both CTAs
   uint64_t* aempty = xfull + SA;                // [SA] activation slot consumed by the UMMAs
-  uint64_t* bdone = aempty + SA;                // [SB] (even CTA) both CTAs' decoded tile written
-  uint64_t* bempty = bdone + SB;                // [SB] decoded-tile slot consumed by the UMMAs
-  uint64_t* accfull = bempty + SB;              // [2] accumulator complete
+  uint64_t* bdone = aempty + SA;                // [G] (even CTA) both CTAs' decoded tile written
+  uint64_t* bempty = bdone + G;                 // [G] decoded-tile slot consumed by the UMMAs
+  uint64_t* accfull = bempty + G;              // [2] accumulator complete
   uint64_t* accempty = accfull + 2;             // [2] (even CTA) accumulator drained in both CTAs
   uint64_t* drain = accfull + 4;                // (even CTA) all issued UMMAs finished
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accfull + 5);
@@ -685,7 +687,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   if (threadIdx.x == 0) {
-    for (int r = 0; r < RAW_STAGES; ++r) {
+    for (int r = 0; r < RS; ++r) {
       mbar_init(&raw_full[r], 1);
       mbar_init(&raw_empty[r], 2 * NB);
     }
@@ -693,7 +695,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
       mbar_init(&xfull[s], 1);
       mbar_init(&aempty[s], 1);
     }
-    for (int s = 0; s < SB; ++s) {
+    for (int s = 0; s < G; ++s) {
       mbar_init(&bdone[s], 2 * NB);
       mbar_init(&bempty[s], 1);
     }
@@ -732,16 +734,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
       for (int u = pair; u < n_units && ok; u += n_pairs) {
         const int c0 = (u % p.n_nt) * kCols + (int)rank * 64 * NB;  // this CTA's output columns
         for (int kc = 0; kc < kchunks; ++kc, ++j) {
-          const uint32_t r = j % RAW_STAGES, ph = (j / RAW_STAGES) & 1;
+          const uint32_t r = j % RS, ph = (j / RS) & 1;
           if (!(ok = mbar_wait_lazy(&raw_empty[r], ph ^ 1, ctl, p.err, p.timeout_ns, 311, 64))) break;
-          uint8_t* slot = rawbuf + r * RAW_BYTES;
+          uint8_t* slot = rawbuf + r * kRawSlot;
           mbar_arrive_expect_tx(&raw_full[r], (uint32_t)(2048 * NB));
           tma_load_2d(slot, &map_raw, &raw_full[r], c0 / 2, kc * BK);
           issued |= 1u << r;
           last_par = (last_par & ~(1u << r)) | (ph << r);
         }
       }
-      if (!ok) let_land(raw_full, RAW_STAGES, issued, last_par, p.timeout_ns);
+      if (!ok) let_land(raw_full, RS, issued, last_par, p.timeout_ns);
     }
     __syncwarp();
   } else if (warp == 3) {
@@ -827,14 +829,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
           if (!(ok = mbar_wait_cluster(&bdone[sb], phb, ctl, p.err, p.timeout_ns, 324))) break;
           tc_fence_after();
           const uint64_t adesc = adesc0 + (uint64_t)(sa * (A_BYTES >> 4));
-          const uint64_t bdesc = bdesc0 + (uint64_t)(sb * (B_BYTES >> 4));
+          const uint64_t bdesc = bdesc0 + (uint64_t)(sb * (kTileSlot >> 4));
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
             umma_bf16_2sm(d, adesc + 2 * kk, bdesc + bstep * kk, idesc, (kc > 0 || kk > 0) ? 1u : 0u);
           umma_commit_2sm(&aempty[sa], 0x3);
           umma_commit_2sm(&bempty[sb], 0x3);
           next_a();
-          if (++sb == SB) {
+          if (++sb == G) {
             sb = 0;
             phb ^= 1;
           }
@@ -869,18 +871,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
     __syncwarp();
   } else if (warp >= 4 && warp < kEpiWarp0) {
     // ------------------------------------------------ NF4 decode, groups take the k-chunks round robin
-    const uint32_t grp = (warp - 4) >> 2;
+    const uint32_t grp = (warp - 4) / (2 * NB);
     const uint32_t bdone_even = mapa_shared(smem_u32(bdone + grp), 0), sig_even = mapa_shared(smem_u32(sig), 0);
-    const int t = (threadIdx.x - 128) & 127;  // stored row t % 64, block of 64 columns t / 64
+    const int t = (threadIdx.x - 128) & (64 * NB - 1);  // stored row t % 64, block of 64 columns t / 64
     const Nf4Shift ks = nf4_shift_consts();
     const int raw_off = (t & 63) * 32 * NB + (t >> 6) * 32;
     const int drow = t & 63;
     const uint32_t drow_off = (t >> 6) * 8192 + (drow >> 3) * 1024 + (drow & 7) * 128;
-    const uint32_t b_u = smem_u32(bring) + grp * B_BYTES;
+    const uint32_t b_u = smem_u32(bring) + grp * kTileSlot;
     // A cursor over this group's chunks, one chunk ahead of the decode (for the block scales).
     const uint32_t my_units = pair < n_units ? (uint32_t)((n_units - pair + n_pairs - 1) / n_pairs) : 0;
-    // (NB = 1: a group's second pair of warps has nothing to do)
-    const uint32_t n_chunks = (t >> 6) < NB ? my_units * (uint32_t)kchunks : 0;
+    const uint32_t n_chunks = my_units * (uint32_t)kchunks;
     int c_kc = (int)grp, c_u = pair;
     while (c_kc >= kchunks) {
       c_kc -= kchunks;
@@ -888,7 +889,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
     }
     int c_nt = c_u % p.n_nt;
     auto advance = [&]() {
-      c_kc += kGroups;
+      c_kc += G;
       while (c_kc >= kchunks) {
         c_kc -= kchunks;
         c_u += n_pairs;
@@ -904,13 +905,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
     };
     float amax_next = block_scale();
     bool ok = true;
-    for (uint32_t jj = grp; jj < n_chunks && ok; jj += kGroups) {
+    for (uint32_t jj = grp; jj < n_chunks && ok; jj += G) {
       const float amax = amax_next;
       advance();
-      const uint32_t r = jj % RAW_STAGES, rph = (jj / RAW_STAGES) & 1;
+      const uint32_t r = jj % RS, rph = (jj / RS) & 1;
       ok = __all_sync(kFull, mbar_wait(&raw_full[r], rph, ctl, p.err, p.timeout_ns, 330));
       if (!ok) break;
-      const uint8_t* slot = rawbuf + r * RAW_BYTES;
+      const uint8_t* slot = rawbuf + r * kRawSlot;
       const uint4 q0 = *reinterpret_cast<const uint4*>(slot + raw_off);
       const uint4 q1 = *reinterpret_cast<const uint4*>(slot + raw_off + 16);
       const uint32_t codes[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
@@ -922,7 +923,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
       uint32_t v[32];
 #pragma unroll
       for (int c = 0; c < 8; ++c) nf4_decode_word(codes[c], pl, ks, &v[4 * c]);
-      ok = __all_sync(kFull, mbar_wait(&bempty[grp], ((jj / kGroups) & 1) ^ 1, ctl, p.err, p.timeout_ns, 331));
+      ok = __all_sync(kFull, mbar_wait(&bempty[grp], ((jj / G) & 1) ^ 1, ctl, p.err, p.timeout_ns, 331));
       if (!ok) break;
       const uint32_t dbase = b_u + drow_off;
 #pragma unroll
@@ -933,7 +934,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
       if (lane == 0) {
         if (rank)
           st_async_signal(sig_even, bdone_even, 1u);
-        else if ((warp & 3) == 0)
+        else if (t < 32)
           mbar_arrive_expect_tx(&bdone[grp], 8 * NB);  // and the odd CTA's 2 NB signals of 4 bytes
         else
           mbar_arrive(&bdone[grp]);
