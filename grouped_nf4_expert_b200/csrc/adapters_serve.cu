@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvPar
 // ----------------------------------------------------------------------------
 // y for up to 256 tokens: 128 rows of W x all tokens x a share of K per block
 // ----------------------------------------------------------------------------
-// After the blocks of p: warp 0 loads x tiles (TMA), warp 1 owns tensor memory and issues the UMMAs,
+// After the blocks of p (or under a launch of p of its own): warp 0 loads x tiles (TMA), warp 1 owns tensor memory and issues the UMMAs,
 // warp 2 sorts the tokens into tiles of eight of one adapter, warps 4-15 are
 // three decode teams that take the k-chunks round robin: a thread owns a row of
 // W, reads 32 bytes of codes and a scale a chunk straight into registers two of
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvPar
 // reading them from there instead took 4.7 us at 256 tokens, one round trip
 // after another), added, and the adapters' part is added in the fragment
 // layout of the warp instruction, tile by tile, so that no adapter's values
-// meet another's tokens.  256 tokens, 4096 -> 4096, 32 adapters of rank 32: 29 us,
+// meet another's tokens.  256 tokens, 4096 -> 4096, 32 adapters of rank 32: 25 us,
 // bound by the L2 reads of x (64 KB/us a block; all of x for every 128 rows of W,
 // 64 MB) and the exchange of shares; 57 tokens, 2048 -> 512: 14.3 us, the chain p,
 // hand-over, join.
@@ -379,8 +379,16 @@ struct SplitParams {
   long long timeout_ns;
   int T, NT, K, N, n, r;  // NT: T rounded up to 16
   int ring;               // bytes of the x ring / partial sums
-  int p_blocks;           // blocks of p, ahead of the others (whole clusters)
+  int p_blocks;           // blocks of p, ahead of the others (whole clusters); 0: p has a launch of its own
 };
+
+// Shared memory of a block of p of kWarps warps.
+constexpr int kLowRankBytes = kWarps * 16 * (kTokenTile + 1) * 4 + (3 * kAdapterSmallTokens + kTokenTile + kWarps) * 2;
+
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
@@ -406,10 +414,10 @@ __device__ __forceinline__ uint4 ldcg16(const void* p, bool ok) {
 }
 
 // p for the split kernel: the tokens of an adapter in tiles of up to eight, in token order; an item is (tile, 16
-// ranks), and the blocks of p take the items in turn.
-__device__ void split_low_rank(uint8_t* smem, const SplitParams& p) {
-  constexpr int kW = ads::kThreadsSplit / 32;
-  static_assert(kAdapterSmallTokens <= ads::kThreadsSplit, "a token a thread");
+// ranks), and the `blocks` blocks of kW warps take the items in turn.
+template <int kW>
+__device__ __forceinline__ void split_low_rank(uint8_t* smem, const SplitParams& p, int blocks) {
+  static_assert(kAdapterSmallTokens <= 32 * kW, "a token a thread");
   float(*red)[16][kTokenTile + 1] = reinterpret_cast<float(*)[16][kTokenTile + 1]>(smem);
   int16_t* ids = reinterpret_cast<int16_t*>(red + kW);    // [kAdapterSmallTokens] -1: no adapter
   int16_t* first = ids + kAdapterSmallTokens;             // first tokens of the tiles
@@ -449,7 +457,7 @@ __device__ void split_low_rank(uint8_t* smem, const SplitParams& p) {
     ranks[at] = (int16_t)rank;
   }
   const int slices = (p.r + 15) / 16;
-  for (int item = (int)blockIdx.x; item < n_tiles * slices; item += p.p_blocks) {
+  for (int item = (int)blockIdx.x; item < n_tiles * slices; item += blocks) {
     const int tile = item / slices, j0 = (item - tile * slices) * 16;
     __syncthreads();  // the list; the last item's tokens and sums are read
     if (tid < kTokenTile) tok[tid] = -1;
@@ -471,17 +479,25 @@ __device__ void split_low_rank(uint8_t* smem, const SplitParams& p) {
       }
     }
   }
-  signal_ready(p.err);
+}
+
+// The same as a launch of its own, which the products start under: with 64 registers and 256 threads a block fits
+// beside one of theirs.
+__global__ void __launch_bounds__(kThreads, 4) adapter_low_rank_kernel(const SplitParams p) {
+  __shared__ __align__(16) uint8_t smem[kLowRankBytes];
+  grid_launch_dependents();
+  split_low_rank<kWarps>(smem, p, (int)gridDim.x);
 }
 
 template <int S, bool WIDE>  // blocks of a cluster, the shares of K; r > 32
-__global__ void __launch_bounds__(ads::kThreadsSplit, 1)
+__global__ void __launch_bounds__(ads::kThreadsSplit + 128, 1)  // 96 registers: the launch of p beside
     adapter_split_kernel(const __grid_constant__ CUtensorMap map_x, const SplitParams p) {
   using namespace ads;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = align1024(smem_dyn);
   if ((int)blockIdx.x < p.p_blocks) {
-    split_low_rank(smem, p);
+    split_low_rank<kThreadsSplit / 32>(smem, p, p.p_blocks);
+    signal_ready(p.err);
     return;
   }
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.ring);
@@ -694,12 +710,15 @@ __global__ void __launch_bounds__(ads::kThreadsSplit, 1)
       at[0] = v;
     }
   }
-  if (tid == 0) {
-    ctl->pad = wait_ready(p.err, p.p_blocks, p.timeout_ns, 641);
+  if (p.p_blocks == 0) {
+    grid_wait();  // p, from the launch ahead
+    __syncthreads();
+  } else {
+    if (tid == 0) ctl->pad = wait_ready(p.err, p.p_blocks, p.timeout_ns, 641);
+    __syncthreads();
+    if (!ctl->pad) return;
+    if (tid == 0) leave(p.err, (int)gridDim.x - p.p_blocks);
   }
-  __syncthreads();
-  if (!ctl->pad) return;
-  if (tid == 0) leave(p.err, (int)gridDim.x - p.p_blocks);
   // The adapters' part: item = (tile of 8 tokens of one adapter, group of 16 rows), fragments of B and p
   // fetched two items ahead.
   {
@@ -773,24 +792,26 @@ int adapter_gemv_shares(int T, int r, int N) {
   return 4 * items <= places ? 4 : (2 * items <= places ? 2 : 1);
 }
 
-// The shares S of K and the blocks of p, by an estimate in microseconds of what bounds each part: a block reads A
-// at 90 KB/us and needs 1.7 us an item; a chunk of the product costs 0.3 us of decoding or its x tile at 80 KB/us;
-// shares travel at 27 KB/us a block; one SM holds one block, and clusters of 2, 4, 8 find 74, 33, 15 places.
-// Either p has places of its own beside the products, or every SM works on p first.  Measured both ways: 128
-// tokens at 2048 -> 2048, S = 8 (16 clusters in 15 places) 26.7 us, S = 4 14.4 us; 57 tokens of 64 adapters of
-// rank 64 at 2048 -> 512, p beside 16.4 us, before 20.5 us; 32 tokens of 32 such at 4096 -> 4096 28.7 and 24.7 us.
+// The shares S of K and the blocks of p, by an estimate in microseconds of what bounds each part: a block of p reads
+// A at 90 KB/us and needs 1.7 us an item (2.5 us with 8 warps); a chunk of the product costs 0.3 us of decoding or its
+// x tile at 80 KB/us; shares travel at 27 KB/us a block; one SM holds one block, and clusters of 2, 4, 8 find 74, 33,
+// 15 places.  Either p has places of its own beside the products, or a launch of its own ahead of them (2 us).
+// Measured both ways: 128 tokens at 2048 -> 2048, S = 8 (16 clusters in 15 places) 26.7 us, S = 4 14.4 us; p of 57
+// tokens of 64 adapters of rank 64 at 2048 -> 512 in the launch 14.4 us, in its own 20.6 us; 256 tokens of 32 of rank
+// 32 at 4096 -> 4096 26.8 and 24.6 us.
 struct SplitPlan {
   int S, p_blocks;
+  bool own;  // p in a launch of its own
 };
 static SplitPlan split_plan(const AdapterProjHost& h, int NT, int tiles, int chunks) {
   const int slices = (h.r + 15) / 16, named = h.T < h.n ? h.T : h.n;
   const int items = (h.T / kTokenTile + named < h.T ? h.T / kTokenTile + named : h.T) * slices;
   const float a_kb = (float)named * h.r * h.K * 2e-3f;
-  auto p_time = [&](int blocks) {
-    const float read = a_kb / (90.0f * blocks), turns = 1.7f * ((items + blocks - 1) / blocks);
+  auto p_time = [&](int blocks, float turn) {
+    const float read = a_kb / (90.0f * blocks), turns = turn * ((items + blocks - 1) / blocks);
     return 1.5f + (read > turns ? read : turns);
   };
-  SplitPlan best{1, 1};
+  SplitPlan best{1, 1, true};
   float best_time = 1e30f;
   const int places[4] = {148, 74, 33, 15};
   for (int i = 0; i < 4 && (i == 0 || chunks >= (2 << i)); ++i) {
@@ -798,16 +819,17 @@ static SplitPlan split_plan(const AdapterProjHost& h, int NT, int tiles, int chu
     const float x_time = NT * 0.128f / 80.0f, step = x_time > 0.3f ? x_time : 0.3f;
     const float product = 2.5f + step * ((chunks + S - 1) / S) + NT * 0.512f * (S - 1) / S / 27.0f;
     const int turns = (tiles + places[i] - 1) / places[i];
-    for (int beside = 0; beside < 2; ++beside) {
-      int blocks = (beside ? places[i] - tiles : places[i]) * S;
-      const int most = (items + S - 1) / S * S;
+    for (int own = 0; own < 2; ++own) {
+      int blocks = own ? 148 : (places[i] - tiles) * S;
+      const int most = own ? items : (items + S - 1) / S * S;
       if (blocks > most) blocks = most;
       if (blocks <= 0) continue;
-      const float pt = p_time(blocks);
-      const float time = beside ? (pt > product ? pt : product) : pt + turns * product;
+      const float pt = p_time(blocks, own ? 2.5f : 1.7f), all = turns * product;
+      float time = pt > all ? pt : all;
+      if (own) time = time + 2.0f > 14.0f ? time + 2.0f : 14.0f;  // two launches are most of 12 us of host time
       if (time < best_time) {
         best_time = time;
-        best = SplitPlan{S, blocks};
+        best = SplitPlan{S, blocks, own != 0};
       }
     }
   }
@@ -831,13 +853,22 @@ cudaError_t launch_adapter_small(const AdapterProjHost& h, const int32_t* ids, c
   }
   const int NT = (h.T + 15) / 16 * 16, tiles = (h.N + ads::BM - 1) / ads::BM, chunks = h.K / ads::BK;
   const SplitPlan plan = split_plan(h, NT, tiles, chunks);
-  const int S = plan.S, p_blocks = plan.p_blocks;
+  const int S = plan.S, p_blocks = plan.own ? 0 : plan.p_blocks;
   CUtensorMap mx;
   cudaError_t err = map_bf16_2d(&mx, x, h.K, h.T, 64, (uint32_t)NT, CU_TENSOR_MAP_SWIZZLE_128B);
   if (err != cudaSuccess) return err;
   const int ring = ads::ring_bytes(NT, S), smem = ring + ads::kBarBytes + ads::kListBytes + 1024;
   const SplitParams p{h.nf4, h.absmax, x,   A,  B,   h.scale, static_cast<uint16_t*>(low), ids, y,    h.err, h.timeout_ns,
                       h.T,   NT,       h.K, h.N, h.n, h.r,    ring,                        p_blocks};
+  if (plan.own) {
+    LaunchScope scope("adapter_low_rank", stream);
+    // an SM splits its memory for one kernel's blocks as for the other's, or they would not share it
+    cudaError_t e = cudaFuncSetAttribute(adapter_low_rank_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    adapter_low_rank_kernel<<<plan.p_blocks, kThreads, 0, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
   LaunchScope scope("adapter_split", stream);
   auto run = [&](auto kernel) -> cudaError_t {
     // the same limit in every call: calls of several host threads may meet here
@@ -848,12 +879,14 @@ cudaError_t launch_adapter_small(const AdapterProjHost& h, const int32_t* ids, c
     cfg.blockDim = dim3(ads::kThreadsSplit);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)S;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // it may start under the launch of p
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = plan.own ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, mx, p);
   };
   if (h.r > 32)

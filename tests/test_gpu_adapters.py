@@ -286,9 +286,25 @@ def test_graphs_that_share_a_workspace():
     assert pj.check_device_error() == e4b.E4B_OK
 
 
+def test_a_graph_of_two_launches_under_one_another():
+    c = Case(256, 4096, 4096, 32, 32, "zipf", seed=60)
+    want = serve(c).y.clone()
+    pj, base, ad = e4b.Projection(c.dims, c.T, train=False), c.base(), c.adapters()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(3):
+            pj.e4b_multi_lora_serve_fwd(c.ids, c.x, base, ad)
+    for _ in range(3):
+        pj.y.zero_()
+        g.replay()
+        assert torch.equal(pj.y, want)
+    assert pj.check_device_error() == e4b.E4B_OK
+
+
 def test_calls_on_several_streams_at_once():
     # each with an object of its own: blocks that wait inside one launch wait only for earlier blocks of it
     cases = [Case(T, 1024, 2048, 8, 16, "zipf", seed=20 + i) for i, T in enumerate((3, 16, 60, 200, 256, 300))]
+    cases.append(Case(256, 4096, 4096, 32, 32, "zipf", seed=60))
     want = [serve(c).y.clone() for c in cases]
     objs = [(e4b.Projection(c.dims, c.T, train=False), c.base(), c.adapters(), torch.cuda.Stream()) for c in cases]
     torch.cuda.synchronize()
@@ -385,6 +401,7 @@ def test_gradient_offsets_past_32_bits():
     ((9, 4096, 4096, 3, 8, "zipf"), {"adapter_split": 1}),
     ((17, 256, 136, 3, 8, "zipf"), {"adapter_split": 1}),
     ((256, 256, 136, 3, 8, "zipf"), {"adapter_split": 1}),
+    ((256, 4096, 4096, 32, 32, "zipf"), {"adapter_low_rank": 1, "adapter_split": 1}),
     ((257, 256, 136, 3, 8, "zipf"), {"adapter_group": 1, "adapter_proj_x": 1, "adapter_fwd": 1}),
 ])
 def test_what_a_serving_call_launches(shape, kernels):
@@ -405,6 +422,8 @@ def test_what_a_serving_call_launches(shape, kernels):
     (9, 4096, 4096, 3, 24, "zipf"), (30, 512, 8200, 5, 16, "zipf"), (30, 2048, 1024, 30, 64, "each"),
     (250, 1024, 2056, 40, 64, "zipf"), (120, 4096, 264, 3, 32, "runs"), (12, 1024, 4104, 12, 40, "each"),
     (400, 2048, 4096, 4, 16, "runs"), (700, 512, 12800, 6, 8, "zipf"),
+    # p in a launch of its own
+    (256, 4096, 4096, 32, 32, "zipf"), (200, 2048, 18952, 100, 64, "each"),
 ], ids=lambda s: "-".join(map(str, s)))
 def test_serve_wide(shape):
     c = Case(*shape)
