@@ -4,6 +4,7 @@
 //   y[t] = W x[t] + B[a] p[t],  p[t] = s[a] A[a] x[t]
 #include "e4b_device.cuh"
 #include "e4b_internal.h"
+#include "launch.cuh"
 
 namespace e4b {
 
@@ -27,6 +28,8 @@ constexpr int kGroupWarps = kGroupThreads / 32;
 __global__ void __launch_bounds__(kGroupThreads, 1)
     adapter_group_kernel(const int32_t* __restrict__ ids, int T, int n, int rows_cap, int32_t* __restrict__ order,
                          int32_t* __restrict__ offsets, int32_t* __restrict__ steps) {
+  grid_wait();
+  grid_launch_dependents();
   extern __shared__ int32_t table[];  // [kGroupWarps][n + 1]
   __shared__ int32_t wsum[2][kGroupWarps];
   __shared__ int32_t none_total;
@@ -158,9 +161,8 @@ cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int32_t* orde
                                                kGroupWarps * (E4B_MAX_ADAPTERS + 1) * 4);
   if (err != cudaSuccess) return err;
   LaunchScope scope("adapter_group", stream);
-  adapter_group_kernel<<<1, kGroupThreads, smem, stream>>>(ids, T, n, (int)adapter_rows_cap(T, n), order, offsets,
-                                                           steps);
-  return cudaGetLastError();
+  return launch_following(adapter_group_kernel, 1, kGroupThreads, smem, 0, stream, ids, T, n,
+                          (int)adapter_rows_cap(T, n), order, offsets, steps);
 }
 
 }  // namespace e4b

@@ -29,6 +29,7 @@
 
 #include "e4b_device.cuh"
 #include "e4b_internal.h"
+#include "launch.cuh"
 
 namespace e4b {
 
@@ -62,11 +63,6 @@ __device__ __forceinline__ void umma_bf16_2sm_ta(uint32_t d_tmem, uint32_t a_tme
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-
-// The launches of a step follow one another closely: each may start while the one before it still runs, sets up its
-// barriers and tensor memory, and waits for the other's end before it touches memory.
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // After a wait ran out, time for copies in flight to land before the shared memory goes away.
 constexpr uint64_t kLandNs = 1000000;
@@ -1581,32 +1577,12 @@ __global__ void __launch_bounds__(adw::kThreads, 2)
 namespace {
 int rank_padded(int r) { return r <= 16 ? 16 : (r <= 32 ? 32 : 64); }
 
-template <typename K>
-cudaError_t set_smem(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
-// Launches `kernel` so that it may start before the launch ahead of it has ended (it calls grid_wait); S > 0: in
-// clusters of S blocks.
+// launch_following with the kernel's limit of dynamic shared memory set to `smem`, the same in every call.
 template <typename... Params, typename... Args>
-cudaError_t launch_following(void (*kernel)(Params...), int grid, int threads, int smem, int S, cudaStream_t stream,
-                             const Args&... args) {
-  const cudaError_t err = set_smem(kernel, smem);
-  if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)S;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = S > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+cudaError_t launch_tiles(void (*kernel)(Params...), int grid, int threads, int smem, int S, cudaStream_t stream,
+                         const Args&... args) {
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  return err != cudaSuccess ? err : launch_following(kernel, grid, threads, smem, S, stream, args...);
 }
 
 // 2-D byte matrix [rows, bytes].
@@ -1671,8 +1647,7 @@ cudaError_t launch_adapter_fwd(const AdapterProjHost& h, const uint16_t* rows, c
   const int64_t units = (h.rows_cap + unit_rows - 1) / unit_rows * n_mt;
   const int grid = 2 * (int)(units < num_sms / 2 ? units : num_sms / 2);
   LaunchScope scope("adapter_fwd", stream);
-  return launch_following(adapter_fwd_kernel, grid, adf::kThreads, adf::SMEM_BYTES, 0, stream, mx0, mx1, mraw, mp, mb,
-                          p);
+  return launch_tiles(adapter_fwd_kernel, grid, adf::kThreads, adf::SMEM_BYTES, 0, stream, mx0, mx1, mraw, mp, mb, p);
 }
 
 cudaError_t launch_adapter_dgrad(const AdapterProjHost& h, const uint16_t* rows, const uint16_t* low,
@@ -1702,7 +1677,7 @@ cudaError_t launch_adapter_dgrad(const AdapterProjHost& h, const uint16_t* rows,
   const int64_t units = row_units * p.n_nt;
   const int grid = 2 * (int)(units < num_sms / 2 ? units : num_sms / 2);
   LaunchScope scope("adapter_dgrad", stream);
-  return launch_following(nb == 1 ? adapter_dgrad_kernel<1> : adapter_dgrad_kernel<2>, grid, adg::kThreads,
+  return launch_tiles(nb == 1 ? adapter_dgrad_kernel<1> : adapter_dgrad_kernel<2>, grid, adg::kThreads,
                           adg::SMEM_BYTES, 0, stream, ma, mraw, mla, mlb, p);
 }
 
@@ -1738,8 +1713,8 @@ cudaError_t launch_adapter_rows(const AdapterProjHost& h, bool mn, const uint16_
   while (p.S < 8 && 2 * p.S * cap <= fit && chunks >= 4 * p.S) p.S *= 2;
   const int grid = p.S * (int)(cap < fit / p.S ? cap : fit / p.S);
   LaunchScope scope(mn ? "adapter_proj_dy" : "adapter_proj_x", stream);
-  return mn ? launch_following(adapter_proj_kernel<true>, grid, adp::kThreads, adp::SMEM_BYTES, p.S, stream, ms, mw, p)
-            : launch_following(adapter_proj_kernel<false>, grid, adp::kThreads, adp::SMEM_BYTES, p.S, stream, ms, mw,
+  return mn ? launch_tiles(adapter_proj_kernel<true>, grid, adp::kThreads, adp::SMEM_BYTES, p.S, stream, ms, mw, p)
+            : launch_tiles(adapter_proj_kernel<false>, grid, adp::kThreads, adp::SMEM_BYTES, p.S, stream, ms, mw,
                               p);
 }
 
@@ -1775,7 +1750,7 @@ cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, co
   while (p.S < 8 && 2 * p.S * units <= 2 * cap && h.T / h.n >= 8 * p.S * adw::BK) p.S *= 2;
   const int grid = (int)(p.S > 1 ? units * p.S : (units < cap ? units : cap));
   LaunchScope scope("adapter_wgrad", stream);
-  return launch_following(adapter_wgrad_kernel, grid, adw::kThreads, adw::SMEM_BYTES, p.S, stream, mq, mp, p);
+  return launch_tiles(adapter_wgrad_kernel, grid, adw::kThreads, adw::SMEM_BYTES, p.S, stream, mq, mp, p);
 }
 
 }  // namespace e4b

@@ -25,6 +25,7 @@
 
 #include "e4b_device.cuh"
 #include "e4b_internal.h"
+#include "launch.cuh"
 
 namespace e4b {
 
@@ -166,6 +167,8 @@ template <int NT>  // tiles of 8 tokens
 __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvParams p) {
   __shared__ float red[2][kWarps * 8 * NT * 17];  // a unit's partial sums, in turn; a block of p: [warp][16][9]
   static_assert(2 * 8 * NT * 17 >= 16 * 9, "a block of p fits");
+  grid_wait();
+  grid_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   if ((int)blockIdx.x < p.p_blocks) {
     const int slices = (p.r + 15) / 16;
@@ -385,11 +388,6 @@ struct SplitParams {
 // Shared memory of a block of p of kWarps warps.
 constexpr int kLowRankBytes = kWarps * 16 * (kTokenTile + 1) * 4 + (3 * kAdapterSmallTokens + kTokenTile + kWarps) * 2;
 
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -485,6 +483,7 @@ __device__ __forceinline__ void split_low_rank(uint8_t* smem, const SplitParams&
 // beside one of theirs.
 __global__ void __launch_bounds__(kThreads, 4) adapter_low_rank_kernel(const SplitParams p) {
   __shared__ __align__(16) uint8_t smem[kLowRankBytes];
+  grid_wait();
   grid_launch_dependents();
   split_low_rank<kWarps>(smem, p, (int)gridDim.x);
 }
@@ -496,6 +495,8 @@ __global__ void __launch_bounds__(ads::kThreadsSplit + 128, 1)  // 96 registers:
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = align1024(smem_dyn);
   if ((int)blockIdx.x < p.p_blocks) {
+    grid_wait();
+    grid_launch_dependents();
     split_low_rank<kThreadsSplit / 32>(smem, p, p.p_blocks);
     signal_ready(p.err);
     return;
@@ -537,6 +538,10 @@ __global__ void __launch_bounds__(ads::kThreadsSplit + 128, 1)  // 96 registers:
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (p.p_blocks > 0) {  // else the launch of p has waited, and only p is still to come
+    grid_wait();
+    grid_launch_dependents();
+  }
   const int x_bytes = p.NT * BK * 2;
   bool done = false;  // (teams) the accumulator is complete
 
@@ -712,6 +717,7 @@ __global__ void __launch_bounds__(ads::kThreadsSplit + 128, 1)  // 96 registers:
   }
   if (p.p_blocks == 0) {
     grid_wait();  // p, from the launch ahead
+    grid_launch_dependents();
     __syncthreads();
   } else {
     if (tid == 0) ctl->pad = wait_ready(p.err, p.p_blocks, p.timeout_ns, 641);
@@ -845,11 +851,8 @@ cudaError_t launch_adapter_small(const AdapterProjHost& h, const int32_t* ids, c
                        h.T, h.K, h.N,   h.n,      h.r, kq,  items * kq};
     LaunchScope scope("adapter_gemv", stream);
     const int units = (h.N + 15) / 16, grid = p.p_blocks + (units < kPlaces ? units : kPlaces);
-    if (h.T <= kTokenTile)
-      adapter_gemv_kernel<1><<<grid, kThreads, 0, stream>>>(p);
-    else
-      adapter_gemv_kernel<2><<<grid, kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_following(h.T <= kTokenTile ? adapter_gemv_kernel<1> : adapter_gemv_kernel<2>, grid, kThreads, 0, 0,
+                            stream, p);
   }
   const int NT = (h.T + 15) / 16 * 16, tiles = (h.N + ads::BM - 1) / ads::BM, chunks = h.K / ads::BK;
   const SplitPlan plan = split_plan(h, NT, tiles, chunks);
@@ -866,28 +869,15 @@ cudaError_t launch_adapter_small(const AdapterProjHost& h, const int32_t* ids, c
     cudaError_t e = cudaFuncSetAttribute(adapter_low_rank_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                                          cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
-    adapter_low_rank_kernel<<<plan.p_blocks, kThreads, 0, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_following(adapter_low_rank_kernel, plan.p_blocks, kThreads, 0, 0, stream, p)) != cudaSuccess)
+      return e;
   }
   LaunchScope scope("adapter_split", stream);
   auto run = [&](auto kernel) -> cudaError_t {
     // the same limit in every call: calls of several host threads may meet here
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ads::kMaxSmem);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p_blocks + tiles * S));
-    cfg.blockDim = dim3(ads::kThreadsSplit);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)S;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // it may start under the launch of p
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = plan.own ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, mx, p);
+    return launch_following(kernel, p_blocks + tiles * S, ads::kThreadsSplit, smem, S, stream, mx, p);
   };
   if (h.r > 32)
     return S == 1   ? run(adapter_split_kernel<1, true>)

@@ -27,6 +27,7 @@
 
 #include "e4b_device.cuh"
 #include "e4b_internal.h"
+#include "launch.cuh"
 
 namespace e4b {
 
@@ -302,6 +303,8 @@ constexpr int fwd_blocks(int V) { return V == 8 ? 2 : 4; }
 // covers the batch; its pieces are the sequences and need no records.
 template <int G, int V, bool ALIGNED, bool ONE>
 __global__ void __launch_bounds__(kThreads, fwd_blocks(V)) balance_fwd_kernel(const FwdParams p) {
+  grid_wait();
+  grid_launch_dependents();
   if (!ONE && (int)blockIdx.x >= p.blocks) {
     join_block(p);
     return;
@@ -512,6 +515,8 @@ constexpr int bwd_blocks(int V) { return V == 8 ? 2 : 3; }
 template <int G, int V, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, bwd_blocks(V)) balance_bwd_kernel(const BwdParams p) {
   constexpr int kTok = 32 / G;
+  grid_wait();
+  grid_launch_dependents();
   const int lane = threadIdx.x & 31, g = lane % G, sub = lane / G;
   const int64_t w0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.per_warp;
   if (w0 >= p.T) return;
@@ -636,18 +641,15 @@ template <int G, int V, bool ALIGNED>
 struct RunFwd {
   static cudaError_t run(FwdParams p, int grid, cudaStream_t stream) {
     const int smem = (kWarps * p.E + p.E + 2 * kWarps) * 4;
-    if (p.blocks == 1)
-      balance_fwd_kernel<G, V, ALIGNED, true><<<grid, kThreads, smem, stream>>>(p);
-    else
-      balance_fwd_kernel<G, V, ALIGNED, false><<<grid, kThreads, smem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_following(p.blocks == 1 ? balance_fwd_kernel<G, V, ALIGNED, true>
+                                          : balance_fwd_kernel<G, V, ALIGNED, false>,
+                            grid, kThreads, smem, 0, stream, p);
   }
 };
 template <int G, int V, bool ALIGNED>
 struct RunBwd {
   static cudaError_t run(BwdParams p, int grid, cudaStream_t stream) {
-    balance_bwd_kernel<G, V, ALIGNED><<<grid, kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_following(balance_bwd_kernel<G, V, ALIGNED>, grid, kThreads, 0, 0, stream, p);
   }
 };
 

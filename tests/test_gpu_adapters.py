@@ -301,6 +301,38 @@ def test_a_graph_of_two_launches_under_one_another():
     assert pj.check_device_error() == e4b.E4B_OK
 
 
+@pytest.mark.parametrize("T", [5, 14, 60, 256, 300])
+def test_a_chain_of_launches_under_one_another(T):
+    # every projection reads what the one before it wrote; launches may start early, reads may not
+    cases = [Case(T, K, N, n, 16, "zipf", seed=70 + i) for i, (K, N, n) in enumerate(
+        ((2048, 4096, 4), (4096, 1024, 40), (1024, 128, 3), (128, 4096, 7), (4096, 2048, 32)))]
+    first = cases[0].x
+    steps = [(e4b.Projection(c.dims, T, train=False), c) for c in cases]
+    args = [(c.base(), c.adapters()) for c in cases]
+
+    def run(sync):
+        x = first
+        for (pj, c), (base, ad) in zip(steps, args):
+            pj.e4b_multi_lora_serve_fwd(c.ids, x, base, ad)
+            if sync:
+                torch.cuda.synchronize()
+            x = pj.y
+        return x
+
+    want = run(True).clone()
+    for _ in range(30):
+        for pj, _c in steps:
+            pj.y.fill_(float("nan"))
+        assert torch.equal(run(False), want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(False)
+        y = run(False)
+    for _ in range(5):
+        g.replay()
+        assert torch.equal(y, want)
+
+
 def test_calls_on_several_streams_at_once():
     # each with an object of its own: blocks that wait inside one launch wait only for earlier blocks of it
     cases = [Case(T, 1024, 2048, 8, 16, "zipf", seed=20 + i) for i, T in enumerate((3, 16, 60, 200, 256, 300))]
