@@ -15,8 +15,8 @@ constexpr uint32_t kFull = 0xffffffffu;
 // ----------------------------------------------------------------------------
 // Grouping: a stable counting sort of the tokens by adapter in one block.
 // Every warp owns a contiguous run of tokens and a histogram row of its own in
-// shared memory; lanes with equal ids find one another with a warp match, so
-// that there are no shared-memory atomics and the order is fixed.  Two passes
+// shared memory; to place the tokens, lanes with equal ids find one another with a
+// warp match, so that the order is fixed.  Two passes
 // over the ids (count, place) around one scan over the adapters, thread a owning
 // adapter a.  Latency bounds it (one read of the ids and a dozen block-wide
 // steps; 777 tokens of 16 adapters 5 us, 16384 of 64 12 us), so the scan's sums go
@@ -33,6 +33,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
   extern __shared__ int32_t table[];  // [kGroupWarps][n + 1]
   __shared__ int32_t wsum[2][kGroupWarps];
   __shared__ int32_t none_total;
+  __shared__ int32_t first_row[E4B_MAX_ADAPTERS + 1], first_task[E4B_MAX_ADAPTERS + 1];
+  __shared__ int32_t last_row[E4B_MAX_ADAPTERS];  // one past an adapter's tokens
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cols = n + 1;
   const int per = ((T + kGroupWarps - 1) / kGroupWarps + 31) / 32 * 32;
@@ -57,10 +59,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
     if (tb > t0) load(tb);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int a = ad[i];
-      const uint32_t same = __match_any_sync(kFull, a);
-      if (a >= 0 && (same & ((1u << lane) - 1)) == 0) mine[a] += __popc(same);
-      __syncwarp();
+      if (ad[i] >= 0) atomicAdd(&mine[ad[i]], 1);  // this warp's row: integers, any order
     }
   }
   __syncthreads();
@@ -106,7 +105,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
     return __shfl_sync(kFull, x - v, warp);
   };
   int none0, adapter_tasks;
-  const int start = before(0, none0) + in_rows - padded, end = start + padded;
+  const int start = before(0, none0) + in_rows - padded;
   const int task0 = before(1, adapter_tasks) + in_tasks - ntask;
   const int nnone = none_total, none_tasks = (nnone + kAdapterTaskRows - 1) / kAdapterTaskRows;
   const int used = none0 + nnone;
@@ -116,12 +115,34 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
 #pragma unroll
     for (int w = 0; w < kGroupWarps; ++w) table[w * cols + tid] = start + at[w];
   }
-  __syncthreads();
   if (tid < n) {
+    first_row[tid] = start;
+    first_task[tid] = task0;
+    last_row[tid] = start + count;
     offsets[tid] = start;
-    for (int i = start / kAdapterRowAlign; i < end / kAdapterRowAlign; ++i) granules[i] = tid;
-    for (int i = 0; i < ntask; ++i) tasks[task0 + i] = make_int4(tid, start + i * kAdapterTaskRows, end, 0);
-    for (int i = start + count; i < end; ++i) order[i] = T;  // padding rows
+  }
+  if (tid == 0) {
+    first_row[n] = none0;
+    first_task[n] = adapter_tasks;
+  }
+  __syncthreads();
+  // The adapter of a row or task: the last that starts at or before it (one without rows starts where the next does).
+  auto owner = [&](const int32_t* firsts, int at) -> int {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      (firsts[mid] <= at ? lo : hi) = mid;
+    }
+    return lo;
+  };
+  for (int i = tid; i < none0 / kAdapterRowAlign; i += kGroupThreads) granules[i] = owner(first_row, i * kAdapterRowAlign);
+  for (int i = tid; i < adapter_tasks; i += kGroupThreads) {
+    const int a = owner(first_task, i);
+    tasks[i] = make_int4(a, first_row[a] + (i - first_task[a]) * kAdapterTaskRows, first_row[a + 1], 0);
+  }
+  for (int a = warp; a < n; a += kGroupWarps) {  // padding rows, fewer than 32 an adapter
+    const int i = last_row[a] + lane;
+    if (i < first_row[a + 1]) order[i] = T;
   }
   if (tid == 0) {
     steps[0] = used;
