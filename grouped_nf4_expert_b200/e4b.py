@@ -578,7 +578,10 @@ class _OnDevice:
             handle = stream.cuda_stream
         fn = self._fns.get(name)
         if fn is None:
-            fn = self._fns[name] = getattr(lib(), name)
+            # structs go in by address: a handle of its own converts its arguments in two thirds of the time
+            fn = self._fns[name] = lib()[name]
+            fn.restype, args_of = _SIGNATURES[name]
+            fn.argtypes = [c_vp if issubclass(a, ctypes._Pointer) else a for a in args_of]
         if self._current_device() == index:
             status = fn(*args, handle)
         else:
@@ -629,7 +632,7 @@ class Projection(_OnDevice):
         self.y = _alloc((T, dims.N), bf, dev)
         self.ws = _alloc((int(max(sz.workspace_bytes, sz.serve_workspace_bytes)),), torch.uint8, dev)
         self._dims_c = dims.c()
-        self._dims_p = ctypes.byref(self._dims_c)
+        self._dims_p = ctypes.addressof(self._dims_c)
         self._base_need = {"nf4": dims.N * dims.K // 2, "absmax": dims.N * dims.K // 64}
         self._adapters_need = {"A": n * r * dims.K, "B": n * dims.N * r, "scale": n}
         self._y_p, self._ws_p, self._ws_n = _ptr(self.y), _ptr(self.ws), self.ws.numel()
@@ -644,18 +647,22 @@ class Projection(_OnDevice):
             self.dA = self.lora_grads[:na].view(n, r, dims.K)
             self.dB = self.lora_grads[na:].view(n, dims.N, r)
             self._groups = AdapterGroups(_ptr(self.order), _ptr(self.offsets), _ptr(self.steps))
-            self._groups_p = ctypes.byref(self._groups)
+            self._groups_p = ctypes.addressof(self._groups)
             self._low_p = (_ptr(self.p), _ptr(self.q))
             self._dx_p, self._grad_p = _ptr(self.dx), (_ptr(self.dA), _ptr(self.dB))
         self._call("e4b_workspace_init", None, self._ws_p, self._ws_n)
 
     def _base(self, base: Nf4Matrix):
+        if type(base) is not Nf4Matrix:
+            raise TypeError("base: an Nf4Matrix (nf4_matrix) is required, got %s" % type(base).__name__)
         _check_struct(base, self._base_need, self.device, "base")
-        return ctypes.byref(base)
+        return ctypes.addressof(base)
 
     def _adapters(self, ad: AdapterFactors):
+        if type(ad) is not AdapterFactors:
+            raise TypeError("adapters: AdapterFactors (adapter_factors) are required, got %s" % type(ad).__name__)
         _check_struct(ad, self._adapters_need, self.device, "adapters")
-        return ctypes.byref(ad)
+        return ctypes.addressof(ad)
 
     def _training(self):
         if not self.train:
@@ -727,7 +734,7 @@ class RouterBalance(_OnDevice):
         import torch
         self.E, self.top_k, self.T, self.S = E, top_k, T, S
         self._dims_c = BalanceDims(E, top_k, S, 0.0, 0.0)
-        self._dims_p = ctypes.byref(self._dims_c)
+        self._dims_p = ctypes.addressof(self._dims_c)
         ws_bytes = e4b_balance_get_sizes(self._dims_c, T)
         dev = self._on(device)
         f32, i32 = torch.float32, torch.int32
@@ -737,7 +744,7 @@ class RouterBalance(_OnDevice):
         self.lse, self.loss = _alloc((T,), f32, dev), _alloc((3,), f32, dev)
         self.ws = _alloc((ws_bytes,), torch.uint8, dev)
         self._stats = BalanceStats(*(_ptr(t) for t in (self.counts, self.prob_sum, self._tokens, self.lse)))
-        self._stats_p = ctypes.byref(self._stats)
+        self._stats_p = ctypes.addressof(self._stats)
         self._loss_p, self._ws_p, self._ws_n = _ptr(self.loss), _ptr(self.ws), self.ws.numel()
         self._call("e4b_workspace_init", None, self._ws_p, self._ws_n)
 

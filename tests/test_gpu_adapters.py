@@ -10,6 +10,8 @@ sum of absolute values bounds) and round the result once:
 and the same with the roles swapped for dx, dA and dB.
 """
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -468,9 +470,10 @@ def test_rows_behind_the_last_token_stay():
     c = Case(37, 128, 136, 3, 8, "zipf")
     big = torch.full((64, 136), 3.0, dtype=torch.bfloat16, device="cuda")
     pj = e4b.Projection(c.dims, c.T)
-    e4b._check(e4b.lib().e4b_multi_lora_serve_fwd(pj._dims_p, c.T, c.ids.data_ptr(), c.x.data_ptr(),
-                                                  pj._base(c.base()), pj._adapters(c.adapters()), big.data_ptr(),
-                                                  pj._ws_p, pj._ws_n, e4b._stream(None)), "serve")
+    ref = ctypes.byref
+    e4b._check(e4b.lib().e4b_multi_lora_serve_fwd(ref(pj._dims_c), c.T, c.ids.data_ptr(), c.x.data_ptr(),
+                                                  ref(c.base()), ref(c.adapters()), big.data_ptr(), pj._ws_p,
+                                                  pj._ws_n, e4b._stream(None)), "serve")
     assert torch.equal(big[:37], serve(c).y) and bool((big[37:] == 3.0).all())
 
 
@@ -506,6 +509,10 @@ def test_the_binding_refuses_before_any_launch():
         pj.e4b_adapter_group(c.ids.cpu())
     with pytest.raises(ValueError, match="a tensor is required"):
         pj.e4b_multi_lora_wgrad(c.x, None)
+    with pytest.raises(TypeError, match="base: an Nf4Matrix"):
+        pj.e4b_multi_lora_serve_fwd(c.ids, c.x, ad, ad)
+    with pytest.raises(TypeError, match="adapters: AdapterFactors"):
+        pj.e4b_multi_lora_serve_fwd(c.ids, c.x, base, None)
     with pytest.raises(ValueError, match="base.nf4: .* the dims need"):
         pj.e4b_multi_lora_fwd(c.x, e4b.nf4_matrix(c.nf4[:1], c.absmax), ad)
     with pytest.raises(ValueError, match="adapters.scale: .* the dims need"):
