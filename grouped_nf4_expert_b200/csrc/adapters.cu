@@ -19,7 +19,7 @@ constexpr uint32_t kFull = 0xffffffffu;
 // warp match, so that the order is fixed.  Two passes
 // over the ids (count, place) around one scan over the adapters, thread a owning
 // adapter a.  Latency bounds it (one read of the ids and a dozen block-wide
-// steps; 777 tokens of 16 adapters 5 us, 16384 of 64 12 us), so the scan's sums go
+// steps; 777 tokens of 16 adapters 5 us, 8192 of 64 10 us), so the scan's sums go
 // through one barrier and the histogram is read once, all warps' rows at a time.
 // ----------------------------------------------------------------------------
 constexpr int kGroupThreads = 1024;

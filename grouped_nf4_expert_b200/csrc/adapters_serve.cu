@@ -1,4 +1,4 @@
-// Small batches of the NF4 projection with adapters of many requests, one
+// Small batches of the NF4 projection with adapters of many requests, mostly one
 // launch each:
 //
 //   adapter_gemv_kernel:  y[t] = W x[t] + B[a] p[t], p[t] = s[a] A[a] x[t], for
@@ -350,8 +350,11 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvPar
 // layout of the warp instruction, tile by tile, so that no adapter's values
 // meet another's tokens.  256 tokens, 4096 -> 4096, 32 adapters of rank 32: 25 us,
 // bound by the L2 reads of x (64 KB/us a block; all of x for every 128 rows of W,
-// 64 MB) and the exchange of shares; 57 tokens, 2048 -> 512: 14.3 us, the chain p,
-// hand-over, join.
+// 64 MB) and the exchange of shares; 57 tokens, 2048 -> 512: 12 us, the chain p,
+// hand-over, join; 64 tokens, 4096 -> 14336, 16 adapters: 29 us, the ALU pipe (the
+// decode's byte permutes) 95% busy in the loop.  A fourth team, or coalesced code
+// loads, change nothing there; a quarter of the words by a table of byte pairs
+// gains 4%.
 namespace ads {
 constexpr int BM = 128, BK = 64;
 constexpr int kXStages = 4, kTeams = 3, kABufs = 2 * kTeams, kACols = BK / 2;
