@@ -552,7 +552,7 @@ class _OnDevice:
     def _arg(self, t, dtype, numel, name, optional=False):
         """Device address of ``t`` after the checks of :func:`_dev`; the tests a sound tensor passes come
         first, since a small batch's call costs the host more than the GPU."""
-        if (type(t) is self._tensor and t.dtype is dtype[1] and t.device == self.device and t.is_contiguous()
+        if (type(t) is self._tensor and t.dtype is dtype[1] and t.get_device() == self._index and t.is_contiguous()
                 and t.numel() >= numel > 0):
             return t.data_ptr()
         return _dev(t, dtype[0], numel, name, self.device, optional=optional or self.T == 0)
@@ -560,16 +560,18 @@ class _OnDevice:
     def _on(self, device):
         import torch
         self.device = _cuda_device(device)
+        self._index = self.device.index
         self._tensor = torch.Tensor
         self._raw_stream = torch._C._cuda_getCurrentRawStream  # the handle, without a Stream object a call
-        self._current_device = torch.cuda.current_device
+        torch.cuda.init()
+        self._current_device = torch._C._cuda_getDevice
         self._bf16, self._f32 = ("bf16", torch.bfloat16), ("f32", torch.float32)
         self._i32, self._u8 = ("i32", torch.int32), ("u8", torch.uint8)
         self._fns = {}
         return self.device
 
     def _call(self, name, stream, *args):
-        index = self.device.index
+        index = self._index
         if stream is None:
             handle = self._raw_stream(index)
         elif stream.device != self.device:
@@ -652,17 +654,15 @@ class Projection(_OnDevice):
             self._dx_p, self._grad_p = _ptr(self.dx), (_ptr(self.dA), _ptr(self.dB))
         self._call("e4b_workspace_init", None, self._ws_p, self._ws_n)
 
-    def _base(self, base: Nf4Matrix):
+    def _structs(self, base: Nf4Matrix, ad: AdapterFactors):
+        """Addresses of the call's structs, after their checks."""
         if type(base) is not Nf4Matrix:
             raise TypeError("base: an Nf4Matrix (nf4_matrix) is required, got %s" % type(base).__name__)
-        _check_struct(base, self._base_need, self.device, "base")
-        return ctypes.addressof(base)
-
-    def _adapters(self, ad: AdapterFactors):
         if type(ad) is not AdapterFactors:
             raise TypeError("adapters: AdapterFactors (adapter_factors) are required, got %s" % type(ad).__name__)
+        _check_struct(base, self._base_need, self.device, "base")
         _check_struct(ad, self._adapters_need, self.device, "adapters")
-        return ctypes.addressof(ad)
+        return ctypes.addressof(base), ctypes.addressof(ad)
 
     def _training(self):
         if not self.train:
@@ -681,8 +681,9 @@ class Projection(_OnDevice):
         """Serving forward into ``self.y`` (ids int32 [T], any id outside [0, n) for no adapter)."""
         pi = self._arg(ids, self._i32, self.T, "ids")
         px = self._arg(x, self._bf16, self.T * self.dims.K, "x")
-        self._call("e4b_multi_lora_serve_fwd", stream, self._dims_p, self.T, pi, px, self._base(base),
-                   self._adapters(adapters), self._y_p, self._ws_p, self._ws_n)
+        pb, pa = self._structs(base, adapters)
+        self._call("e4b_multi_lora_serve_fwd", stream, self._dims_p, self.T, pi, px, pb, pa, self._y_p, self._ws_p,
+                   self._ws_n)
 
     def e4b_adapter_group(self, ids, stream=None):
         """Groups the step's tokens by adapter for the training calls."""
@@ -695,7 +696,7 @@ class Projection(_OnDevice):
         """``y`` of the grouped tokens; keeps ``p`` for the adapter gradients."""
         self._training()
         px = self._arg(x, self._bf16, self.T * self.dims.K, "x")
-        pb, pa = self._base(base), self._adapters(adapters)
+        pb, pa = self._structs(base, adapters)
         self._after(1)
         self._call("e4b_multi_lora_fwd", stream, self._dims_p, self.T, self._groups_p, px, pb, pa,
                    self._low_p[0], self._y_p, self._ws_p, self._ws_n)
@@ -705,7 +706,7 @@ class Projection(_OnDevice):
         """``dx``; keeps ``q`` for the adapter gradients."""
         self._training()
         pd = self._arg(dY, self._bf16, self.T * self.dims.N, "dY")
-        pb, pa = self._base(base), self._adapters(adapters)
+        pb, pa = self._structs(base, adapters)
         self._after(1)
         self._call("e4b_multi_lora_dgrad", stream, self._dims_p, self.T, self._groups_p, pd, pb, pa,
                    self._low_p[1], self._dx_p, self._ws_p, self._ws_n)
