@@ -67,11 +67,11 @@ __device__ __forceinline__ void umma_bf16_2sm_ta(uint32_t d_tmem, uint32_t a_tme
 // After a wait ran out, time for copies in flight to land before the shared memory goes away.
 constexpr uint64_t kLandNs = 1000000;
 
-// The adapters of a unit of up to 256 rows from row0 on, one run of rows [lo, hi) (relative to row0) at a time: the
+// The adapters of a unit of up to 32 kMost rows from row0 on, one run of rows [lo, hi) (relative to row0) at a time: the
 // adapter of every 32 rows is in `granules` (n for the tokens without one), and every adapter starts such a granule.
-// All eight are read at once, when the unit starts.
+// All of them are read at once, when the unit starts.
+template <int kMost>
 struct AdapterRun {
-  static constexpr int kMost = 256 / kAdapterRowAlign;
   int id[kMost];
   int n, granule = 0;
   int lo = 0, hi = 0, adapter = -1;
@@ -178,8 +178,9 @@ __device__ __forceinline__ void let_land(uint64_t* bars, int n, uint32_t issued,
 // =============================================================================
 // Forward: y[t] = W x[t] + B[a] p[t], W as the M operand
 // =============================================================================
-// A unit is 256 rows of W (128 a CTA of the pair) x up to 256 token rows (a
-// multiple of 32, chosen so that the units fill the GPU's pairs evenly).  A thread of
+// A unit is 256 rows of W (128 a CTA of the pair) x up to 256 token rows, or 384
+// where one turn of the pairs does then (a multiple of 32, chosen so that the units
+// fill the pairs evenly).  A thread of
 // the decode groups owns a row of W: it decodes 64 weights of a k-chunk into
 // registers and writes them to tensor memory, where the UMMAs read their M
 // operand.  Written to shared memory instead (as the expert block's tiles are,
@@ -187,15 +188,16 @@ __device__ __forceinline__ void let_land(uint64_t* bars, int n, uint32_t issued,
 // KB of operand reads a chunk on top of the token rows' 32 KB: more
 // shared-memory time than the chunk's 512 tensor cycles.
 //
-// The accumulator is a half of 128 token rows and one of the rest, in three TMEM
-// slots used in turn, and each half has an issuing warp of its own: while the
-// epilogue empties a unit's first half, the next unit's first half fills, and the
-// second follows once its slot is free.  (One warp handing in both halves'
-// products took 720 cycles a chunk, against 512 in the tensor pipe: its
-// instruction stream, not the operands, was the limit.)  Token rows are
-// accumulator columns, so an adapter's K = r product is issued at its own
-// columns: adapters' rows start at multiples of 32, the column granule of a pair
-// UMMA.
+// The accumulator is in parts of 128 token rows (the last one may be smaller), in
+// three TMEM slots used in turn, and each part has an issuing warp of its own: while
+// the epilogue empties the first part of a unit of two, the next unit's first part
+// fills, and the second follows once its slot is free.  (One warp handing in two
+// parts' products took 720 cycles a chunk, against 512 in the tensor pipe: its
+// instruction stream, not the operands, was the limit.)  Units of three parts have
+// no slot to spare and are used for a single turn: 1111 tokens, 2048 -> 4096 in 64
+// units of 384 rows 27 us, in 128 of 160 33 us.  Token rows are accumulator columns, so
+// an adapter's K = r product is issued at its own columns: adapters' rows start at
+// multiples of 32, the column granule of a pair UMMA.
 //
 // The issuers see both CTAs' operands on barriers of the even CTA: the odd CTA's
 // TMA loads count their bytes there, and its decode warps signal with a 4-byte
@@ -208,30 +210,33 @@ __device__ __forceinline__ void let_land(uint64_t* bars, int n, uint32_t issued,
 // pipe 53% active (3.5 turns of units); 16384 tokens, 4096 -> 14336: 1.15 PFLOP/s.
 //
 // Roles per CTA: warp 0 codes, warp 1 TMEM owner and (even CTA) issuer of the
-// first halves, warp 2 (even CTA) issuer of the second halves, warp 3 token rows
-// and low-rank operands, warps 4-19 four decode groups taking the chunks round
-// robin, warps 20-23 epilogue (32 rows of W each).
+// first parts, warp 2 (even CTA) issuer of the second parts, warp 3 token rows and
+// low-rank operands, warps 4-19 four decode groups taking the chunks round robin,
+// warps 20-23 epilogue (32 rows of W each), warp 24 issuer of third parts.
 namespace adf {
 constexpr int BM = 128, BK = 64;
-constexpr int kHalf = 128;                    // token rows of an accumulator half
-constexpr int X_BYTES = kHalf * BK * 2;       // a CTA's 64 + 64 token rows of a chunk
-constexpr int SA = 8;                         // token-row ring
+constexpr int kHalf = 128;                    // token rows of an accumulator part
+constexpr int kPartBytes = kHalf / 2 * BK * 2;  // a CTA's 64 token rows of a part and chunk
+constexpr int slot_bytes(int parts) { return parts * kPartBytes; }
+constexpr int slots(int parts) { return parts > 2 ? 5 : 8; }  // token-row ring
 constexpr int kGroups = 4, kGroupWarps = 4;
-constexpr int kSlots = 3;                     // accumulator halves
-constexpr int kAOff = kSlots * kHalf;         // TMEM: the halves, then one decoded chunk (32 columns) a group
+constexpr int kSlots = 3;                     // accumulator parts
+constexpr int kAOff = kSlots * kHalf;         // TMEM: the parts, then one decoded chunk (32 columns) a group
 constexpr int RAW_STAGES = 2 * kGroups, RAW_BYTES = BM * BK / 2;
-constexpr int RAW_OFF = SA * X_BYTES;
+constexpr int RAW_OFF = slots(2) * slot_bytes(2);
 constexpr int EPI_OFF = RAW_OFF + RAW_STAGES * RAW_BYTES;
 constexpr int kEpiPitch = 80;                 // bytes of a token's 32 outputs of a warp, padded
 constexpr int kEpiWarpBytes = 32 * kEpiPitch;
 constexpr int BAR_OFF = EPI_OFF + 4 * kEpiWarpBytes;
 constexpr int SMEM_BYTES = BAR_OFF + 1024 + 1024;
 constexpr int kEpiWarp0 = 4 + kGroups * kGroupWarps;
-constexpr int kThreads = 32 * (kEpiWarp0 + 4);
+constexpr int kThirdWarp = kEpiWarp0 + 4;
+constexpr int threads(int parts) { return 32 * (kThirdWarp + (parts > 2)); }
 constexpr int kTmemCols = 512;
 static_assert(kAOff + kGroups * BK / 2 <= kTmemCols, "TMEM budget");
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-static_assert(BM * E4B_MAX_RANK * 2 <= X_BYTES && kHalf * E4B_MAX_RANK * 2 <= X_BYTES, "low-rank operands fit a slot");
+static_assert(slots(3) * slot_bytes(3) <= RAW_OFF, "the ring of three parts fits");
+static_assert(BM * E4B_MAX_RANK * 2 <= slot_bytes(2) && 64 * E4B_MAX_RANK * 2 <= kPartBytes, "low-rank operands fit");
 }  // namespace adf
 
 struct AdapterFwdParams {
@@ -241,21 +246,24 @@ struct AdapterFwdParams {
   uint16_t* out;
   DeviceError* err;
   long long timeout_ns;
-  int K, N, T, n, r_pad, n_mt;
-  int n0, n1;  // token rows of a unit's halves, multiples of 32 (n1 may be 0)
+  int K, N, T, n_adapters, r_pad, n_mt;
+  int n[3];  // token rows of a unit's parts, multiples of 32: 128 where another part follows, 0 where there is none
 };
 
-// Rows [lo, hi) of a unit in its half h, relative to the half.
-__device__ __forceinline__ int2 half_range(const AdapterRun& run, int h, int n0, int n1) {
-  const int base = h ? n0 : 0, n = h ? n1 : n0;
-  return make_int2(min(max(run.lo - base, 0), n), min(max(run.hi - base, 0), n));
+// Rows [lo, hi) of a run in part i of its unit (n rows from 128 i on), relative to the part.
+template <typename Run>
+__device__ __forceinline__ int2 part_range(const Run& run, int i, int n) {
+  return make_int2(min(max(run.lo - adf::kHalf * i, 0), n), min(max(run.hi - adf::kHalf * i, 0), n));
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
+template <int PARTS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::threads(PARTS), 1)
     adapter_fwd_kernel(const __grid_constant__ CUtensorMap map_x0, const __grid_constant__ CUtensorMap map_x1,
                        const __grid_constant__ CUtensorMap map_raw, const __grid_constant__ CUtensorMap map_p,
                        const __grid_constant__ CUtensorMap map_b, const AdapterFwdParams p) {
   using namespace adf;
+  using Run = AdapterRun<4 * PARTS>;
+  constexpr int X_BYTES = slot_bytes(PARTS), SA = slots(PARTS);
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = align1024(smem_dyn);
   uint8_t* rawbuf = smem + RAW_OFF;
@@ -266,16 +274,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
   uint64_t* xempty = xfull + SA;                // [SA] ring slot consumed by the UMMAs
   uint64_t* adone = xempty + SA;                // [kGroups] (even CTA) both CTAs' decoded chunk is in tensor memory
   uint64_t* aempty = adone + kGroups;           // [kGroups] decoded chunk consumed by the UMMAs
-  uint64_t* accfull = aempty + kGroups;         // [kSlots] accumulator half complete
-  uint64_t* accempty = accfull + kSlots;        // [kSlots] (even CTA) half drained in both CTAs
-  uint64_t* drain = accempty + kSlots;          // [2] (even CTA) all of an issuer's UMMAs finished
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
-  CtaControl* ctl = reinterpret_cast<CtaControl*>(drain + 3);
-  uint32_t* sig = reinterpret_cast<uint32_t*>(drain + 4);
+  uint64_t* accfull = aempty + kGroups;         // [kSlots] accumulator part complete
+  uint64_t* accempty = accfull + kSlots;        // [kSlots] (even CTA) part drained in both CTAs
+  uint64_t* drain = accempty + kSlots;          // [3] (even CTA) all of an issuer's UMMAs finished
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 3);
+  CtaControl* ctl = reinterpret_cast<CtaControl*>(drain + 4);
+  uint32_t* sig = reinterpret_cast<uint32_t*>(drain + 5);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  const int halves = p.n1 ? 2 : 1;
+  const int parts = 1 + (p.n[1] > 0) + (PARTS > 2);
   if (threadIdx.x == 0) {
     for (int r = 0; r < RAW_STAGES; ++r) {
       mbar_init(&raw_full[r], 1);
@@ -283,18 +291,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
     }
     for (int s = 0; s < SA; ++s) {
       mbar_init(&xfull[s], 1);
-      mbar_init(&xempty[s], halves);
+      mbar_init(&xempty[s], parts);
     }
     for (int g = 0; g < kGroups; ++g) {
       mbar_init(&adone[g], kGroupWarps);
-      mbar_init(&aempty[g], halves);
+      mbar_init(&aempty[g], parts);
     }
     for (int b = 0; b < kSlots; ++b) {
       mbar_init(&accfull[b], 1);
       mbar_init(&accempty[b], 8);
     }
-    mbar_init(&drain[0], 1);
-    mbar_init(&drain[1], 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&drain[i], 1);
     ctl->abort = 0;
     fence_mbar_init();
   }
@@ -309,7 +316,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
   grid_wait();
   grid_launch_dependents();
 
-  const int rows_used = p.steps[0], unit_rows = p.n0 + p.n1;
+  const int rows_used = p.steps[0], unit_rows = p.n[0] + p.n[1] + (PARTS > 2 ? p.n[2] : 0);
   const int n_units = (rows_used + unit_rows - 1) / unit_rows * p.n_mt;
   const int kchunks = p.K / BK;
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
@@ -337,8 +344,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
     __syncwarp();
   } else if (warp == 3) {
     // ------------------------------------------------ token rows, then a unit's low-rank operands (one lane)
-    // This CTA's rows of a half: 64 of its 128 (of an adapter's columns: its half of them).  A low-rank use is
-    // two slots: the adapter's 128 rows of B, then its p rows of both halves.
+    // This CTA's rows of a part: 64 of its 128 (of an adapter's columns: half of them).  A low-rank use is
+    // two slots: the adapter's 128 rows of B, then its p rows of every part.
     if (lane == 0) {
       tma_prefetch_desc(&map_x0);
       tma_prefetch_desc(&map_p);
@@ -355,14 +362,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
       bool ok = true;
       for (int u = pair; u < n_units && ok; u += n_pairs) {
         const int w0 = (u % p.n_mt) * 256 + (int)rank * BM, t0 = u / p.n_mt * unit_rows;
-        AdapterRun run(granules, t0, rows_used, unit_rows, p.n);
+        Run run(granules, t0, rows_used, unit_rows, p.n_adapters);
         for (int kc = 0; kc < kchunks; ++kc) {
           if (!(ok = mbar_wait(&xempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 212))) break;
           uint8_t* x = smem + s * X_BYTES;
           const uint32_t bar = xfull_even + 8 * s;
           if (rank == 0) mbar_arrive_expect_tx(&xfull[s], (uint32_t)(2 * unit_rows * BK));
-          tma_load_2d_pair(x, &map_x0, bar, kc * BK, t0 + p.n0 / 2 * (int)rank);
-          if (p.n1) tma_load_2d_pair(x + X_BYTES / 2, &map_x1, bar, kc * BK, t0 + p.n0 + p.n1 / 2 * (int)rank);
+          tma_load_2d_pair(x, &map_x0, bar, kc * BK, t0 + p.n[0] / 2 * (int)rank);
+          if (PARTS > 2) {
+            tma_load_2d_pair(x + kPartBytes, &map_x0, bar, kc * BK, t0 + kHalf + p.n[1] / 2 * (int)rank);
+            tma_load_2d_pair(x + 2 * kPartBytes, &map_x1, bar, kc * BK, t0 + 2 * kHalf + p.n[2] / 2 * (int)rank);
+          } else if (p.n[1]) {
+            tma_load_2d_pair(x + kPartBytes, &map_x1, bar, kc * BK, t0 + kHalf + p.n[1] / 2 * (int)rank);
+          }
           issued_next();
         }
         if (!ok) break;
@@ -370,22 +382,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
           const uint32_t s1 = (s + 1 == SA) ? 0 : s + 1, ph1 = (s + 1 == SA) ? ph ^ 1 : ph;
           if (!(ok = mbar_wait(&xempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 210))) break;
           if (!(ok = mbar_wait(&xempty[s1], ph1 ^ 1, ctl, p.err, p.timeout_ns, 210))) break;
-          const int2 h0 = half_range(run, 0, p.n0, p.n1), h1 = half_range(run, 1, p.n0, p.n1);
-          const int n0 = (h0.y - h0.x) / 2, n1 = (h1.y - h1.x) / 2;  // this CTA's p rows, multiples of 16
+          int rows[PARTS], first[PARTS], all = 0;  // this CTA's p rows of each part, multiples of 16
+#pragma unroll
+          for (int i = 0; i < PARTS; ++i) {
+            const int2 h = part_range(run, i, p.n[i]);
+            rows[i] = (h.y - h.x) / 2;
+            first[i] = t0 + kHalf * i + h.x + rows[i] * (int)rank;
+            all += rows[i];
+          }
           const uint32_t bar = xfull_even + 8 * s;
           if (rank == 0) {
-            mbar_arrive_expect_tx(&xfull[s], (uint32_t)((BM + n0 + n1) * 4 * p.r_pad));
+            mbar_arrive_expect_tx(&xfull[s], (uint32_t)((BM + all) * 4 * p.r_pad));
             mbar_arrive(&xfull[s1]);
           }
           uint8_t* b = smem + s * X_BYTES;
           tma_load_3d_pair(b, &map_b, bar, 0, w0, run.adapter);
           tma_load_3d_pair(b + 128 * p.r_pad, &map_b, bar, 0, w0 + 64, run.adapter);
           uint8_t* pr = smem + s1 * X_BYTES;
-          for (int k = 0; k < n0; k += 16)
-            tma_load_2d_pair(pr + k * 2 * p.r_pad, &map_p, bar, 0, t0 + h0.x + n0 * (int)rank + k);
-          pr += 64 * 2 * p.r_pad;
-          for (int k = 0; k < n1; k += 16)
-            tma_load_2d_pair(pr + k * 2 * p.r_pad, &map_p, bar, 0, t0 + p.n0 + h1.x + n1 * (int)rank + k);
+#pragma unroll
+          for (int i = 0; i < PARTS; ++i)
+            for (int k = 0; k < rows[i]; k += 16)
+              tma_load_2d_pair(pr + (64 * i + k) * 2 * p.r_pad, &map_p, bar, 0, first[i] + k);
           issued_next();
           issued_next();
         }
@@ -398,15 +415,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1 || warp == 2) {
+  } else if (warp == 1 || warp == 2 || warp == kThirdWarp) {
     // ------------------------------------------------ UMMA issuers (even CTA, one elected lane each)
-    const int h = warp == 1 ? 0 : 1;
-    if (rank == 0 && h < halves && elect_one_sync()) {
-      const uint32_t idesc = make_idesc_bf16(256, h ? p.n1 : p.n0, false, false);
+    const int h = warp == kThirdWarp ? 2 : warp - 1;  // its part
+    if (rank == 0 && h < parts && elect_one_sync()) {
+      const int rows = h == 0 ? p.n[0] : h == 1 ? p.n[1] : p.n[2];
+      const uint32_t idesc = make_idesc_bf16(256, rows, false, false);
       const uint32_t lswz = swz_for_row_bytes(2 * p.r_pad);
       const uint32_t x_u = smem_u32(smem);
-      const uint64_t xdesc0 = make_sdesc(x_u + h * (X_BYTES / 2), 16, 1024, kSw128);
-      uint32_t sx = 0, phx = 0, g = 0, pha = 0, hs = h;  // ring slot, decode group, accumulator half used
+      const uint64_t xdesc0 = make_sdesc(x_u + h * kPartBytes, 16, 1024, kSw128);
+      uint32_t sx = 0, phx = 0, g = 0, pha = 0, hs = h;  // ring slot, decode group, accumulator part used
       bool ok = true;
       auto next_x = [&]() {
         if (++sx == SA) {
@@ -415,9 +433,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
         }
       };
       auto wait_x = [&]() -> bool { return mbar_wait_cluster(&xfull[sx], phx, ctl, p.err, p.timeout_ns, 223); };
-      for (int u = pair; u < n_units && ok; u += n_pairs, hs += halves) {
+      for (int u = pair; u < n_units && ok; u += n_pairs, hs += parts) {
         const uint32_t slot = hs % kSlots, d = tmem + slot * kHalf;
-        AdapterRun run(granules, u / p.n_mt * unit_rows, rows_used, unit_rows, p.n);
+        Run run(granules, u / p.n_mt * unit_rows, rows_used, unit_rows, p.n_adapters);
         if (!(ok = mbar_wait_cluster(&accempty[slot], ((hs / kSlots) & 1) ^ 1, ctl, p.err, p.timeout_ns, 220))) break;
         tc_fence_after();
         for (int kc = 0; kc < kchunks; ++kc) {
@@ -438,13 +456,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
           }
         }
         if (!ok) break;
-        // One K = r product per adapter, at the adapter's columns of this half.
+        // One K = r product per adapter, at the adapter's columns of this part.
         while (run.next()) {
           if (!(ok = wait_x())) break;
           tc_fence_after();
           const uint32_t sx1 = (sx + 1 == SA) ? 0 : sx + 1;
           const uint32_t b_u = x_u + sx * X_BYTES, p_u = x_u + sx1 * X_BYTES + h * 128 * p.r_pad;
-          const int2 hr = half_range(run, h, p.n0, p.n1);
+          const int2 hr = part_range(run, h, rows);
           if (hr.y > hr.x) {
             const uint32_t id = make_idesc_bf16(256, hr.y - hr.x, false, false);
             for (int ks = 0; ks < p.r_pad / 16; ++ks)
@@ -526,7 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
           mbar_arrive(&adone[grp]);
       }
     }
-  } else if (warp >= kEpiWarp0) {
+  } else if (warp >= kEpiWarp0) {  // (the third issuer is taken above)
     // ------------------------------------------------ epilogue: 32 rows of W x the token rows
     // A lane holds a row of W; 32 token rows at a time pass through shared memory so that a store writes 64
     // contiguous bytes of each of eight tokens.
@@ -539,15 +557,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
       const int t0 = u / p.n_mt * unit_rows, w0 = (u % p.n_mt) * 256 + (int)rank * BM + 32 * qrt;
       const int col = w0 + 8 * (lane & 3);
       // the tokens of the unit's rows, 32 in a register across the warp
-      int toks[AdapterRun::kMost];
+      int toks[4 * PARTS];
 #pragma unroll
-      for (int i = 0; i < AdapterRun::kMost; ++i) {
+      for (int i = 0; i < 4 * PARTS; ++i) {
         const int row = t0 + 32 * i;
         toks[i] = 32 * i < unit_rows && row < rows_used ? __ldg(p.order + row + lane) : p.T;
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (h == halves) break;
+      for (int h = 0; h < PARTS; ++h) {
+        if (h == parts) break;
         const uint32_t b = hs % kSlots;
         ok = __all_sync(kFull, mbar_wait(&accfull[b], (hs / kSlots) & 1, ctl, p.err, p.timeout_ns, 240));
         if (!ok) break;
@@ -555,9 +573,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::kThreads, 1)
         const uint32_t tl = tmem + b * kHalf + ((uint32_t)(qrt * 32) << 16);
 #pragma unroll
         for (int j = 0; j < kHalf / 32; ++j) {
-          // (a second half follows a full first one)
+          // (a part follows full ones)
           const int jj = 32 * j, tok = toks[h * (kHalf / 32) + j];
-          if (jj >= (h ? p.n1 : p.n0)) break;
+          if (jj >= p.n[h]) break;
           if (!__any_sync(kFull, tok < p.T)) continue;
           float v[32];
           tmem_ld32(tl + jj, v);
@@ -760,7 +778,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
       for (int u = pair; u < n_units && ok; u += n_pairs) {
         const int mu = u / p.n_nt, c0 = (u % p.n_nt) * kCols + (int)rank * 64 * NB;
         const int row0 = mu * kAdapterUnitRows + (int)rank * BM;
-        AdapterRun run(granules, mu * kAdapterUnitRows, rows_used, kAdapterUnitRows, p.n);
+        AdapterRun<8> run(granules, mu * kAdapterUnitRows, rows_used, kAdapterUnitRows, p.n);
         for (int kc = 0; kc < kchunks; ++kc) {
           if (!(ok = mbar_wait(&aempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 312))) break;
           if (rank == 0) mbar_arrive_expect_tx(&xfull[s], (uint32_t)(2 * A_BYTES));
@@ -815,7 +833,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
       auto wait_a = [&]() -> bool { return mbar_wait_cluster(&xfull[sa], pha, ctl, p.err, p.timeout_ns, 323); };
       for (int u = pair; u < n_units && ok; u += n_pairs, ++ti) {
         const int mu = u / p.n_nt;
-        AdapterRun run(granules, mu * kAdapterUnitRows, rows_used, kAdapterUnitRows, p.n);
+        AdapterRun<8> run(granules, mu * kAdapterUnitRows, rows_used, kAdapterUnitRows, p.n);
         const uint32_t b = ti & 1, use = ti >> 1;
         const uint32_t d = tmem + b * 256;
         if (!(ok = mbar_wait_cluster(&accempty[b], (use & 1) ^ 1, ctl, p.err, p.timeout_ns, 320))) break;
@@ -1597,14 +1615,15 @@ cudaError_t map_u8_2d(CUtensorMap* m, const void* base, uint64_t bytes, uint64_t
 }  // namespace
 
 // Token rows of a forward unit: the ones that take the pairs the least time.  Measured cycles a 64-wide chunk: 680 up
-// to 128 rows (decoding it), 790 with 160, 840 with 256.
+// to 128 rows (decoding it), 790 with 160, 840 with 256, 1400 with 384.
 static int fwd_unit_rows(const AdapterProjHost& h, int n_mt, int pairs) {
   const int64_t rows = h.T + 16 * (int64_t)(h.T < h.n + 1 ? h.T : h.n + 1);  // with an average of padding
   int best = 256;
   int64_t best_cost = INT64_MAX;
-  for (int nt = 256; nt >= 96; nt -= 32) {
+  for (int nt = 384; nt >= 96; nt -= 32) {
     const int64_t turns = ((rows + nt - 1) / nt * n_mt + pairs - 1) / pairs;
-    const int64_t cost = turns * (nt > 128 ? 707 + 13 * nt / 25 : 680);
+    if (nt > 256 && turns > 1) continue;  // all three accumulator slots: nothing left for a next unit
+    const int64_t cost = turns * (nt > 256 ? 1400 : nt > 128 ? 707 + 13 * nt / 25 : 680);
     if (cost < best_cost) {
       best = nt;
       best_cost = cost;
@@ -1619,15 +1638,17 @@ cudaError_t launch_adapter_fwd(const AdapterProjHost& h, const uint16_t* rows, c
   const CUtensorMapSwizzle rswz = swizzle_for_bytes(2 * rp);
   const int n_mt = (h.N + 255) / 256, unit_rows = fwd_unit_rows(h, n_mt, num_sms / 2);
   AdapterFwdParams p;
-  p.n0 = unit_rows < adf::kHalf ? unit_rows : adf::kHalf;
-  p.n1 = unit_rows - p.n0;
+  int last = 0;
+  for (int i = 0; i < 3; ++i) {
+    const int left = unit_rows - i * adf::kHalf;
+    p.n[i] = left <= 0 ? 0 : (left < adf::kHalf ? left : adf::kHalf);
+    if (p.n[i]) last = p.n[i];
+  }
   CUtensorMap mx0, mx1, mraw, mp, mb;
   cudaError_t err;
-  if ((err = map_bf16_2d(&mx0, rows, h.K, h.rows_cap, 64, p.n0 / 2, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess)
+  if ((err = map_bf16_2d(&mx0, rows, h.K, h.rows_cap, 64, p.n[0] / 2, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess)
     return err;
-  mx1 = mx0;
-  if (p.n1 &&
-      (err = map_bf16_2d(&mx1, rows, h.K, h.rows_cap, 64, p.n1 / 2, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess)
+  if ((err = map_bf16_2d(&mx1, rows, h.K, h.rows_cap, 64, last / 2, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess)
     return err;
   if ((err = map_u8_2d(&mraw, h.nf4, h.K / 2, h.N, 32, 128)) != cudaSuccess) return err;
   if ((err = map_bf16_2d(&mp, low, h.r, h.rows_cap, rp, 16, rswz)) != cudaSuccess) return err;
@@ -1642,12 +1663,13 @@ cudaError_t launch_adapter_fwd(const AdapterProjHost& h, const uint16_t* rows, c
   p.N = h.N;
   p.T = h.T;
   p.r_pad = rp;
-  p.n = h.n;
+  p.n_adapters = h.n;
   p.n_mt = n_mt;
   const int64_t units = (h.rows_cap + unit_rows - 1) / unit_rows * n_mt;
   const int grid = 2 * (int)(units < num_sms / 2 ? units : num_sms / 2);
   LaunchScope scope("adapter_fwd", stream);
-  return launch_tiles(adapter_fwd_kernel, grid, adf::kThreads, adf::SMEM_BYTES, 0, stream, mx0, mx1, mraw, mp, mb, p);
+  return launch_tiles(p.n[2] ? adapter_fwd_kernel<3> : adapter_fwd_kernel<2>, grid, adf::threads(p.n[2] ? 3 : 2),
+                      adf::SMEM_BYTES, 0, stream, mx0, mx1, mraw, mp, mb, p);
 }
 
 cudaError_t launch_adapter_dgrad(const AdapterProjHost& h, const uint16_t* rows, const uint16_t* low,

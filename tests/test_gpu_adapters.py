@@ -335,6 +335,16 @@ def test_a_chain_of_launches_under_one_another(T):
         assert torch.equal(y, want)
 
 
+def test_more_padding_than_the_unit_was_chosen_for():
+    # three groups of 97 tokens take 353 rows where 339 were expected: units of 352 rows, the last one alone in its own
+    c = Case(291, 128, 16384, 2, 16, "runs", seed=80)
+    ids = torch.arange(291) % 3
+    ids[ids == 2] = -1
+    c.ids = ids.to(torch.int32).cuda()
+    y, tol, _ = bounds(c)
+    check(serve(c).y, y, tol, "y")
+
+
 def test_calls_on_several_streams_at_once():
     # each with an object of its own: blocks that wait inside one launch wait only for earlier blocks of it
     cases = [Case(T, 1024, 2048, 8, 16, "zipf", seed=20 + i) for i, T in enumerate((3, 16, 60, 200, 256, 300))]
@@ -456,6 +466,9 @@ def test_what_a_serving_call_launches(shape, kernels):
     (9, 4096, 4096, 3, 24, "zipf"), (30, 512, 8200, 5, 16, "zipf"), (30, 2048, 1024, 30, 64, "each"),
     (250, 1024, 2056, 40, 64, "zipf"), (120, 4096, 264, 3, 32, "runs"), (12, 1024, 4104, 12, 40, "each"),
     (400, 2048, 4096, 4, 16, "runs"), (700, 512, 12800, 6, 8, "zipf"),
+    # units of three parts, the third of 64 to 128 rows, ranks padded and not, an adapter over all of them, none at all
+    (1111, 256, 4096, 8, 16, "runs"), (260, 128, 16384, 1, 64, "one"), (262, 192, 18000, 2, 24, "zipf"),
+    (300, 320, 16384, 2, 40, "runs"), (340, 128, 16392, 1, 8, "zipf"), (270, 64, 16384, 2, 8, "none"),
     # p in a launch of its own
     (256, 4096, 4096, 32, 32, "zipf"), (200, 2048, 18952, 100, 64, "each"),
 ], ids=lambda s: "-".join(map(str, s)))
