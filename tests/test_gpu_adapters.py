@@ -335,6 +335,24 @@ def test_a_chain_of_launches_under_one_another(T):
         assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("shape", [(5, 512, 264, 6, 16), (60, 512, 264, 6, 16), (256, 4096, 4096, 32, 32),
+                                   (300, 512, 264, 6, 16)], ids=lambda s: "-".join(map(str, s)))
+def test_inputs_written_between_calls(shape):
+    # the same buffers filled with another batch ahead of each call, on the stream: each call sees its own batch, its
+    # own adapters and its own matrix
+    batches = [Case(*shape, "zipf", seed=90 + i) for i in range(4)]
+    want = [serve(b).y.clone() for b in batches]
+    c = Case(*shape, "zipf", seed=90)
+    pj, base, ad = e4b.Projection(c.dims, c.T, train=False), c.base(), c.adapters()
+    for i in (1, 3, 0, 2, 2, 1, 0, 3):
+        b = batches[i]
+        for name in ("ids", "x", "nf4", "absmax", "A", "B", "scale"):
+            getattr(c, name).copy_(getattr(b, name))
+        pj.e4b_multi_lora_serve_fwd(c.ids, c.x, base, ad)
+        pj.e4b_multi_lora_serve_fwd(c.ids, c.x, base, ad)
+        assert torch.equal(pj.y, want[i])
+
+
 def test_more_padding_than_the_unit_was_chosen_for():
     # three groups of 97 tokens take 353 rows where 339 were expected: units of 352 rows, the last one alone in its own
     c = Case(291, 128, 16384, 2, 16, "runs", seed=80)
