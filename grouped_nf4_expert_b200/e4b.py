@@ -536,13 +536,14 @@ def _cuda_device(device):
     return dev if dev.index is not None else torch.device("cuda", torch.cuda.current_device())
 
 
-def _alloc(shape, dtype, device):
-    """Zeroed tensor of ``shape`` whose address is valid (and 16-byte aligned) even when it is empty."""
+def _alloc(shape, dtype, device, zero=True):
+    """Zeroed tensor of ``shape`` whose address is valid (and 16-byte aligned) even when it is empty; with ``zero``
+    false its values are left as they come, for what a call writes whole."""
     import torch
     n = 1
     for d in shape:
         n *= d
-    return torch.zeros(max(n, 8), dtype=dtype, device=device)[:n].view(*shape)
+    return (torch.zeros if zero else torch.empty)(max(n, 8), dtype=dtype, device=device)[:n].view(*shape)
 
 
 class _OnDevice:
@@ -631,8 +632,8 @@ class Projection(_OnDevice):
         dev = self._on(device)
         n, r, R = dims.n_adapters, dims.r, sz.rows_cap
         bf, i32 = torch.bfloat16, torch.int32
-        self.y = _alloc((T, dims.N), bf, dev)
-        self.ws = _alloc((int(max(sz.workspace_bytes, sz.serve_workspace_bytes)),), torch.uint8, dev)
+        self.y = _alloc((T, dims.N), bf, dev, zero=False)
+        self.ws = _alloc((int(max(sz.workspace_bytes, sz.serve_workspace_bytes)),), torch.uint8, dev, zero=False)
         self._dims_c = dims.c()
         self._dims_p = ctypes.addressof(self._dims_c)
         self._base_need = {"nf4": dims.N * dims.K // 2, "absmax": dims.N * dims.K // 64}
@@ -642,7 +643,7 @@ class Projection(_OnDevice):
             self.order, self.offsets = _alloc((R,), i32, dev), _alloc((n + 2,), i32, dev)
             self.steps = _alloc((sz.steps_cap,), i32, dev)
             self.p, self.q = _alloc((R, r), bf, dev), _alloc((R, r), bf, dev)
-            self.dx = _alloc((T, dims.K), bf, dev)
+            self.dx = _alloc((T, dims.K), bf, dev, zero=False)
             # the two gradients are views of one flat buffer (one collective in a data-parallel step)
             na, nb = n * r * dims.K, n * dims.N * r
             self.lora_grads = _alloc((na + nb,), bf, dev)
@@ -743,7 +744,7 @@ class RouterBalance(_OnDevice):
         self._tokens = _alloc((S + 2,), i32, dev)
         self.tokens = self._tokens[:S]
         self.lse, self.loss = _alloc((T,), f32, dev), _alloc((3,), f32, dev)
-        self.ws = _alloc((ws_bytes,), torch.uint8, dev)
+        self.ws = _alloc((ws_bytes,), torch.uint8, dev, zero=False)
         self._stats = BalanceStats(*(_ptr(t) for t in (self.counts, self.prob_sum, self._tokens, self.lse)))
         self._stats_p = ctypes.addressof(self._stats)
         self._loss_p, self._ws_p, self._ws_n = _ptr(self.loss), _ptr(self.ws), self.ws.numel()

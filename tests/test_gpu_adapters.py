@@ -335,6 +335,26 @@ def test_a_chain_of_launches_under_one_another(T):
         assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("T,n", [(7, 3), (60, 5), (300, 5), (700, 40)])
+def test_what_a_workspace_held_does_not_matter(T, n):
+    # a workspace full of NaN behind its header
+    c = Case(T, 320, 264, n, 24, "zipf", seed=95)
+    want, want_t = serve(c).y.clone(), train(c)
+    pj = e4b.Projection(c.dims, c.T)
+    pj.ws[256:].fill_(0xff)
+    pj.e4b_multi_lora_serve_fwd(c.ids, c.x, c.base(), c.adapters())
+    assert torch.equal(pj.y, want)
+    for t in (pj.p, pj.q):
+        t.fill_(float("nan"))
+    pj.ws[256:].fill_(0xff)
+    pj.e4b_adapter_group(c.ids)
+    pj.e4b_multi_lora_fwd(c.x, c.base(), c.adapters())
+    pj.e4b_multi_lora_dgrad(c.dY, c.base(), c.adapters())
+    pj.e4b_multi_lora_wgrad(c.x, c.dY)
+    for k in ("y", "dx", "dA", "dB"):
+        assert torch.equal(getattr(pj, k), getattr(want_t, k)), k
+
+
 @pytest.mark.parametrize("shape", [(5, 512, 264, 6, 16), (60, 512, 264, 6, 16), (256, 4096, 4096, 32, 32),
                                    (300, 512, 264, 6, 16)], ids=lambda s: "-".join(map(str, s)))
 def test_inputs_written_between_calls(shape):

@@ -281,3 +281,13 @@ def test_what_a_call_launches():
     finally:
         e4b.e4b_profiler_enable(False)
     assert {k: n for k, (n, _) in e4b.e4b_profiler_read().items()} == {"balance_fwd": 1, "balance_bwd": 1}
+
+
+def test_what_a_workspace_held_does_not_matter():
+    logits, ids, seq, mask = make(700, 60, 4, 5, 0.9)
+    w, wd = run(60, 4, logits, ids, seq, mask)
+    b, d = e4b.RouterBalance(60, 4, 700, 5), torch.empty_like(logits)
+    b.ws[256:].fill_(0xff)
+    b.e4b_balance_fwd(logits, ids, seq, mask, 0.7, 0.3)
+    b.e4b_balance_bwd(logits, d, seq, mask, 0.7, 0.3)
+    assert torch.equal(b.loss, w.loss) and torch.equal(b.counts, w.counts) and torch.equal(d, wd)
