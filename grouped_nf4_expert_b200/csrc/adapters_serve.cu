@@ -728,8 +728,8 @@ __global__ void __launch_bounds__(ads::kThreadsSplit + 128, 1)  // 96 registers:
     if (!ctl->pad) return;
     if (tid == 0) leave(p.err, (int)gridDim.x - p.p_blocks);
   }
-  // The adapters' part: item = (tile of 8 tokens of one adapter, group of 16 rows), fragments of B and p
-  // fetched two items ahead.
+  // The adapters' part: item = (tile of 8 tokens of one adapter, group of 16 rows), several items' fragments of B and p
+  // fetched together.
   {
     constexpr int kGroupsOf16 = kRows / 16, kItemWarps = kThreadsSplit / 32, kC = WIDE ? 2 : 1;
     const int g = lane >> 2, q = lane & 3;
@@ -753,23 +753,28 @@ __global__ void __launch_bounds__(ads::kThreadsSplit + 128, 1)  // 96 registers:
       }
       return w;
     };
-    Low w0 = fetch(warp), w1 = fetch(warp + kItemWarps);
-    for (int item = warp; item < items; item += kItemWarps) {
-      const Low w2 = fetch(item + 2 * kItemWarps);
-      const int tile = item / kGroupsOf16, lrow = 16 * (item % kGroupsOf16);
-      const int t0 = tile_tok[tile * kTokenTile + 2 * q], t1 = tile_tok[tile * kTokenTile + 2 * q + 1];
-      float* c0 = part + (t0 < 0 ? 0 : t0) * kPitch + lrow + g;
-      float* c1 = part + (t1 < 0 ? 0 : t1) * kPitch + lrow + g;
-      float d[4] = {c0[0], c1[0], c0[8], c1[8]};
+    constexpr int kAtOnce = WIDE ? 2 : 4;
+    for (int first = warp; first < items; first += kAtOnce * kItemWarps) {
+      Low w[kAtOnce];
 #pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        mma_bf16(d, w0.b0[c].x, w0.b1[c].x, w0.b0[c].y, w0.b1[c].y, w0.p[c].x, w0.p[c].y);
-        mma_bf16(d, w0.b0[c].z, w0.b1[c].z, w0.b0[c].w, w0.b1[c].w, w0.p[c].z, w0.p[c].w);
+      for (int i = 0; i < kAtOnce; ++i) w[i] = fetch(first + i * kItemWarps);
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int item = first + i * kItemWarps;
+        if (item >= items) break;
+        const int tile = item / kGroupsOf16, lrow = 16 * (item % kGroupsOf16);
+        const int t0 = tile_tok[tile * kTokenTile + 2 * q], t1 = tile_tok[tile * kTokenTile + 2 * q + 1];
+        float* c0 = part + (t0 < 0 ? 0 : t0) * kPitch + lrow + g;
+        float* c1 = part + (t1 < 0 ? 0 : t1) * kPitch + lrow + g;
+        float d[4] = {c0[0], c1[0], c0[8], c1[8]};
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+          mma_bf16(d, w[i].b0[c].x, w[i].b1[c].x, w[i].b0[c].y, w[i].b1[c].y, w[i].p[c].x, w[i].p[c].y);
+          mma_bf16(d, w[i].b0[c].z, w[i].b1[c].z, w[i].b0[c].w, w[i].b1[c].w, w[i].p[c].z, w[i].p[c].w);
+        }
+        if (t0 >= 0) c0[0] = d[0], c0[8] = d[2];
+        if (t1 >= 0) c1[0] = d[1], c1[8] = d[3];
       }
-      if (t0 >= 0) c0[0] = d[0], c0[8] = d[2];
-      if (t1 >= 0) c1[0] = d[1], c1[8] = d[3];
-      w0 = w1;
-      w1 = w2;
     }
   }
   __syncthreads();
