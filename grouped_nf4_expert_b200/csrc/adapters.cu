@@ -16,11 +16,11 @@ constexpr uint32_t kFull = 0xffffffffu;
 // Grouping: a stable counting sort of the tokens by adapter in one block.
 // Every warp owns a contiguous run of tokens and a histogram row of its own in
 // shared memory; to place the tokens, lanes with equal ids find one another with a
-// warp match, so that the order is fixed.  Two passes
-// over the ids (count, place) around one scan over the adapters, thread a owning
-// adapter a.  Latency bounds it (one read of the ids and a dozen block-wide
-// steps; 777 tokens of 16 adapters 5 us, 8192 of 64 10 us), so the scan's sums go
-// through one barrier and the histogram is read once, all warps' rows at a time.
+// warp match, so that the order is fixed.  Two passes over the ids (count, place)
+// around one scan over the adapters, thread a owning adapter a.  Latency bounds it
+// (one read of the ids and a dozen block-wide steps; 777 tokens of 16 adapters 5 us,
+// 8192 of 64 10 us), so the scan's sums go through one barrier and the histogram is
+// read once, all warps' rows at a time.
 // ----------------------------------------------------------------------------
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupWarps = kGroupThreads / 32;
@@ -135,7 +135,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
     }
     return lo;
   };
-  for (int i = tid; i < none0 / kAdapterRowAlign; i += kGroupThreads) granules[i] = owner(first_row, i * kAdapterRowAlign);
+  for (int i = tid; i < none0 / kAdapterRowAlign; i += kGroupThreads)
+    granules[i] = owner(first_row, i * kAdapterRowAlign);
   for (int i = tid; i < adapter_tasks; i += kGroupThreads) {
     const int a = owner(first_task, i);
     tasks[i] = make_int4(a, first_row[a] + (i - first_task[a]) * kAdapterTaskRows, first_row[a + 1], 0);

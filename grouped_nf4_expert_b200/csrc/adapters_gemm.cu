@@ -2,7 +2,7 @@
 // 5th-generation tensor cores:
 //
 //  * adapter_fwd_kernel, adapter_dgrad_kernel: persistent CTA pairs, 256 token
-//    rows x 256 outputs per work unit (cta_group::2 UMMAs): the base product with
+//    rows (forward: up to 384) x 256 outputs per work unit (cta_group::2 UMMAs): the base product with
 //    the NF4 matrix decoded on the way, then one K = r step per adapter with rows
 //    in the tile, written to that adapter's rows only.
 //  * adapter_proj_kernel: p = s x A^T and q = s dY B, 128 rows of one adapter

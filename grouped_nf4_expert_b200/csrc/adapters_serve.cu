@@ -139,11 +139,11 @@ __device__ __forceinline__ void low_rank_tile(const uint16_t* x, const uint16_t*
 // ----------------------------------------------------------------------------
 // Blocks stay for several units of rows, the next unit's codes in flight while one
 // ends and p read once: 4096 -> 14336, 1 token 22.6 us (a block a unit: 24.6 us), 8
-// tokens 26.7 us (30.2 us).  1 token at 2048 -> 4096 takes 8.2 us alone and 5.9
-// us after another, the chain of loads and waits; on the large matrix the byte permutes of the decoding fill their
-// pipe for 13 us and what is left is between the steps.  Decoding by a table of byte
-// pairs in shared memory instead: 20.4 us at 1 token, but 32.8 us at 8, whose rows
-// of x come through the same pipe.
+// tokens 26.7 us (30.2 us).  1 token at 2048 -> 4096 takes 8.2 us alone and 5.9 us
+// after another, the chain of loads and waits; on the large matrix the byte permutes
+// of the decoding fill their pipe for 13 us and what is left is between the steps.
+// Decoding by a table of byte pairs in shared memory instead: 20.4 us at 1 token, but
+// 32.8 us at 8, whose rows of x come through the same pipe.
 // The blocks of p take (token, 16 ranks, share of K) each; with few of them K is
 // split (kq shares, added in order by the readers), since one block's loads
 // would be the longest chain of the launch.
@@ -339,21 +339,21 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvPar
 // y for up to 256 tokens: 128 rows of W x all tokens x a share of K per block
 // ----------------------------------------------------------------------------
 // After the blocks of p (or under a launch of p of its own): warp 0 loads x tiles
-// (TMA), warp 1 owns tensor memory and issues the UMMAs, warp 2 sorts the tokens into tiles of eight of one adapter, warps 4-15 are
-// three decode teams that take the k-chunks round robin: a thread owns a row of
-// W, reads 32 bytes of codes and a scale a chunk straight into registers two of
-// its chunks ahead, and writes the decoded row to the A buffer in tensor
-// memory.  Each of the cluster's S blocks then owns 128 / S of the rows: the
-// partial sums are stored into their owners' shared memory (over the x tiles;
-// reading them from there instead took 4.7 us at 256 tokens, one round trip
-// after another), added, and the adapters' part is added in the fragment
-// layout of the warp instruction, tile by tile, so that no adapter's values
-// meet another's tokens.  256 tokens, 4096 -> 4096, 32 adapters of rank 32: 24 us,
-// bound by the L2 reads of x (64 KB/us a block; all of x for every 128 rows of W,
-// 64 MB) and the exchange of shares; 57 tokens, 2048 -> 512: 11 us, the chain p,
-// hand-over, join; 64 tokens, 4096 -> 14336, 16 adapters: 29 us, the ALU pipe (the
-// decode's byte permutes) 95% busy in the loop.  A fourth team, or coalesced code
-// loads, change nothing there; a quarter of the words by a table of byte pairs
+// (TMA), warp 1 owns tensor memory and issues the UMMAs, warp 2 sorts the tokens
+// into tiles of eight of one adapter, warps 4-15 are three decode teams that take
+// the k-chunks round robin: a thread owns a row of W, reads 32 bytes of codes and a
+// scale a chunk straight into registers two of its chunks ahead, and writes the
+// decoded row to the A buffer in tensor memory.  Each of the cluster's S blocks then
+// owns 128 / S of the rows: the partial sums are stored into their owners' shared
+// memory (over the x tiles; reading them from there instead took 4.7 us at 256
+// tokens, one round trip after another), added, and the adapters' part is added in
+// the fragment layout of the warp instruction, tile by tile, so that no adapter's
+// values meet another's tokens.  256 tokens, 4096 -> 4096, 32 adapters of rank 32:
+// 24 us, bound by the L2 reads of x (64 KB/us a block; all of x for every 128 rows
+// of W, 64 MB) and the exchange of shares; 57 tokens, 2048 -> 512: 11 us, the chain
+// p, hand-over, join; 64 tokens, 4096 -> 14336, 16 adapters: 29 us, the ALU pipe
+// (the decode's byte permutes) 95% busy in the loop.  A fourth team, or coalesced
+// code loads, change nothing there; a quarter of the words by a table of byte pairs
 // gains 4%.
 namespace ads {
 constexpr int BM = 128, BK = 64;

@@ -68,8 +68,8 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 
 // exp(x) for x up to 0: the exponential of 2 of x log2(e), three operations a value where expf has about nine (131072
-// tokens of 64 experts, both directions: expf 34.9 us, this 29.5 us).  Relative error (1.3 |x| + 4) 2^-24: the product's rounding and the
-// constant's, and the instruction's.  -inf gives 0; probabilities below 2^-126 are 0.
+// tokens of 64 experts, both directions: expf 34.9 us, this 29.5 us).  Relative error (1.3 |x| + 4) 2^-24: the
+// product's rounding and the constant's, and the instruction's.  -inf gives 0; probabilities below 2^-126 are 0.
 __device__ __forceinline__ float exp_of(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));

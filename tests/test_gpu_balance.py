@@ -91,7 +91,8 @@ def compare(b, d, want, E, k, logits, cb=0.7, cz=0.3, up=1.0):
             if lse[t] == -np.inf:
                 continue
             p = np.exp(l64[t] - lse[t])
-            bound[t] = p * (cb / (n_seq * n_s[s]) * (f + p @ f) + 2 * cz / n * abs(lse[t])) * (2 * r + (abs(lse[t]) + E + 16) * H)
+            bound[t] = p * (cb / (n_seq * n_s[s]) * (f + p @ f) + 2 * cz / n * abs(lse[t]))
+            bound[t] *= 2 * r + (abs(lse[t]) + E + 16) * H
             bound[t] += p * 2 * cz / n * (abs(lse[t]) * H + r)  # the error of lse itself
     assert np.all(np.abs(g - up * grad) <= up * bound * 1.01 + 1e-37), np.abs(g - up * grad).max()
 
