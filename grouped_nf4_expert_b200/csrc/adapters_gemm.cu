@@ -321,6 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::threads(PARTS),
   const int kchunks = p.K / BK;
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   const int32_t* granules = p.steps + kAdapterStepsHeader;
+  const bool pack = p.r_pad <= 32;  // both halves of the low-rank rows in one slot
 
   if (warp == 0) {
     // ------------------------------------------------ NF4 codes: 128 rows x 32 bytes a chunk (one lane)
@@ -345,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::threads(PARTS),
   } else if (warp == 3) {
     // ------------------------------------------------ token rows, then a unit's low-rank operands (one lane)
     // This CTA's rows of a part: 64 of its 128 (of an adapter's columns: half of them).  A low-rank use is
-    // two slots: the adapter's 128 rows of B, then its p rows of every part.
+    // two slots, the adapter's 128 rows of B, then both halves of its p rows of every part, or (64 ranks) three.
     if (lane == 0) {
       tma_prefetch_desc(&map_x0);
       tma_prefetch_desc(&map_p);
@@ -380,8 +381,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::threads(PARTS),
         if (!ok) break;
         while (run.next()) {
           const uint32_t s1 = (s + 1 == SA) ? 0 : s + 1, ph1 = (s + 1 == SA) ? ph ^ 1 : ph;
+          const uint32_t s2 = (s1 + 1 == SA) ? 0 : s1 + 1, ph2 = (s1 + 1 == SA) ? ph1 ^ 1 : ph1;
           if (!(ok = mbar_wait(&xempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 210))) break;
           if (!(ok = mbar_wait(&xempty[s1], ph1 ^ 1, ctl, p.err, p.timeout_ns, 210))) break;
+          if (!pack && !(ok = mbar_wait(&xempty[s2], ph2 ^ 1, ctl, p.err, p.timeout_ns, 210))) break;
           int rows[PARTS], first[PARTS], all = 0;  // this CTA's p rows of each part, multiples of 16
 #pragma unroll
           for (int i = 0; i < PARTS; ++i) {
@@ -392,19 +395,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::threads(PARTS),
           }
           const uint32_t bar = xfull_even + 8 * s;
           if (rank == 0) {
-            mbar_arrive_expect_tx(&xfull[s], (uint32_t)((BM + all) * 4 * p.r_pad));
+            mbar_arrive_expect_tx(&xfull[s], (uint32_t)((BM + 2 * all) * 4 * p.r_pad));
             mbar_arrive(&xfull[s1]);
+            if (!pack) mbar_arrive(&xfull[s2]);
           }
           uint8_t* b = smem + s * X_BYTES;
           tma_load_3d_pair(b, &map_b, bar, 0, w0, run.adapter);
           tma_load_3d_pair(b + 128 * p.r_pad, &map_b, bar, 0, w0 + 64, run.adapter);
-          uint8_t* pr = smem + s1 * X_BYTES;
+          uint8_t* high = smem + s1 * X_BYTES;
+          uint8_t* low = pack ? high + X_BYTES / 2 : smem + s2 * X_BYTES;
 #pragma unroll
           for (int i = 0; i < PARTS; ++i)
-            for (int k = 0; k < rows[i]; k += 16)
-              tma_load_2d_pair(pr + (64 * i + k) * 2 * p.r_pad, &map_p, bar, 0, first[i] + k);
+            for (int k = 0; k < rows[i]; k += 16) {
+              const int at = (64 * i + k) * 2 * p.r_pad;
+              tma_load_3d_pair(high + at, &map_p, bar, 0, 0, first[i] + k);
+              tma_load_3d_pair(low + at, &map_p, bar, 0, 1, first[i] + k);
+            }
           issued_next();
           issued_next();
+          if (!pack) issued_next();
         }
       }
       // (After a wait ran out: copies of either CTA may be in flight; they are given time to land.)
@@ -460,19 +469,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::threads(PARTS),
         while (run.next()) {
           if (!(ok = wait_x())) break;
           tc_fence_after();
-          const uint32_t sx1 = (sx + 1 == SA) ? 0 : sx + 1;
-          const uint32_t b_u = x_u + sx * X_BYTES, p_u = x_u + sx1 * X_BYTES + h * 128 * p.r_pad;
+          const uint32_t sx1 = (sx + 1 == SA) ? 0 : sx + 1, sx2 = (sx1 + 1 == SA) ? 0 : sx1 + 1;
+          const uint32_t b_u = x_u + sx * X_BYTES, part = x_u + h * 128 * p.r_pad;
+          const uint32_t p_u[2] = {part + sx1 * X_BYTES, part + (pack ? sx1 * X_BYTES + X_BYTES / 2 : sx2 * X_BYTES)};
           const int2 hr = part_range(run, h, rows);
           if (hr.y > hr.x) {
             const uint32_t id = make_idesc_bf16(256, hr.y - hr.x, false, false);
             for (int ks = 0; ks < p.r_pad / 16; ++ks)
-              umma_bf16_2sm(d + hr.x, make_sdesc(b_u + 32 * ks, 16, 16 * p.r_pad, lswz),
-                            make_sdesc(p_u + 32 * ks, 16, 16 * p.r_pad, lswz), id, 1u);
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                umma_bf16_2sm(d + hr.x, make_sdesc(b_u + 32 * ks, 16, 16 * p.r_pad, lswz),
+                              make_sdesc(p_u[i] + 32 * ks, 16, 16 * p.r_pad, lswz), id, 1u);
           }
           umma_commit_2sm(&xempty[sx], 0x3);
           umma_commit_2sm(&xempty[sx1], 0x3);
+          if (!pack) umma_commit_2sm(&xempty[sx2], 0x3);
           next_x();
           next_x();
+          if (!pack) next_x();
         }
         if (!ok) break;
         umma_commit_2sm(&accfull[slot], 0x3);
@@ -628,8 +642,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::threads(PARTS),
 // activation tiles and low-rank operands, warps 4-19 decode groups taking the
 // k-chunks round robin, warps 20-23 epilogue; operands of both CTAs are
 // counted on the even CTA's barriers, as in the forward.  The low-rank steps
-// come after the k-chunks: a unit's two ring slots per adapter hold its 128 q
-// rows and 64 NB columns of A.
+// come after the k-chunks: a unit's two ring slots per adapter (three for 64 ranks)
+// hold 64 NB columns of A and both halves of its 128 q rows.
 // A unit is 256 rows x 128 NB columns.  NB = 1 where NB = 2 would leave half the
 // pairs without one: a unit's chunks are a chain whose step is a decode (777
 // rows of 512 columns over 2048: 22 us with NB = 2, 14 us with 1).  8192 rows of
@@ -738,6 +752,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
   const int blocks_per_row = p.K / 64;
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   const int32_t* granules = p.steps + kAdapterStepsHeader;
+  const bool pack = p.r_pad <= 32;  // both halves of the low-rank rows in one slot
 
   if (warp == 0) {
     // ------------------------------------------------ NF4 codes (one lane)
@@ -788,20 +803,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
         if (!ok) break;
         while (run.next()) {
           const uint32_t s1 = (s + 1 == SA) ? 0 : s + 1, ph1 = (s + 1 == SA) ? ph ^ 1 : ph;
+          const uint32_t s2 = (s1 + 1 == SA) ? 0 : s1 + 1, ph2 = (s1 + 1 == SA) ? ph1 ^ 1 : ph1;
           if (!(ok = mbar_wait(&aempty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 310))) break;
           if (!(ok = mbar_wait(&aempty[s1], ph1 ^ 1, ctl, p.err, p.timeout_ns, 310))) break;
-          uint8_t* la = aring + s * A_BYTES;
-          uint8_t* lb = aring + s1 * A_BYTES;
+          if (!pack && !(ok = mbar_wait(&aempty[s2], ph2 ^ 1, ctl, p.err, p.timeout_ns, 310))) break;
+          uint8_t* lb = aring + s * A_BYTES;
+          uint8_t* high = aring + s1 * A_BYTES;
+          uint8_t* low = pack ? high + A_BYTES / 2 : aring + s2 * A_BYTES;
           const uint32_t bar = xfull_even + 8 * s;
           if (rank == 0) {
-            mbar_arrive_expect_tx(&xfull[s], (uint32_t)((512 + 256 * NB) * p.r_pad));
+            mbar_arrive_expect_tx(&xfull[s], (uint32_t)((1024 + 256 * NB) * p.r_pad));
             mbar_arrive(&xfull[s1]);
+            if (!pack) mbar_arrive(&xfull[s2]);
           }
-          tma_load_2d_pair(la, &map_la, bar, 0, row0);
+          tma_load_3d_pair(high, &map_la, bar, 0, 0, row0);
+          tma_load_3d_pair(low, &map_la, bar, 0, 1, row0);
           tma_load_3d_pair(lb, &map_lb, bar, c0, 0, run.adapter);
           if (NB == 2) tma_load_3d_pair(lb + 128 * p.r_pad, &map_lb, bar, c0 + 64, 0, run.adapter);
           issued_next();
           issued_next();
+          if (!pack) issued_next();
         }
       }
       // (After a wait ran out: copies of either CTA may be in flight; they are given time to land.)
@@ -860,19 +881,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
         while (run.next()) {
           if (!(ok = wait_a())) break;
           tc_fence_after();
-          const uint32_t sa1 = (sa + 1 == SA) ? 0 : sa + 1;
-          const uint32_t la_u = a_u + sa * A_BYTES, lb_u = a_u + sa1 * A_BYTES;
+          const uint32_t sa1 = (sa + 1 == SA) ? 0 : sa + 1, sa2 = (sa1 + 1 == SA) ? 0 : sa1 + 1;
+          const uint32_t lb_u = a_u + sa * A_BYTES, high = a_u + sa1 * A_BYTES;
+          const uint32_t la_u[2] = {high, pack ? high + A_BYTES / 2 : a_u + sa2 * A_BYTES};
           uint32_t off[8];
 #pragma unroll
           for (int w = 0; w < 8; ++w) off[w] = rows_off(run.lo, run.hi, w);
           for (int ks = 0; ks < p.r_pad / 16; ++ks) {
             const uint64_t bd = make_sdesc(lb_u + 2048 * ks, 128 * p.r_pad, 1024, kSw128);
-            umma_bf16_2sm_masked(d, make_sdesc(la_u + 32 * ks, 16, 16 * p.r_pad, lswz), bd, idesc, off);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              umma_bf16_2sm_masked(d, make_sdesc(la_u[i] + 32 * ks, 16, 16 * p.r_pad, lswz), bd, idesc, off);
           }
           umma_commit_2sm(&aempty[sa], 0x3);
           umma_commit_2sm(&aempty[sa1], 0x3);
+          if (!pack) umma_commit_2sm(&aempty[sa2], 0x3);
           next_a();
           next_a();
+          if (!pack) next_a();
         }
         if (!ok) break;
         umma_commit_2sm(&accfull[b], 0x3);
@@ -1023,7 +1049,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
 // =============================================================================
 // Row gather with the low-rank projection:
 //   dst[row] = src[token of row]  (zero for padding rows)
-//   out[row] = bf16(s[a] dst[row] . F[a])
+//   out[row] = s[a] dst[row] . F[a], as bf16 pairs
 // A task is up to 128 rows of one adapter (or of the tokens without one, which
 // are only gathered).  Four loader warps copy the rows' 128-byte pieces into
 // the UMMA's swizzled tile with cp.async (zeros for padding rows), the tensor
@@ -1050,7 +1076,7 @@ struct AdapterRowsParams {
   const int32_t* order;
   const int32_t* steps;
   const float* scale;
-  uint16_t* out;
+  uint16_t* out;  // [rows, 2, r]
   DeviceError* err;
   long long timeout_ns;
   int R, T, n, r, r_pad, tasks;  // tasks: place of the task list in `steps`
@@ -1266,13 +1292,20 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
       for (int j = 0; project && j < p.r_pad; j += 16) {
         float v[16];
         tmem_ld16(tl + j, v);
-        uint32_t w[8];
+        uint32_t w[8], l[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(sc * v[2 * i], sc * v[2 * i + 1]);
-        uint4* d = reinterpret_cast<uint4*>(p.out + (size_t)row * p.r + j);
+        for (int i = 0; i < 8; ++i) split_bf16x2(sc * v[2 * i], sc * v[2 * i + 1], w[i], l[i]);
+        uint16_t* at = p.out + (size_t)row * 2 * p.r + j;
+        uint4 *d = reinterpret_cast<uint4*>(at), *e = reinterpret_cast<uint4*>(at + p.r);
         if (row < tk.z) {
-          if (j < p.r) d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          if (j + 8 < p.r) d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          if (j < p.r) {
+            d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            e[0] = make_uint4(l[0], l[1], l[2], l[3]);
+          }
+          if (j + 8 < p.r) {
+            d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            e[1] = make_uint4(l[4], l[5], l[6], l[7]);
+          }
         }
       }
       tc_fence_before();
@@ -1295,8 +1328,12 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
         const int row = i % rows, j = 4 * (i / rows), to = tk.y + rank * rows + row;
         if (to < tk.z) {
           const float4 v = sum_share(smem, p.S, row, j, p.r_pad);
-          *reinterpret_cast<uint2*>(p.out + (size_t)to * p.r + j) =
-              make_uint2(pack_bf16x2(sc * v.x, sc * v.y), pack_bf16x2(sc * v.z, sc * v.w));
+          uint2 high, low;
+          split_bf16x2(sc * v.x, sc * v.y, high.x, low.x);
+          split_bf16x2(sc * v.z, sc * v.w, high.y, low.y);
+          uint16_t* at = p.out + (size_t)to * 2 * p.r + j;
+          *reinterpret_cast<uint2*>(at) = high;
+          *reinterpret_cast<uint2*>(at + p.r) = low;
         }
       }
     }
@@ -1316,17 +1353,23 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
 // 41 us, 1.8 TB/s of their 69 MB: 512 blocks of 8 chunks in two waves, and a join of
 // 6 us a cluster.
 namespace adw {
-constexpr int BM = 128, BK = 64, STAGES = 4;
-constexpr int A_BYTES = BK * BM * 2;            // 64 rows x 128 features, MN-major SW128
-constexpr int B_BYTES = BK * E4B_MAX_RANK * 2;  // 64 rows x r_pad, MN-major
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 1024;
+constexpr int BM = 128, BK = 64;
+constexpr int A_BYTES = BK * BM * 2;  // 64 rows x 128 features, MN-major SW128
+// A stage is the features and both halves of 64 rows x r_pad, MN-major; two blocks an SM leave room for four stages
+// of up to 32 ranks and three of 64.
+constexpr int stages(bool wide) { return wide ? 3 : 4; }
+constexpr int half_bytes(bool wide) { return BK * (wide ? E4B_MAX_RANK : E4B_MAX_RANK / 2) * 2; }
+constexpr int stage_bytes(bool wide) { return A_BYTES + 2 * half_bytes(wide); }
+constexpr int smem_bytes(bool wide) { return stages(wide) * stage_bytes(wide) + 1024 + 1024; }
 // warps 0-3 row loaders, 4 low-rank rows, 5 UMMA issuer + TMEM owner, 6-9 epilogue
 constexpr int kLoadWarps = 4, kLowWarp = 4, kIssueWarp = 5;
 constexpr int kThreads = 10 * 32;
 constexpr int kAccCols = 64;
 constexpr int kTmemCols = 2 * kAccCols;
-static_assert(STAGE_BYTES % 1024 == 0, "stage alignment");
+static_assert(stage_bytes(false) % 1024 == 0 && stage_bytes(true) % 1024 == 0, "stage alignment");
+static_assert(share_bytes(E4B_MAX_RANK, 8) <= stages(true) * stage_bytes(true) &&
+                  share_bytes(E4B_MAX_RANK / 2, 8) <= stages(false) * stage_bytes(false),
+              "the shares fit the stages");
 }  // namespace adw
 
 struct AdapterWgradParams {
@@ -1360,10 +1403,12 @@ __device__ __forceinline__ AdapterWgradUnit adapter_wgrad_unit(const AdapterWgra
   return w;
 }
 
+template <bool WIDE>  // r > 32
 __global__ void __launch_bounds__(adw::kThreads, 2)
     adapter_wgrad_kernel(const __grid_constant__ CUtensorMap low0, const __grid_constant__ CUtensorMap low1,
                          const AdapterWgradParams p) {
   using namespace adw;
+  constexpr int STAGES = stages(WIDE), HALF_BYTES = half_bytes(WIDE), STAGE_BYTES = stage_bytes(WIDE);
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = align1024(smem_dyn);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
@@ -1453,8 +1498,10 @@ __global__ void __launch_bounds__(adw::kThreads, 2)
         const CUtensorMap* low = w.g ? &low1 : &low0;
         for (int kc = w.k_lo; kc < w.k_hi; ++kc) {
           if (!(ok = mbar_wait(&empty[s], ph ^ 1, ctl, p.err, p.timeout_ns, 511))) break;
-          mbar_arrive_expect_tx(&full[s], b_bytes);
-          tma_load_2d(smem + s * STAGE_BYTES + A_BYTES, low, &full[s], 0, w.row0 + kc * BK);
+          mbar_arrive_expect_tx(&full[s], 2 * b_bytes);
+          uint8_t* b = smem + s * STAGE_BYTES + A_BYTES;
+          tma_load_3d(b, low, &full[s], 0, 0, w.row0 + kc * BK);
+          tma_load_3d(b + HALF_BYTES, low, &full[s], 0, 1, w.row0 + kc * BK);
           issued |= 1u << s;
           last_par = (last_par & ~(1u << s)) | (ph << s);
           if (++s == STAGES) {
@@ -1486,8 +1533,11 @@ __global__ void __launch_bounds__(adw::kThreads, 2)
           const int steps = min(BK, w.rows - kc * BK) / 16;  // rows past the adapter's end take no part
           for (int kk = 0; kk < steps; ++kk) {
             const uint64_t ad = make_sdesc(a0 + 2048 * kk, A_BYTES / 2, 1024, kSw128);
-            const uint64_t bd = make_sdesc(b0 + 32 * p.r_pad * kk, b_bytes, 16 * p.r_pad, lswz);
-            umma_bf16(acc, ad, bd, idesc, (kc > w.k_lo || kk > 0) ? 1u : 0u);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint64_t bd = make_sdesc(b0 + i * HALF_BYTES + 32 * p.r_pad * kk, b_bytes, 16 * p.r_pad, lswz);
+              umma_bf16(acc, ad, bd, idesc, (kc > w.k_lo || kk > 0 || i > 0) ? 1u : 0u);
+            }
           }
           umma_commit(&empty[s]);
           if (++s == STAGES) {
@@ -1612,6 +1662,14 @@ cudaError_t map_u8_2d(CUtensorMap* m, const void* base, uint64_t bytes, uint64_t
   return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box,
                            CU_TENSOR_MAP_SWIZZLE_NONE);
 }
+// Halves of p or q, bf16 [rows, 2, r]: a tile is one half of `box_rows` rows.
+cudaError_t map_halves(CUtensorMap* m, const void* base, int r, uint64_t rows, int r_pad, uint32_t box_rows) {
+  const uint64_t dims[3] = {(uint64_t)r, 2, rows};
+  const uint64_t strides[2] = {(uint64_t)r * 2, (uint64_t)r * 4};
+  const uint32_t box[3] = {(uint32_t)r_pad, 1, box_rows};
+  return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box,
+                           swizzle_for_bytes(2 * r_pad));
+}
 }  // namespace
 
 // Token rows of a forward unit: the ones that take the pairs the least time.  Measured cycles a 64-wide chunk: 680 up
@@ -1651,7 +1709,7 @@ cudaError_t launch_adapter_fwd(const AdapterProjHost& h, const uint16_t* rows, c
   if ((err = map_bf16_2d(&mx1, rows, h.K, h.rows_cap, 64, last / 2, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess)
     return err;
   if ((err = map_u8_2d(&mraw, h.nf4, h.K / 2, h.N, 32, 128)) != cudaSuccess) return err;
-  if ((err = map_bf16_2d(&mp, low, h.r, h.rows_cap, rp, 16, rswz)) != cudaSuccess) return err;
+  if ((err = map_halves(&mp, low, h.r, h.rows_cap, rp, 16)) != cudaSuccess) return err;
   if ((err = map_bf16_3d(&mb, B, h.r, h.N, h.n, rp, 64, rswz)) != cudaSuccess) return err;
   p.absmax = h.absmax;
   p.order = h.order;
@@ -1681,7 +1739,7 @@ cudaError_t launch_adapter_dgrad(const AdapterProjHost& h, const uint16_t* rows,
   const int64_t row_units = h.rows_cap / kAdapterUnitRows;
   const int nb = 2 * row_units * ((h.K + 255) / 256) <= num_sms / 2 ? 1 : 2;
   if ((err = map_u8_2d(&mraw, h.nf4, h.K / 2, h.N, 32 * nb, 64)) != cudaSuccess) return err;
-  if ((err = map_bf16_2d(&mla, low, h.r, h.rows_cap, rp, 128, swizzle_for_bytes(2 * rp))) != cudaSuccess) return err;
+  if ((err = map_halves(&mla, low, h.r, h.rows_cap, rp, 128)) != cudaSuccess) return err;
   if ((err = map_bf16_3d(&mlb, A, h.K, h.r, h.n, 64, rp, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return err;
   AdapterDgradParams p;
   p.absmax = h.absmax;
@@ -1745,9 +1803,8 @@ cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, co
   const int rp = rank_padded(h.r);
   CUtensorMap mq, mp;
   cudaError_t err;
-  const CUtensorMapSwizzle rswz = swizzle_for_bytes(2 * rp);
-  if ((err = map_bf16_2d(&mq, q_low, h.r, h.rows_cap, rp, 64, rswz)) != cudaSuccess) return err;
-  if ((err = map_bf16_2d(&mp, p_low, h.r, h.rows_cap, rp, 64, rswz)) != cudaSuccess) return err;
+  if ((err = map_halves(&mq, q_low, h.r, h.rows_cap, rp, 64)) != cudaSuccess) return err;
+  if ((err = map_halves(&mp, p_low, h.r, h.rows_cap, rp, 64)) != cudaSuccess) return err;
   AdapterWgradParams p;
   p.act[0] = x;
   p.act[1] = dY;
@@ -1772,7 +1829,10 @@ cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, co
   while (p.S < 8 && 2 * p.S * units <= 2 * cap && h.T / h.n >= 8 * p.S * adw::BK) p.S *= 2;
   const int grid = (int)(p.S > 1 ? units * p.S : (units < cap ? units : cap));
   LaunchScope scope("adapter_wgrad", stream);
-  return launch_tiles(adapter_wgrad_kernel, grid, adw::kThreads, adw::SMEM_BYTES, p.S, stream, mq, mp, p);
+  return rp > 32 ? launch_tiles(adapter_wgrad_kernel<true>, grid, adw::kThreads, adw::smem_bytes(true), p.S, stream,
+                                mq, mp, p)
+                 : launch_tiles(adapter_wgrad_kernel<false>, grid, adw::kThreads, adw::smem_bytes(false), p.S, stream,
+                                mq, mp, p);
 }
 
 }  // namespace e4b

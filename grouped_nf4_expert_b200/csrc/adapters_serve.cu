@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvPar
       if (!have) return;
       first = false;
       if (tid == 0) leave(p.err, step);
-      // p[t, j] = bf16(s[a] sum of the shares), 16 threads a token
+      // p[t, j] = s[a] sum of the shares, 16 threads a token
       if (adapted) {
         const float sc = __ldg(p.scale + a);
         for (int j = 4 * row; j < p.r; j += 64) {
@@ -306,9 +306,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvPar
             v.z += w.z;
             v.w += w.w;
           }
-          const uint32_t u0 = pack_bf16x2(sc * v.x, sc * v.y), u1 = pack_bf16x2(sc * v.z, sc * v.w);
-          *reinterpret_cast<float4*>(&ps[t][j]) =
-              make_float4(bf16lo_to_f32(u0), bf16hi_to_f32(u0), bf16lo_to_f32(u1), bf16hi_to_f32(u1));
+          *reinterpret_cast<float4*>(&ps[t][j]) = make_float4(sc * v.x, sc * v.y, sc * v.z, sc * v.w);
         }
       }
       __syncwarp();  // a token's 16 threads are of one warp
@@ -378,7 +376,7 @@ struct SplitParams {
   const uint16_t* A;
   const uint16_t* B;
   const float* scale;
-  uint16_t* p;         // [T, r]
+  uint16_t* p;         // [T, 2, r] pairs
   const int32_t* ids;
   uint16_t* y;
   DeviceError* err;
@@ -475,8 +473,11 @@ __device__ __forceinline__ void split_low_rank(uint8_t* smem, const SplitParams&
         float v = 0.0f;
 #pragma unroll
         for (int w = 0; w < kW; ++w) v += red[w][j][c];
-        const __nv_bfloat16 h = __float2bfloat16_rn(__ldg(p.scale + ad) * v);
-        p.p[(size_t)t * p.r + j0 + j] = *reinterpret_cast<const uint16_t*>(&h);
+        uint32_t high, low;
+        split_bf16x2(__ldg(p.scale + ad) * v, 0.0f, high, low);
+        uint16_t* at = p.p + (size_t)t * 2 * p.r + j0 + j;
+        at[0] = (uint16_t)high;
+        at[p.r] = (uint16_t)low;
       }
     }
   }
@@ -735,7 +736,7 @@ __global__ void __launch_bounds__(ads::kThreadsSplit + 128, 1)  // 96 registers:
     const int g = lane >> 2, q = lane & 3;
     const int items = *n_tiles * kGroupsOf16;
     struct Low {
-      uint4 b0[kC], b1[kC], p[kC];
+      uint4 b0[kC], b1[kC], p[kC], p_low[kC];
     };
     auto fetch = [&](int item) -> Low {
       Low w;
@@ -749,7 +750,9 @@ __global__ void __launch_bounds__(ads::kThreadsSplit + 128, 1)  // 96 registers:
         const uint16_t* b = p.B + ((size_t)a * p.N + (go ? row + g : 0)) * p.r + (go ? j : 0);
         w.b0[c] = ldg16(b, go);
         w.b1[c] = ldg16(b + 8 * p.r, go && row + 8 < p.N);  // N is a multiple of 8
-        w.p[c] = ldcg16(p.p + (size_t)(t >= 0 ? t : 0) * p.r + (go ? j : 0), go && t >= 0);
+        const uint16_t* pt = p.p + (size_t)(t >= 0 ? t : 0) * 2 * p.r + (go ? j : 0);
+        w.p[c] = ldcg16(pt, go && t >= 0);
+        w.p_low[c] = ldcg16(pt + p.r, go && t >= 0);
       }
       return w;
     };
@@ -771,6 +774,8 @@ __global__ void __launch_bounds__(ads::kThreadsSplit + 128, 1)  // 96 registers:
         for (int c = 0; c < kC; ++c) {
           mma_bf16(d, w[i].b0[c].x, w[i].b1[c].x, w[i].b0[c].y, w[i].b1[c].y, w[i].p[c].x, w[i].p[c].y);
           mma_bf16(d, w[i].b0[c].z, w[i].b1[c].z, w[i].b0[c].w, w[i].b1[c].w, w[i].p[c].z, w[i].p[c].w);
+          mma_bf16(d, w[i].b0[c].x, w[i].b1[c].x, w[i].b0[c].y, w[i].b1[c].y, w[i].p_low[c].x, w[i].p_low[c].y);
+          mma_bf16(d, w[i].b0[c].z, w[i].b1[c].z, w[i].b0[c].w, w[i].b1[c].w, w[i].p_low[c].z, w[i].p_low[c].w);
         }
         if (t0 >= 0) c0[0] = d[0], c0[8] = d[2];
         if (t1 >= 0) c1[0] = d[1], c1[8] = d[3];

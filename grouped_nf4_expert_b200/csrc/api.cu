@@ -138,7 +138,7 @@ ServeProjLayout serve_proj_layout(const e4b_proj_dims* d, int32_t T) {
   l.offsets = l.order + up((size_t)rows * 4);
   l.steps = l.offsets + up((size_t)(d->n_adapters + 2) * 4);
   l.low = l.steps + up((size_t)adapter_steps_cap(rows, d->n_adapters) * 4);
-  size_t low = (size_t)rows * d->r * 2;
+  size_t low = (size_t)rows * d->r * 4;
   if (adapter_gemv_serves(T, d->K, d->N)) low = (size_t)adapter_gemv_shares(T, d->r, d->N) * T * d->r * 4;
   l.rows = l.low + up(low);
   l.total = l.rows + up((size_t)rows * d->K * 2);
@@ -799,7 +799,7 @@ e4b_status e4b_multi_lora_serve_fwd(const e4b_proj_dims* dims, int32_t T, const 
 
 e4b_status e4b_multi_lora_fwd(const e4b_proj_dims* dims, int32_t T, const e4b_adapter_groups* groups,
                               const e4b_bf16* x, const e4b_nf4_matrix* base, const e4b_adapter_factors* adapters,
-                              e4b_bf16* p, e4b_bf16* y, void* ws, size_t ws_bytes, e4b_stream_t stream) {
+                              float* p, e4b_bf16* y, void* ws, size_t ws_bytes, e4b_stream_t stream) {
   E4B_TRY(check_proj_dims(dims, T));
   if (T == 0) return E4B_OK;
   if (!aligned16(ws)) return E4B_ERR_INVALID_ARG;
@@ -812,14 +812,15 @@ e4b_status e4b_multi_lora_fwd(const e4b_proj_dims* dims, int32_t T, const e4b_ad
   int sms = 0;
   E4B_CUDA(device_sms(&sms));
   const AdapterProjHost h = proj_host(dims, T, base, adapters, groups->order, groups->offsets, groups->steps, ws);
-  E4B_CUDA(launch_adapter_rows(h, false, x, adapters->A, rows, p, sms, st));
-  E4B_CUDA(launch_adapter_fwd(h, rows, p, adapters->B, y, sms, st));
+  uint16_t* pairs = reinterpret_cast<uint16_t*>(p);
+  E4B_CUDA(launch_adapter_rows(h, false, x, adapters->A, rows, pairs, sms, st));
+  E4B_CUDA(launch_adapter_fwd(h, rows, pairs, adapters->B, y, sms, st));
   return E4B_OK;
 }
 
 e4b_status e4b_multi_lora_dgrad(const e4b_proj_dims* dims, int32_t T, const e4b_adapter_groups* groups,
                                 const e4b_bf16* dY, const e4b_nf4_matrix* base, const e4b_adapter_factors* adapters,
-                                e4b_bf16* q, e4b_bf16* dx, void* ws, size_t ws_bytes, e4b_stream_t stream) {
+                                float* q, e4b_bf16* dx, void* ws, size_t ws_bytes, e4b_stream_t stream) {
   E4B_TRY(check_proj_dims(dims, T));
   if (T == 0) return E4B_OK;
   if (!aligned16(ws)) return E4B_ERR_INVALID_ARG;
@@ -832,13 +833,14 @@ e4b_status e4b_multi_lora_dgrad(const e4b_proj_dims* dims, int32_t T, const e4b_
   int sms = 0;
   E4B_CUDA(device_sms(&sms));
   const AdapterProjHost h = proj_host(dims, T, base, adapters, groups->order, groups->offsets, groups->steps, ws);
-  E4B_CUDA(launch_adapter_rows(h, true, dY, adapters->B, rows, q, sms, st));
-  E4B_CUDA(launch_adapter_dgrad(h, rows, q, adapters->A, dx, sms, st));
+  uint16_t* pairs = reinterpret_cast<uint16_t*>(q);
+  E4B_CUDA(launch_adapter_rows(h, true, dY, adapters->B, rows, pairs, sms, st));
+  E4B_CUDA(launch_adapter_dgrad(h, rows, pairs, adapters->A, dx, sms, st));
   return E4B_OK;
 }
 
 e4b_status e4b_multi_lora_wgrad(const e4b_proj_dims* dims, int32_t T, const e4b_adapter_groups* groups,
-                                const e4b_bf16* x, const e4b_bf16* dY, const e4b_bf16* p, const e4b_bf16* q,
+                                const e4b_bf16* x, const e4b_bf16* dY, const float* p, const float* q,
                                 e4b_bf16* dA, e4b_bf16* dB, void* ws, size_t ws_bytes, e4b_stream_t stream) {
   E4B_TRY(check_proj_dims(dims, T));
   if (!aligned16(ws)) return E4B_ERR_INVALID_ARG;
@@ -856,7 +858,8 @@ e4b_status e4b_multi_lora_wgrad(const e4b_proj_dims* dims, int32_t T, const e4b_
   int sms = 0;
   E4B_CUDA(device_sms(&sms));
   const AdapterProjHost h = proj_host(dims, T, nullptr, nullptr, groups->order, groups->offsets, groups->steps, ws);
-  E4B_CUDA(launch_adapter_wgrad(h, x, dY, p, q, dA, dB, sms, st));
+  E4B_CUDA(launch_adapter_wgrad(h, x, dY, reinterpret_cast<const uint16_t*>(p), reinterpret_cast<const uint16_t*>(q),
+                                dA, dB, sms, st));
   return E4B_OK;
 }
 

@@ -533,6 +533,14 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 __device__ __forceinline__ float bf16lo_to_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi_to_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// Float32 sums as the operand of another bf16 product: each as a pair, the value rounded and what that rounding left,
+// together within 2^-16 of it (two roundings of at most 2^-8 each).  An infinity or NaN has nothing left over.
+__device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t& high, uint32_t& low) {
+  high = pack_bf16x2(a, b);
+  const float la = a - bf16lo_to_f32(high), lb = b - bf16hi_to_f32(high);  // exact
+  low = pack_bf16x2(fabsf(la) < INFINITY ? la : 0.0f, fabsf(lb) < INFINITY ? lb : 0.0f);
+}
+
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t d;
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));

@@ -226,7 +226,8 @@ struct AdapterProjHost {
   DeviceError* err;
   long long timeout_ns;
 };
-// rows[row] = src[t], out[row, :r] = bf16(s[a] src[t] . factor[a]): A [n, r, K] over x, or (mn) B [n, N, r] over dY.
+// rows[row] = src[t], out[row] = s[a] src[t] . factor[a] (A [n, r, K] over x, or (mn) B [n, N, r] over dY).  p and q
+// are held as bf16 pairs, [rows, 2, r]: the value rounded, then what that rounding left (split_bf16x2).
 cudaError_t launch_adapter_rows(const AdapterProjHost& h, bool mn, const uint16_t* src, const uint16_t* fac,
                                 uint16_t* rows, uint16_t* out, int num_sms, cudaStream_t stream);
 // y[t] = rows[row] W^T + low[row] B[a]^T.
@@ -237,7 +238,7 @@ cudaError_t launch_adapter_dgrad(const AdapterProjHost& h, const uint16_t* rows,
                                  const uint16_t* A, uint16_t* dx, int num_sms, cudaStream_t stream);
 cudaError_t launch_adapter_wgrad(const AdapterProjHost& h, const uint16_t* x, const uint16_t* dY, const uint16_t* p,
                                  const uint16_t* q, uint16_t* dA, uint16_t* dB, int num_sms, cudaStream_t stream);
-// y for up to kAdapterSmallTokens tokens in one launch (scratch: low [T, r] bf16, or, where adapter_gemv_serves,
+// y for up to kAdapterSmallTokens tokens in one launch (scratch: low [T, 2, r] bf16, or, where adapter_gemv_serves,
 // [adapter_gemv_shares, T, r] float32).
 bool adapter_gemv_serves(int T, int K, int N);
 int adapter_gemv_shares(int T, int r, int N);

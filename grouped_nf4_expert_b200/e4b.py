@@ -642,7 +642,9 @@ class Projection(_OnDevice):
         if train:
             self.order, self.offsets = _alloc((R,), i32, dev), _alloc((n + 2,), i32, dev)
             self.steps = _alloc((sz.steps_cap,), i32, dev)
-            self.p, self.q = _alloc((R, r), bf, dev), _alloc((R, r), bf, dev)
+            # by row: the values rounded to bf16 (p, q), then what that rounding left
+            self._p_pairs, self._q_pairs = _alloc((R, 2, r), bf, dev), _alloc((R, 2, r), bf, dev)
+            self.p, self.q = self._p_pairs[:, 0], self._q_pairs[:, 0]
             self.dx = _alloc((T, dims.K), bf, dev, zero=False)
             # the two gradients are views of one flat buffer (one collective in a data-parallel step)
             na, nb = n * r * dims.K, n * dims.N * r
@@ -651,7 +653,7 @@ class Projection(_OnDevice):
             self.dB = self.lora_grads[na:].view(n, dims.N, r)
             self._groups = AdapterGroups(_ptr(self.order), _ptr(self.offsets), _ptr(self.steps))
             self._groups_p = ctypes.addressof(self._groups)
-            self._low_p = (_ptr(self.p), _ptr(self.q))
+            self._low_p = (_ptr(self._p_pairs), _ptr(self._q_pairs))
             self._dx_p, self._grad_p = _ptr(self.dx), (_ptr(self.dA), _ptr(self.dB))
         self._call("e4b_workspace_init", None, self._ws_p, self._ws_n)
 

@@ -26,9 +26,10 @@ extern "C" {
  *
  *     y[t] = W x[t] + B[a] p[t],   p[t] = s[a] A[a] x[t],   a = ids[t]
  *
- * A token whose id lies outside [0, n) has no adapter: y[t] = W x[t].  p is
- * rounded to bf16, as p_gu and p_d of the expert block are; sums are float32
- * and y is rounded once.  An adapter's values reach the rows of its own tokens
+ * A token whose id lies outside [0, n) has no adapter: y[t] = W x[t].  Sums are
+ * float32, p and q are held in 32 bits between the two products (few tokens:
+ * float32; else two bf16 values that together are within 2^-16 of it), and
+ * y is rounded once.  An adapter's values reach the rows of its own tokens
  * only, whatever they are (an infinity or NaN in one adapter or one token
  * leaves every other request as it was).
  * The pages have no counterpart (their adapters sit in the expert stacks);
@@ -95,18 +96,19 @@ e4b_status e4b_multi_lora_serve_fwd(const e4b_proj_dims *dims, int32_t T, const 
                                     const e4b_nf4_matrix *base, const e4b_adapter_factors *adapters, e4b_bf16 *y,
                                     void *ws, size_t ws_bytes, e4b_stream_t stream);
 
-/* Training forward over grouped tokens: y (bf16 [T, N]) and p (bf16
- * [rows_cap, r], by row; kept for e4b_multi_lora_wgrad). */
+/* Training forward over grouped tokens: y (bf16 [T, N]) and p (32 bits a value,
+ * rows_cap * r of them, by row; kept for e4b_multi_lora_wgrad).  A row of p is
+ * bf16 [2, r]: its values rounded to bf16, then what that rounding left. */
 e4b_status e4b_multi_lora_fwd(const e4b_proj_dims *dims, int32_t T, const e4b_adapter_groups *groups,
                               const e4b_bf16 *x, const e4b_nf4_matrix *base, const e4b_adapter_factors *adapters,
-                              e4b_bf16 *p, e4b_bf16 *y, void *ws, size_t ws_bytes, e4b_stream_t stream);
+                              float *p, e4b_bf16 *y, void *ws, size_t ws_bytes, e4b_stream_t stream);
 
-/* Input gradient for dY (bf16 [T, N]): q[row] = s[a] dY[t] B[a] (bf16
- * [rows_cap, r], kept for e4b_multi_lora_wgrad) and
+/* Input gradient for dY (bf16 [T, N]): q[row] = s[a] dY[t] B[a] (laid out as p,
+ * kept for e4b_multi_lora_wgrad) and
  * dx[t] = dY[t] W + q[t] A[a] (bf16 [T, K]); the base is decoded again. */
 e4b_status e4b_multi_lora_dgrad(const e4b_proj_dims *dims, int32_t T, const e4b_adapter_groups *groups,
                                 const e4b_bf16 *dY, const e4b_nf4_matrix *base,
-                                const e4b_adapter_factors *adapters, e4b_bf16 *q, e4b_bf16 *dx, void *ws,
+                                const e4b_adapter_factors *adapters, float *q, e4b_bf16 *dx, void *ws,
                                 size_t ws_bytes, e4b_stream_t stream);
 
 /* Adapter gradients, float32 sums, bf16 out, for every adapter (an adapter
@@ -116,7 +118,7 @@ e4b_status e4b_multi_lora_dgrad(const e4b_proj_dims *dims, int32_t T, const e4b_
  * p and q as the two calls above wrote them (they carry s[a]).  The frozen base
  * gets no gradient.  Deterministic. */
 e4b_status e4b_multi_lora_wgrad(const e4b_proj_dims *dims, int32_t T, const e4b_adapter_groups *groups,
-                                const e4b_bf16 *x, const e4b_bf16 *dY, const e4b_bf16 *p, const e4b_bf16 *q,
+                                const e4b_bf16 *x, const e4b_bf16 *dY, const float *p, const float *q,
                                 e4b_bf16 *dA, e4b_bf16 *dB, void *ws, size_t ws_bytes, e4b_stream_t stream);
 
 /* ---- Balance loss of the router ----------------------------------------------
