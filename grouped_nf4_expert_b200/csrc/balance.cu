@@ -13,7 +13,7 @@
 // sequence's records in range order, so that the sums do not depend on which
 // block ran first, and the last of them adds up their shares of the loss.  A
 // second launch in their place cost the host 4.5 us and the GPU 10 to 15.
-// Backward: one pass over the logits with lse given.
+// Backward: one pass over the logits with lse given, each row's probabilities divided by their sum.
 //
 // What bounds them: HBM reads of the logits (forward) and reads plus writes
 // of T x E float32 (backward); for small batches the launch.  131072 tokens of
@@ -67,7 +67,7 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// exp(x) for x up to 0: the exponential of 2 of x log2(e), three operations a value where expf has about nine (131072
+// exp(x) for x up to 0 (or a rounding above): the exponential of 2 of x log2(e), three operations a value where expf has about nine (131072
 // tokens of 64 experts, both directions: expf 34.9 us, this 29.5 us).  Relative error (1.3 |x| + 4) 2^-24: the
 // product's rounding and the constant's, and the instruction's.  -inf gives 0; probabilities below 2^-126 are 0.
 __device__ __forceinline__ float exp_of(float x) {
@@ -577,13 +577,18 @@ __global__ void __launch_bounds__(kThreads, bwd_blocks(V)) balance_bwd_kernel(co
       const float lse = in ? __ldg(p.lse + t) : 0.0f;
       const bool live = in && inside && (p.mask == nullptr || __ldg(p.mask + t) != 0);
       const bool some = lse != -INFINITY;  // a row of -inf alone has no probabilities
-      float dot = 0.0f;
+      // lse is rounded by 2^-24 of the logits' common offset, so exp(l - lse) is off by one factor in all of a row
+      // (logits around 1000: 3e-5): their sum takes it out.
+      float sum = 0.0f, dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4 * V; ++i) {
         l[i] = some && live ? exp_of(l[i] - lse) : 0.0f;
+        sum += l[i];
         dot = fmaf(l[i], live ? f[i] : 0.0f, dot);
       }
-      dot = group_sum<G>(dot);
+      sum = group_sum<G>(sum);
+      const float inv = some && live ? 1.0f / sum : 0.0f;
+      dot = group_sum<G>(dot) * inv;
       const float zt = some ? zc * lse : 0.0f;
       if (!in) continue;
       float* row = p.d_logits + (size_t)t * E;
@@ -592,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, bwd_blocks(V)) balance_bwd_kernel(co
         const int c = 4 * (v * G + g);
         float d[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = live ? l[4 * v + i] * fmaf(bc, f[4 * v + i] - dot, zt) : 0.0f;
+        for (int i = 0; i < 4; ++i) d[i] = live ? l[4 * v + i] * inv * fmaf(bc, f[4 * v + i] - dot, zt) : 0.0f;
         if (ALIGNED) {
           if (c < E) {
             float4* q = reinterpret_cast<float4*>(row + c);
