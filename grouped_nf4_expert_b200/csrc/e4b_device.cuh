@@ -533,12 +533,17 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 __device__ __forceinline__ float bf16lo_to_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi_to_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// Float32 sums as the operand of another bf16 product: each as a pair, the value rounded and what that rounding left,
-// together within 2^-16 of it (two roundings of at most 2^-8 each).  An infinity or NaN has nothing left over.
+// Float32 sums as the operand of another bf16 product: each as a pair, the value cut to bf16 and what the cut left,
+// together within 2^-16 of it (of the 2^-7 that a cut leaves at most, a rounding takes 2^-9).  Both parts have the
+// value's sign, and neither is zero unless it is, so that the pair times an infinity is the infinity that the value
+// times it is, not NaN.  The part left is 2^-126 where there is none (beside an infinity too).
+__device__ __forceinline__ float left_by_cut(float v, float cut) {
+  const float left = fabsf(v) == INFINITY ? 0.0f : v - cut;  // exact; NaN stays
+  return left == 0.0f && v != 0.0f ? copysignf(1.17549435e-38f, v) : left;
+}
 __device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t& high, uint32_t& low) {
-  high = pack_bf16x2(a, b);
-  const float la = a - bf16lo_to_f32(high), lb = b - bf16hi_to_f32(high);  // exact
-  low = pack_bf16x2(fabsf(la) < INFINITY ? la : 0.0f, fabsf(lb) < INFINITY ? lb : 0.0f);
+  high = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  low = pack_bf16x2(left_by_cut(a, bf16lo_to_f32(high)), left_by_cut(b, bf16hi_to_f32(high)));
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {

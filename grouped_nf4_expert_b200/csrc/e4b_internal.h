@@ -227,7 +227,7 @@ struct AdapterProjHost {
   long long timeout_ns;
 };
 // rows[row] = src[t], out[row] = s[a] src[t] . factor[a] (A [n, r, K] over x, or (mn) B [n, N, r] over dY).  p and q
-// are held as bf16 pairs, [rows, 2, r]: the value rounded, then what that rounding left (split_bf16x2).
+// are held as bf16 pairs, [rows, 2, r]: the value cut to bf16, then what the cut left (split_bf16x2).
 cudaError_t launch_adapter_rows(const AdapterProjHost& h, bool mn, const uint16_t* src, const uint16_t* fac,
                                 uint16_t* rows, uint16_t* out, int num_sms, cudaStream_t stream);
 // y[t] = rows[row] W^T + low[row] B[a]^T.

@@ -98,7 +98,7 @@ e4b_status e4b_multi_lora_serve_fwd(const e4b_proj_dims *dims, int32_t T, const 
 
 /* Training forward over grouped tokens: y (bf16 [T, N]) and p (32 bits a value,
  * rows_cap * r of them, by row; kept for e4b_multi_lora_wgrad).  A row of p is
- * bf16 [2, r]: its values rounded to bf16, then what that rounding left. */
+ * bf16 [2, r]: its values cut to bf16, then what the cut left. */
 e4b_status e4b_multi_lora_fwd(const e4b_proj_dims *dims, int32_t T, const e4b_adapter_groups *groups,
                               const e4b_bf16 *x, const e4b_nf4_matrix *base, const e4b_adapter_factors *adapters,
                               float *p, e4b_bf16 *y, void *ws, size_t ws_bytes, e4b_stream_t stream);

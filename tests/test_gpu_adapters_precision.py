@@ -1,6 +1,7 @@
 """What the projection with adapters keeps between its two low-rank products (GPU).
 
-p and q are held in 32 bits, at worst as two bf16 values: two roundings of at most 2^-8 each, 2^-16 together.  The
+p and q are held in 32 bits, at worst as two bf16 values: a cut of less than 2^-7 (the last place), and what it left
+rounded by 2^-9 of that last place, 2^-16 together.  The
 inputs make the ranks cancel in pairs (A's rows of a pair are equal but for one value, B's columns are opposite), and
 for the adapter gradients the tokens too, while the frozen matrix is next to nothing; so an error of p stands out that
 bf16's last place would hide otherwise.  Bounds as in ``test_gpu_adapters.py``, with 2^-16 in the place of bf16's 2^-8
@@ -99,7 +100,7 @@ def test_training(shape):
         check(getattr(pj, name), *want[name], name)
 
 
-def test_the_buffers_hold_a_value_and_what_its_rounding_left():
+def test_the_buffers_hold_a_value_and_what_its_cut_left():
     c = Case(100, 192, 136, 3, 24, "zipf", seed=202)
     pj = train(c)
     order, m = pj.order.cpu().numpy(), c.ref()
@@ -114,4 +115,4 @@ def test_the_buffers_hold_a_value_and_what_its_rounding_left():
         e = (m_ + 4) * F * want_abs[order[rows]]
         w = want[order[rows]]
         check(two.sum(1), w, PAIR * np.abs(w) + (1 + U) * e, "pair")
-        check(f64(high)[rows], w, U * np.abs(w) + (1 + U) * e, "rounded value")
+        check(f64(high)[rows], w, 2 * U * np.abs(w) + (1 + U) * e, "cut value")
