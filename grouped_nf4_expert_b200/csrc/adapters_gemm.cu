@@ -1049,7 +1049,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adg::kThreads, 1)
 // =============================================================================
 // Row gather with the low-rank projection:
 //   dst[row] = src[token of row]  (zero for padding rows)
-//   out[row] = s[a] dst[row] . F[a], as bf16 pairs
+//   out[row] = s[a] dst[row] . F[a], as bf16 pairs (zero for padding rows, whatever the factor holds)
 // A task is up to 128 rows of one adapter (or of the tokens without one, which
 // are only gathered).  Four loader warps copy the rows' 128-byte pieces into
 // the UMMA's swizzled tile with cp.async (zeros for padding rows), the tensor
@@ -1281,6 +1281,7 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
       const uint32_t b = ti & 1, use = ti >> 1;
       const uint32_t tl = tmem + b * kAccCols + ((uint32_t)(32 * (warp & 3)) << 16);
       const int row = tk.y + q;
+      const bool live = project && row < tk.z && __ldg(p.order + row) < p.T;
       ok = __all_sync(kFull, mbar_wait(&accfull[b], use & 1, ctl, p.err, p.timeout_ns, 430));
       if (!ok) break;
       tc_fence_after();
@@ -1292,9 +1293,11 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
       for (int j = 0; project && j < p.r_pad; j += 16) {
         float v[16];
         tmem_ld16(tl + j, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = live ? sc * v[i] : 0.0f;
         uint32_t w[8], l[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) split_bf16x2(sc * v[2 * i], sc * v[2 * i + 1], w[i], l[i]);
+        for (int i = 0; i < 8; ++i) split_bf16x2(v[2 * i], v[2 * i + 1], w[i], l[i]);
         uint16_t* at = p.out + (size_t)row * 2 * p.r + j;
         uint4 *d = reinterpret_cast<uint4*>(at), *e = reinterpret_cast<uint4*>(at + p.r);
         if (row < tk.z) {
@@ -1327,10 +1330,12 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
       for (int i = threadIdx.x; i < rows * (p.r / 4); i += kThreads) {
         const int row = i % rows, j = 4 * (i / rows), to = tk.y + rank * rows + row;
         if (to < tk.z) {
-          const float4 v = sum_share(smem, p.S, row, j, p.r_pad);
-          uint2 high, low;
-          split_bf16x2(sc * v.x, sc * v.y, high.x, low.x);
-          split_bf16x2(sc * v.z, sc * v.w, high.y, low.y);
+          uint2 high = make_uint2(0, 0), low = high;
+          if (__ldg(p.order + to) < p.T) {
+            const float4 v = sum_share(smem, p.S, row, j, p.r_pad);
+            split_bf16x2(sc * v.x, sc * v.y, high.x, low.x);
+            split_bf16x2(sc * v.z, sc * v.w, high.y, low.y);
+          }
           uint16_t* at = p.out + (size_t)to * 2 * p.r + j;
           *reinterpret_cast<uint2*>(at) = high;
           *reinterpret_cast<uint2*>(at + p.r) = low;

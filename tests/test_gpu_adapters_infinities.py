@@ -1,7 +1,8 @@
 """Infinities in the projection with adapters come out as the formulas have them (GPU).
 
 An infinity in a factor, a token or a gradient makes an infinity, or NaN where two of them meet or one meets a zero, of
-exactly the elements that the formulas in 64 bits make so, and leaves the bits of all others as they were.
+exactly the elements that the formulas in 64 bits make so, and leaves the bits of all others as they were.  (The rows
+that pad an adapter's to a multiple of 32 take no part: an infinite factor times their zeros is no NaN of the gradients.)
 """
 
 import numpy as np
@@ -38,9 +39,9 @@ def put(c, where):
     """One infinity in `where`, in adapter 0 or its first token ("+": beside factors of one sign, so that the sums that
     it enters are infinite and not NaN)."""
     t = int(np.flatnonzero(c.ids.cpu().numpy() == 0)[0])
-    if where == "A":
+    if where[0] == "A":
         c.A[0, 3, 5] = INF
-    elif where == "B":
+    elif where[0] == "B":
         c.B[0, 2, 3] = -INF
     elif where[0] == "x":
         c.x[t, 5] = INF
@@ -55,6 +56,9 @@ def case(T, r, where):
     if where.endswith("+"):
         c.A.abs_()
         c.B.abs_()
+    if where in ("A+", "B+"):  # p (A) and dY, or q (B) and x, of one sign as well
+        c.x.abs_()
+        c.dY.abs_()
     return c
 
 
@@ -75,7 +79,7 @@ def test_serving(T, r, where):
     same(serve(c).y, good, results(c)[0], "y")
 
 
-@pytest.mark.parametrize("where", ["x", "x+", "dY", "dY+"])
+@pytest.mark.parametrize("where", ["x", "x+", "dY", "dY+", "A", "A+", "B", "B+"])
 @pytest.mark.parametrize("T,r", [(40, 8), (300, 24), (700, 64)])
 def test_training(T, r, where):
     good, c = train(case(T, r, where)), case(T, r, where)
