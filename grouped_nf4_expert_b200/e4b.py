@@ -737,6 +737,7 @@ class RouterBalance(_OnDevice):
     def __init__(self, E: int, top_k: int, T: int, S: int = 1, device="cuda"):
         import torch
         self.E, self.top_k, self.T, self.S = E, top_k, T, S
+        self._done = False
         self._dims_c = BalanceDims(E, top_k, S, 0.0, 0.0)
         self._dims_p = ctypes.addressof(self._dims_c)
         ws_bytes = e4b_balance_get_sizes(self._dims_c, T)
@@ -769,13 +770,17 @@ class RouterBalance(_OnDevice):
         self._dims_c.balance_coef, self._dims_c.z_coef = balance_coef, z_coef
         self._call("e4b_balance_fwd", stream, self._dims_p, self.T, pl, pi, ps, pm, self._stats_p, self._loss_p,
                    self._ws_p, self._ws_n)
+        self._done = True
 
     def e4b_balance_bwd(self, logits, d_logits, seq_offsets=None, token_mask=None, balance_coef=1.0, z_coef=0.0,
                         dloss=None, accumulate=False, stream=None):
-        """d_logits = dloss * dloss/dlogits (dloss: float32 [1], None for 1), or += with ``accumulate``."""
+        """d_logits = dloss * dloss/dlogits (dloss: float32 [1], None for 1), or += with ``accumulate``; after
+        :meth:`e4b_balance_fwd`, whose counts and lse it reads."""
         pl, ps, pm = self._inputs(logits, seq_offsets, token_mask)
         pd = self._arg(d_logits, self._f32, self.T * self.E, "d_logits")
         pg = self._arg(dloss, self._f32, 1, "dloss", optional=True)
+        if not self._done and self.T:
+            raise ValueError("call e4b_balance_fwd first")
         self._dims_c.balance_coef, self._dims_c.z_coef = balance_coef, z_coef
         self._call("e4b_balance_bwd", stream, self._dims_p, self.T, pl, ps, pm, self._stats_p, pg,
                    1 if accumulate else 0, pd)
