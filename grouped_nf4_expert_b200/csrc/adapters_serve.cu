@@ -814,10 +814,12 @@ int adapter_gemv_shares(int T, int r, int N) {
 // The shares S of K and the blocks of p, by an estimate in microseconds of what bounds each part: a block of p reads
 // A at 90 KB/us and needs 1.7 us an item (2.5 us with 8 warps); a chunk of the product costs 0.3 us of decoding or its
 // x tile at 80 KB/us; shares travel at 27 KB/us a block; one SM holds one block, and clusters of 2, 4, 8 find 74, 33,
-// 15 places.  Either p has places of its own beside the products, or a launch of its own ahead of them (2 us).
-// Measured both ways: 128 tokens at 2048 -> 2048, S = 8 (16 clusters in 15 places) 26.7 us, S = 4 14.4 us; p of 57
-// tokens of 64 adapters of rank 64 at 2048 -> 512 in the launch 14.4 us, in its own 20.6 us; 256 tokens of 32 of rank
-// 32 at 4096 -> 4096 26.8 and 24.6 us.
+// 15 places.  Either p has places of its own beside the products, or a launch of its own ahead of them (2 us).  Only
+// the GPU's time counts: with the host's for two launches held against the second one, 20 of 189 sizes measured took
+// up to a quarter longer, replayed from a graph and called alike (p in the launch and in its own, replayed: 57 tokens
+// of 32 adapters of rank 32 at 4096 -> 4096 17.9 and 15.4 us, 17 tokens at 2048 -> 4096 11.2 and 9.9 us, 57 of 64 of
+// rank 64 at 2048 -> 512 11.1 and 11.7 us).  S measured: 128 tokens at 2048 -> 2048, S = 8 (16 clusters in 15 places)
+// 26.7 us, S = 4 14.4 us.
 struct SplitPlan {
   int S, p_blocks;
   bool own;  // p in a launch of its own
@@ -845,7 +847,7 @@ static SplitPlan split_plan(const AdapterProjHost& h, int NT, int tiles, int chu
       if (blocks <= 0) continue;
       const float pt = p_time(blocks, own ? 2.5f : 1.7f), all = turns * product;
       float time = pt > all ? pt : all;
-      if (own) time = time + 2.0f > 14.0f ? time + 2.0f : 14.0f;  // two launches are most of 12 us of host time
+      if (own) time += 2.0f;
       if (time < best_time) {
         best_time = time;
         best = SplitPlan{S, blocks, own != 0};
