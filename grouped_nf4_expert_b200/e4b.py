@@ -643,7 +643,7 @@ class Projection(_OnDevice):
             self.order, self.offsets = _alloc((R,), i32, dev), _alloc((n + 2,), i32, dev)
             self.steps = _alloc((sz.steps_cap,), i32, dev)
             # by row: the values cut to bf16 (p, q), then what the cut left
-            self._p_pairs, self._q_pairs = _alloc((R, 2, r), bf, dev), _alloc((R, 2, r), bf, dev)
+            self._p_pairs, self._q_pairs = (_alloc((R, 2, r), bf, dev, zero=False) for _ in range(2))
             self.p, self.q = self._p_pairs[:, 0], self._q_pairs[:, 0]
             self.dx = _alloc((T, dims.K), bf, dev, zero=False)
             # the two gradients are views of one flat buffer (one collective in a data-parallel step)

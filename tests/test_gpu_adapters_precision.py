@@ -116,3 +116,17 @@ def test_the_buffers_hold_a_value_and_what_its_cut_left():
         w = want[order[rows]]
         check(two.sum(1), w, PAIR * np.abs(w) + (1 + U) * e, "pair")
         check(f64(high)[rows], w, 2 * U * np.abs(w) + (1 + U) * e, "cut value")
+
+
+@pytest.mark.parametrize("T,r", [(90, 8), (300, 40), (2500, 24)])
+def test_what_the_buffers_held_does_not_matter(T, r):
+    c = Case(T, 64, 136, 4, r, "zipf", seed=203)
+    want, pj = train(c), e4b.Projection(c.dims, T)
+    for t in (pj._p_pairs, pj._q_pairs, pj.ws[256:].view(torch.bfloat16)):
+        t.fill_(float("nan"))
+    pj.e4b_adapter_group(c.ids)
+    pj.e4b_multi_lora_fwd(c.x, c.base(), c.adapters())
+    pj.e4b_multi_lora_dgrad(c.dY, c.base(), c.adapters())
+    pj.e4b_multi_lora_wgrad(c.x, c.dY)
+    for name in ("y", "dx", "dA", "dB"):
+        assert torch.equal(getattr(pj, name), getattr(want, name)), name
