@@ -194,8 +194,8 @@ __device__ __forceinline__ void let_land(uint64_t* bars, int n, uint32_t issued,
 // fills, and the second follows once its slot is free.  (One warp handing in two
 // parts' products took 720 cycles a chunk, against 512 in the tensor pipe: its
 // instruction stream, not the operands, was the limit.)  Units of three parts have
-// no slot to spare and are used for a single turn: 1111 tokens, 2048 -> 4096 in 64
-// units of 384 rows 27 us, in 128 of 160 33 us.  Token rows are accumulator columns, so
+// no slot to spare and are used for a single turn: 1111 tokens, 2048 -> 4096, the
+// whole call with 64 units of 384 rows 40.7 us, with 128 of 160 45.4 us.  Token rows are accumulator columns, so
 // an adapter's K = r product is issued at its own columns: adapters' rows start at
 // multiples of 32, the column granule of a pair UMMA.
 //
@@ -205,9 +205,10 @@ __device__ __forceinline__ void let_land(uint64_t* bars, int n, uint32_t issued,
 // signal on took about 690 cycles a chunk: beside four decode warps on its
 // scheduler, every instruction of it waits for a turn.)
 //
-// The tensor pipe bounds it, with the decode beside it: 840 cycles a chunk of 256
-// rows, 680 of 128 and less.  8192 tokens, 2048 -> 2048: 71 us, 970 TFLOP/s, tensor
-// pipe 53% active (3.5 turns of units); 16384 tokens, 4096 -> 14336: 1.15 PFLOP/s.
+// A chunk bounds it, the tensor pipe's part and the decode beside it: 840 cycles with
+// 256 rows (512 in the tensor pipe), 680 with 128 and less.  8192 tokens, 2048 -> 2048:
+// 72 us, 960 TFLOP/s, tensor pipe 52% active: 224-row units in four full turns, 448 of
+// a chunk's 823 cycles; 16384 tokens, 4096 -> 14336: 1.08 PFLOP/s over the whole call.
 //
 // Roles per CTA: warp 0 codes, warp 1 TMEM owner and (even CTA) issuer of the
 // first parts, warp 2 (even CTA) issuer of the second parts, warp 3 token rows and
@@ -645,9 +646,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::threads(PARTS),
 // come after the k-chunks: a unit's two ring slots per adapter (three for 64 ranks)
 // hold 64 NB columns of A and both halves of its 128 q rows.
 // A unit is 256 rows x 128 NB columns.  NB = 1 where NB = 2 would leave half the
-// pairs without one: a unit's chunks are a chain whose step is a decode (777
-// rows of 512 columns over 2048: 22 us with NB = 2, 14 us with 1).  8192 rows of
-// 2048 columns over 2048: 77 us, 890 TFLOP/s, tensor pipe 47% active.
+// pairs without one: a unit's chunks are a chain whose step is a decode (training
+// step of 777 tokens, 512 -> 2048: 62.7 us with NB = 2, 57.3 us with 1).  8192 rows of
+// 2048 columns over 2048: 77 us, 890 TFLOP/s, tensor pipe 50% active: 264 units on 74
+// pairs, the last of four turns a good half full.
 namespace adg {
 constexpr int BM = 128, BK = 64;
 constexpr int A_BYTES = BM * BK * 2;
@@ -1354,9 +1356,9 @@ __global__ void __launch_bounds__(adp::kThreads, 2)
 // =============================================================================
 // Adapter gradients: dA[a] = q^T x (stored transposed), dB[a] = dY^T p
 // =============================================================================
-// Reading x and dY bounds them.  8192 tokens of 4 adapters, 2048 + 2048 features:
-// 41 us, 1.8 TB/s of their 69 MB: 512 blocks of 8 chunks in two waves, and a join of
-// 6 us a cluster.
+// Reading x and dY bounds them.  8192 tokens of 4 adapters of rank 64, 2048 + 2048
+// features: 41 us, 1.7 TB/s of their 69 MB: 512 blocks of 8 chunks in two waves, and a
+// join of 6 us a cluster.
 namespace adw {
 constexpr int BM = 128, BK = 64;
 constexpr int A_BYTES = BK * BM * 2;  // 64 rows x 128 features, MN-major SW128

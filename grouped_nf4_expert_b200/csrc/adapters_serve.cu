@@ -138,12 +138,13 @@ __device__ __forceinline__ void low_rank_tile(const uint16_t* x, const uint16_t*
 // y for up to 16 tokens: 16 rows of W at a time, K split over the block's warps
 // ----------------------------------------------------------------------------
 // Blocks stay for several units of rows, the next unit's codes in flight while one
-// ends and p read once: 4096 -> 14336, 1 token 22.6 us (a block a unit: 24.6 us), 8
-// tokens 26.7 us (30.2 us).  1 token at 2048 -> 4096 takes 8.2 us alone and 5.9 us
-// after another, the chain of loads and waits; on the large matrix the byte permutes
-// of the decoding fill their pipe for 13 us and what is left is between the steps.
-// Decoding by a table of byte pairs in shared memory instead: 20.4 us at 1 token, but
-// 32.8 us at 8, whose rows of x come through the same pipe.
+// ends and p read once: 4096 -> 14336, 1 token 20.2 us, 8 tokens 24.6 us (a block a
+// unit: 9 and 13% more).  1 token at 2048 -> 4096 takes 8.1 us alone and 5.9 us after
+// another, the chain of loads and waits; on the large matrix the byte permutes of the
+// decoding keep the ALU pipe busy for 58% of the active cycles, 11 us, and what is left
+// is between the steps.  Decoding by a table of byte pairs in shared memory instead
+// takes 10% less at 1 token, but 23% more at 8, whose rows of x come through the same
+// pipe (L1 77% busy there as it is).
 // The blocks of p take (token, 16 ranks, share of K) each; with few of them K is
 // split (kq shares, added in order by the readers), since one block's loads
 // would be the longest chain of the launch.
@@ -347,10 +348,11 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_gemv_kernel(const GemvPar
 // tokens, one round trip after another), added, and the adapters' part is added in
 // the fragment layout of the warp instruction, tile by tile, so that no adapter's
 // values meet another's tokens.  256 tokens, 4096 -> 4096, 32 adapters of rank 32:
-// 24 us, bound by the L2 reads of x (64 KB/us a block; all of x for every 128 rows
-// of W, 64 MB) and the exchange of shares; 57 tokens, 2048 -> 512: 11 us, the chain
-// p, hand-over, join; 64 tokens, 4096 -> 14336, 16 adapters: 29 us, the ALU pipe
-// (the decode's byte permutes) 95% busy in the loop.  A fourth team, or coalesced
+// 22.3 us with inputs that stay in L2, 25.6 us with others in every call, bound by the
+// L2 reads of x (64 KB/us a block; all of x for every 128 rows of W, 64 MB) and the
+// exchange of shares; 57 tokens, 2048 -> 512: 12 us, the chain p, hand-over, join; 64
+// tokens, 4096 -> 14336, 16 adapters: 30 us, the ALU pipe (the decode's byte permutes)
+// 95% busy in the loop.  A fourth team, or coalesced
 // code loads, change nothing there; a quarter of the words by a table of byte pairs
 // gains 4%.
 namespace ads {
@@ -798,14 +800,14 @@ __global__ void __launch_bounds__(ads::kThreadsSplit + 128, 1)  // 96 registers:
 
 // Warp products for up to eight tokens, and for up to 16 of a matrix below 2^24 weights: with two token tiles their
 // reads of x and their decoding for every 16 rows cost more than the UMMA kernel's set-up (16 tokens, warp products
-// and UMMAs: 2048 -> 4096 10.3 and 14.4 us, 4096 -> 4096 16.4 and 16.4 us, 4096 -> 14336 46.6 and 30.7 us; 8 tokens
-// at 4096 -> 14336 26.7 and 28.7 us).
+// and UMMAs: 2048 -> 4096 9.2 and 10.6 us, 4096 -> 4096 14.4 and 15.2 us, 4096 -> 14336 42.6 and 29.7 us; 8 tokens
+// at 4096 -> 14336 24.6 and 26.9 us).
 bool adapter_gemv_serves(int T, int K, int N) {
   return T <= kTokenTile || (T <= 2 * kTokenTile && (int64_t)K * N < (1 << 24));
 }
 
 // Shares of K of the blocks of p of the warp products: as many as leave every block of the launch a place (two an
-// SM; with 24 of 320 blocks in a second wave, 16 tokens at 2048 -> 4096 took 8.7 us, not 7.5).
+// SM; with 24 of 320 blocks in a second wave, 16 tokens at 2048 -> 4096 take 10.5 us, not 9.2).
 int adapter_gemv_shares(int T, int r, int N) {
   const int items = T * ((r + 15) / 16), places = kPlaces - (N + 15) / 16;
   return 4 * items <= places ? 4 : (2 * items <= places ? 2 : 1);
