@@ -195,9 +195,9 @@ __device__ __forceinline__ void let_land(uint64_t* bars, int n, uint32_t issued,
 // parts' products took 720 cycles a chunk, against 512 in the tensor pipe: its
 // instruction stream, not the operands, was the limit.)  Units of three parts have
 // no slot to spare and are used for a single turn: 1111 tokens, 2048 -> 4096, the
-// whole call with 64 units of 384 rows 40.7 us, with 128 of 160 45.4 us.  Token rows are accumulator columns, so
-// an adapter's K = r product is issued at its own columns: adapters' rows start at
-// multiples of 32, the column granule of a pair UMMA.
+// whole call with 64 units of 384 rows 40.7 us, with 128 of 160 45.4 us.  Token rows
+// are accumulator columns, so an adapter's K = r product is issued at its own columns:
+// adapters' rows start at multiples of 32, the column granule of a pair UMMA.
 //
 // The issuers see both CTAs' operands on barriers of the even CTA: the odd CTA's
 // TMA loads count their bytes there, and its decode warps signal with a 4-byte
@@ -649,7 +649,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(adf::threads(PARTS),
 // pairs without one: a unit's chunks are a chain whose step is a decode (training
 // step of 777 tokens, 512 -> 2048: 62.7 us with NB = 2, 57.3 us with 1).  8192 rows of
 // 2048 columns over 2048: 77 us, 890 TFLOP/s, tensor pipe 50% active: 264 units on 74
-// pairs, the last of four turns a good half full.
+// pairs, 42 of them in the fourth turn.
 namespace adg {
 constexpr int BM = 128, BK = 64;
 constexpr int A_BYTES = BM * BK * 2;
